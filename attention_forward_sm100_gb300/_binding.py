@@ -101,6 +101,14 @@ def lib():
             L.attn_fwd_params_init.restype = None
             L.attn_fwd_params_size.argtypes = []
             L.attn_fwd_params_size.restype = ctypes.c_size_t
+            # parameter structs packed as bytes (see paged.py)
+            for name in ("attn_cache_append", "attn_cache_read", "attn_paged_fwd"):
+                getattr(L, name).argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+                getattr(L, name).restype = ctypes.c_int
+            L.attn_paged_workspace_bytes.argtypes = [ctypes.c_char_p]
+            L.attn_paged_workspace_bytes.restype = ctypes.c_size_t
+            L.attn_paged_params_size.argtypes = [ctypes.c_int32]
+            L.attn_paged_params_size.restype = ctypes.c_size_t
             L.attn_status_string.argtypes = [ctypes.c_int]
             L.attn_status_string.restype = ctypes.c_char_p
             L.attn_fwd_last_error.argtypes = []
@@ -116,6 +124,7 @@ def last_error() -> str:
 
 
 _workspaces = {}
+_paged_workspaces = {}   # (device index, stream handle) -> buffer of the paged-cache operators
 _workspaces_lock = threading.Lock()
 
 
@@ -429,16 +438,26 @@ def prepare(q, k, v, **kw) -> PreparedForward:
 
 
 def check(workspace=None, device=None, stream=None):
-    """Synchronises and raises if a kernel wait ran out of time."""
+    """Synchronises and raises if a kernel wait ran out of time, or if a call
+    found offsets, lengths or page numbers out of range on the device. Without
+    a ``workspace``, the default one of ``forward`` and the one the paged-cache
+    operators use on this stream are looked at."""
     L = lib()
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     ws = workspace if workspace is not None else default_workspace(dev)
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    st = L.attn_fwd_check(ctypes.c_void_p(ws.data_ptr()), ctypes.c_void_p(handle))
-    if st != ATTN_OK:
-        raise AttnError(st, last_error())
+    buffers = [ws]
+    if workspace is None:
+        index = dev.index if dev.index is not None else torch.cuda.current_device()
+        paged = _paged_workspaces.get((index, handle))
+        if paged is not None:
+            buffers.append(paged)
+    for buf in buffers:
+        st = L.attn_fwd_check(ctypes.c_void_p(buf.data_ptr()), ctypes.c_void_p(handle))
+        if st != ATTN_OK:
+            raise AttnError(st, last_error())
 
 
 def plan(p: Params) -> PlanInfo:

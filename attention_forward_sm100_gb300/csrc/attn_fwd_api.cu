@@ -500,6 +500,8 @@ attn_status af::report_error(attn_status st, const char* fmt, ...) {
   return st;
 }
 
+int af::sm_count() { return sm_count_cached(); }
+
 extern "C" {
 
 void attn_fwd_params_init(attn_fwd_params* p) {
@@ -548,6 +550,9 @@ attn_status attn_fwd_check(void* workspace, attn_stream_t stream) {
     cudaDeviceSynchronize();
     if (w[af::kWsErrorCode] == af::kDevErrBadSeqlens)
       return fail(ATTN_ERR_INVALID_ARG, "cu_seqlens of sequence %u are decreasing or exceed total_q / total_k "
+                  "(nothing of that call's output can be trusted)", info);
+    if (w[af::kWsErrorCode] == af::kDevErrBadCache)
+      return fail(ATTN_ERR_INVALID_ARG, "paged cache: a length, offset or page number of sequence %u is out of range "
                   "(nothing of that call's output can be trusted)", info);
     return fail(ATTN_ERR_DEVICE_TIMEOUT, "device wait timed out (code %u, block %u, role %u, barrier %u)",
                 w[af::kWsErrorCode], info >> 16, (info >> 8) & 0xffu, info & 0xffu);

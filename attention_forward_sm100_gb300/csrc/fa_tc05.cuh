@@ -55,9 +55,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include <atomic>
-
 #include "internal.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "schedule.cuh"
 
@@ -1285,34 +1284,6 @@ cudaLaunchConfig_t pair_config(int grid, cudaStream_t stream, cudaLaunchAttribut
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cfg;
-}
-
-// Raises a kernel's dynamic shared-memory limit once per device (the
-// attribute stays set for the life of the context); `force` sets it again
-// (after a context was torn down and recreated).
-template <auto KERN>
-cudaError_t set_smem_once(int bytes, bool force = false) {
-  static std::atomic<uint64_t> done{0};   // one per kernel
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? (1ull << dev) : 0ull;
-  if (!force && bit != 0ull && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && bit != 0ull) done.fetch_or(bit, std::memory_order_acq_rel);
-  return e;
-}
-
-// Launches `launch()`; if that fails, sets the kernel's shared-memory limit
-// again and retries once.
-template <auto KERN, class F>
-cudaError_t launch_with_smem(int bytes, F launch) {
-  cudaError_t e = set_smem_once<KERN>(bytes);
-  if (e != cudaSuccess) return e;
-  e = launch();
-  if (e == cudaSuccess) return e;
-  if ((e = set_smem_once<KERN>(bytes, true)) != cudaSuccess) return e;
-  return launch();
 }
 
 template <class T, int CAUSAL>

@@ -30,6 +30,7 @@ enum DeviceError : uint32_t {
   kDevErrNone = 0,
   kDevErrTimeout = 1,
   kDevErrBadSeqlens = 3,   // packed offsets out of order or past total_q / total_k (info: sequence)
+  kDevErrBadCache = 4,     // paged cache: a length, offset or page number out of range (info: sequence)
 };
 
 // Everything the tcgen05 kernel needs, passed as one __grid_constant__ struct.
@@ -103,6 +104,9 @@ struct Tc05Config {
 // Records the calling thread's last-error text (attn_fwd_last_error) and
 // returns `st`.
 attn_status report_error(attn_status st, const char* fmt, ...);
+
+// SMs of the current device (148 when it cannot be asked).
+int sm_count();
 
 // Static configuration of a variant (host).
 Tc05Config tc05_config(int variant);

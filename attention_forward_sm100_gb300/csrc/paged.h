@@ -1,0 +1,132 @@
+// Declarations shared by the paged-cache kernels and their host API.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/attn_paged.h"
+#include "internal.h"
+
+namespace af {
+
+constexpr int kStreamTile = 64;      // keys per work unit of the streaming attention kernel
+constexpr int kMinPage = 16;         // smallest page: one warp's step of keys lies in one page
+
+// The cache as the kernels see it; strides in bytes.
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  int64_t k_page, k_tok, k_head;
+  int64_t v_page, v_tok, v_head;
+  int64_t table_stride;   // elements
+  int32_t num_pages, page_shift, max_pages, heads_kv;
+};
+
+// The new rows of each sequence (fixed: b * seqlen_q; packed: cu_q) and the
+// cached lengths.
+struct NewRows {
+  const int32_t* cu_q;       // NULL when fixed
+  const int32_t* seqlens_k;
+  int32_t batch, seqlen_q, total_q, max_k;
+};
+
+struct AppendParams {
+  CacheView c;
+  NewRows s;
+  const uint8_t* k;
+  const uint8_t* v;
+  int64_t k_b, k_t, k_h, v_b, v_t, v_h;   // bytes
+  int64_t tokens;
+  uint32_t* ws;
+};
+
+struct ReadParams {
+  CacheView c;
+  const int32_t* cu_k;
+  uint8_t* k;
+  uint8_t* v;
+  int64_t k_t, k_h, v_t, v_h;   // bytes
+  int32_t batch, total_k;
+  uint32_t* ws;
+};
+
+// One CTA's segment that continues in later CTAs (streaming kernel to merge).
+struct StreamMeta {
+  int32_t b;      // sequence, or -1: no such segment
+  int32_t seg;    // row tile * Hkv + KV head
+  int32_t last;   // CTA that ends the segment
+  int32_t pad;
+};
+
+struct StreamParams {
+  CacheView c;
+  NewRows s;
+  const uint8_t* q;
+  int64_t q_b, q_t, q_h;     // bytes
+  uint16_t* o;
+  float* lse;
+  int64_t o_b, o_t, o_h;     // elements
+  int32_t heads_q, group, causal;
+  int32_t split;             // 1: units are key tiles, segments may span CTAs; 0: units are segments
+  float scale_log2;
+  uint32_t* ws;
+  StreamMeta* meta;          // [grid]
+  float2* part_ml;           // [2 * grid][rows]: running maximum (log2 units) and sum
+  float* part_o;             // [2 * grid][rows][D], not normalised
+};
+
+cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream);
+cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream);
+// Streaming attention over `grid` CTAs with row tiles of 16 * row_groups rows
+// (1, 2 or 4), then the merge of split segments if p.split.
+cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_groups, int grid,
+                                cudaStream_t stream);
+
+#ifdef __CUDACC__
+// Records the first invalid length, offset or page of a call.
+__device__ __forceinline__ void record_bad_cache(uint32_t* ws, int b) {
+  if (atomicCAS(&ws[kWsErrorCode], 0u, (uint32_t)kDevErrBadCache) == 0u) atomicExch(&ws[kWsErrorInfo], (uint32_t)b);
+}
+
+struct SeqRows {
+  int lq, lk, q0;   // new rows, cached keys, first row (packed) or 0
+};
+
+// Lengths of sequence b; out of range ones are recorded and cut to what the
+// tensors hold.
+__device__ __forceinline__ SeqRows load_seq(const NewRows& s, int b, uint32_t* ws) {
+  SeqRows r;
+  r.lk = s.seqlens_k[b];
+  r.lq = s.seqlen_q;
+  r.q0 = 0;
+  bool bad = r.lk < 0 || r.lk > s.max_k;
+  if (bad) r.lk = r.lk < 0 ? 0 : s.max_k;
+  if (s.cu_q != nullptr) {
+    const int a = s.cu_q[b], e = s.cu_q[b + 1];
+    r.q0 = a;
+    r.lq = e - a;
+    if (a < 0 || e < a || e > s.total_q) {
+      bad = true;
+      r.q0 = r.lq = 0;
+    } else if (r.lq > s.seqlen_q) {
+      bad = true;
+      r.lq = s.seqlen_q;
+    }
+  }
+  if (bad) record_bad_cache(ws, b);
+  return r;
+}
+
+// Page of column `col` of sequence b's table row; a number outside the cache
+// is recorded and replaced by page 0.
+__device__ __forceinline__ int load_page(const CacheView& c, int b, int col, uint32_t* ws) {
+  const int p = __ldg(c.table + (int64_t)b * c.table_stride + col);
+  if ((unsigned)p < (unsigned)c.num_pages) return p;
+  record_bad_cache(ws, b);
+  return 0;
+}
+#endif
+
+}  // namespace af

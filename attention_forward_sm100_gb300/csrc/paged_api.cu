@@ -1,0 +1,298 @@
+// Host side of the C ABI declared in include/attn_paged.h: argument
+// validation, launch planning and workspace layout of the paged-cache
+// operators.
+#include <string.h>
+
+#include "paged.h"
+#include "schedule.cuh"
+
+namespace {
+
+using af::report_error;
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+attn_status check_cache(const attn_kv_cache& c) {
+  if (c.dtype != ATTN_DTYPE_BF16 && c.dtype != ATTN_DTYPE_FP8_E4M3)
+    return report_error(ATTN_ERR_INVALID_ARG, "unknown cache dtype %d", c.dtype);
+  if (c.batch < 0 || c.max_pages < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative batch or max_pages");
+  if (c.num_pages <= 0 || c.num_heads_kv <= 0)
+    return report_error(ATTN_ERR_INVALID_ARG, "the cache needs at least one page and one head");
+  if (c.head_dim != 64 && c.head_dim != 128)
+    return report_error(ATTN_ERR_UNSUPPORTED, "head_dim %d: the paged cache supports 64 and 128", c.head_dim);
+  if (c.page_size < af::kMinPage || c.page_size > 65536 || (c.page_size & (c.page_size - 1)))
+    return report_error(ATTN_ERR_UNSUPPORTED, "page_size %d is not a power of two from %d to 65536", c.page_size,
+                        af::kMinPage);
+  if ((int64_t)c.max_pages * c.page_size > 0x7fff0000ll)
+    return report_error(ATTN_ERR_UNSUPPORTED, "max_pages * page_size is past 2^31");
+  if (c.k == nullptr || c.v == nullptr || !aligned(c.k, 16) || !aligned(c.v, 16))
+    return report_error(ATTN_ERR_INVALID_ARG, "cache k and v must be non-NULL and 16-byte aligned");
+  if (c.batch > 0 && c.max_pages > 0 && (c.block_table == nullptr || !aligned(c.block_table, 4)))
+    return report_error(ATTN_ERR_INVALID_ARG, "block_table must be non-NULL and 4-byte aligned");
+  if (c.table_stride < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative table_stride");
+  const int es = c.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2;
+  for (int i = 0; i < 3; ++i) {
+    if (c.k_stride[i] < 0 || c.v_stride[i] < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative cache stride");
+    if ((c.k_stride[i] * es) % 16 || (c.v_stride[i] * es) % 16)
+      return report_error(ATTN_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
+  }
+  if (c.dtype == ATTN_DTYPE_FP8_E4M3) {
+    if (c.k_scale == nullptr || c.v_scale == nullptr || !aligned(c.k_scale, 16) || !aligned(c.v_scale, 16))
+      return report_error(ATTN_ERR_INVALID_ARG, "an e4m3 cache needs 16-byte aligned k_scale and v_scale");
+  }
+  return ATTN_OK;
+}
+
+attn_status check_rows(const char* what, const void* p, const int64_t* stride, int first, int n) {
+  if (p == nullptr || !aligned(p, 16))
+    return report_error(ATTN_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", what);
+  for (int i = first; i < n; ++i)
+    if (stride[i] < 0 || (stride[i] * 2) % 16)
+      return report_error(ATTN_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes", what);
+  return ATTN_OK;
+}
+
+attn_status check_offsets(const char* what, const int32_t* p, bool needed) {
+  if ((needed && p == nullptr) || !aligned(p, 4))
+    return report_error(ATTN_ERR_INVALID_ARG, "%s must be non-NULL and 4-byte aligned", what);
+  return ATTN_OK;
+}
+
+attn_status check_workspace(const void* ws) {
+  if (ws == nullptr || !aligned(ws, 256))
+    return report_error(ATTN_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+  return ATTN_OK;
+}
+
+af::CacheView view_of(const attn_kv_cache& c) {
+  const int es = c.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2;
+  af::CacheView v;
+  v.k = static_cast<uint8_t*>(c.k);
+  v.v = static_cast<uint8_t*>(c.v);
+  v.k_scale = c.k_scale;
+  v.v_scale = c.v_scale;
+  v.table = c.block_table;
+  v.k_page = c.k_stride[0] * es;
+  v.k_tok = c.k_stride[1] * es;
+  v.k_head = c.k_stride[2] * es;
+  v.v_page = c.v_stride[0] * es;
+  v.v_tok = c.v_stride[1] * es;
+  v.v_head = c.v_stride[2] * es;
+  v.table_stride = c.table_stride;
+  v.num_pages = c.num_pages;
+  v.page_shift = 0;
+  while ((1 << v.page_shift) < c.page_size) ++v.page_shift;
+  v.max_pages = c.max_pages;
+  v.heads_kv = c.num_heads_kv;
+  return v;
+}
+
+attn_status check_append(const attn_cache_append_params* p) {
+  if (p == nullptr) return report_error(ATTN_ERR_INVALID_ARG, "params is NULL");
+  attn_status st = check_cache(p->cache);
+  if (st != ATTN_OK) return st;
+  if (p->seqlen_q < 0 || p->total_q < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative size");
+  const bool packed = p->cu_seqlens_q != nullptr;
+  if (p->cache.batch == 0 || (packed ? p->total_q : p->seqlen_q) == 0) return ATTN_OK;
+  if ((st = check_rows("k", p->k, p->k_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
+  if ((st = check_rows("v", p->v, p->v_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
+  if ((st = check_offsets("seqlens_k", p->seqlens_k, true)) != ATTN_OK) return st;
+  if ((st = check_offsets("cu_seqlens_q", p->cu_seqlens_q, false)) != ATTN_OK) return st;
+  return check_workspace(p->workspace);
+}
+
+attn_status check_read(const attn_cache_read_params* p) {
+  if (p == nullptr) return report_error(ATTN_ERR_INVALID_ARG, "params is NULL");
+  attn_status st = check_cache(p->cache);
+  if (st != ATTN_OK) return st;
+  if (p->total_k < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative size");
+  if (p->cache.batch == 0 || p->total_k == 0) return ATTN_OK;
+  if ((st = check_rows("k", p->k, p->k_stride, 0, 2)) != ATTN_OK) return st;
+  if ((st = check_rows("v", p->v, p->v_stride, 0, 2)) != ATTN_OK) return st;
+  if ((st = check_offsets("cu_seqlens_k", p->cu_seqlens_k, true)) != ATTN_OK) return st;
+  return check_workspace(p->workspace);
+}
+
+bool no_rows(const attn_paged_params* p) {
+  return p->cache.batch == 0 || p->seqlen_q == 0 || (p->cu_seqlens_q != nullptr && p->total_q == 0);
+}
+
+// Everything but the workspace.
+attn_status check_paged(const attn_paged_params* p) {
+  if (p == nullptr) return report_error(ATTN_ERR_INVALID_ARG, "params is NULL");
+  attn_status st = check_cache(p->cache);
+  if (st != ATTN_OK) return st;
+  const attn_kv_cache& c = p->cache;
+  if (p->seqlen_q < 0 || p->seqlen_k < 0 || p->total_q < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative size");
+  if (p->num_heads_q <= 0 || p->num_heads_q % c.num_heads_kv)
+    return report_error(ATTN_ERR_INVALID_ARG, "num_heads_q %d is not a positive multiple of num_heads_kv %d",
+                        p->num_heads_q, c.num_heads_kv);
+  if (!(p->softmax_scale > 0.f)) return report_error(ATTN_ERR_INVALID_ARG, "softmax_scale must be a positive number");
+  if (p->seqlen_k > (int64_t)c.max_pages * c.page_size)
+    return report_error(ATTN_ERR_INVALID_ARG, "seqlen_k %d is past max_pages * page_size", p->seqlen_k);
+  if (no_rows(p)) return ATTN_OK;
+  const bool packed = p->cu_seqlens_q != nullptr;
+  if ((st = check_rows("q", p->q, p->q_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
+  if ((st = check_rows("o", p->o, p->o_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
+  if ((st = check_offsets("seqlens_k", p->seqlens_k, true)) != ATTN_OK) return st;
+  if ((st = check_offsets("cu_seqlens_q", p->cu_seqlens_q, false)) != ATTN_OK) return st;
+  if (!aligned(p->lse, 4)) return report_error(ATTN_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  return ATTN_OK;
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct StreamPlan {
+  int row_groups;      // 16-row groups of a row tile
+  int split;
+  int64_t grid;
+  int64_t units;       // upper bound of the work units
+  size_t meta_bytes, ml_bytes, o_bytes;
+};
+
+// Row tiles of 16, 32 or 64 rows, the smallest that holds a sequence's rows;
+// two CTAs per SM. Segments of up to kUnsplitTiles key tiles are not cut: the
+// merge would cost more than the longer CTA.
+constexpr int kUnsplitTiles = 4;
+StreamPlan plan_stream(const attn_paged_params* p) {
+  StreamPlan s = {};
+  const int64_t rows = (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
+  s.row_groups = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  const int64_t rt = 16 * s.row_groups;
+  const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
+  const int64_t tiles = af::tiles_for(p->seqlen_k, af::kStreamTile);
+  s.split = tiles > kUnsplitTiles ? 1 : 0;
+  s.units = segments * (s.split ? tiles : 1);
+  const int64_t most = s.split ? 2ll * af::sm_count() : s.units;
+  s.grid = s.units < most ? s.units : most;
+  if (s.split) {
+    s.meta_bytes = round256((size_t)s.grid * sizeof(af::StreamMeta));
+    s.ml_bytes = round256((size_t)(2 * s.grid * rt) * sizeof(float2));
+    s.o_bytes = (size_t)(2 * s.grid * rt) * p->cache.head_dim * sizeof(float);
+  }
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_paged_params_size(int32_t which) {
+  switch (which) {
+    case 0: return sizeof(attn_cache_append_params);
+    case 1: return sizeof(attn_cache_read_params);
+    case 2: return sizeof(attn_paged_params);
+  }
+  return 0;
+}
+
+attn_status attn_cache_append(const attn_cache_append_params* p, attn_stream_t stream) {
+  report_error(ATTN_OK, "%s", "");
+  const attn_status st = check_append(p);
+  if (st != ATTN_OK) return st;
+  const bool packed = p->cu_seqlens_q != nullptr;
+  if (p->cache.batch == 0 || (packed ? p->total_q : p->seqlen_q) == 0) return ATTN_OK;
+  af::AppendParams a;
+  memset(&a, 0, sizeof(a));
+  a.c = view_of(p->cache);
+  a.s.cu_q = p->cu_seqlens_q;
+  a.s.seqlens_k = p->seqlens_k;
+  a.s.batch = p->cache.batch;
+  a.s.seqlen_q = p->seqlen_q;
+  a.s.total_q = p->total_q;
+  a.s.max_k = p->cache.max_pages * p->cache.page_size;
+  a.k = static_cast<const uint8_t*>(p->k);
+  a.v = static_cast<const uint8_t*>(p->v);
+  a.k_b = packed ? 0 : p->k_stride[0] * 2;
+  a.k_t = p->k_stride[1] * 2;
+  a.k_h = p->k_stride[2] * 2;
+  a.v_b = packed ? 0 : p->v_stride[0] * 2;
+  a.v_t = p->v_stride[1] * 2;
+  a.v_h = p->v_stride[2] * 2;
+  a.tokens = packed ? p->total_q : (int64_t)p->cache.batch * p->seqlen_q;
+  a.ws = static_cast<uint32_t*>(p->workspace);
+  const cudaError_t e = af::cache_append_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3,
+                                                reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "cache append launch failed: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t stream) {
+  report_error(ATTN_OK, "%s", "");
+  const attn_status st = check_read(p);
+  if (st != ATTN_OK) return st;
+  if (p->cache.batch == 0 || p->total_k == 0) return ATTN_OK;
+  af::ReadParams r;
+  memset(&r, 0, sizeof(r));
+  r.c = view_of(p->cache);
+  r.cu_k = p->cu_seqlens_k;
+  r.k = static_cast<uint8_t*>(p->k);
+  r.v = static_cast<uint8_t*>(p->v);
+  r.k_t = p->k_stride[0] * 2;
+  r.k_h = p->k_stride[1] * 2;
+  r.v_t = p->v_stride[0] * 2;
+  r.v_h = p->v_stride[1] * 2;
+  r.batch = p->cache.batch;
+  r.total_k = p->total_k;
+  r.ws = static_cast<uint32_t*>(p->workspace);
+  const cudaError_t e = af::cache_read_launch(r, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3,
+                                              reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "cache read launch failed: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+size_t attn_paged_workspace_bytes(const attn_paged_params* p) {
+  if (check_paged(p) != ATTN_OK || no_rows(p)) return ATTN_FWD_WORKSPACE_BYTES;
+  const StreamPlan s = plan_stream(p);
+  return ATTN_FWD_WORKSPACE_BYTES + s.meta_bytes + s.ml_bytes + s.o_bytes;
+}
+
+attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
+  report_error(ATTN_OK, "%s", "");
+  attn_status st = check_paged(p);
+  if (st != ATTN_OK) return st;
+  if (no_rows(p)) return ATTN_OK;
+  if ((st = check_workspace(p->workspace)) != ATTN_OK) return st;
+  const StreamPlan plan = plan_stream(p);
+  const size_t need = ATTN_FWD_WORKSPACE_BYTES + plan.meta_bytes + plan.ml_bytes + plan.o_bytes;
+  if (p->workspace_bytes < need)
+    return report_error(ATTN_ERR_INVALID_ARG, "workspace of at least %zu bytes is required", need);
+  if (plan.units > 0x3fffffffll) return report_error(ATTN_ERR_UNSUPPORTED, "too much work for one call");
+  const bool packed = p->cu_seqlens_q != nullptr;
+  af::StreamParams a;
+  memset(&a, 0, sizeof(a));
+  a.c = view_of(p->cache);
+  a.s.cu_q = p->cu_seqlens_q;
+  a.s.seqlens_k = p->seqlens_k;
+  a.s.batch = p->cache.batch;
+  a.s.seqlen_q = p->seqlen_q;
+  a.s.total_q = p->total_q;
+  a.s.max_k = p->seqlen_k;
+  a.q = static_cast<const uint8_t*>(p->q);
+  a.q_b = packed ? 0 : p->q_stride[0] * 2;
+  a.q_t = p->q_stride[1] * 2;
+  a.q_h = p->q_stride[2] * 2;
+  a.o = static_cast<uint16_t*>(p->o);
+  a.o_b = packed ? 0 : p->o_stride[0];
+  a.o_t = p->o_stride[1];
+  a.o_h = p->o_stride[2];
+  a.lse = p->lse;
+  a.heads_q = p->num_heads_q;
+  a.group = p->num_heads_q / p->cache.num_heads_kv;
+  a.causal = p->causal != 0;
+  a.split = plan.split;
+  a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+  a.ws = reinterpret_cast<uint32_t*>(ws);
+  ws += ATTN_FWD_WORKSPACE_BYTES;
+  a.meta = reinterpret_cast<af::StreamMeta*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + plan.meta_bytes);
+  a.part_o = reinterpret_cast<float*>(ws + plan.meta_bytes + plan.ml_bytes);
+  const cudaError_t e =
+      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_groups,
+                              (int)plan.grid, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
+
+}  // extern "C"

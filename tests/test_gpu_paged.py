@@ -1,0 +1,409 @@
+"""The paged-cache operators on the GPU against their definitions in 64 bits:
+writing (bit for bit), reading back (bit for bit), attention (every element
+within the bound its roundings imply), what only the device can refuse, and
+runs of them together. Slots that no sequence holds are NaN throughout, and
+table columns past a sequence's pages hold numbers outside the cache."""
+import math
+
+import pytest
+import torch
+
+import paged_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import attention_forward_sm100_gb300 as m
+    return m
+
+
+# ---------------------------------------------------------------- append
+APPEND = {
+    # lens_k, lens_q, Hkv, D, page, packed, head-major
+    "one_token": ([1], [1], 1, 64, 16, False, False),
+    "step": ([5, 16, 17, 300], [1] * 4, 8, 128, 16, False, False),
+    "chunk_crosses_pages": ([40, 100], [37, 37], 2, 128, 16, False, True),
+    "packed_ragged": ([70, 9, 200, 33], [70, 1, 0, 30], 3, 64, 32, True, False),
+    "packed_first_empty": ([8, 0, 130, 4], [0, 0, 129, 0], 5, 128, 64, True, True),
+    "many_sequences": ([3 + b % 40 for b in range(300)], [1 + b % 3 for b in range(300)], 1, 64, 16, True, False),
+    "long": ([5000, 4097], [4090, 4090], 4, 128, 128, False, False),
+}
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("name", list(APPEND))
+def test_append_writes_exactly_its_slots(pkg, name, fp8):
+    lens_k, lens_q, hkv, dim, page, packed, head_major = APPEND[name]
+    p = R.make(lens_k, lens_q, hkv, hkv, dim, page, fp8=fp8, packed=packed, head_major=head_major, seed=3)
+    want = R.append(p)
+    pkg.cache_append(p.k_new, p.v_new, *p.cache, cu_seqlens_q=p.cu_q, **p.scales)
+    pkg.check()
+    got = (p.k_cache, p.v_cache, p.k_scale, p.v_scale)
+    for g, w in zip(got, want):
+        assert (g is None) == (w is None)
+        if g is not None:
+            assert torch.equal(R.bits(g), R.bits(w))
+
+
+def test_append_e4m3_of_special_values(pkg):
+    """Zeros, subnormals, the largest finite values, ties, infinities and NaN."""
+    p = R.make([24], [24], 2, 2, 64, 16, fp8=True, seed=5)
+    x = p.k_new
+    x[0, 0] = 0.0
+    x[0, 1] = 2.0 ** -133                      # the smallest bf16
+    x[0, 2, 0] = 2.0 ** -126
+    x[0, 3] = torch.finfo(torch.bfloat16).max
+    x[0, 4, 0, 3] = math.inf
+    x[0, 5, 1, 7] = -math.inf
+    x[0, 6, 0, 9] = math.nan
+    x[0, 7] = math.inf
+    x[0, 8] = math.nan
+    x[0, 9] = 448.0
+    x[0, 10] = 450.0                           # just past 448: the next scale
+    x[0, 11] = torch.linspace(-447, 447, 64).to(torch.bfloat16)
+    x[0, 12] = (torch.arange(64) * 0.0625 + 16).to(torch.bfloat16)   # ties of the 3-bit mantissa
+    x[0, 13, :, 0] = 3.0e38
+    want = R.append(p)
+    pkg.cache_append(p.k_new, p.v_new, *p.cache, **p.scales)
+    pkg.check()
+    for g, w in zip((p.k_cache, p.v_cache, p.k_scale, p.v_scale), want):
+        if g.dtype == R.E4M3:   # NaN has two codes
+            g, w = g.float(), w.float()
+            assert torch.equal(torch.isnan(g), torch.isnan(w))
+            g, w = g.nan_to_num(-1.0), w.nan_to_num(-1.0)
+        assert torch.equal(R.bits(g), R.bits(w))
+
+
+def test_append_leaves_rows_behind_the_last_sequence(pkg):
+    p = R.make([20, 30], [5, 7], 2, 2, 64, 16, packed=True, seed=6)
+    want = R.append(p)
+    tail = torch.full((9, 2, 64), math.nan, dtype=torch.bfloat16, device="cuda")
+    pkg.cache_append(torch.cat([p.k_new, tail]), torch.cat([p.v_new, tail]), *p.cache, cu_seqlens_q=p.cu_q)
+    pkg.check()
+    assert torch.equal(R.bits(p.k_cache), R.bits(want[0])) and torch.equal(R.bits(p.v_cache), R.bits(want[1]))
+
+
+# ---------------------------------------------------------------- read
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lens_k,hkv,dim,page,head_major", [
+    ([1], 1, 64, 16, False), ([33, 0, 64, 1, 250], 3, 128, 32, True), ([3000, 2049], 8, 128, 64, False),
+    ([1 + b % 7 for b in range(200)], 2, 64, 16, False)])
+def test_read_gives_the_cached_values(pkg, lens_k, hkv, dim, page, head_major, fp8):
+    p = R.make(lens_k, [0] * len(lens_k), hkv, hkv, dim, page, fp8=fp8, packed=True, head_major=head_major, seed=7)
+    total = sum(lens_k)
+    cu = torch.tensor([sum(lens_k[:b]) for b in range(len(lens_k) + 1)], dtype=torch.int32, device="cuda")
+    k, v = pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, total_k=total, **p.scales)
+    # strided outputs with rows behind the last sequence
+    both = torch.full((total + 5, 2, hkv, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, out_k=both[:, 0], out_v=both[:, 1], **p.scales)
+    pkg.check()
+    want = [torch.cat(x).to(torch.bfloat16) for x in zip(*(R.gather(p, b) for b in range(len(lens_k))))]
+    assert torch.equal(R.bits(k), R.bits(want[0])) and torch.equal(R.bits(v), R.bits(want[1]))
+    assert torch.equal(R.bits(both[:total, 0]), R.bits(want[0])) and torch.equal(R.bits(both[:total, 1]), R.bits(want[1]))
+    assert bool((both[total:] == 7.0).all())
+
+
+# ---------------------------------------------------------------- attend
+ATTEND = {
+    # lens_k, lens_q, Hq, Hkv, D, page, packed, head-major
+    "one_key": ([1], [1], 1, 1, 64, 16, False, False),
+    "short": ([7, 16, 17, 63], [1] * 4, 8, 2, 128, 16, False, False),
+    "two_tiles": ([64, 65, 128, 129], [1] * 4, 4, 4, 64, 32, False, True),
+    "decode": ([1000, 3, 2049, 777], [1] * 4, 32, 8, 128, 64, False, False),
+    "decode_mha": ([515, 2000], [1, 1], 16, 16, 64, 16, False, False),
+    "decode_mqa": ([4000], [1], 16, 1, 128, 128, False, False),
+    "decode_group_5": ([333, 1200], [1, 1], 15, 3, 128, 32, False, True),
+    "decode_group_20": ([900, 40], [1, 1], 20, 1, 64, 16, False, False),
+    "decode_group_71": ([700], [1], 71, 1, 64, 64, False, False),
+    "verify_5": ([300, 5, 1111], [5] * 3, 8, 4, 128, 16, False, False),
+    "verify_more_new_than_cached": ([3, 1, 20], [6] * 3, 4, 2, 64, 16, False, False),
+    "rows_33_of_64": ([500, 70], [11, 11], 3, 1, 128, 32, False, False),
+    "empty_cache": ([0, 10, 0], [1] * 3, 4, 2, 64, 16, False, False),
+    "packed_ragged": ([600, 0, 33, 1025, 64], [3, 0, 1, 9, 0], 8, 2, 128, 16, True, False),
+    "packed_empty_keys": ([0, 40], [4, 4], 2, 2, 64, 16, True, False),
+    "chunk_100": ([100, 260], [100, 100], 4, 2, 128, 64, False, False),
+    "chunk_whole_prompt": ([257], [257], 8, 2, 64, 16, False, True),
+    "chunk_packed": ([400, 1300, 129], [129, 1, 128], 6, 2, 128, 32, True, False),
+    "chunk_late": ([3000], [200], 8, 1, 128, 128, False, False),
+    "chunk_more_new_than_cached": ([150, 300, 1], [300] * 3, 4, 2, 128, 16, False, False),
+    "many_sequences": ([1 + 13 * b % 700 for b in range(150)], [1] * 150, 4, 2, 64, 16, False, False),
+    "large_page": ([5000, 1], [2, 2], 8, 8, 128, 4096, False, False),
+}
+
+
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("name", list(ATTEND))
+def test_attend(pkg, name, fp8, causal):
+    lens_k, lens_q, hq, hkv, dim, page, packed, head_major = ATTEND[name]
+    p = R.make(lens_k, lens_q, hq, hkv, dim, page, fp8=fp8, packed=packed, head_major=head_major, seed=11)
+    o, lse = pkg.paged_forward(p.q, *p.cache, causal=causal, cu_seqlens_q=p.cu_q,
+                               max_seqlen_q=max(lens_q) if packed else None, **p.scales)
+    pkg.check()
+    R.check_attend(p, o, lse, causal)
+    again, lse2 = pkg.paged_forward(p.q, *p.cache, causal=causal, cu_seqlens_q=p.cu_q,
+                                    max_seqlen_q=max(lens_q) if packed else None, **p.scales)
+    assert torch.equal(R.bits(o), R.bits(again)) and torch.equal(R.bits(lse), R.bits(lse2))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_attend_long_context_of_few_rows(pkg, fp8):
+    """One KV head over 70000 keys: every CTA holds a part of one segment."""
+    p = R.make([70000], [1], 2, 1, 128, 64, fp8=fp8, seed=12)
+    o, lse = pkg.paged_forward(p.q, *p.cache, **p.scales)
+    pkg.check()
+    R.check_attend(p, o, lse, True)
+
+
+def test_attend_large_scores(pkg):
+    """Scores of both signs in the thousands: the running maximum has to move
+    and no exponential may overflow. (The reference bound for LSE assumes
+    ordinary scores: here it is one ulp of the score's magnitude, 2^-11, times
+    the few roundings on its way.)"""
+    p = R.make([700, 90], [3, 3], 4, 2, 64, 16, seed=13)
+    p.q *= 200
+    o, lse = pkg.paged_forward(p.q, *p.cache, softmax_scale=1.0)
+    pkg.check()
+    for b, (ro, rl, ra) in enumerate(R.attend(p, True, 1.0)):
+        assert torch.isfinite(lse[b]).all() and torch.isfinite(o[b].float()).all()
+        assert (lse[b].double() - rl).abs().max() <= 8 * 2.0 ** -24 * rl.abs().max() * 8
+
+
+def test_attend_views_and_scale(pkg):
+    """q inside a fused projection, out inside a wider tensor, a table that is
+    a view of a larger one, a bound on the lengths, no LSE."""
+    p = R.make([130, 70], [2, 2], 8, 2, 128, 32, seed=14)
+    fused = torch.randn(2, 2, 12, 128, device="cuda").to(torch.bfloat16)
+    fused[:, :, 2:10] = p.q
+    wide = torch.zeros(2, 2, 8, 256, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((2, 40), -5, dtype=torch.int32, device="cuda")
+    table[:, :p.table.shape[1]] = p.table
+    o, lse = pkg.paged_forward(fused[:, :, 2:10], p.k_cache, p.v_cache, table[:, :p.table.shape[1]], p.seqlens,
+                               softmax_scale=0.3, max_seqlen_k=130, out=wide[..., 128:], return_lse=False)
+    pkg.check()
+    assert lse is None and bool((wide[..., :128] == 0).all())
+    _, l = pkg.paged_forward(p.q, *p.cache, softmax_scale=0.3)
+    R.check_attend(p, o, l, True, 0.3)
+
+
+def test_attend_leaves_rows_behind_the_last_sequence(pkg):
+    for lens_q, hq in (([2, 1], 4), ([150, 90], 4)):
+        p = R.make([300, 95], lens_q, hq, 2, 64, 16, packed=True, seed=15)
+        n = sum(lens_q)
+        q = torch.cat([p.q, torch.full((6, hq, 64), math.nan, dtype=torch.bfloat16, device="cuda")])
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((hq, n + 6), 7.0, device="cuda")
+        pkg.paged_forward(q, *p.cache, cu_seqlens_q=p.cu_q, max_seqlen_q=max(lens_q), out=out, lse=lse)
+        pkg.check()
+        assert bool((out[n:] == 7.0).all()) and bool((lse[:, n:] == 7.0).all())
+        R.check_attend(p, out[:n], lse[:, :n], True)
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_cache_beyond_32_bit_offsets(pkg, new):
+    """Pages whose element offsets pass 2^31 (a 4.4 GB K cache)."""
+    p = R.make([new + 40], [new], 4, 2, 128, 64, seed=16, high_pages=(1 << 31) // (64 * 2 * 128) + 3)
+    pkg.cache_append(p.k_new, p.v_new, *p.cache)
+    o, lse = pkg.paged_forward(p.q, *p.cache)
+    pkg.check()
+    R.check_attend(p, o, lse, True)
+    k, _ = R.gather(p, 0)
+    assert torch.equal(k[-new:], p.k_new[0].double())
+    cu = torch.tensor([0, new + 40], dtype=torch.int32, device="cuda")
+    kr, _ = pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, total_k=new + 40)
+    assert torch.equal(kr.double(), k)
+
+
+# ---------------------------------------------------------------- what only the device sees
+def _bad(pkg, p, **kw):
+    with pytest.raises(pkg.AttnError, match="paged cache"):
+        pkg.check()
+    pkg.check()   # reported once
+
+
+@pytest.mark.parametrize("new", [1, 130])
+@pytest.mark.parametrize("what", ["page_high", "page_negative", "length_high", "length_negative", "offsets"])
+def test_bad_device_values_are_reported(pkg, what, new):
+    """Reported by check(); rows of the other sequence are right, nothing faults."""
+    packed = what == "offsets"
+    p = R.make([200, 150], [new] * 2, 4, 2, 64, 16, packed=packed, seed=17)
+    table, seqlens, cu = p.table.clone(), p.seqlens.clone(), p.cu_q
+    if what == "page_high":
+        table[1, 3] = p.k_cache.shape[0]
+    elif what == "page_negative":
+        table[1, 0] = -1
+    elif what == "length_high":
+        seqlens[1] = 1 << 30
+    elif what == "length_negative":
+        seqlens[1] = -4
+    else:
+        cu = torch.tensor([0, new, new - 1], dtype=torch.int32, device="cuda")
+    before = p.k_cache.clone()
+    o, lse = pkg.paged_forward(p.q, p.k_cache, p.v_cache, table, seqlens, cu_seqlens_q=cu,
+                               max_seqlen_q=new if packed else None)
+    _bad(pkg, p)
+    (ro, rl, ra) = R.attend(p, True)[0]
+    got = o[:new] if packed else o[0]
+    assert ((got.double() - ro).abs() <= 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14) * ra + 1e-6).all()
+    # append: pages that no longer hold sequence 1 are not written
+    if what != "offsets":
+        if what.startswith("page"):
+            table[1] = -1 if what == "page_negative" else p.k_cache.shape[0]
+        pkg.cache_append(p.k_new, p.v_new, p.k_cache, p.v_cache, table, seqlens)
+        _bad(pkg, p)
+        for b, c in ((1, c) for c in range(10)):
+            at = int(p.table[b, c])
+            assert torch.equal(R.bits(p.k_cache[at]), R.bits(before[at]))
+
+
+def test_bad_reads_are_reported(pkg):
+    p = R.make([40, 30], [1, 1], 2, 2, 64, 16, seed=18)
+    out = torch.full((70, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    long = torch.tensor([0, 40, 40 + 16 * p.table.shape[1] + 1], dtype=torch.int32, device="cuda")
+    n = int(long[-1])
+    big = torch.full((n, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    table = p.table.clamp(max=p.k_cache.shape[0] - 1)   # every column names a page
+    pkg.cache_read(p.k_cache, p.v_cache, table, long, out_k=big, out_v=big.clone())
+    _bad(pkg, p)
+    assert bool((big[n - 1] == 7.0).all())
+    table = p.table.clone()
+    table[1, 1] = -7
+    cu = torch.tensor([0, 40, 70], dtype=torch.int32, device="cuda")
+    pkg.cache_read(p.k_cache, p.v_cache, table, cu, out_k=out, out_v=out.clone())
+    _bad(pkg, p)
+    assert bool((out[40 + 16:] == 7.0).all())
+    assert torch.equal(out[:40].double(), R.gather(p, 0)[0])
+
+
+# ---------------------------------------------------------------- as they are used
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_prompt_chunks_then_steps_match_contiguous_attention(pkg, fp8):
+    """Two prompts enter the cache in chunks, tokens follow one by one; every
+    output matches forward()'s causal attention over what cache_read returns
+    (both round the same quantities, so their difference is at most twice the
+    bound of one)."""
+    hq, hkv, dim, page, n = 8, 2, 128, 32, 333
+    g = torch.Generator(device="cuda").manual_seed(20)
+    q, k, v = (torch.randn(2, n, h, dim, generator=g, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+    pages = 2 * (-(-n // page))
+    dt = R.E4M3 if fp8 else torch.bfloat16
+    kc, vc = (torch.zeros(pages, page, hkv, dim, device="cuda").to(dt) for _ in range(2))
+    sc = dict(k_scale=torch.zeros(pages, hkv, page, device="cuda"),
+              v_scale=torch.zeros(pages, hkv, page, device="cuda")) if fp8 else {}
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(2, -1)
+    outs, lses, at = [], [], 0
+    for step in (150, 150, 17, 9, 1, 1, 1, 1, 1, 1, 1):
+        lens = torch.full((2,), at + step, dtype=torch.int32, device="cuda")
+        new = slice(at, at + step)
+        pkg.cache_append(k[:, new], v[:, new], kc, vc, table, lens, **sc)
+        o, lse = pkg.paged_forward(q[:, new], kc, vc, table, lens, **sc)
+        outs.append(o)
+        lses.append(lse)
+        at += step
+    assert at == n
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    kr, vr = pkg.cache_read(kc, vc, table, cu, total_k=2 * n, **sc)
+    kr, vr = kr.view(2, n, hkv, dim), vr.view(2, n, hkv, dim)
+    o_ref, lse_ref = pkg.forward(q, kr, vr, causal=True)
+    pkg.check()
+    if not fp8:
+        assert torch.equal(R.bits(kr), R.bits(k)) and torch.equal(R.bits(vr), R.bits(v))
+    o, lse = torch.cat(outs, 1), torch.cat(lses, 2)
+    _, _, absv = zip(*_contiguous(q, kr, vr))
+    bound = 2 * (2.0 ** -8 * o_ref.double().abs() + (2.0 ** -8 + 2.0 ** -14) * torch.stack(absv) + 1e-6)
+    assert bool(((o.double() - o_ref.double()).abs() <= bound).all())
+    assert (lse - lse_ref).abs().max().item() <= 1e-4
+
+
+def _contiguous(q, k, v):
+    n, (hq, dim), hkv = q.shape[1], q.shape[2:], k.shape[2]
+    p = R.Problem(k, v, None, None, torch.arange(q.shape[0])[:, None], None, [n] * q.shape[0], [n] * q.shape[0], None,
+                  q, k, v)
+    return R.attend(p, True)
+
+
+def _graph(pkg, p, out, lse, o2=None):
+    graph = torch.cuda.CUDAGraph()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        pkg.cache_append(p.k_new, p.v_new, *p.cache, cu_seqlens_q=p.cu_q, **p.scales)
+        pkg.paged_forward(p.q, *p.cache, cu_seqlens_q=p.cu_q,
+                          max_seqlen_q=None if p.cu_q is None else max(p.lens_q), out=out, lse=lse, **p.scales)
+    return graph
+
+
+@pytest.mark.parametrize("new,hq", [(1, 8), (160, 8)])
+def test_captured_step_follows_the_lengths(pkg, new, hq):
+    """A captured append + attention replayed with other lengths on the device
+    (a serving loop) gives what eager calls give; two such graphs replayed at
+    once on two streams do not disturb each other. The first use of the
+    library on a stream may be the capture itself."""
+    graphs = []
+    for seed in (21, 22):
+        p = R.make([new + 900, new + 500], [new] * 2, hq, 2, 128, 32, seed=seed, poison=False)
+        out, lse = torch.empty_like(p.q), torch.empty(2, hq, new, device="cuda")
+        graphs.append((p, out, lse, _graph(pkg, p, out, lse)))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for lens in ([new + 900, new + 500], [new, new + 333], [new + 17, new + 400]):
+        want = []
+        for p, out, lse, _ in graphs:
+            p.seqlens.copy_(torch.tensor(lens, dtype=torch.int32))
+            p.lens_k[:] = lens
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, (p, out, lse, graph) in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for p, out, lse, _ in graphs:
+            o, l = pkg.paged_forward(p.q, *p.cache)
+            pkg.check()
+            assert torch.equal(R.bits(o), R.bits(out)) and torch.equal(R.bits(l), R.bits(lse))
+            R.check_attend(p, out, lse, True)
+
+
+def test_two_streams_at_once(pkg):
+    """Calls of different sizes on two streams share no workspace."""
+    ps = [R.make([3000, 2000], [n] * 2, 8, 2, 128, 64, seed=s) for n, s in ((1, 23), (1, 24), (140, 25))]
+    want = [pkg.paged_forward(p.q, *p.cache) for p in ps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ps]
+    got = []
+    for _ in range(10):
+        got = [pkg.paged_forward(p.q, *p.cache, stream=s) for s, p in zip(streams, ps)]
+    torch.cuda.synchronize()
+    for (o, l), (wo, wl) in zip(got, want):
+        assert torch.equal(R.bits(o), R.bits(wo)) and torch.equal(R.bits(l), R.bits(wl))
+    for s in streams:
+        pkg.check(stream=s)
+
+
+def test_own_workspace(pkg):
+    p = R.make([300, 40], [1, 1], 8, 2, 64, 16, seed=26)
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    pkg.cache_append(p.k_new, p.v_new, *p.cache, workspace=ws)
+    o, lse = pkg.paged_forward(p.q, *p.cache, workspace=ws)
+    pkg.check(workspace=ws)
+    R.check_attend(p, o, lse, True)
+    with pytest.raises(pkg.AttnError, match="workspace"):
+        pkg.paged_forward(p.q, *p.cache, workspace=ws[:256])
+    table = p.table.clone()
+    table[0, 0] = -1
+    pkg.paged_forward(p.q, p.k_cache, p.v_cache, table, p.seqlens, workspace=ws)
+    with pytest.raises(pkg.AttnError, match="sequence 0"):
+        pkg.check(workspace=ws)
+
+
+def test_no_rows(pkg):
+    p = R.make([20], [1], 2, 2, 64, 16, seed=27)
+    o, lse = pkg.paged_forward(p.q[:, :0], *p.cache)
+    assert o.shape == (1, 0, 2, 64) and lse.shape == (1, 2, 0)
+    o, lse = pkg.paged_forward(p.q[:0], p.k_cache, p.v_cache, p.table[:0], p.seqlens[:0])
+    assert o.shape == (0, 1, 2, 64)
+    pkg.cache_append(p.k_new[:0], p.v_new[:0], p.k_cache, p.v_cache, p.table[:0], p.seqlens[:0])
+    k, v = pkg.cache_read(p.k_cache, p.v_cache, p.table, torch.zeros(2, dtype=torch.int32, device="cuda"), total_k=0)
+    assert k.shape == (0, 2, 64) and v.shape == (0, 2, 64)
+    pkg.check()
