@@ -484,6 +484,7 @@ attn_status launch_tc05(const attn_fwd_params* p, cudaStream_t stream) {
     cp.o_stride_b = packed ? 0 : p->o_stride[0];
     cp.o_stride_t = p->o_stride[1];
     cp.o_stride_h = p->o_stride[2];
+    cp.cu_q = nullptr;
     e = af::splitkv_combine_launch(cp, p->head_dim_v, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "split-KV merge launch failed: %s", cudaGetErrorString(e));
   }
@@ -501,6 +502,26 @@ attn_status af::report_error(attn_status st, const char* fmt, ...) {
 }
 
 int af::sm_count() { return sm_count_cached(); }
+
+attn_status af::encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, const int64_t (&dims)[4],
+                           const int64_t (&strides)[3], const int (&box)[4]) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], es[4] = {1u, 1u, 1u, 1u};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    bx[i] = (cuuint32_t)box[i];
+    if (i < 3) st[i] = (cuuint64_t)strides[i];
+  }
+  const CUresult r = fn(map, type, 4, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(ATTN_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for a %lldx%lldx%lldx%lld tensor", (int)r,
+                (long long)dims[0], (long long)dims[1], (long long)dims[2], (long long)dims[3]);
+  return ATTN_OK;
+}
 
 extern "C" {
 

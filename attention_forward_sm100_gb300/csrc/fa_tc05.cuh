@@ -47,6 +47,16 @@
 //     epilogue warps of the second CTA report to the first CTA's barriers
 //     through the cluster window. Work indices are fetched by the first CTA
 //     and forwarded to the second through its shared memory.
+//   * paged K/V (Tc05Traits<..., PAGED = true>; the newest tokens of each
+//     sequence over its paged cache): a K or V tile is gathered page by page
+//     (one TMA box per page and 64 depth columns, the page numbers looked up
+//     a tile ahead by the producer's lanes), and a 128-row MMA tile packs
+//     2^pack_shift query heads that share the KV head times as many tokens
+//     as fill it, so each K/V byte that reaches shared memory serves that many
+//     heads. The causal mask is aligned to the end of the keys. The slots
+//     behind a sequence's last key may hold anything, NaN too: K's are masked
+//     as scores, V's are zeroed in shared memory before the tile is handed
+//     to the MMAs (a zero weight does not cancel a NaN).
 // Every wait is bounded: on timeout the CTA records an error in the
 // workspace, raises a shared abort flag that all waits poll (and, in a pair,
 // the peer's flag), drains its outstanding copies and MMAs, frees tensor
@@ -57,6 +67,7 @@
 
 #include "internal.h"
 #include "launch.cuh"
+#include "paged.h"
 #include "ptx.cuh"
 #include "schedule.cuh"
 
@@ -96,7 +107,7 @@ constexpr int kSlotBytes = 48;   // shared-memory bytes of one SchedSlot entry
 // correction warpgroup and the V producer lane.
 constexpr uint32_t kSchedConsumers = 2 + 128 + 128 + 128 + 1;
 
-template <int DQK_, int DR_, int DV_, bool FP8_, bool V8_ = false, bool PAIR_ = false>
+template <int DQK_, int DR_, int DV_, bool FP8_, bool V8_ = false, bool PAIR_ = false, bool PAGED_ = false>
 struct Tc05Traits {
   static constexpr int DQK = DQK_, DR = DR_, DV = DV_;
   static constexpr bool FP8 = FP8_;
@@ -108,6 +119,9 @@ struct Tc05Traits {
   // 64 keys of each K tile and 64 depth columns of each V tile.
   static constexpr bool PAIR = PAIR_;
   static_assert(!PAIR || (!FP8 && DQK == 128 && DV == 128), "CTA pairs: bf16 with Dqk = Dv = 128");
+  // K and V gathered from a paged cache, query heads packed into the rows.
+  static constexpr bool PAGED = PAGED_;
+  static_assert(!PAGED || (!FP8 && !PAIR && DR == 0 && DQK == DV), "paged: bf16 tiles, one CTA, no rope");
   static constexpr int BM = kBlockM, BN = kBlockN, NQ = 2;
   static constexpr int MMA_M = PAIR ? 2 * kBlockM : kBlockM;   // rows of one MMA tile (both CTAs)
   static constexpr int ROWS_PER_WORK = NQ * MMA_M;              // rows of one work tile
@@ -138,7 +152,7 @@ struct Tc05Traits {
   static constexpr int OFF_SCHED = OFF_KS + KS_BYTES;               // 2 slots x kSlotBytes
   static constexpr int OFF_WORK = OFF_SCHED + 2 * kSlotBytes;       // CTA pairs: 2 x int64 work index
   static constexpr int OFF_BAR = OFF_WORK + 16;
-  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV;
+  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV + (PAGED ? 1 : 0);
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 12;
@@ -149,6 +163,7 @@ struct Tc05Traits {
   static constexpr int BAR_K_EMPTY = BAR_FIXED + NK;
   static constexpr int BAR_V_FULL = BAR_FIXED + 2 * NK;
   static constexpr int BAR_V_EMPTY = BAR_FIXED + 2 * NK + NV;
+  static constexpr int BAR_V_TAIL = BAR_FIXED + 2 * NK + 2 * NV;   // paged: copies of a V tile that ends inside
 
   static constexpr uint32_t TMEM_COLS = 512;
   // Tensor-memory columns: S_0, S_1 (P_i overwrites the first 64 columns of
@@ -186,7 +201,10 @@ struct Tc05Traits {
 };
 
 // One decoded work tile as published to every role. With split-KV, k_start
-// and lk already describe the tile's own key range.
+// and lk already describe the tile's own key range. Paged variants: k_start
+// and v_start are the first and the end key TILE of the range, lk all keys of
+// the sequence, koff the keys in front of its first new token (lk - lq, may be
+// negative).
 struct SchedSlot {
   int32_t valid, b, h, t, q_start, lq, k_start, lk, split;
   int32_t v_start;   // first key of the tile's range along V's key dimension (packed e4m3 V: own offsets)
@@ -299,8 +317,23 @@ struct Geo {
 };
 
 template <class T, int CAUSAL>
-__device__ __forceinline__ Geo tile_geo(const SchedSlot& s, uint32_t rank) {
+__device__ __forceinline__ Geo tile_geo(const SchedSlot& s, uint32_t rank, int pack_shift) {
   Geo g;
+  if constexpr (T::PAGED) {
+    const int tok = kBlockM >> pack_shift;   // tokens of an MMA tile
+    g.q0 = s.t * 2 * tok;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      g.row[i] = g.q0 + tok * i;
+      const int kv_end = (CAUSAL & kMaskCausal) ? min(s.lk, s.koff + min(s.lq, g.row[i] + tok)) : s.lk;
+      const int end = min(s.v_start, kv_end > 0 ? (kv_end + kBlockN - 1) / kBlockN : 0);
+      g.n[i] = max(0, end - s.k_start);
+    }
+    // Tile 0 visits at least one key tile of a range that tile 1 visits (all
+    // of it masked for tile 0): the roles hand over by visited tiles.
+    if (g.n[1] > 0 && g.n[0] == 0) g.n[0] = 1;
+    return g;
+  }
   g.q0 = s.t * T::ROWS_PER_WORK;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -319,14 +352,15 @@ __device__ __forceinline__ constexpr bool splits_keys(const Tc05Params&) {
   return (CAUSAL & kMaskNoneSplit) != 0;
 }
 
-// The range's key offset travels only in the causal split flavour (its only user).
-template <int CAUSAL>
+// The range's key offset travels only in the flavours that use it (causal
+// split-KV, paged).
+template <int CAUSAL, bool PAGED>
 __device__ __forceinline__ SchedSlot read_slot(const Ctx& c, int slot, int off_sched) {
   const volatile int32_t* p = reinterpret_cast<const volatile int32_t*>(c.smem + off_sched + kSlotBytes * slot);
   SchedSlot s;
   s.valid = p[0]; s.b = p[1]; s.h = p[2]; s.t = p[3];
   s.q_start = p[4]; s.lq = p[5]; s.k_start = p[6]; s.lk = p[7]; s.split = p[8]; s.v_start = p[9];
-  s.koff = CAUSAL == kMaskCausalSplit ? p[10] : 0;
+  s.koff = (CAUSAL == kMaskCausalSplit || PAGED) ? p[10] : 0;
   return s;
 }
 
@@ -429,6 +463,89 @@ __device__ __forceinline__ SchedSlot decode_work(const Tc05Params& P, int64_t w,
   }
 }
 
+// The same for a paged problem: every sequence has its own number of keys
+// (and of new tokens when packed), so the work is found by a scan over the
+// sequences, whose offsets and lengths are checked on the way.
+template <int CAUSAL>
+__device__ __forceinline__ SchedSlot decode_paged(const Tc05Params& P, int64_t w, Cursor& cur) {
+  SchedSlot s;
+  s.valid = s.b = s.h = s.t = s.q_start = s.lq = s.k_start = s.lk = s.split = s.v_start = s.koff = 0;
+  const int lane = threadIdx.x & 31;
+  const NewRows rows = {P.cu_q, P.seqlens_k, P.batch, P.seqlen_q, P.total_q, P.max_k};
+  while (cur.b < P.batch) {
+    const int bb = cur.b + lane;
+    SeqRows r = {0, 0, 0};
+    int64_t u = 0;
+    if (bb < P.batch) {
+      r = load_seq(rows, bb, P.ws);
+      u = (int64_t)tiles_for(r.lq, P.rows_per_tile) * P.heads_q * P.num_splits;
+    }
+    int64_t incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t n = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += n;
+    }
+    const unsigned hit = __ballot_sync(kFull, bb < P.batch && w < cur.base + incl);
+    if (hit) {
+      const int L = __ffs(hit) - 1;
+      const int64_t first = cur.base + __shfl_sync(kFull, incl - u, L);
+      s.b = cur.b + L;
+      s.lq = __shfl_sync(kFull, r.lq, L);
+      s.lk = __shfl_sync(kFull, r.lk, L);
+      s.q_start = __shfl_sync(kFull, r.q0, L);
+      const WorkTile wt = decode_in_sequence(w - first, s.b, tiles_for(s.lq, P.rows_per_tile) * P.num_splits, P.group,
+                                             P.heads_kv, P.kv_chunk);
+      s.valid = 1;
+      s.h = wt.h;
+      s.t = wt.t / P.num_splits;
+      s.split = wt.t % P.num_splits;
+      s.koff = s.lk - s.lq;
+      // the key tiles the work tile's rows see, cut into ranges
+      const int kv_end =
+          (CAUSAL & kMaskCausal) ? min(s.lk, s.koff + min(s.lq, (s.t + 1) * P.rows_per_tile)) : s.lk;
+      int32_t j0, j1;
+      split_range(s.split, P.num_splits, kv_end > 0 ? tiles_for(kv_end, kBlockN) : 0, &j0, &j1);
+      s.k_start = j0;
+      s.v_start = j1;
+      return s;
+    }
+    cur.base += __shfl_sync(kFull, incl, 31);
+    cur.b += 32;
+  }
+  return s;
+}
+
+// Page of this lane's part of the 128-key tile `tile` of sequence b, -1 if the
+// part starts at or past the sequence's end: lane i holds the page of keys
+// [i * page_size, (i + 1) * page_size) of the tile (all of it in lane 0's page
+// when pages are 128 keys or longer).
+__device__ __forceinline__ int tile_page(const Tc05Params& P, const Ctx& c, int b, int lk, int tile) {
+  const int lane = threadIdx.x & 31;
+  const int key = tile * kBlockN + (lane << P.cache.page_shift);
+  if ((lane << P.cache.page_shift) >= kBlockN || key >= lk) return -1;
+  return load_page(P.cache, b, key >> P.cache.page_shift, c.ws);
+}
+
+// Copies the pages of one K or V tile into a stage (the whole warp; `page` from
+// tile_page), completing on `bar`, whose one arrival this is.
+template <class T>
+__device__ __forceinline__ void load_paged_tile(const Tc05Params& P, const CUtensorMap* map, uint32_t dst,
+                                                uint32_t bar, int hk, int tile, int page) {
+  const int lane = threadIdx.x & 31;
+  const int rows = min(kBlockN, 1 << P.cache.page_shift);
+  const int parts = __popc(__ballot_sync(kFull, page >= 0));
+  if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)(parts * rows * 128 * T::V_CHUNKS));
+  __syncwarp();
+  if (page >= 0) {
+    const int slot = (tile * kBlockN) & ((1 << P.cache.page_shift) - 1);   // 0 unless pages are longer than a tile
+#pragma unroll
+    for (int ch = 0; ch < T::V_CHUNKS; ++ch)
+      ptx::tma_load_4d(dst + ch * T::CHUNK_BYTES + lane * rows * 128, map, bar, ch * 64, hk, slot, page);
+  }
+  __syncwarp();
+}
+
 // ---------------------------------------------------------------------------------------------
 // TMA load of one box into this CTA's shared memory, completing on barrier
 // `bar` (in a pair: on that barrier of the pair's first CTA).
@@ -468,19 +585,21 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
   const int64_t units = T::PAIR ? (int64_t)ptx::nclusters_x() : (int64_t)gridDim.x;
   bool aborted = false;
   while (true) {
-    const SchedSlot s = decode_work<CAUSAL>(P, w, cur);
+    SchedSlot s;
+    if constexpr (T::PAGED) s = decode_paged<CAUSAL>(P, w, cur);
+    else s = decode_work<CAUSAL>(P, w, cur);
     if (!wait_warp(c, BAR_SCHED_EMPTY + sched.idx, sched.phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
     if (lane == 0) {
       volatile int32_t* p = reinterpret_cast<volatile int32_t*>(c.smem + T::OFF_SCHED + kSlotBytes * sched.idx);
       p[0] = s.valid; p[1] = s.b; p[2] = s.h; p[3] = s.t;
       p[4] = s.q_start; p[5] = s.lq; p[6] = s.k_start; p[7] = s.lk; p[8] = s.split; p[9] = s.v_start;
-      if (CAUSAL == kMaskCausalSplit) p[10] = s.koff;
+      if (CAUSAL == kMaskCausalSplit || T::PAGED) p[10] = s.koff;
       ptx::mbar_arrive(c.bar(BAR_SCHED_FULL + sched.idx));
     }
     __syncwarp();
     sched.next();
     if (!s.valid) break;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
     const int n1 = g.n[1];
     if (n1 > 0) {
       const int hk = s.h / P.group;
@@ -490,9 +609,11 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
         const uint32_t dst = c.sbase + T::OFF_Q + i * T::Q_TILE_BYTES;
         const int row = s.q_start + g.row[i];
         if (lead) ptx::mbar_expect_tx(bar, T::Q_TX);
+        // paged: one box is 2^pack_shift heads of 128 >> pack_shift tokens
+        const int head = T::PAGED ? s.h << P.pack_shift : s.h;
 #pragma unroll
         for (int ch = 0; ch < T::QK_CHUNKS; ++ch)
-          load_box<T>(c, dst + ch * T::CHUNK_BYTES, &P.tm_q, bar, ch * T::QK_CHUNK_ELEMS, s.h, row, qb);
+          load_box<T>(c, dst + ch * T::CHUNK_BYTES, &P.tm_q, bar, ch * T::QK_CHUNK_ELEMS, head, row, qb);
         if (T::DR > 0) load_box<T>(c, dst + T::QK_CHUNKS * T::CHUNK_BYTES, &P.tm_qr, bar, 0, s.h, row, qb);
       };
       // Q tile 0, K_0, then Q tile 1: each Q region is refilled as soon as
@@ -502,9 +623,15 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
       q_fill_parity = q_empty_phase;   // parity of the Q_FULL phases these loads complete
       q_loaded[0] = true;
       q_loaded[1] = false;
+      [[maybe_unused]] int page = -1;   // this lane's part of the next K tile
+      if constexpr (T::PAGED) page = tile_page(P, c, s.b, s.lk, s.k_start);
       for (int j = 0; j < n1; ++j) {
         if (!wait_warp(c, T::BAR_K_EMPTY + kr.idx, kr.phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
-        if (lane == 0) {
+        if constexpr (T::PAGED) {
+          load_paged_tile<T>(P, &P.tm_k, c.sbase + T::OFF_K + kr.idx * T::K_STAGE_BYTES,
+                             c.bar(T::BAR_K_FULL + kr.idx), hk, s.k_start + j, page);
+          page = tile_page(P, c, s.b, s.lk, s.k_start + j + 1);
+        } else if (lane == 0) {
           const uint32_t bar = c.bar(T::BAR_K_FULL + kr.idx);
           const uint32_t dst = c.sbase + T::OFF_K + kr.idx * T::K_STAGE_BYTES;
           // a pair's CTA r holds keys [64 r, 64 r + 64) of the tile
@@ -589,17 +716,53 @@ __device__ void role_load_v(const Tc05Params& P, const Ctx& c) {
   for (int s = 0; s < T::NV; ++s) { v_fill_parity[s] = 0; v_used[s] = false; }
   bool first_v = true;
   bool aborted = false;
+  [[maybe_unused]] uint32_t tail_phase = 0;
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, kRoleLoadV)) { aborted = true; break; }
-    const SchedSlot s = read_slot<CAUSAL>(c, sched.idx, T::OFF_SCHED);
+    const SchedSlot s = read_slot<CAUSAL, T::PAGED>(c, sched.idx, T::OFF_SCHED);
     if (lane == 0) ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) break;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
     const int hk = s.h / P.group;
     const int vb = P.packed ? 0 : s.b;
+    [[maybe_unused]] int page = -1;
+    if constexpr (T::PAGED) {
+      if (g.n[1] > 0) page = tile_page(P, c, s.b, s.lk, s.k_start);
+    }
     for (int j = 0; j < g.n[1]; ++j) {
       if (!wait_warp(c, T::BAR_V_EMPTY + vr.idx, vr.phase ^ 1u, kRoleLoadV)) { aborted = true; break; }
+      if constexpr (T::PAGED) {
+        const uint32_t dst = c.sbase + T::OFF_V + vr.idx * T::V_STAGE_BYTES;
+        const uint32_t full = c.bar(T::BAR_V_FULL + vr.idx);
+        const int tile = s.k_start + j, keys = s.lk - tile * kBlockN;
+        if (keys >= kBlockN) {
+          load_paged_tile<T>(P, &P.tm_v, dst, full, hk, tile, page);
+          v_used[vr.idx] = true;
+        } else {
+          // The sequence ends inside this tile: its copies land on a barrier
+          // of their own, then the rows behind the end (parts of a page, or
+          // whatever the stage held) become zeros.
+          load_paged_tile<T>(P, &P.tm_v, dst, c.bar(T::BAR_V_TAIL), hk, tile, page);
+          if (!wait_warp(c, T::BAR_V_TAIL, tail_phase, kRoleLoadV)) {
+            wait_drain(c, T::BAR_V_TAIL, tail_phase);
+            aborted = true;
+            break;
+          }
+          tail_phase ^= 1u;
+          for (int x = keys * 8 + lane; x < kBlockN * 8; x += 32)
+#pragma unroll
+            for (int ch = 0; ch < T::V_CHUNKS; ++ch) ptx::st_shared_zero16(dst + ch * T::CHUNK_BYTES + 16 * x);
+          ptx::fence_async_shared();   // before the MMAs read what these stores wrote
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(full);
+          v_used[vr.idx] = false;      // nothing of this stage is in flight
+        }
+        v_fill_parity[vr.idx] = vr.phase;
+        vr.next();
+        page = tile_page(P, c, s.b, s.lk, tile + 1);
+        continue;
+      }
       // Fault injection (testing only): block 0 never loads its first V tile,
       // so the MMA issuer's bounded wait for it runs out.
       const bool withhold = P.withhold_v && blockIdx.x == 0 && first_v;
@@ -735,11 +898,11 @@ __device__ void role_mma(const Tc05Params& P, const Ctx& c, const int i) {
   }
   while (true) {
     if (!wait_one(c, BAR_SCHED_FULL + sched.idx, sched.phase, role)) { aborted = true; break; }
-    const SchedSlot s = read_slot<CAUSAL>(c, sched.idx, T::OFF_SCHED);
+    const SchedSlot s = read_slot<CAUSAL, T::PAGED>(c, sched.idx, T::OFF_SCHED);
     ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) break;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
     const int n = g.n[i], n1 = g.n[1];
     if (n1 == 0) {
       // No keys: keep the per-tile O-free handshake in step with the epilogue.
@@ -813,6 +976,13 @@ __device__ void role_mma(const Tc05Params& P, const Ctx& c, const int i) {
 }
 
 // ---------------------------------------------------------------------------------------------
+// Paged variants: LSE element of token qi and query head h (copy `sp` of the
+// layout for a split-KV range).
+__device__ __forceinline__ int64_t paged_lse_index(const Tc05Params& P, const SchedSlot& s, int sp, int qi, int h) {
+  return P.packed ? ((int64_t)sp * P.heads_total + h) * P.total_q + s.q_start + qi
+                  : (((int64_t)sp * P.batch + s.b) * P.heads_total + h) * P.seqlen_q + qi;
+}
+
 template <class T, int CAUSAL>
 __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
   const int tid = threadIdx.x - 128 * i;          // row of the Q tile == TMEM lane
@@ -827,24 +997,34 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
   const uint32_t turn_flip = i == 0 ? 1u : 0u;   // warpgroup 0 takes the first turn
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, role)) return;
-    const SchedSlot s = read_slot<CAUSAL>(c, sched.idx, T::OFF_SCHED);
+    const SchedSlot s = read_slot<CAUSAL, T::PAGED>(c, sched.idx, T::OFF_SCHED);
     ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) return;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
     const int n = g.n[i];
-    const int qi = g.row[i] + tid;               // row within the sequence
+    const int qi = T::PAGED ? g.row[i] + (tid >> P.pack_shift) : g.row[i] + tid;   // row within the sequence
     const bool row_valid = qi < s.lq;
     // keys of the range visible to this row (causal: keys 0..qi of the
     // sequence, the range starting at key koff of it)
-    const int lim = (CAUSAL & kMaskCausal) ? min(s.lk, qi + 1 - s.koff) : s.lk;
-    const int first_row = g.row[i];
+    // (paged: keys 0 .. koff + qi, the range starting at key tile k_start)
+    int lim, klen, first_row;   // visible keys, keys of the range, first row's last key in the range
+    if constexpr (T::PAGED) {
+      klen = s.lk - s.k_start * kBlockN;
+      lim = (CAUSAL & kMaskCausal) ? min(klen, s.koff + qi + 1 - s.k_start * kBlockN) : klen;
+      first_row = s.koff + g.row[i] - s.k_start * kBlockN;
+    } else {
+      klen = s.lk;
+      lim = (CAUSAL & kMaskCausal) ? min(s.lk, qi + 1 - s.koff) : s.lk;
+      first_row = g.row[i] - s.koff;
+    }
     // LSE element: [B][Hq][Sq] (or [Hq][Tq] packed); a split-KV range writes
     // its partial LSE to copy `split` of that layout, [split][B][Hq][Sq] (or
     // [split][Hq][Tq]).
     const bool split_kv = splits_keys<CAUSAL>(P);
     const int sp = split_kv ? s.split : 0;
-    const int64_t lse_idx = P.packed ? ((int64_t)sp * P.heads_q + s.h) * P.total_q + s.q_start + qi
+    const int64_t lse_idx = T::PAGED ? paged_lse_index(P, s, sp, qi, (s.h << P.pack_shift) + (tid & ((1 << P.pack_shift) - 1)))
+                          : P.packed ? ((int64_t)sp * P.heads_q + s.h) * P.total_q + s.q_start + qi
                                      : (((int64_t)sp * P.batch + s.b) * P.heads_q + s.h) * P.seqlen_q + qi;
     float c_row = P.scale_log2;
     int64_t ks_base = 0;
@@ -899,7 +1079,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
           sv[2 * e + 1] = a1;
         }
       }
-      const bool need_mask = (kb + kBlockN > s.lk) || ((CAUSAL & kMaskCausal) && s.koff + kb + kBlockN - 1 > first_row);
+      const bool need_mask = (kb + kBlockN > klen) || ((CAUSAL & kMaskCausal) && kb + kBlockN - 1 > first_row);
       if (need_mask) {
         const int vis = lim - kb;
         if constexpr (T::V8) {
@@ -940,7 +1120,10 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
         alpha = ptx::ex2(m - m_new);
       }
       const uint64_t c2 = ptx::f2_pack(c_row, c_row);
-      const uint64_t n2 = ptx::f2_pack(-m_use, -m_use);
+      // paged: a row may see no key of a tile it visits; its maximum stays -inf
+      // and its weights are 0, not exp(-inf + inf)
+      const float neg = T::PAGED && m_use == -INFINITY ? 0.f : -m_use;
+      const uint64_t n2 = ptx::f2_pack(neg, neg);
       uint64_t acc0 = 0, acc1 = 0;   // (+0.0f, +0.0f) pairs
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -1041,10 +1224,10 @@ __device__ __forceinline__ void store_row_chunk(uint16_t* dst, const uint32_t (&
 
 // Split-KV: row of the partial O array [split][rows][Hq] (rows = B*Sq, or Tq
 // when packed) of query row qi of work tile s.
-__device__ __forceinline__ int64_t partial_row(const Tc05Params& P, const SchedSlot& s, int qi) {
+__device__ __forceinline__ int64_t partial_row(const Tc05Params& P, const SchedSlot& s, int qi, int h, int heads) {
   const int64_t rows = P.packed ? (int64_t)P.total_q : (int64_t)P.batch * P.seqlen_q;
   const int64_t row = P.packed ? (int64_t)s.q_start + qi : (int64_t)s.b * P.seqlen_q + qi;
-  return ((int64_t)s.split * rows + row) * P.heads_q + s.h;
+  return ((int64_t)s.split * rows + row) * heads + h;
 }
 
 // Split-KV: one 32-column chunk of a row of normalised partial O, in fp32,
@@ -1066,11 +1249,11 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
   uint32_t stats_phase[2] = {0, 0}, ofinal_phase[2] = {0, 0};
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, kRoleCorrection)) return;
-    const SchedSlot s = read_slot<CAUSAL>(c, sched.idx, T::OFF_SCHED);
+    const SchedSlot s = read_slot<CAUSAL, T::PAGED>(c, sched.idx, T::OFF_SCHED);
     ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) return;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       // Epilogue of Q tile i: O = O / l, rounded once to bf16, stored row by row.
@@ -1078,10 +1261,12 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
       stats_phase[i] ^= 1u;
       const float rl = rcpl_sm[i * kBlockM + tid];
       ptx::mbar_arrive(c.bar(BAR_STATS_FREE + i));
-      const int qi = g.row[i] + tid;
+      const int qi = T::PAGED ? g.row[i] + (tid >> P.pack_shift) : g.row[i] + tid;
+      const int h = T::PAGED ? (s.h << P.pack_shift) + (tid & ((1 << P.pack_shift) - 1)) : s.h;
+      const int heads = T::PAGED ? P.heads_total : P.heads_q;
       const bool row_valid = qi < s.lq;
       uint16_t* orow = P.o + (int64_t)s.b * P.o_stride_b + (int64_t)(s.q_start + qi) * P.o_stride_t +
-                       (int64_t)s.h * P.o_stride_h;
+                       (int64_t)h * P.o_stride_h;
       if (g.n[i] > 0) {
         if (!wait_warp(c, BAR_O_FINAL + i, ofinal_phase[i], kRoleCorrection)) return;
         ofinal_phase[i] ^= 1u;
@@ -1089,7 +1274,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
         const uint32_t tO = c.tmem + lane_base + T::tm_o(i);
         if (splits_keys<CAUSAL>(P)) {
           // Split-KV range: normalised partial O in fp32 for the merge.
-          float* prow = P.o_part + partial_row(P, s, qi) * T::DV;
+          float* prow = P.o_part + partial_row(P, s, qi, h, heads) * T::DV;
 #pragma unroll 1
           for (int q = 0; q < T::DV / 32; ++q) {
             uint32_t r[32];
@@ -1110,7 +1295,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
         // An empty key range (a short packed sequence, or under the causal
         // mask a range this tile's rows do not reach): a zero partial row
         // (its LSE is -inf, so the merge gives it no weight).
-        float4* d = reinterpret_cast<float4*>(P.o_part + partial_row(P, s, qi) * T::DV);
+        float4* d = reinterpret_cast<float4*>(P.o_part + partial_row(P, s, qi, h, heads) * T::DV);
 #pragma unroll 1
         for (int e = 0; e < T::DV / 4; ++e) d[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       } else if (row_valid) {
@@ -1193,6 +1378,7 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
       ptx::mbar_init(c.bar(T::BAR_V_FULL + s), 1);
       ptx::mbar_init(c.bar(T::BAR_V_EMPTY + s), 2);
     }
+    if constexpr (T::PAGED) ptx::mbar_init(c.bar(T::BAR_V_TAIL), 1);
     *c.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -1370,6 +1556,8 @@ using TraitsFp8D128 = Tc05Traits<128, 0, 128, true>;
 using TraitsFp8QkvD128 = Tc05Traits<128, 0, 128, true, true>;
 using TraitsD128Pair = Tc05Traits<128, 0, 128, false, false, true>;
 using TraitsD128R64Pair = Tc05Traits<128, 64, 128, false, false, true>;
+using TraitsPagedD64 = Tc05Traits<64, 0, 64, false, false, false, true>;
+using TraitsPagedD128 = Tc05Traits<128, 0, 128, false, false, false, true>;
 
 cudaError_t tc05_launch_d64(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 cudaError_t tc05_launch_d128(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
@@ -1378,6 +1566,8 @@ cudaError_t tc05_launch_fp8d128(int mask, const Tc05Params& prm, int grid, cudaS
 cudaError_t tc05_launch_fp8qkvd128(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 cudaError_t tc05_launch_d128pair(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 cudaError_t tc05_launch_d128r64pair(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
+cudaError_t tc05_launch_pagedd64(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
+cudaError_t tc05_launch_pagedd128(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 int tc05_max_clusters_d128pair();
 int tc05_max_clusters_d128r64pair();
 

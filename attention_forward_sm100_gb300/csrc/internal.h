@@ -33,6 +33,19 @@ enum DeviceError : uint32_t {
   kDevErrBadCache = 4,     // paged cache: a length, offset or page number out of range (info: sequence)
 };
 
+// The cache as the kernels see it; strides in bytes.
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  int64_t k_page, k_tok, k_head;
+  int64_t v_page, v_tok, v_head;
+  int64_t table_stride;   // elements
+  int32_t num_pages, page_shift, max_pages, heads_kv;
+};
+
 // Everything the tcgen05 kernel needs, passed as one __grid_constant__ struct.
 struct Tc05Params {
   CUtensorMap tm_q;        // Q (nope part): box {64 or 128 elements, 1, 128, 1}
@@ -68,6 +81,14 @@ struct Tc05Params {
   int32_t kv_tiles;        // split-KV: ceil(seqlen_k / kBlockN)
   float* lse_part;         // split-KV: partial LSE [splits][B][Hq][Sq] / [splits][Hq][Tq]
   float* o_part;           // split-KV: partial O (normalised, fp32) [splits][rows][Hq][Dv]
+  // Paged variants only. heads_q then counts tiles of 2^pack_shift query heads
+  // that share a KV head, group the tiles of one KV head, rows_per_tile the
+  // tokens of a work tile; tm_k / tm_v map (depth, head, slot, page).
+  CacheView cache;
+  const int32_t* seqlens_k;   // [B] cached keys
+  int32_t max_k;           // upper bound of them
+  int32_t pack_shift;      // log2 of the query heads in a tile
+  int32_t heads_total;     // Hq
 };
 
 // Arguments of the split-KV merge kernel.
@@ -79,6 +100,7 @@ struct SplitCombineParams {
   int32_t splits, batch, seqlen_q, heads_q;
   int32_t packed, total_q;
   int64_t o_stride_b, o_stride_t, o_stride_h;   // elements
+  const int32_t* cu_q;     // packed, or NULL: rows outside [cu_q[0], cu_q[batch]) are left as they are
 };
 
 // Kernel variants of the tcgen05 path.
@@ -90,7 +112,9 @@ enum Tc05Variant : int {
   kVarFp8QkvD128 = 4, // fp8 e4m3 Q/K/V (depth-major V, P rounded to e4m3), Dqk = Dv = 128
   kVarD128Pair = 5,   // kVarD128 on CTA pairs (M = 256 MMAs over two CTAs)
   kVarD128Rope64Pair = 6, // kVarD128Rope64 on CTA pairs
-  kVarCount = 7
+  kVarPagedD64 = 7,    // bf16 paged cache, D = 64
+  kVarPagedD128 = 8,   // bf16 paged cache, D = 128
+  kVarCount = 9
 };
 
 struct Tc05Config {
@@ -105,6 +129,10 @@ struct Tc05Config {
 // returns `st`.
 attn_status report_error(attn_status st, const char* fmt, ...);
 
+// 4-D tensor map of a 128-byte-swizzled box (strides of dimensions 1 to 3 in
+// bytes); the calling thread's last error says why it failed.
+attn_status encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, const int64_t (&dims)[4],
+                       const int64_t (&strides)[3], const int (&box)[4]);
 // SMs of the current device (148 when it cannot be asked).
 int sm_count();
 

@@ -11,19 +11,6 @@ namespace af {
 constexpr int kStreamTile = 64;      // keys per work unit of the streaming attention kernel
 constexpr int kMinPage = 16;         // smallest page: one warp's step of keys lies in one page
 
-// The cache as the kernels see it; strides in bytes.
-struct CacheView {
-  uint8_t* k;
-  uint8_t* v;
-  float* k_scale;
-  float* v_scale;
-  const int32_t* table;
-  int64_t k_page, k_tok, k_head;
-  int64_t v_page, v_tok, v_head;
-  int64_t table_stride;   // elements
-  int32_t num_pages, page_shift, max_pages, heads_kv;
-};
-
 // The new rows of each sequence (fixed: b * seqlen_q; packed: cu_q) and the
 // cached lengths.
 struct NewRows {

@@ -10,6 +10,8 @@ namespace {
 
 using af::report_error;
 
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 attn_status check_cache(const attn_kv_cache& c) {
@@ -140,7 +142,43 @@ attn_status check_paged(const attn_paged_params* p) {
   return ATTN_OK;
 }
 
-size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+// Two kernels. R = Lq * Hq / Hkv rows share the keys of a (sequence, KV head).
+// The streaming kernel reads the cache at close to the copy bandwidth but its
+// tensor instructions and its registers give out as R grows; the tcgen05
+// kernel computes 256-row tiles, mostly padding while R is small.
+constexpr int kStreamRows = 64;
+int64_t shared_rows(const attn_paged_params* p) {
+  return (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
+}
+bool use_tc05(const attn_paged_params* p) {
+  return p->cache.dtype == ATTN_DTYPE_BF16 && shared_rows(p) > kStreamRows;
+}
+
+// tcgen05 kernel: query heads packed into a 128-row tile (the largest power of
+// two that divides the group), tokens of a 256-row work tile, split-KV ranges.
+struct TilePlan {
+  int pack_shift;
+  int tokens;
+  int64_t work;      // upper bound of the work tiles, without the split
+  int32_t splits;
+  size_t lse_bytes, o_bytes;
+};
+TilePlan plan_tiles(const attn_paged_params* p) {
+  TilePlan t = {};
+  const int group = p->num_heads_q / p->cache.num_heads_kv;
+  while (t.pack_shift < 7 && group % (2 << t.pack_shift) == 0) ++t.pack_shift;
+  t.tokens = af::kRowsPerTile >> t.pack_shift;
+  t.work = (int64_t)p->cache.batch * (p->num_heads_q >> t.pack_shift) * af::tiles_for(p->seqlen_q, t.tokens);
+  const int64_t rows =
+      (p->cu_seqlens_q != nullptr ? (int64_t)p->total_q : (int64_t)p->cache.batch * p->seqlen_q) * p->num_heads_q;
+  t.splits = af::choose_splits_paged(t.work, af::tiles_for(p->seqlen_k, af::kBlockN), rows, p->cache.head_dim,
+                                     af::sm_count(), af::kMaxSplits);
+  if (t.splits > 1) {
+    t.lse_bytes = round256((size_t)t.splits * rows * sizeof(float));
+    t.o_bytes = (size_t)t.splits * rows * p->cache.head_dim * sizeof(float);
+  }
+  return t;
+}
 
 struct StreamPlan {
   int row_groups;      // 16-row groups of a row tile
@@ -156,7 +194,7 @@ struct StreamPlan {
 constexpr int kUnsplitTiles = 4;
 StreamPlan plan_stream(const attn_paged_params* p) {
   StreamPlan s = {};
-  const int64_t rows = (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
+  const int64_t rows = shared_rows(p);
   s.row_groups = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
   const int64_t rt = 16 * s.row_groups;
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
@@ -171,6 +209,104 @@ StreamPlan plan_stream(const attn_paged_params* p) {
     s.o_bytes = (size_t)(2 * s.grid * rt) * p->cache.head_dim * sizeof(float);
   }
   return s;
+}
+
+size_t workspace_need(const attn_paged_params* p) {
+  if (use_tc05(p)) {
+    const TilePlan t = plan_tiles(p);
+    return ATTN_FWD_WORKSPACE_BYTES + t.lse_bytes + t.o_bytes;
+  }
+  const StreamPlan s = plan_stream(p);
+  return ATTN_FWD_WORKSPACE_BYTES + s.meta_bytes + s.ml_bytes + s.o_bytes;
+}
+
+// Stride of a dimension of size 1 (never used, but a tensor map wants a legal one).
+int64_t legal(int64_t stride, int64_t size) { return size > 1 ? stride : 16; }
+
+attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
+  const TilePlan plan = plan_tiles(p);
+  const attn_kv_cache& c = p->cache;
+  const bool packed = p->cu_seqlens_q != nullptr;
+  const int pack = 1 << plan.pack_shift;
+  af::Tc05Params prm;
+  memset(&prm, 0, sizeof(prm));
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int64_t q_tokens = packed ? p->total_q : p->seqlen_q, q_batches = packed ? 1 : c.batch;
+  const int page_rows = c.page_size < af::kBlockN ? c.page_size : af::kBlockN;
+  attn_status st = af::encode_map(
+      &prm.tm_q, bf16, p->q, {c.head_dim, p->num_heads_q, q_tokens, q_batches},
+      {legal(p->q_stride[2] * 2, p->num_heads_q), legal(p->q_stride[1] * 2, q_tokens), legal(p->q_stride[0] * 2, q_batches)},
+      {64, pack, af::kBlockM / pack, 1});
+  if (st != ATTN_OK) return st;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t* s = i ? c.v_stride : c.k_stride;
+    st = af::encode_map(i ? &prm.tm_v : &prm.tm_k, bf16, i ? c.v : c.k,
+                        {c.head_dim, c.num_heads_kv, c.page_size, c.num_pages},
+                        {legal(s[2] * 2, c.num_heads_kv), s[1] * 2, legal(s[0] * 2, c.num_pages)}, {64, 1, page_rows, 1});
+    if (st != ATTN_OK) return st;
+  }
+  prm.cu_q = p->cu_seqlens_q;
+  prm.o = static_cast<uint16_t*>(p->o);
+  prm.lse = p->lse;
+  prm.ws = static_cast<uint32_t*>(p->workspace);
+  prm.o_stride_b = packed ? 0 : p->o_stride[0];
+  prm.o_stride_t = p->o_stride[1];
+  prm.o_stride_h = p->o_stride[2];
+  prm.o_store32 = aligned(p->o, 32) && (p->o_stride[2] * 2) % 32 == 0 && (p->o_stride[1] * 2) % 32 == 0 &&
+                  (packed || (p->o_stride[0] * 2) % 32 == 0);
+  prm.batch = c.batch;
+  prm.seqlen_q = p->seqlen_q;
+  prm.seqlen_k = p->seqlen_k;
+  prm.heads_q = p->num_heads_q >> plan.pack_shift;
+  prm.heads_kv = c.num_heads_kv;
+  prm.group = prm.heads_q / c.num_heads_kv;
+  prm.rows_per_tile = plan.tokens;
+  prm.tiles_per_seq = af::tiles_for(p->seqlen_q, plan.tokens);
+  prm.kv_chunk = af::choose_kv_chunk(p->seqlen_k, 4ll * c.head_dim, c.num_heads_kv, af::kL2ChunkBudget);
+  prm.packed = packed ? 1 : 0;
+  prm.total_q = packed ? p->total_q : 0;
+  prm.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  prm.timeout_ns = 2000000000ull;
+  prm.schedule = ATTN_SCHEDULE_DYNAMIC;
+  prm.num_splits = plan.splits;
+  prm.cache = view_of(c);
+  prm.seqlens_k = p->seqlens_k;
+  prm.max_k = p->seqlen_k;
+  prm.pack_shift = plan.pack_shift;
+  prm.heads_total = p->num_heads_q;
+  if (plan.splits > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+    prm.lse_part = reinterpret_cast<float*>(ws + ATTN_FWD_WORKSPACE_BYTES);
+    prm.o_part = reinterpret_cast<float*>(ws + ATTN_FWD_WORKSPACE_BYTES + plan.lse_bytes);
+  }
+  const int64_t work = plan.work * plan.splits;
+  const int sms = af::sm_count();
+  const int grid = (int)(work < sms ? work : sms);
+  prm.dependent_launch = grid < sms ? 1 : 0;
+  const int mask = (p->causal ? af::kMaskCausal : 0) | (plan.splits > 1 ? af::kMaskNoneSplit : 0);
+  cudaError_t e = af::tc05_launch(c.head_dim == 64 ? af::kVarPagedD64 : af::kVarPagedD128, mask, prm, grid, stream);
+  if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
+  if (plan.splits > 1) {
+    af::SplitCombineParams cp;
+    memset(&cp, 0, sizeof(cp));
+    cp.lse_part = prm.lse_part;
+    cp.o_part = prm.o_part;
+    cp.o = prm.o;
+    cp.lse = p->lse;
+    cp.splits = plan.splits;
+    cp.batch = c.batch;
+    cp.seqlen_q = p->seqlen_q;
+    cp.heads_q = p->num_heads_q;
+    cp.packed = prm.packed;
+    cp.total_q = prm.total_q;
+    cp.o_stride_b = prm.o_stride_b;
+    cp.o_stride_t = prm.o_stride_t;
+    cp.o_stride_h = prm.o_stride_h;
+    cp.cu_q = p->cu_seqlens_q;
+    e = af::splitkv_combine_launch(cp, c.head_dim, stream);
+    if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "split-KV merge launch failed: %s", cudaGetErrorString(e));
+  }
+  return ATTN_OK;
 }
 
 }  // namespace
@@ -243,8 +379,7 @@ attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t strea
 
 size_t attn_paged_workspace_bytes(const attn_paged_params* p) {
   if (check_paged(p) != ATTN_OK || no_rows(p)) return ATTN_FWD_WORKSPACE_BYTES;
-  const StreamPlan s = plan_stream(p);
-  return ATTN_FWD_WORKSPACE_BYTES + s.meta_bytes + s.ml_bytes + s.o_bytes;
+  return workspace_need(p);
 }
 
 attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
@@ -253,10 +388,11 @@ attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
   if (st != ATTN_OK) return st;
   if (no_rows(p)) return ATTN_OK;
   if ((st = check_workspace(p->workspace)) != ATTN_OK) return st;
-  const StreamPlan plan = plan_stream(p);
-  const size_t need = ATTN_FWD_WORKSPACE_BYTES + plan.meta_bytes + plan.ml_bytes + plan.o_bytes;
+  const size_t need = workspace_need(p);
   if (p->workspace_bytes < need)
     return report_error(ATTN_ERR_INVALID_ARG, "workspace of at least %zu bytes is required", need);
+  if (use_tc05(p)) return launch_tiles(p, reinterpret_cast<cudaStream_t>(stream));
+  const StreamPlan plan = plan_stream(p);
   if (plan.units > 0x3fffffffll) return report_error(ATTN_ERR_UNSUPPORTED, "too much work for one call");
   const bool packed = p->cu_seqlens_q != nullptr;
   af::StreamParams a;

@@ -11,6 +11,8 @@ Tc05Config tc05_config(int variant) {
     case kVarFp8QkvD128: return tc05_config_t<TraitsFp8QkvD128>();
     case kVarD128Pair: return tc05_config_t<TraitsD128Pair>();
     case kVarD128Rope64Pair: return tc05_config_t<TraitsD128R64Pair>();
+    case kVarPagedD64: return tc05_config_t<TraitsPagedD64>();
+    case kVarPagedD128: return tc05_config_t<TraitsPagedD128>();
     default: return tc05_config_t<TraitsFp8D128>();
   }
 }
@@ -24,6 +26,8 @@ cudaError_t tc05_launch(int variant, int mask, const Tc05Params& prm, int grid, 
     case kVarFp8QkvD128: return tc05_launch_fp8qkvd128(mask, prm, grid, stream);
     case kVarD128Pair: return tc05_launch_d128pair(mask, prm, grid, stream);
     case kVarD128Rope64Pair: return tc05_launch_d128r64pair(mask, prm, grid, stream);
+    case kVarPagedD64: return tc05_launch_pagedd64(mask, prm, grid, stream);
+    case kVarPagedD128: return tc05_launch_pagedd128(mask, prm, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
