@@ -57,6 +57,14 @@
 //     behind a sequence's last key may hold anything, NaN too: K's are masked
 //     as scores, V's are zeroed in shared memory before the tile is handed
 //     to the MMAs (a zero weight does not cancel a NaN).
+//   * an e4m3 paged cache (Tc05Traits<..., PAGED, C8 = true>): warpgroup 2 also
+//     fills the K and V stages. Its threads read 16 codes at a time straight
+//     from the pages (the next tile's loads are issued as the current one's
+//     registers are used up), widen them to bf16 (exactly) and store them where
+//     TMA would have put a bf16 tile, zeros behind the sequence's end. The key
+//     scales multiply the fp32 scores, the value scales the fp32 weights before
+//     their rounding to bf16; both travel through a four-tile ring in shared
+//     memory.
 // Every wait is bounded: on timeout the CTA records an error in the
 // workspace, raises a shared abort flag that all waits poll (and, in a pair,
 // the peer's flag), drains its outstanding copies and MMAs, frees tensor
@@ -101,13 +109,15 @@ enum BarId : int {
   BAR_FIXED = 33         // then K_FULL[NK], K_EMPTY[NK], V_FULL[NV], V_EMPTY[NV]
 };
 
+constexpr int kScaleSlots = 4;   // tiles of scales in flight (C8)
 constexpr int kSlotBytes = 48;   // shared-memory bytes of one SchedSlot entry
 
 // Consumers of a scheduler slot: the two MMA lanes, 2 softmax warpgroups, the
 // correction warpgroup and the V producer lane.
 constexpr uint32_t kSchedConsumers = 2 + 128 + 128 + 128 + 1;
 
-template <int DQK_, int DR_, int DV_, bool FP8_, bool V8_ = false, bool PAIR_ = false, bool PAGED_ = false>
+template <int DQK_, int DR_, int DV_, bool FP8_, bool V8_ = false, bool PAIR_ = false, bool PAGED_ = false,
+          bool C8_ = false>
 struct Tc05Traits {
   static constexpr int DQK = DQK_, DR = DR_, DV = DV_;
   static constexpr bool FP8 = FP8_;
@@ -122,6 +132,9 @@ struct Tc05Traits {
   // K and V gathered from a paged cache, query heads packed into the rows.
   static constexpr bool PAGED = PAGED_;
   static_assert(!PAGED || (!FP8 && !PAIR && DR == 0 && DQK == DV), "paged: bf16 tiles, one CTA, no rope");
+  // The paged cache holds e4m3 codes, widened to bf16 on their way to a stage.
+  static constexpr bool C8 = C8_;
+  static_assert(!C8 || PAGED, "an e4m3 cache is a paged one");
   static constexpr int BM = kBlockM, BN = kBlockN, NQ = 2;
   static constexpr int MMA_M = PAIR ? 2 * kBlockM : kBlockM;   // rows of one MMA tile (both CTAs)
   static constexpr int ROWS_PER_WORK = NQ * MMA_M;              // rows of one work tile
@@ -135,7 +148,7 @@ struct Tc05Traits {
   static constexpr int Q_TILE_BYTES = (QK_CHUNKS + R_CHUNKS) * CHUNK_BYTES;
   static constexpr int K_STAGE_BYTES = (QK_CHUNKS + R_CHUNKS) * K_CHUNK_BYTES;
   static constexpr int V_STAGE_BYTES = V8 ? DV * 128 : V_CHUNKS * CHUNK_BYTES;
-  static constexpr int NK = PAIR ? (DR > 0 ? 3 : 5) : (DR > 0 ? 2 : (FP8 ? 4 : (DQK == 64 ? 4 : 3)));
+  static constexpr int NK = PAIR ? (DR > 0 ? 3 : 5) : (DR > 0 ? 2 : (FP8 ? 4 : (DQK == 64 ? 4 : (C8 ? 2 : 3))));
   static constexpr int NV = PAIR ? (DR > 0 ? 3 : 4) : (DR > 0 ? 1 : (V8 ? 4 : (FP8 ? 3 : (DQK == 64 ? 4 : 2))));
   // Bytes one phase of a Q / K / V full barrier waits for (a pair's first CTA
   // counts both CTAs' copies).
@@ -148,11 +161,11 @@ struct Tc05Traits {
   static constexpr int OFF_V = OFF_K + NK * K_STAGE_BYTES;
   static constexpr int OFF_RCPL = OFF_V + NV * V_STAGE_BYTES;       // float [NQ][BM]
   static constexpr int OFF_KS = OFF_RCPL + NQ * BM * 4;             // float [NQ][2][BN] (fp8)
-  static constexpr int KS_BYTES = FP8 ? NQ * 2 * BN * 4 : 0;
+  static constexpr int KS_BYTES = FP8 ? NQ * 2 * BN * 4 : (C8 ? kScaleSlots * 2 * BN * 4 : 0);   // C8: [slot][K, V][BN]
   static constexpr int OFF_SCHED = OFF_KS + KS_BYTES;               // 2 slots x kSlotBytes
   static constexpr int OFF_WORK = OFF_SCHED + 2 * kSlotBytes;       // CTA pairs: 2 x int64 work index
   static constexpr int OFF_BAR = OFF_WORK + 16;
-  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV + (PAGED ? 1 : 0);
+  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV + (C8 ? kScaleSlots : (PAGED ? 1 : 0));
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 12;
@@ -164,6 +177,8 @@ struct Tc05Traits {
   static constexpr int BAR_V_FULL = BAR_FIXED + 2 * NK;
   static constexpr int BAR_V_EMPTY = BAR_FIXED + 2 * NK + NV;
   static constexpr int BAR_V_TAIL = BAR_FIXED + 2 * NK + 2 * NV;   // paged: copies of a V tile that ends inside
+  static constexpr int BAR_SCALES = BAR_FIXED + 2 * NK + 2 * NV;   // C8: +slot, a tile's scales are in shared memory
+  static constexpr uint32_t FILL_COUNT = C8 ? 4 : 1;   // arrivals that fill a K or V stage (C8: one per warp)
 
   static constexpr uint32_t TMEM_COLS = 512;
   // Tensor-memory columns: S_0, S_1 (P_i overwrites the first 64 columns of
@@ -189,7 +204,9 @@ struct Tc05Traits {
   // The FP8 softmax (k-scale multiply, e4m3 packing) takes 192 registers; its
   // epilogue warpgroup then fits in 64 (measured: +1-3 % on the FP8
   // workloads, no change for bf16).
-  static constexpr int REG_SOFTMAX = FP8 ? 192 : 184, REG_CORR = FP8 ? 64 : 80, REG_MISC = 64;
+    // With an e4m3 cache the epilogue warpgroup also widens K and V (96), and
+  // the single-thread roles, which load only Q, get by with 48.
+  static constexpr int REG_SOFTMAX = FP8 ? 192 : 184, REG_CORR = FP8 ? 64 : (C8 ? 96 : 80), REG_MISC = C8 ? 48 : 64;
   // Softmax turn: 0 = the two softmax warpgroups run freely; 1 / 2 = they
   // take turns, handing over after the first half of P / after the tile.
   // With FP8 Q/K a tile's MMAs take less time than a softmax, and two
@@ -623,9 +640,15 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
       q_fill_parity = q_empty_phase;   // parity of the Q_FULL phases these loads complete
       q_loaded[0] = true;
       q_loaded[1] = false;
+      if constexpr (T::C8) {   // warpgroup 2 brings K and V
+        if (!wait_warp(c, BAR_Q_EMPTY1, q_empty_phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
+        if (lane == 0) load_q(1);
+        q_loaded[1] = true;
+        q_empty_phase ^= 1u;
+      }
       [[maybe_unused]] int page = -1;   // this lane's part of the next K tile
-      if constexpr (T::PAGED) page = tile_page(P, c, s.b, s.lk, s.k_start);
-      for (int j = 0; j < n1; ++j) {
+      if constexpr (T::PAGED && !T::C8) page = tile_page(P, c, s.b, s.lk, s.k_start);
+      for (int j = 0; j < (T::C8 ? 0 : n1); ++j) {
         if (!wait_warp(c, T::BAR_K_EMPTY + kr.idx, kr.phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
         if constexpr (T::PAGED) {
           load_paged_tile<T>(P, &P.tm_k, c.sbase + T::OFF_K + kr.idx * T::K_STAGE_BYTES,
@@ -994,6 +1017,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
   const int role = i == 0 ? kRoleSoftmax0 : kRoleSoftmax1;
   Ring<2> sched;
   uint32_t s_phase = 0, ks_phase = 0, stats_phase = 0, turn_phase = 0;
+  [[maybe_unused]] uint32_t sc_tile = 0;   // C8: key tiles before this work tile's first
   const uint32_t turn_flip = i == 0 ? 1u : 0u;   // warpgroup 0 takes the first turn
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, role)) return;
@@ -1079,6 +1103,19 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
           sv[2 * e + 1] = a1;
         }
       }
+      [[maybe_unused]] const float4* sc4 = nullptr;   // C8: this tile's key scales, then its value scales
+      if constexpr (T::C8) {
+        // (complete since before S was: the wait orders the reads after the writes)
+        const uint32_t x = sc_tile + (uint32_t)j;
+        if (!wait_warp(c, T::BAR_SCALES + (int)(x % kScaleSlots), (x / kScaleSlots) & 1u, role)) return;
+        sc4 = reinterpret_cast<const float4*>(c.smem + T::OFF_KS) + (x % kScaleSlots) * (2 * kBlockN / 4);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float4 kv = sc4[e];
+          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(sv[4 * e], sv[4 * e + 1]), ptx::f2_pack(kv.x, kv.y)), sv[4 * e], sv[4 * e + 1]);
+          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(sv[4 * e + 2], sv[4 * e + 3]), ptx::f2_pack(kv.z, kv.w)), sv[4 * e + 2], sv[4 * e + 3]);
+        }
+      }
       const bool need_mask = (kb + kBlockN > klen) || ((CAUSAL & kMaskCausal) && kb + kBlockN - 1 > first_row);
       if (need_mask) {
         const int vis = lim - kb;
@@ -1136,7 +1173,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
           const int el = 64 * half + 2 * e;
           float x0, x1;
           ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(sv[el], sv[el + 1]), c2, n2), x0, x1);
-          const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+          float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
           if (e & 1) acc1 = ptx::f2_add(acc1, ptx::f2_pack(p0, p1));
           else acc0 = ptx::f2_add(acc0, ptx::f2_pack(p0, p1));
           if constexpr (T::V8) {
@@ -1144,6 +1181,11 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
             q0 = p0;
             q1 = p1;
           } else {
+            if constexpr (T::C8) {
+              const float4 vv = sc4[kBlockN / 4 + 16 * half + (e >> 1)];
+              ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(p0, p1), (e & 1) ? ptx::f2_pack(vv.z, vv.w) : ptx::f2_pack(vv.x, vv.y)),
+                             p0, p1);
+            }
             pk[e] = ptx::pack_bf16(p0, p1);
           }
         }
@@ -1181,6 +1223,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
       l = l * alpha + ((s0 + s1) + (s2 + s3));
       m = m_use;
     }
+    if constexpr (T::C8) sc_tile += (uint32_t)g.n[1];
     if (T::SM_TURN) {
       // K/V tiles only the other Q tile visits: pass the turn on.
       for (int j = n; j < g.n[1]; ++j) {
@@ -1240,6 +1283,146 @@ __device__ __forceinline__ void store_row_chunk_f32(float* dst, const uint32_t (
   for (int e = 0; e < 4; ++e) ptx::st_global_v8(dst + 8 * e, v + 8 * e);
 }
 
+// ---------------------------------------------------------------------------------------------
+// C8: warpgroup 2 as the K/V producer. A tile is 128 rows of D codes; warp w
+// brings rows 32 w .. 32 w + 31, D / 16 lanes to a row (16 codes each), in
+// D / 16 loads per thread. In every pair of rows the lanes of the upper 64
+// depths take the other row: the two 16-byte halves that a lane stores then
+// fall on different banks across its eight neighbours.
+template <class T>
+struct Widen {
+  static constexpr int LPR = T::DQK / 16;        // lanes per row
+  static constexpr int RPL = 32 / LPR;           // rows a warp loads at a time
+  static constexpr int NP = 32 / RPL;            // loads per thread
+  static constexpr int PB = 16 / RPL;            // of them in a 16-key block
+
+  const uint8_t* src[2];   // this lane's first row in each 16-key block of its warp's rows
+  int64_t step;            // bytes between its rows of a block
+  int keys;                // rows of the tile in front of the sequence's end
+
+  __device__ static int row0() {   // this lane's first row of the tile
+    const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, col = lane % LPR;
+    return 32 * w + ((lane / LPR) ^ (T::DQK == 128 && col >= 4 ? 1 : 0));
+  }
+  __device__ __forceinline__ void aim(const CacheView& cv, const uint8_t* base, int64_t page_stride, int64_t tok,
+                                      const int (&page)[2], int tile, int lk) {
+    const int col = (threadIdx.x & 31) % LPR, r0 = row0();
+    const int mask = (1 << cv.page_shift) - 1;
+    keys = lk - tile * kBlockN;
+    step = tok * RPL;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      src[h] = base + page[h] * page_stride + (int64_t)((tile * kBlockN + r0 + 16 * h) & mask) * tok + col * 16;
+  }
+  __device__ __forceinline__ uint4 load(int i) const {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (row0() + RPL * i < keys) v = ptx::ld_global_stream(src[i / PB] + (i % PB) * step);
+    return v;
+  }
+  // Byte offset in a stage of this lane's first 8 values of piece 0; the other
+  // 8 follow at ^ 16, piece i RPL rows on (the swizzle is the row modulo 8).
+  __device__ static uint32_t lane_offset() {
+    const int col = (threadIdx.x & 31) % LPR, r = row0();
+    return ((2 * col) >> 3) * T::CHUNK_BYTES + r * 128 + ((((2 * col) & 7) ^ (r & 7)) << 4);
+  }
+  // 16 codes of piece i as bf16 at `at` (stage + lane_offset).
+  __device__ static __forceinline__ void store(uint32_t at, int i, const uint4& v) {
+    const uint32_t a = (RPL == 4 && (i & 1) ? at ^ 64u : at) + i * RPL * 128;
+    ptx::st_shared_v4(a, ptx::e4m3x2_to_bf16x2(v.x & 0xffffu), ptx::e4m3x2_to_bf16x2(v.x >> 16),
+                      ptx::e4m3x2_to_bf16x2(v.y & 0xffffu), ptx::e4m3x2_to_bf16x2(v.y >> 16));
+    ptx::st_shared_v4(a ^ 16u, ptx::e4m3x2_to_bf16x2(v.z & 0xffffu), ptx::e4m3x2_to_bf16x2(v.z >> 16),
+                      ptx::e4m3x2_to_bf16x2(v.w & 0xffffu), ptx::e4m3x2_to_bf16x2(v.w >> 16));
+  }
+};
+
+template <class T>
+struct WidenState {
+  Ring<T::NK> kr;
+  Ring<T::NV> vr;
+  uint32_t tile = 0;   // key tiles so far (scale slots)
+};
+
+// All K and V tiles of one work tile. False: a wait ran out.
+template <class T>
+__device__ __forceinline__ bool widen_tiles(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int n,
+                                            WidenState<T>& st) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, tid = threadIdx.x & 127;
+  const int hk = s.h / P.group;
+  const CacheView& cv = P.cache;
+  const uint8_t* kbase = cv.k + hk * cv.k_head;
+  const uint8_t* vbase = cv.v + hk * cv.v_head;
+  const int mask = (1 << cv.page_shift) - 1;
+  auto pages_of = [&](int tile, int (&page)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = tile * kBlockN + 32 * w + 16 * h;
+      page[h] = key < s.lk ? load_page(cv, s.b, key >> cv.page_shift, c.ws) : 0;
+    }
+  };
+  auto scales_of = [&](int tile, const int (&page)[2], float& ks, float& vs) {
+    const int key = tile * kBlockN + tid;
+    ks = vs = 0.f;
+    if (key < s.lk) {
+      const int64_t at = (((int64_t)page[lane >> 4] * cv.heads_kv + hk) << cv.page_shift) + (key & mask);
+      ks = __ldg(cv.k_scale + at);
+      vs = __ldg(cv.v_scale + at);
+    }
+  };
+  const uint32_t lane_at = c.sbase + Widen<T>::lane_offset();
+  int page[2];
+  float ks, vs;
+  uint4 x[Widen<T>::NP];
+  Widen<T> next;
+  pages_of(s.k_start, page);
+  next.aim(cv, kbase, cv.k_page, cv.k_tok, page, s.k_start, s.lk);
+#pragma unroll
+  for (int i = 0; i < Widen<T>::NP; ++i) x[i] = next.load(i);
+  scales_of(s.k_start, page, ks, vs);
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    const int tile = s.k_start + j;
+    const bool more = j + 1 < n;
+    next.aim(cv, vbase, cv.v_page, cv.v_tok, page, tile, s.lk);
+    if (more) pages_of(tile + 1, page);
+    if (!wait_warp(c, T::BAR_K_EMPTY + st.kr.idx, st.kr.phase ^ 1u, kRoleLoadQK)) return false;
+    uint32_t stage = lane_at + T::OFF_K + st.kr.idx * T::K_STAGE_BYTES;
+#pragma unroll
+    for (int i = 0; i < Widen<T>::NP; ++i) {
+      const uint4 v = x[i];
+      x[i] = next.load(i);
+      Widen<T>::store(stage, i, v);
+    }
+    float* sc = reinterpret_cast<float*>(c.smem + T::OFF_KS) + (st.tile % kScaleSlots) * (2 * kBlockN);
+    sc[tid] = ks;
+    sc[kBlockN + tid] = vs;
+    ptx::fence_async_shared();   // before the MMAs read the stage
+    __syncwarp();
+    if (lane == 0) {
+      ptx::mbar_arrive(c.bar(T::BAR_SCALES + (int)(st.tile % kScaleSlots)));
+      ptx::mbar_arrive(c.bar(T::BAR_K_FULL + st.kr.idx));
+    }
+    ++st.tile;
+    st.kr.next();
+    if (more) {
+      next.aim(cv, kbase, cv.k_page, cv.k_tok, page, tile + 1, s.lk);
+      scales_of(tile + 1, page, ks, vs);
+    }
+    if (!wait_warp(c, T::BAR_V_EMPTY + st.vr.idx, st.vr.phase ^ 1u, kRoleLoadV)) return false;
+    stage = lane_at + T::OFF_V + st.vr.idx * T::V_STAGE_BYTES;
+#pragma unroll
+    for (int i = 0; i < Widen<T>::NP; ++i) {
+      const uint4 v = x[i];
+      if (more) x[i] = next.load(i);
+      Widen<T>::store(stage, i, v);
+    }
+    ptx::fence_async_shared();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(c.bar(T::BAR_V_FULL + st.vr.idx));
+    st.vr.next();
+  }
+  return true;
+}
+
 template <class T, int CAUSAL>
 __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
   const int tid = threadIdx.x - 256;
@@ -1247,6 +1430,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
   const float* rcpl_sm = reinterpret_cast<const float*>(c.smem + T::OFF_RCPL);
   Ring<2> sched;
   uint32_t stats_phase[2] = {0, 0}, ofinal_phase[2] = {0, 0};
+  [[maybe_unused]] WidenState<T> widen;
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, kRoleCorrection)) return;
     const SchedSlot s = read_slot<CAUSAL, T::PAGED>(c, sched.idx, T::OFF_SCHED);
@@ -1254,6 +1438,9 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
     sched.next();
     if (!s.valid) return;
     const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
+    if constexpr (T::C8) {
+      if (g.n[1] > 0 && !widen_tiles<T>(P, c, s, g.n[1], widen)) return;
+    }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       // Epilogue of Q tile i: O = O / l, rounded once to bf16, stored row by row.
@@ -1359,8 +1546,8 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
       ptx::mbar_init(c.bar(BAR_STATS_FREE + i), 128);
       ptx::mbar_init(c.bar(BAR_KS + i), 128);
       ptx::mbar_init(c.bar(BAR_SCHED_FULL + i), 1);
-      // a pair's second CTA runs no MMA issuers
-      ptx::mbar_init(c.bar(BAR_SCHED_EMPTY + i), kSchedConsumers - (c.rank != 0 ? 2u : 0u));
+      // a pair's second CTA runs no MMA issuers, an e4m3 cache no V producer warp
+      ptx::mbar_init(c.bar(BAR_SCHED_EMPTY + i), kSchedConsumers - (c.rank != 0 ? 2u : 0u) - (T::C8 ? 1u : 0u));
       ptx::mbar_init(c.bar(BAR_WORK_FULL + i), 1);
       ptx::mbar_init(c.bar(BAR_WORK_EMPTY + i), 1);
       ptx::mbar_init(c.bar(BAR_SM_TURN + i), 128);
@@ -1370,15 +1557,20 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
     ptx::mbar_init(c.bar(BAR_DRAIN), 2);
 #pragma unroll
     for (int s = 0; s < T::NK; ++s) {
-      ptx::mbar_init(c.bar(T::BAR_K_FULL + s), 1);
+      ptx::mbar_init(c.bar(T::BAR_K_FULL + s), T::FILL_COUNT);
       ptx::mbar_init(c.bar(T::BAR_K_EMPTY + s), 2);
     }
 #pragma unroll
     for (int s = 0; s < T::NV; ++s) {
-      ptx::mbar_init(c.bar(T::BAR_V_FULL + s), 1);
+      ptx::mbar_init(c.bar(T::BAR_V_FULL + s), T::FILL_COUNT);
       ptx::mbar_init(c.bar(T::BAR_V_EMPTY + s), 2);
     }
-    if constexpr (T::PAGED) ptx::mbar_init(c.bar(T::BAR_V_TAIL), 1);
+    if constexpr (T::C8) {
+#pragma unroll
+      for (int s = 0; s < kScaleSlots; ++s) ptx::mbar_init(c.bar(T::BAR_SCALES + s), 4);
+    } else if constexpr (T::PAGED) {
+      ptx::mbar_init(c.bar(T::BAR_V_TAIL), 1);
+    }
     *c.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -1393,8 +1585,10 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
   }
   if (warp == 14 && lane == 0) {
     ptx::prefetch_tmap(&P.tm_q);
-    ptx::prefetch_tmap(&P.tm_k);
-    ptx::prefetch_tmap(&P.tm_v);
+    if constexpr (!T::C8) {
+      ptx::prefetch_tmap(&P.tm_k);
+      ptx::prefetch_tmap(&P.tm_v);
+    }
     if (T::DR > 0) {
       ptx::prefetch_tmap(&P.tm_qr);
       ptx::prefetch_tmap(&P.tm_kr);
@@ -1431,7 +1625,7 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
       __syncwarp();
     }
     else if (warp == 14) role_load_qk<T, CAUSAL>(P, c);
-    else role_load_v<T, CAUSAL>(P, c);
+    else if constexpr (!T::C8) role_load_v<T, CAUSAL>(P, c);
   }
 
   ptx::tc_fence_before();
@@ -1558,6 +1752,8 @@ using TraitsD128Pair = Tc05Traits<128, 0, 128, false, false, true>;
 using TraitsD128R64Pair = Tc05Traits<128, 64, 128, false, false, true>;
 using TraitsPagedD64 = Tc05Traits<64, 0, 64, false, false, false, true>;
 using TraitsPagedD128 = Tc05Traits<128, 0, 128, false, false, false, true>;
+using TraitsPaged8D64 = Tc05Traits<64, 0, 64, false, false, false, true, true>;
+using TraitsPaged8D128 = Tc05Traits<128, 0, 128, false, false, false, true, true>;
 
 cudaError_t tc05_launch_d64(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 cudaError_t tc05_launch_d128(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
@@ -1568,6 +1764,8 @@ cudaError_t tc05_launch_d128pair(int mask, const Tc05Params& prm, int grid, cuda
 cudaError_t tc05_launch_d128r64pair(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 cudaError_t tc05_launch_pagedd64(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 cudaError_t tc05_launch_pagedd128(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
+cudaError_t tc05_launch_paged8d64(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
+cudaError_t tc05_launch_paged8d128(int mask, const Tc05Params& prm, int grid, cudaStream_t stream);
 int tc05_max_clusters_d128pair();
 int tc05_max_clusters_d128r64pair();
 

@@ -114,7 +114,9 @@ enum Tc05Variant : int {
   kVarD128Rope64Pair = 6, // kVarD128Rope64 on CTA pairs
   kVarPagedD64 = 7,    // bf16 paged cache, D = 64
   kVarPagedD128 = 8,   // bf16 paged cache, D = 128
-  kVarCount = 9
+  kVarPaged8D64 = 9,   // e4m3 paged cache, D = 64
+  kVarPaged8D128 = 10, // e4m3 paged cache, D = 128
+  kVarCount = 11
 };
 
 struct Tc05Config {

@@ -150,9 +150,7 @@ constexpr int kStreamRows = 64;
 int64_t shared_rows(const attn_paged_params* p) {
   return (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
 }
-bool use_tc05(const attn_paged_params* p) {
-  return p->cache.dtype == ATTN_DTYPE_BF16 && shared_rows(p) > kStreamRows;
-}
+bool use_tc05(const attn_paged_params* p) { return shared_rows(p) > kStreamRows; }
 
 // tcgen05 kernel: query heads packed into a 128-row tile (the largest power of
 // two that divides the group), tokens of a 256-row work tile, split-KV ranges.
@@ -238,7 +236,8 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
       {legal(p->q_stride[2] * 2, p->num_heads_q), legal(p->q_stride[1] * 2, q_tokens), legal(p->q_stride[0] * 2, q_batches)},
       {64, pack, af::kBlockM / pack, 1});
   if (st != ATTN_OK) return st;
-  for (int i = 0; i < 2; ++i) {
+  const bool fp8 = c.dtype == ATTN_DTYPE_FP8_E4M3;
+  for (int i = 0; i < 2 && !fp8; ++i) {   // (an e4m3 cache is read without tensor maps)
     const int64_t* s = i ? c.v_stride : c.k_stride;
     st = af::encode_map(i ? &prm.tm_v : &prm.tm_k, bf16, i ? c.v : c.k,
                         {c.head_dim, c.num_heads_kv, c.page_size, c.num_pages},
@@ -262,7 +261,7 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   prm.group = prm.heads_q / c.num_heads_kv;
   prm.rows_per_tile = plan.tokens;
   prm.tiles_per_seq = af::tiles_for(p->seqlen_q, plan.tokens);
-  prm.kv_chunk = af::choose_kv_chunk(p->seqlen_k, 4ll * c.head_dim, c.num_heads_kv, af::kL2ChunkBudget);
+  prm.kv_chunk = af::choose_kv_chunk(p->seqlen_k, (fp8 ? 2ll : 4ll) * c.head_dim, c.num_heads_kv, af::kL2ChunkBudget);
   prm.packed = packed ? 1 : 0;
   prm.total_q = packed ? p->total_q : 0;
   prm.scale_log2 = p->softmax_scale * 1.4426950408889634f;
@@ -284,7 +283,9 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   const int grid = (int)(work < sms ? work : sms);
   prm.dependent_launch = grid < sms ? 1 : 0;
   const int mask = (p->causal ? af::kMaskCausal : 0) | (plan.splits > 1 ? af::kMaskNoneSplit : 0);
-  cudaError_t e = af::tc05_launch(c.head_dim == 64 ? af::kVarPagedD64 : af::kVarPagedD128, mask, prm, grid, stream);
+  const int variant = c.head_dim == 64 ? (fp8 ? af::kVarPaged8D64 : af::kVarPagedD64)
+                                       : (fp8 ? af::kVarPaged8D128 : af::kVarPagedD128);
+  cudaError_t e = af::tc05_launch(variant, mask, prm, grid, stream);
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
   if (plan.splits > 1) {
     af::SplitCombineParams cp;

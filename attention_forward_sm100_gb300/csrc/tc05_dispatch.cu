@@ -13,6 +13,8 @@ Tc05Config tc05_config(int variant) {
     case kVarD128Rope64Pair: return tc05_config_t<TraitsD128R64Pair>();
     case kVarPagedD64: return tc05_config_t<TraitsPagedD64>();
     case kVarPagedD128: return tc05_config_t<TraitsPagedD128>();
+    case kVarPaged8D64: return tc05_config_t<TraitsPaged8D64>();
+    case kVarPaged8D128: return tc05_config_t<TraitsPaged8D128>();
     default: return tc05_config_t<TraitsFp8D128>();
   }
 }
@@ -28,6 +30,8 @@ cudaError_t tc05_launch(int variant, int mask, const Tc05Params& prm, int grid, 
     case kVarD128Rope64Pair: return tc05_launch_d128r64pair(mask, prm, grid, stream);
     case kVarPagedD64: return tc05_launch_pagedd64(mask, prm, grid, stream);
     case kVarPagedD128: return tc05_launch_pagedd128(mask, prm, grid, stream);
+    case kVarPaged8D64: return tc05_launch_paged8d64(mask, prm, grid, stream);
+    case kVarPaged8D128: return tc05_launch_paged8d128(mask, prm, grid, stream);
     default: return cudaErrorInvalidValue;
   }
 }
