@@ -58,13 +58,12 @@
 //     as scores, V's are zeroed in shared memory before the tile is handed
 //     to the MMAs (a zero weight does not cancel a NaN).
 //   * an e4m3 paged cache (Tc05Traits<..., PAGED, C8 = true>): warpgroup 2 also
-//     fills the K and V stages. Its threads read 16 codes at a time straight
-//     from the pages (the next tile's loads are issued as the current one's
-//     registers are used up), widen them to bf16 (exactly) and store them where
-//     TMA would have put a bf16 tile, zeros behind the sequence's end. The key
-//     scales multiply the fp32 scores, the value scales the fp32 weights before
-//     their rounding to bf16; both travel through a four-tile ring in shared
-//     memory.
+//     fills the K and V stages. Its threads copy 16 codes at a time straight
+//     from the pages into a two-tile ring (cp.async; every thread reads back
+//     only what it copied, so the ring needs no barrier), widen them to bf16 as
+//     code * scale, rounded once (exact for powers of two, which is what
+//     cache_append writes), and store them where TMA would have put a bf16
+//     tile, zeros behind the sequence's end.
 // Every wait is bounded: on timeout the CTA records an error in the
 // workspace, raises a shared abort flag that all waits poll (and, in a pair,
 // the peer's flag), drains its outstanding copies and MMAs, frees tensor
@@ -109,7 +108,6 @@ enum BarId : int {
   BAR_FIXED = 33         // then K_FULL[NK], K_EMPTY[NK], V_FULL[NV], V_EMPTY[NV]
 };
 
-constexpr int kScaleSlots = 4;   // tiles of scales in flight (C8)
 constexpr int kSlotBytes = 48;   // shared-memory bytes of one SchedSlot entry
 
 // Consumers of a scheduler slot: the two MMA lanes, 2 softmax warpgroups, the
@@ -161,11 +159,11 @@ struct Tc05Traits {
   static constexpr int OFF_V = OFF_K + NK * K_STAGE_BYTES;
   static constexpr int OFF_RCPL = OFF_V + NV * V_STAGE_BYTES;       // float [NQ][BM]
   static constexpr int OFF_KS = OFF_RCPL + NQ * BM * 4;             // float [NQ][2][BN] (fp8)
-  static constexpr int KS_BYTES = FP8 ? NQ * 2 * BN * 4 : (C8 ? kScaleSlots * 2 * BN * 4 : 0);   // C8: [slot][K, V][BN]
+  static constexpr int KS_BYTES = FP8 ? NQ * 2 * BN * 4 : (C8 ? 2 * (DQK + 4) * BN : 0);   // C8: codes and scales of two tiles
   static constexpr int OFF_SCHED = OFF_KS + KS_BYTES;               // 2 slots x kSlotBytes
   static constexpr int OFF_WORK = OFF_SCHED + 2 * kSlotBytes;       // CTA pairs: 2 x int64 work index
   static constexpr int OFF_BAR = OFF_WORK + 16;
-  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV + (C8 ? kScaleSlots : (PAGED ? 1 : 0));
+  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV + (PAGED ? 1 : 0);
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 12;
@@ -177,7 +175,6 @@ struct Tc05Traits {
   static constexpr int BAR_V_FULL = BAR_FIXED + 2 * NK;
   static constexpr int BAR_V_EMPTY = BAR_FIXED + 2 * NK + NV;
   static constexpr int BAR_V_TAIL = BAR_FIXED + 2 * NK + 2 * NV;   // paged: copies of a V tile that ends inside
-  static constexpr int BAR_SCALES = BAR_FIXED + 2 * NK + 2 * NV;   // C8: +slot, a tile's scales are in shared memory
   static constexpr uint32_t FILL_COUNT = C8 ? 4 : 1;   // arrivals that fill a K or V stage (C8: one per warp)
 
   static constexpr uint32_t TMEM_COLS = 512;
@@ -1017,7 +1014,6 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
   const int role = i == 0 ? kRoleSoftmax0 : kRoleSoftmax1;
   Ring<2> sched;
   uint32_t s_phase = 0, ks_phase = 0, stats_phase = 0, turn_phase = 0;
-  [[maybe_unused]] uint32_t sc_tile = 0;   // C8: key tiles before this work tile's first
   const uint32_t turn_flip = i == 0 ? 1u : 0u;   // warpgroup 0 takes the first turn
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, role)) return;
@@ -1103,19 +1099,6 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
           sv[2 * e + 1] = a1;
         }
       }
-      [[maybe_unused]] const float4* sc4 = nullptr;   // C8: this tile's key scales, then its value scales
-      if constexpr (T::C8) {
-        // (complete since before S was: the wait orders the reads after the writes)
-        const uint32_t x = sc_tile + (uint32_t)j;
-        if (!wait_warp(c, T::BAR_SCALES + (int)(x % kScaleSlots), (x / kScaleSlots) & 1u, role)) return;
-        sc4 = reinterpret_cast<const float4*>(c.smem + T::OFF_KS) + (x % kScaleSlots) * (2 * kBlockN / 4);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float4 kv = sc4[e];
-          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(sv[4 * e], sv[4 * e + 1]), ptx::f2_pack(kv.x, kv.y)), sv[4 * e], sv[4 * e + 1]);
-          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(sv[4 * e + 2], sv[4 * e + 3]), ptx::f2_pack(kv.z, kv.w)), sv[4 * e + 2], sv[4 * e + 3]);
-        }
-      }
       const bool need_mask = (kb + kBlockN > klen) || ((CAUSAL & kMaskCausal) && kb + kBlockN - 1 > first_row);
       if (need_mask) {
         const int vis = lim - kb;
@@ -1173,7 +1156,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
           const int el = 64 * half + 2 * e;
           float x0, x1;
           ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(sv[el], sv[el + 1]), c2, n2), x0, x1);
-          float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
+          const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1);
           if (e & 1) acc1 = ptx::f2_add(acc1, ptx::f2_pack(p0, p1));
           else acc0 = ptx::f2_add(acc0, ptx::f2_pack(p0, p1));
           if constexpr (T::V8) {
@@ -1181,11 +1164,6 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
             q0 = p0;
             q1 = p1;
           } else {
-            if constexpr (T::C8) {
-              const float4 vv = sc4[kBlockN / 4 + 16 * half + (e >> 1)];
-              ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(p0, p1), (e & 1) ? ptx::f2_pack(vv.z, vv.w) : ptx::f2_pack(vv.x, vv.y)),
-                             p0, p1);
-            }
             pk[e] = ptx::pack_bf16(p0, p1);
           }
         }
@@ -1223,7 +1201,6 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
       l = l * alpha + ((s0 + s1) + (s2 + s3));
       m = m_use;
     }
-    if constexpr (T::C8) sc_tile += (uint32_t)g.n[1];
     if (T::SM_TURN) {
       // K/V tiles only the other Q tile visits: pass the turn on.
       for (int j = n; j < g.n[1]; ++j) {
@@ -1284,40 +1261,30 @@ __device__ __forceinline__ void store_row_chunk_f32(float* dst, const uint32_t (
 }
 
 // ---------------------------------------------------------------------------------------------
-// C8: warpgroup 2 as the K/V producer. A tile is 128 rows of D codes; warp w
-// brings rows 32 w .. 32 w + 31, D / 16 lanes to a row (16 codes each), in
-// D / 16 loads per thread. In every pair of rows the lanes of the upper 64
-// depths take the other row: the two 16-byte halves that a lane stores then
-// fall on different banks across its eight neighbours.
+// C8: warpgroup 2 as the K/V producer. A unit is one K or V tile, 128 rows of D
+// codes; warp w brings rows 32 w .. 32 w + 31, D / 16 lanes to a row (16 codes
+// each), in D / 16 pieces per thread. The pieces of unit u go through half
+// u & 1 of a ring, each refilled with unit u + 2's as soon as it is read: two
+// units (32 KB at D = 128) are in flight, a whole step's bytes. (Registers in
+// place of the ring hold one unit: 1394 us where this takes TBD.) In every
+// pair of rows the lanes of the upper 64 depths take the other row: the two
+// 16-byte halves that a lane stores then fall on different banks across its
+// eight neighbours.
 template <class T>
 struct Widen {
   static constexpr int LPR = T::DQK / 16;        // lanes per row
-  static constexpr int RPL = 32 / LPR;           // rows a warp loads at a time
-  static constexpr int NP = 32 / RPL;            // loads per thread
+  static constexpr int RPL = 32 / LPR;           // rows a warp moves at a time
+  static constexpr int NP = 32 / RPL;            // pieces per thread
   static constexpr int PB = 16 / RPL;            // of them in a 16-key block
+  static constexpr int RING = T::OFF_KS;         // [2][NP][128 threads][16 bytes]
+  static constexpr int SCALES = T::OFF_KS + 2 * NP * 2048;   // [2][128 rows] fp32
 
-  const uint8_t* src[2];   // this lane's first row in each 16-key block of its warp's rows
-  int64_t step;            // bytes between its rows of a block
-  int keys;                // rows of the tile in front of the sequence's end
+  Ring<T::NK> kr;
+  Ring<T::NV> vr;
 
-  __device__ static int row0() {   // this lane's first row of the tile
+  __device__ static int row0() {   // this lane's first row of a unit
     const int w = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, col = lane % LPR;
     return 32 * w + ((lane / LPR) ^ (T::DQK == 128 && col >= 4 ? 1 : 0));
-  }
-  __device__ __forceinline__ void aim(const CacheView& cv, const uint8_t* base, int64_t page_stride, int64_t tok,
-                                      const int (&page)[2], int tile, int lk) {
-    const int col = (threadIdx.x & 31) % LPR, r0 = row0();
-    const int mask = (1 << cv.page_shift) - 1;
-    keys = lk - tile * kBlockN;
-    step = tok * RPL;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      src[h] = base + page[h] * page_stride + (int64_t)((tile * kBlockN + r0 + 16 * h) & mask) * tok + col * 16;
-  }
-  __device__ __forceinline__ uint4 load(int i) const {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row0() + RPL * i < keys) v = ptx::ld_global_stream(src[i / PB] + (i % PB) * step);
-    return v;
   }
   // Byte offset in a stage of this lane's first 8 values of piece 0; the other
   // 8 follow at ^ 16, piece i RPL rows on (the swizzle is the row modulo 8).
@@ -1325,103 +1292,129 @@ struct Widen {
     const int col = (threadIdx.x & 31) % LPR, r = row0();
     return ((2 * col) >> 3) * T::CHUNK_BYTES + r * 128 + ((((2 * col) & 7) ^ (r & 7)) << 4);
   }
-  // 16 codes of piece i as bf16 at `at` (stage + lane_offset).
-  __device__ static __forceinline__ void store(uint32_t at, int i, const uint4& v) {
+  // 16 codes of piece i times their scale as bf16 at `at` (stage + lane_offset).
+  __device__ static __forceinline__ void store(uint32_t at, int i, const uint4& v, float scale) {
     const uint32_t a = (RPL == 4 && (i & 1) ? at ^ 64u : at) + i * RPL * 128;
-    ptx::st_shared_v4(a, ptx::e4m3x2_to_bf16x2(v.x & 0xffffu), ptx::e4m3x2_to_bf16x2(v.x >> 16),
-                      ptx::e4m3x2_to_bf16x2(v.y & 0xffffu), ptx::e4m3x2_to_bf16x2(v.y >> 16));
-    ptx::st_shared_v4(a ^ 16u, ptx::e4m3x2_to_bf16x2(v.z & 0xffffu), ptx::e4m3x2_to_bf16x2(v.z >> 16),
-                      ptx::e4m3x2_to_bf16x2(v.w & 0xffffu), ptx::e4m3x2_to_bf16x2(v.w >> 16));
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    uint32_t y[8];
+    const uint64_t s2 = ptx::f2_pack(scale, scale);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float lo, hi;
+      ptx::e4m3x2_to_float2((e & 1) ? x[e >> 1] >> 16 : x[e >> 1] & 0xffffu, lo, hi);
+      ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(lo, hi), s2), lo, hi);
+      y[e] = ptx::pack_bf16(lo, hi);
+    }
+    ptx::st_shared_v4(a, y[0], y[1], y[2], y[3]);
+    ptx::st_shared_v4(a ^ 16u, y[4], y[5], y[6], y[7]);
   }
-};
 
-template <class T>
-struct WidenState {
-  Ring<T::NK> kr;
-  Ring<T::NV> vr;
-  uint32_t tile = 0;   // key tiles so far (scale slots)
-};
-
-// All K and V tiles of one work tile. False: a wait ran out.
-template <class T>
-__device__ __forceinline__ bool widen_tiles(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int n,
-                                            WidenState<T>& st) {
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, tid = threadIdx.x & 127;
-  const int hk = s.h / P.group;
-  const CacheView& cv = P.cache;
-  const uint8_t* kbase = cv.k + hk * cv.k_head;
-  const uint8_t* vbase = cv.v + hk * cv.v_head;
-  const int mask = (1 << cv.page_shift) - 1;
-  auto pages_of = [&](int tile, int (&page)[2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int key = tile * kBlockN + 32 * w + 16 * h;
-      page[h] = key < s.lk ? load_page(cv, s.b, key >> cv.page_shift, c.ws) : 0;
-    }
+  // Where this thread's pieces of a unit come from.
+  struct Source {
+    const uint8_t *lo, *hi;  // this lane's first row in the two 16-key blocks of its warp's rows
+    int64_t step;            // bytes between its rows of a block
+    int keys;                // rows from its first one to the sequence's end
   };
-  auto scales_of = [&](int tile, const int (&page)[2], float& ks, float& vs) {
-    const int key = tile * kBlockN + tid;
-    ks = vs = 0.f;
-    if (key < s.lk) {
-      const int64_t at = (((int64_t)page[lane >> 4] * cv.heads_kv + hk) << cv.page_shift) + (key & mask);
-      ks = __ldg(cv.k_scale + at);
-      vs = __ldg(cv.v_scale + at);
-    }
-  };
-  const uint32_t lane_at = c.sbase + Widen<T>::lane_offset();
-  int page[2];
-  float ks, vs;
-  uint4 x[Widen<T>::NP];
-  Widen<T> next;
-  pages_of(s.k_start, page);
-  next.aim(cv, kbase, cv.k_page, cv.k_tok, page, s.k_start, s.lk);
+  __device__ static __forceinline__ Source aim(const CacheView& cv, const uint8_t* base, int64_t page_stride,
+                                               int64_t tok, const int (&page)[2], int tile, int lk) {
+    const int r0 = row0(), at = tile * kBlockN + r0, mask = (1 << cv.page_shift) - 1;
+    base += ((threadIdx.x & 31) % LPR) * 16;
+    Source s;
+    s.keys = lk - at;
+    s.step = tok * RPL;
+    s.lo = base + page[0] * page_stride + (int64_t)(at & mask) * tok;
+    s.hi = base + page[1] * page_stride + (int64_t)((at + 16) & mask) * tok;
+    return s;
+  }
+  // Copy of piece i to `dst`; zeros behind the end.
+  __device__ static __forceinline__ void copy(const CacheView& cv, const Source& s, uint32_t dst, int i) {
+    const bool ok = RPL * i < s.keys;
+    const uint8_t* row = i < PB ? s.lo + i * s.step : s.hi + (i - PB) * s.step;
+    ptx::cp_async16(dst, ok ? row : cv.k, ok);
+  }
+  // Copy of the scale of row (thread) of a unit.
+  __device__ static __forceinline__ void copy_scale(const Ctx& c, const CacheView& cv, const float* scales, int hk,
+                                                    const int (&page)[2], int tile, int lk, uint32_t half) {
+    const int tid = threadIdx.x & 127, key = tile * kBlockN + tid;
+    const bool ok = key < lk;
+    const int64_t at = (((int64_t)page[(tid >> 4) & 1] * cv.heads_kv + hk) << cv.page_shift) +
+                       (key & ((1 << cv.page_shift) - 1));
+    ptx::cp_async4(c.sbase + SCALES + half * 512 + tid * 4, ok ? scales + at : scales, ok);
+  }
+  // All K and V tiles of one work tile: units K_0, V_0, K_1, V_1, ... False: a
+  // wait ran out. One small loop for both kinds, unrolled twice only: with the
+  // code of every piece laid out, this warpgroup and the softmax ones evicted
+  // each other's instructions.
+  __device__ __forceinline__ bool run(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int n) {
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
+    const int hk = s.h / P.group;
+    const CacheView& cv = P.cache;
+    auto pages_of = [&](int tile, int (&page)[2]) {
 #pragma unroll
-  for (int i = 0; i < Widen<T>::NP; ++i) x[i] = next.load(i);
-  scales_of(s.k_start, page, ks, vs);
+      for (int h = 0; h < 2; ++h) {
+        const int key = tile * kBlockN + 32 * w + 16 * h;
+        page[h] = key < s.lk ? load_page(cv, s.b, key >> cv.page_shift, c.ws) : 0;
+      }
+    };
+    auto source = [&](bool v, int tile, const int (&page)[2]) {
+      return v ? aim(cv, cv.v + hk * cv.v_head, cv.v_page, cv.v_tok, page, tile, s.lk)
+               : aim(cv, cv.k + hk * cv.k_head, cv.k_page, cv.k_tok, page, tile, s.lk);
+    };
+    const uint32_t at0 = c.sbase + lane_offset();
+    const uint32_t ring0 = c.sbase + RING + (threadIdx.x & 127) * 16;
+    int page[2];
+    pages_of(s.k_start, page);
 #pragma unroll 1
-  for (int j = 0; j < n; ++j) {
-    const int tile = s.k_start + j;
-    const bool more = j + 1 < n;
-    next.aim(cv, vbase, cv.v_page, cv.v_tok, page, tile, s.lk);
-    if (more) pages_of(tile + 1, page);
-    if (!wait_warp(c, T::BAR_K_EMPTY + st.kr.idx, st.kr.phase ^ 1u, kRoleLoadQK)) return false;
-    uint32_t stage = lane_at + T::OFF_K + st.kr.idx * T::K_STAGE_BYTES;
+    for (int half = 0; half < 2; ++half) {
+      const Source src = source(half != 0, s.k_start, page);
 #pragma unroll
-    for (int i = 0; i < Widen<T>::NP; ++i) {
-      const uint4 v = x[i];
-      x[i] = next.load(i);
-      Widen<T>::store(stage, i, v);
+      for (int i = 0; i < NP; ++i) copy(cv, src, ring0 + (half * NP + i) * 2048, i);
+      copy_scale(c, cv, half ? cv.v_scale : cv.k_scale, hk, page, s.k_start, s.lk, half);
+      ptx::cp_async_commit();
     }
-    float* sc = reinterpret_cast<float*>(c.smem + T::OFF_KS) + (st.tile % kScaleSlots) * (2 * kBlockN);
-    sc[tid] = ks;
-    sc[kBlockN + tid] = vs;
-    ptx::fence_async_shared();   // before the MMAs read the stage
-    __syncwarp();
-    if (lane == 0) {
-      ptx::mbar_arrive(c.bar(T::BAR_SCALES + (int)(st.tile % kScaleSlots)));
-      ptx::mbar_arrive(c.bar(T::BAR_K_FULL + st.kr.idx));
+    if (n > 1) pages_of(s.k_start + 1, page);
+#pragma unroll 1
+    for (int u = 0; u < 2 * n; ++u) {
+      const uint32_t half = u & 1;
+      const int tile = s.k_start + (u >> 1) + 1;   // the tile whose copies replace this one's
+      Source next = source(half != 0, tile, page);
+      if (u + 2 >= 2 * n) next.keys = 0;            // (zeros, read by nobody)
+      const int empty = half ? T::BAR_V_EMPTY + (int)vr.idx : T::BAR_K_EMPTY + (int)kr.idx;
+      if (!wait_warp(c, empty, (half ? vr.phase : kr.phase) ^ 1u, half ? kRoleLoadV : kRoleLoadQK)) {
+        ptx::cp_async_wait<0>();
+        return false;
+      }
+      ptx::cp_async_wait<1>();
+      __syncwarp();   // the scales were copied by other lanes
+      const uint32_t at = at0 + (half ? T::OFF_V + vr.idx * T::V_STAGE_BYTES : T::OFF_K + kr.idx * T::K_STAGE_BYTES);
+      const uint32_t ring = ring0 + half * NP * 2048;
+      const float* sc = reinterpret_cast<const float*>(c.smem + SCALES + half * 512) + row0();
+#pragma unroll 1
+      for (int i = 0; i < NP; i += 2) {
+        const uint4 v0 = ptx::ld_shared_v4(ring + i * 2048), v1 = ptx::ld_shared_v4(ring + i * 2048 + 2048);
+        const float s0 = sc[RPL * i], s1 = sc[RPL * i + RPL];
+        store(at + i * RPL * 128, 0, v0, s0);
+        store(at + i * RPL * 128, 1, v1, s1);
+        copy(cv, next, ring + i * 2048, i);
+        copy(cv, next, ring + i * 2048 + 2048, i + 1);
+      }
+      ptx::fence_async_shared();   // before the MMAs read the stage
+      __syncwarp();
+      if (half) {
+        if (lane == 0) ptx::mbar_arrive(c.bar(T::BAR_V_FULL + vr.idx));
+        vr.next();
+      } else {
+        if (lane == 0) ptx::mbar_arrive(c.bar(T::BAR_K_FULL + kr.idx));
+        kr.next();
+      }
+      copy_scale(c, cv, half ? cv.v_scale : cv.k_scale, hk, page, tile, u + 2 < 2 * n ? s.lk : 0, half);
+      ptx::cp_async_commit();
+      if (half && u + 4 <= 2 * n) pages_of(tile + 1, page);
     }
-    ++st.tile;
-    st.kr.next();
-    if (more) {
-      next.aim(cv, kbase, cv.k_page, cv.k_tok, page, tile + 1, s.lk);
-      scales_of(tile + 1, page, ks, vs);
-    }
-    if (!wait_warp(c, T::BAR_V_EMPTY + st.vr.idx, st.vr.phase ^ 1u, kRoleLoadV)) return false;
-    stage = lane_at + T::OFF_V + st.vr.idx * T::V_STAGE_BYTES;
-#pragma unroll
-    for (int i = 0; i < Widen<T>::NP; ++i) {
-      const uint4 v = x[i];
-      if (more) x[i] = next.load(i);
-      Widen<T>::store(stage, i, v);
-    }
-    ptx::fence_async_shared();
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(c.bar(T::BAR_V_FULL + st.vr.idx));
-    st.vr.next();
+    ptx::cp_async_wait<0>();
+    return true;
   }
-  return true;
-}
+};
 
 template <class T, int CAUSAL>
 __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
@@ -1430,7 +1423,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
   const float* rcpl_sm = reinterpret_cast<const float*>(c.smem + T::OFF_RCPL);
   Ring<2> sched;
   uint32_t stats_phase[2] = {0, 0}, ofinal_phase[2] = {0, 0};
-  [[maybe_unused]] WidenState<T> widen;
+  [[maybe_unused]] Widen<T> widen;
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, kRoleCorrection)) return;
     const SchedSlot s = read_slot<CAUSAL, T::PAGED>(c, sched.idx, T::OFF_SCHED);
@@ -1439,7 +1432,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
     if (!s.valid) return;
     const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
     if constexpr (T::C8) {
-      if (g.n[1] > 0 && !widen_tiles<T>(P, c, s, g.n[1], widen)) return;
+      if (g.n[1] > 0 && !widen.run(P, c, s, g.n[1])) return;
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
@@ -1565,12 +1558,7 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
       ptx::mbar_init(c.bar(T::BAR_V_FULL + s), T::FILL_COUNT);
       ptx::mbar_init(c.bar(T::BAR_V_EMPTY + s), 2);
     }
-    if constexpr (T::C8) {
-#pragma unroll
-      for (int s = 0; s < kScaleSlots; ++s) ptx::mbar_init(c.bar(T::BAR_SCALES + s), 4);
-    } else if constexpr (T::PAGED) {
-      ptx::mbar_init(c.bar(T::BAR_V_TAIL), 1);
-    }
+    if constexpr (T::PAGED) ptx::mbar_init(c.bar(T::BAR_V_TAIL), 1);
     *c.abort_flag = 0;
     ptx::fence_mbar_init();
   }
