@@ -10,9 +10,9 @@ grow in a paged cache and attend to it. Build the library with
 ``attention_forward_sm100_gb300.build.build()``.
 """
 from ._binding import (AttnError, Params, PlanInfo, PreparedForward, check, default_workspace, forward, key_range,
-                       last_error, lib, make_params, plan, prepare, schedule, workspace_bytes)
+                       last_error, lib, make_params, paged_native, plan, prepare, schedule, workspace_bytes)
 from .paged import cache_append, cache_read, paged_forward
 
 __all__ = ["AttnError", "Params", "PlanInfo", "PreparedForward", "cache_append", "cache_read", "check",
-           "default_workspace", "forward", "key_range", "last_error", "lib", "make_params", "paged_forward", "plan",
-           "prepare", "schedule", "workspace_bytes"]
+           "default_workspace", "forward", "key_range", "last_error", "lib", "make_params", "paged_forward",
+           "paged_native", "plan", "prepare", "schedule", "workspace_bytes"]

@@ -101,14 +101,6 @@ def lib():
             L.attn_fwd_params_init.restype = None
             L.attn_fwd_params_size.argtypes = []
             L.attn_fwd_params_size.restype = ctypes.c_size_t
-            # parameter structs packed as bytes (see paged.py)
-            for name in ("attn_cache_append", "attn_cache_read", "attn_paged_fwd"):
-                getattr(L, name).argtypes = [ctypes.c_char_p, ctypes.c_void_p]
-                getattr(L, name).restype = ctypes.c_int
-            L.attn_paged_workspace_bytes.argtypes = [ctypes.c_char_p]
-            L.attn_paged_workspace_bytes.restype = ctypes.c_size_t
-            L.attn_paged_params_size.argtypes = [ctypes.c_int32]
-            L.attn_paged_params_size.restype = ctypes.c_size_t
             L.attn_status_string.argtypes = [ctypes.c_int]
             L.attn_status_string.restype = ctypes.c_char_p
             L.attn_fwd_last_error.argtypes = []
@@ -119,12 +111,27 @@ def lib():
     return _lib
 
 
+_native = None
+
+
+def paged_native():
+    """The extension module of the paged-cache operators; raises if it has not been built."""
+    global _native
+    if _native is None:
+        lib()
+        try:
+            from . import _paged_native
+        except ImportError as e:
+            raise RuntimeError("_paged_native is not built: run attention_forward_sm100_gb300.build.build()") from e
+        _native = _paged_native
+    return _native
+
+
 def last_error() -> str:
     return lib().attn_fwd_last_error().decode()
 
 
 _workspaces = {}
-_paged_workspaces = {}   # (device index, stream handle) -> buffer of the paged-cache operators
 _workspaces_lock = threading.Lock()
 
 
@@ -448,14 +455,14 @@ def check(workspace=None, device=None, stream=None):
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    buffers = [ws]
-    if workspace is None:
+    buffers = [ws.data_ptr()]
+    if workspace is None and _native is not None:
         index = dev.index if dev.index is not None else torch.cuda.current_device()
-        paged = _paged_workspaces.get((index, handle))
-        if paged is not None:
-            buffers.append(paged)
-    for buf in buffers:
-        st = L.attn_fwd_check(ctypes.c_void_p(buf.data_ptr()), ctypes.c_void_p(handle))
+        buffers.append(_native.workspace_address(index, handle))
+    for ptr in buffers:
+        if ptr == 0:
+            continue
+        st = L.attn_fwd_check(ctypes.c_void_p(ptr), ctypes.c_void_p(handle))
         if st != ATTN_OK:
             raise AttnError(st, last_error())
 

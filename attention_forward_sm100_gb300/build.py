@@ -2,7 +2,9 @@
 
 Every translation unit under csrc/ is compiled in parallel into _build/ and
 linked into attention_forward_sm100_gb300/libattn_fwd.so (CUDA runtime linked
-statically, driver entry points resolved at run time). The ptxas report of
+statically, driver entry points resolved at run time); python_paged.cpp, which
+needs Python's and torch's headers, becomes the extension module _paged_native
+next to it. The ptxas report of
 each persistent kernel is checked: it must be allocated exactly 128 registers
 per thread (the kernel redistributes them between warpgroups with setmaxnreg,
 whose budget is computed from that number) and may spill at most a few words.
@@ -17,12 +19,15 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build", platform.machine())
 LIB_PATH = os.path.join(HERE, "libattn_fwd.so")
+NATIVE_SRC = os.path.join(CSRC, "python_paged.cpp")
+NATIVE_PATH = os.path.join(HERE, "_paged_native.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
                  "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]
@@ -83,20 +88,65 @@ def _compile(src: str, force: bool) -> str:
     return obj
 
 
+def _compile_native(force: bool) -> str:
+    """Object file of the extension module (host code only)."""
+    import torch
+    obj = os.path.join(BUILD_DIR, "python_paged.o")
+    stamp = obj + ".torch"   # the torch it was compiled against
+    known = open(stamp).read() if os.path.exists(stamp) else ""
+    headers = glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__), NATIVE_SRC]
+    if not force and known == torch.__version__ and os.path.exists(obj) and \
+            os.path.getmtime(obj) >= max(os.path.getmtime(f) for f in headers):
+        return obj
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem",
+           sysconfig.get_paths()["include"], "-c", NATIVE_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for python_paged.cpp:\n{r.stderr[-6000:]}")
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return obj
+
+
+def _link_native(obj: str, force: bool):
+    """_paged_native.so: finds libattn_fwd.so beside it and torch's libraries where torch loaded them."""
+    import torch
+    if not force and os.path.exists(NATIVE_PATH) and \
+            os.path.getmtime(NATIVE_PATH) >= max(os.path.getmtime(obj), os.path.getmtime(LIB_PATH)):
+        return
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda_rt = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "lib64")
+    tmp = NATIVE_PATH + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-lattn_fwd", "-Wl,-rpath,$ORIGIN", "-L" + libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + libs, "-L" + cuda_rt,
+           "-lcudart_static", "-ldl", "-lrt", "-lpthread"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _paged_native failed:\n{r.stderr[-4000:]}")
+    os.replace(tmp, NATIVE_PATH)
+
+
 def build(force: bool = False, jobs: int | None = None) -> str:
-    """Compiles (incrementally) and links the library; returns its path."""
+    """Compiles (incrementally) and links the library and the extension module; returns the library's path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = _sources()
-    jobs = jobs or min(len(srcs), os.cpu_count() or 4)
+    jobs = jobs or min(len(srcs) + 1, (os.cpu_count() or 4) + 1)
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
+        native = ex.submit(_compile_native, force)
         objs = list(ex.map(lambda s: _compile(s, force), srcs))
+        native_obj = native.result()
     if force or not os.path.exists(LIB_PATH) or os.path.getmtime(LIB_PATH) < max(os.path.getmtime(o) for o in objs):
         tmp = LIB_PATH + ".tmp"
-        cmd = [_nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
+        cmd = [_nvcc()] + ARCH + ["-shared", "-o", tmp, "-Xlinker", "-soname=libattn_fwd.so"] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
         os.replace(tmp, LIB_PATH)
+    _link_native(native_obj, force)
     return LIB_PATH
 
 

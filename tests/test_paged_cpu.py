@@ -6,12 +6,19 @@ import ctypes
 import math
 import os
 import re
+import struct
 
 import pytest
 import torch
 
 import __graft_entry__
 import paged_reference as R
+
+# attn_kv_cache, then the rest of each parameter struct (native alignment)
+_CACHE = "5P7q7i4x"
+APPEND = struct.Struct("@" + _CACHE + "5P6q2i")
+READ = struct.Struct("@" + _CACHE + "4P4qi4x")
+PAGED = struct.Struct("@" + _CACHE + "6PN6q5if")
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -30,6 +37,22 @@ def test_header_functions_are_exported(pkg):
     lib = ctypes.CDLL(pkg._binding.LIB_PATH)
     for n in names:
         assert hasattr(lib, n), n
+
+
+def _library(pkg):
+    L = ctypes.CDLL(pkg._binding.LIB_PATH)
+    for f in (L.attn_cache_append, L.attn_cache_read, L.attn_paged_fwd):
+        f.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+    L.attn_paged_workspace_bytes.argtypes = [ctypes.c_char_p]
+    L.attn_paged_workspace_bytes.restype = ctypes.c_size_t
+    L.attn_fwd_last_error.restype = ctypes.c_char_p
+    return L
+
+
+def test_struct_layouts(pkg):
+    L = _library(pkg)
+    L.attn_paged_params_size.restype = ctypes.c_size_t
+    assert [L.attn_paged_params_size(i) for i in range(4)] == [APPEND.size, READ.size, PAGED.size, 0]
 
 
 def _problem(**kw):
@@ -134,7 +157,7 @@ def _paged(pkg, cache=None, **kw):
              q_stride=(256, 256, 64), o_stride=(256, 256, 64), seqlen_q=1, seqlen_k=128, total_q=0, hq=4, causal=1,
              scale=0.125)
     d.update(kw)
-    return pkg.paged._PAGED.pack(*_cache(**(cache or {})), d["q"], d["o"], d["lse"], d["seqlens"], d["cu"], d["ws"],
+    return PAGED.pack(*_cache(**(cache or {})), d["q"], d["o"], d["lse"], d["seqlens"], d["cu"], d["ws"],
                                  d["ws_bytes"], *d["q_stride"], *d["o_stride"], d["seqlen_q"], d["seqlen_k"],
                                  d["total_q"], d["hq"], d["causal"], d["scale"])
 
@@ -148,14 +171,14 @@ CACHE_ERRORS = [(dict(k=0), 1), (dict(v=(2 << 20) + 8), 1), (dict(table=0), 1), 
 
 @pytest.mark.parametrize("change,status", CACHE_ERRORS, ids=[str(c[0]) for c in CACHE_ERRORS])
 def test_library_refuses_caches(pkg, change, status):
-    L = pkg.lib()
+    L = _library(pkg)
     if "heads" not in change:   # zero heads would also divide the query heads
         assert L.attn_paged_fwd(_paged(pkg, change), None) == status
-    assert L.attn_cache_append(pkg.paged._APPEND.pack(*_cache(**change), 4 << 20, 5 << 20, 6 << 20, 0, 7 << 20,
+    assert L.attn_cache_append(APPEND.pack(*_cache(**change), 4 << 20, 5 << 20, 6 << 20, 0, 7 << 20,
                                                       *(128, 128, 64) * 2, 1, 0), None) == status
-    assert L.attn_cache_read(pkg.paged._READ.pack(*_cache(**change), 4 << 20, 5 << 20, 6 << 20, 7 << 20,
+    assert L.attn_cache_read(READ.pack(*_cache(**change), 4 << 20, 5 << 20, 6 << 20, 7 << 20,
                                                   *(128, 64) * 2, 5), None) == status
-    assert pkg.last_error()
+    assert L.attn_fwd_last_error()
 
 
 PAGED_ERRORS = [(dict(q=0), 1), (dict(o=(5 << 20) + 2), 1), (dict(seqlens=0), 1), (dict(lse=(6 << 20) + 2), 1),
@@ -166,14 +189,14 @@ PAGED_ERRORS = [(dict(q=0), 1), (dict(o=(5 << 20) + 2), 1), (dict(seqlens=0), 1)
 
 @pytest.mark.parametrize("change,status", PAGED_ERRORS, ids=[str(c[0]) for c in PAGED_ERRORS])
 def test_library_refuses_calls(pkg, change, status):
-    L = pkg.lib()
+    L = _library(pkg)
     assert L.attn_paged_fwd(_paged(pkg, **change), None) == status
-    assert pkg.last_error()
+    assert L.attn_fwd_last_error()
     assert L.attn_paged_fwd(None, None) == 1 and L.attn_cache_append(None, None) == 1 and L.attn_cache_read(None, None) == 1
 
 
 def test_workspace_depends_on_sizes_only(pkg):
-    L = pkg.lib()
+    L = _library(pkg)
     size = L.attn_paged_workspace_bytes
     assert size(None) == 256
     assert size(_paged(pkg, dict(dim=96))) == 256
