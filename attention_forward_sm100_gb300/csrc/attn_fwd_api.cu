@@ -484,7 +484,6 @@ attn_status launch_tc05(const attn_fwd_params* p, cudaStream_t stream) {
     cp.o_stride_b = packed ? 0 : p->o_stride[0];
     cp.o_stride_t = p->o_stride[1];
     cp.o_stride_h = p->o_stride[2];
-    cp.cu_q = nullptr;
     e = af::splitkv_combine_launch(cp, p->head_dim_v, stream);
     if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "split-KV merge launch failed: %s", cudaGetErrorString(e));
   }

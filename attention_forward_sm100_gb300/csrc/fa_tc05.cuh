@@ -366,6 +366,13 @@ __device__ __forceinline__ constexpr bool splits_keys(const Tc05Params&) {
   return (CAUSAL & kMaskNoneSplit) != 0;
 }
 
+// Paged variants: the split flavours take their work from a list, in which
+// some tiles are cut.
+template <int CAUSAL>
+__device__ __forceinline__ constexpr bool listed() {
+  return (CAUSAL & kMaskNoneSplit) != 0;
+}
+
 // The range's key offset travels only in the flavours that use it (causal
 // split-KV, paged).
 template <int CAUSAL, bool PAGED>
@@ -477,13 +484,15 @@ __device__ __forceinline__ SchedSlot decode_work(const Tc05Params& P, int64_t w,
   }
 }
 
-// The same for a paged problem: every sequence has its own number of keys
-// (and of new tokens when packed), so the work is found by a scan over the
-// sequences, whose offsets and lengths are checked on the way.
+// The same for a paged problem without a work list: every query tile whole.
+// Every sequence has its own number of keys (and of new tokens when packed), so
+// the work is found by a scan over the sequences, whose offsets and lengths
+// are checked on the way.
 template <int CAUSAL>
 __device__ __forceinline__ SchedSlot decode_paged(const Tc05Params& P, int64_t w, Cursor& cur) {
   SchedSlot s;
-  s.valid = s.b = s.h = s.t = s.q_start = s.lq = s.k_start = s.lk = s.split = s.v_start = s.koff = 0;
+  s.valid = s.b = s.h = s.t = s.q_start = s.lq = s.k_start = s.lk = s.v_start = s.koff = 0;
+  s.split = -1;
   const int lane = threadIdx.x & 31;
   const NewRows rows = {P.cu_q, P.seqlens_k, P.batch, P.seqlen_q, P.total_q, P.max_k};
   while (cur.b < P.batch) {
@@ -492,7 +501,7 @@ __device__ __forceinline__ SchedSlot decode_paged(const Tc05Params& P, int64_t w
     int64_t u = 0;
     if (bb < P.batch) {
       r = load_seq(rows, bb, P.ws);
-      u = (int64_t)tiles_for(r.lq, P.rows_per_tile) * P.heads_q * P.num_splits;
+      u = (int64_t)tiles_for(r.lq, P.rows_per_tile) * P.heads_q;
     }
     int64_t incl = u;
 #pragma unroll
@@ -508,20 +517,13 @@ __device__ __forceinline__ SchedSlot decode_paged(const Tc05Params& P, int64_t w
       s.lq = __shfl_sync(kFull, r.lq, L);
       s.lk = __shfl_sync(kFull, r.lk, L);
       s.q_start = __shfl_sync(kFull, r.q0, L);
-      const WorkTile wt = decode_in_sequence(w - first, s.b, tiles_for(s.lq, P.rows_per_tile) * P.num_splits, P.group,
-                                             P.heads_kv, P.kv_chunk);
+      const WorkTile wt =
+          decode_in_sequence(w - first, s.b, tiles_for(s.lq, P.rows_per_tile), P.group, P.heads_kv, P.kv_chunk);
       s.valid = 1;
       s.h = wt.h;
-      s.t = wt.t / P.num_splits;
-      s.split = wt.t % P.num_splits;
+      s.t = wt.t;
       s.koff = s.lk - s.lq;
-      // the key tiles the work tile's rows see, cut into ranges
-      const int kv_end =
-          (CAUSAL & kMaskCausal) ? min(s.lk, s.koff + min(s.lq, (s.t + 1) * P.rows_per_tile)) : s.lk;
-      int32_t j0, j1;
-      split_range(s.split, P.num_splits, kv_end > 0 ? tiles_for(kv_end, kBlockN) : 0, &j0, &j1);
-      s.k_start = j0;
-      s.v_start = j1;
+      s.v_start = tiles_for(s.lk, kBlockN);
       return s;
     }
     cur.base += __shfl_sync(kFull, incl, 31);
@@ -529,6 +531,39 @@ __device__ __forceinline__ SchedSlot decode_paged(const Tc05Params& P, int64_t w
   }
   return s;
 }
+
+// Walk through a work list: items `item` .. `last` belong to the schedule
+// entry this CTA has taken.
+struct ListCursor {
+  int item = 0, last = -1;
+  __device__ __forceinline__ bool more() const { return item < last; }
+  // The items of schedule entry w (none: item > last).
+  __device__ __forceinline__ void take(const Tc05Params& P, int64_t w) {
+    const int whole = P.plan->whole;
+    item = 0;
+    last = -1;
+    if (w < whole) {
+      item = last = (int)w;
+    } else if (w - whole < P.plan->pieces) {
+      item = P.pieces[w - whole].first;
+      last = P.pieces[w - whole].last;
+    }
+  }
+  __device__ __forceinline__ SchedSlot slot(const Tc05Params& P) const {
+    SchedSlot s;
+    s.valid = s.b = s.h = s.t = s.q_start = s.lq = s.k_start = s.lk = s.v_start = s.koff = 0;
+    s.split = -1;
+    if (item <= last) {
+      const PlanItem& x = P.items[item];
+      s.valid = 1;
+      s.b = x.b; s.h = x.h; s.t = x.t;
+      s.q_start = x.q_start; s.lq = x.lq; s.lk = x.lk;
+      s.k_start = x.j0; s.v_start = x.j1; s.split = x.slot;
+      s.koff = x.lk - x.lq;
+    }
+    return s;
+  }
+};
 
 // Page of this lane's part of the 128-key tile `tile` of sequence b, -1 if the
 // part starts at or past the sequence's end: lane i holds the page of keys
@@ -594,14 +629,24 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
 #pragma unroll
   for (int s = 0; s < T::NK; ++s) { k_fill_parity[s] = 0; k_used[s] = false; }
   Cursor cur;
+  [[maybe_unused]] ListCursor list;
   // The first work index is this CTA's own (a pair's: the cluster's).
   int64_t w = T::PAIR ? (int64_t)ptx::cluster_id_x() : (int64_t)blockIdx.x;
   const int64_t units = T::PAIR ? (int64_t)ptx::nclusters_x() : (int64_t)gridDim.x;
   bool aborted = false;
   while (true) {
     SchedSlot s;
-    if constexpr (T::PAGED) s = decode_paged<CAUSAL>(P, w, cur);
-    else s = decode_work<CAUSAL>(P, w, cur);
+    if constexpr (T::PAGED) {
+      if (listed<CAUSAL>()) {
+        if (!list.more()) list.take(P, w);
+        else ++list.item;
+        s = list.slot(P);
+      } else {
+        s = decode_paged<CAUSAL>(P, w, cur);
+      }
+    } else {
+      s = decode_work<CAUSAL>(P, w, cur);
+    }
     if (!wait_warp(c, BAR_SCHED_EMPTY + sched.idx, sched.phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
     if (lane == 0) {
       volatile int32_t* p = reinterpret_cast<volatile int32_t*>(c.smem + T::OFF_SCHED + kSlotBytes * sched.idx);
@@ -677,6 +722,7 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
     // Next work index: from the shared counter (dynamic), one grid stride on
     // (static), or none (one CTA per work tile). A pair's first CTA takes it
     // from the counter and writes it into the second CTA's shared memory.
+    if (T::PAGED && listed<CAUSAL>() && list.more()) continue;   // the next segment of this entry
     if (P.schedule == ATTN_SCHEDULE_DYNAMIC) {
       if (!T::PAIR || lead) {
         int64_t nw = 0;
@@ -996,11 +1042,9 @@ __device__ void role_mma(const Tc05Params& P, const Ctx& c, const int i) {
 }
 
 // ---------------------------------------------------------------------------------------------
-// Paged variants: LSE element of token qi and query head h (copy `sp` of the
-// layout for a split-KV range).
-__device__ __forceinline__ int64_t paged_lse_index(const Tc05Params& P, const SchedSlot& s, int sp, int qi, int h) {
-  return P.packed ? ((int64_t)sp * P.heads_total + h) * P.total_q + s.q_start + qi
-                  : (((int64_t)sp * P.batch + s.b) * P.heads_total + h) * P.seqlen_q + qi;
+// Paged variants: LSE element of token qi and query head h.
+__device__ __forceinline__ int64_t paged_lse_index(const Tc05Params& P, const SchedSlot& s, int qi, int h) {
+  return P.packed ? (int64_t)h * P.total_q + s.q_start + qi : ((int64_t)s.b * P.heads_total + h) * P.seqlen_q + qi;
 }
 
 template <class T, int CAUSAL>
@@ -1043,7 +1087,9 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
     // [split][Hq][Tq]).
     const bool split_kv = splits_keys<CAUSAL>(P);
     const int sp = split_kv ? s.split : 0;
-    const int64_t lse_idx = T::PAGED ? paged_lse_index(P, s, sp, qi, (s.h << P.pack_shift) + (tid & ((1 << P.pack_shift) - 1)))
+    const bool partial = T::PAGED ? listed<CAUSAL>() && s.split >= 0 : splits_keys<CAUSAL>(P);
+    const int64_t lse_idx = T::PAGED ? (partial ? (int64_t)s.split * kRowsPerTile + kBlockM * i + tid
+                                                : paged_lse_index(P, s, qi, (s.h << P.pack_shift) + (tid & ((1 << P.pack_shift) - 1))))
                           : P.packed ? ((int64_t)sp * P.heads_q + s.h) * P.total_q + s.q_start + qi
                                      : (((int64_t)sp * P.batch + s.b) * P.heads_q + s.h) * P.seqlen_q + qi;
     float c_row = P.scale_log2;
@@ -1211,7 +1257,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
     }
     // Row statistics: LSE (natural log) here, 1/l to the epilogue. A split-KV
     // range writes the LSE of its own keys for the merge.
-    float* const lse_dst = splits_keys<CAUSAL>(P) ? P.lse_part : P.lse;
+    float* const lse_dst = partial ? P.lse_part : P.lse;
     if (row_valid && lse_dst != nullptr) {
       const float lse = l > 0.f ? (m + ptx::lg2(l)) * 0.69314718055994531f : -INFINITY;
       lse_dst[lse_idx] = lse;
@@ -1244,10 +1290,10 @@ __device__ __forceinline__ void store_row_chunk(uint16_t* dst, const uint32_t (&
 
 // Split-KV: row of the partial O array [split][rows][Hq] (rows = B*Sq, or Tq
 // when packed) of query row qi of work tile s.
-__device__ __forceinline__ int64_t partial_row(const Tc05Params& P, const SchedSlot& s, int qi, int h, int heads) {
+__device__ __forceinline__ int64_t partial_row(const Tc05Params& P, const SchedSlot& s, int qi) {
   const int64_t rows = P.packed ? (int64_t)P.total_q : (int64_t)P.batch * P.seqlen_q;
   const int64_t row = P.packed ? (int64_t)s.q_start + qi : (int64_t)s.b * P.seqlen_q + qi;
-  return ((int64_t)s.split * rows + row) * heads + h;
+  return ((int64_t)s.split * rows + row) * P.heads_q + s.h;
 }
 
 // Split-KV: one 32-column chunk of a row of normalised partial O, in fp32,
@@ -1443,8 +1489,9 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
       ptx::mbar_arrive(c.bar(BAR_STATS_FREE + i));
       const int qi = T::PAGED ? g.row[i] + (tid >> P.pack_shift) : g.row[i] + tid;
       const int h = T::PAGED ? (s.h << P.pack_shift) + (tid & ((1 << P.pack_shift) - 1)) : s.h;
-      const int heads = T::PAGED ? P.heads_total : P.heads_q;
       const bool row_valid = qi < s.lq;
+      const bool partial = T::PAGED ? listed<CAUSAL>() && s.split >= 0 : splits_keys<CAUSAL>(P);
+      const int64_t part_at = T::PAGED ? (int64_t)s.split * kRowsPerTile + kBlockM * i + tid : partial_row(P, s, qi);
       uint16_t* orow = P.o + (int64_t)s.b * P.o_stride_b + (int64_t)(s.q_start + qi) * P.o_stride_t +
                        (int64_t)h * P.o_stride_h;
       if (g.n[i] > 0) {
@@ -1452,9 +1499,9 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
         ofinal_phase[i] ^= 1u;
         ptx::tc_fence_after();
         const uint32_t tO = c.tmem + lane_base + T::tm_o(i);
-        if (splits_keys<CAUSAL>(P)) {
+        if (partial) {
           // Split-KV range: normalised partial O in fp32 for the merge.
-          float* prow = P.o_part + partial_row(P, s, qi, h, heads) * T::DV;
+          float* prow = P.o_part + part_at * T::DV;
 #pragma unroll 1
           for (int q = 0; q < T::DV / 32; ++q) {
             uint32_t r[32];
@@ -1471,11 +1518,11 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
             if (row_valid) store_row_chunk<T>(orow + 32 * q, r, rl, P.o_store32 != 0);
           }
         }
-      } else if (row_valid && splits_keys<CAUSAL>(P)) {
+      } else if (row_valid && partial) {
         // An empty key range (a short packed sequence, or under the causal
         // mask a range this tile's rows do not reach): a zero partial row
         // (its LSE is -inf, so the merge gives it no weight).
-        float4* d = reinterpret_cast<float4*>(P.o_part + partial_row(P, s, qi, h, heads) * T::DV);
+        float4* d = reinterpret_cast<float4*>(P.o_part + part_at * T::DV);
 #pragma unroll 1
         for (int e = 0; e < T::DV / 4; ++e) d[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       } else if (row_valid) {

@@ -46,6 +46,29 @@ struct CacheView {
   int32_t num_pages, page_shift, max_pages, heads_kv;
 };
 
+// Work list of a paged problem (paged_plan.cu): a query tile and the key tiles
+// [j0, j1) of it to visit.
+struct PlanItem {
+  int32_t b, h, t;         // sequence, tile of heads, tile of tokens
+  int32_t q_start, lq, lk; // the sequence's first row, new tokens, keys
+  int32_t j0, j1;
+  int32_t slot;            // partial result to write, or -1: the tile is whole
+};
+struct PlanPiece {
+  int32_t first, last;     // items of one schedule entry
+};
+struct PlanCut {
+  PlanItem item;           // slot: the first part's
+  int32_t parts;
+};
+struct PlanHead {
+  int32_t whole, pieces, cut;
+  int32_t pad;
+};
+constexpr int kPlanMaxBatch = 1024;
+constexpr int64_t kPlanMaxTiles = 8192;
+constexpr int kMinPieceUnits = 8;   // key tiles of a piece worth its set-up and its share of the merge
+
 // Everything the tcgen05 kernel needs, passed as one __grid_constant__ struct.
 struct Tc05Params {
   CUtensorMap tm_q;        // Q (nope part): box {64 or 128 elements, 1, 128, 1}
@@ -89,6 +112,9 @@ struct Tc05Params {
   int32_t max_k;           // upper bound of them
   int32_t pack_shift;      // log2 of the query heads in a tile
   int32_t heads_total;     // Hq
+  const PlanHead* plan;    // work list, or NULL: every query tile whole, in order
+  const PlanItem* items;
+  const PlanPiece* pieces;
 };
 
 // Arguments of the split-KV merge kernel.
@@ -100,7 +126,6 @@ struct SplitCombineParams {
   int32_t splits, batch, seqlen_q, heads_q;
   int32_t packed, total_q;
   int64_t o_stride_b, o_stride_t, o_stride_h;   // elements
-  const int32_t* cu_q;     // packed, or NULL: rows outside [cu_q[0], cu_q[batch]) are left as they are
 };
 
 // Kernel variants of the tcgen05 path.

@@ -64,6 +64,26 @@ struct StreamParams {
   float* part_o;             // [2 * grid][rows][D], not normalised
 };
 
+// Arguments of the plan and merge kernels of a paged problem on the tcgen05 kernel.
+struct PlanParams {
+  NewRows s;
+  int32_t heads_kv, group, kv_chunk, tokens, causal, ctas;   // as in Tc05Params (tokens = rows_per_tile)
+  int32_t pack_shift, heads_total;
+  int32_t max_tiles;         // room in the list
+  uint32_t* ws;
+  PlanHead* head;
+  PlanItem* items;
+  PlanPiece* pieces;
+  PlanCut* cuts;
+  const float* lse_part;     // [slots][256]
+  const float* o_part;       // [slots][256][D], normalised
+  uint16_t* o;
+  float* lse;
+  int64_t o_b, o_t, o_h;     // elements
+};
+cudaError_t paged_plan_launch(const PlanParams& p, cudaStream_t stream);
+cudaError_t paged_tile_merge_launch(const PlanParams& p, int head_dim, int max_cut, cudaStream_t stream);
+
 cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream);
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream);
 // Streaming attention over `grid` CTAs with row tiles of 16 * row_groups rows

@@ -153,27 +153,42 @@ int64_t shared_rows(const attn_paged_params* p) {
 bool use_tc05(const attn_paged_params* p) { return shared_rows(p) > kStreamRows; }
 
 // tcgen05 kernel: query heads packed into a 128-row tile (the largest power of
-// two that divides the group), tokens of a 256-row work tile, split-KV ranges.
+// two that divides the group), tokens of a 256-row work tile, and the work
+// list's memory. Without a list (few keys, where nothing is worth cutting, or
+// so many tiles that their whole number per CTA does not matter) every tile is
+// taken whole.
 struct TilePlan {
   int pack_shift;
   int tokens;
-  int64_t work;      // upper bound of the work tiles, without the split
-  int32_t splits;
-  size_t lse_bytes, o_bytes;
+  int64_t work;      // upper bound of the work tiles
+  bool list;
+  int max_cut, max_pieces;
+  size_t items, pieces, cuts, lse, o;   // bytes, in this order behind the plan's head
+  size_t bytes;
 };
 TilePlan plan_tiles(const attn_paged_params* p) {
   TilePlan t = {};
-  const int group = p->num_heads_q / p->cache.num_heads_kv;
+  const attn_kv_cache& c = p->cache;
+  const int group = p->num_heads_q / c.num_heads_kv;
   while (t.pack_shift < 7 && group % (2 << t.pack_shift) == 0) ++t.pack_shift;
   t.tokens = af::kRowsPerTile >> t.pack_shift;
-  t.work = (int64_t)p->cache.batch * (p->num_heads_q >> t.pack_shift) * af::tiles_for(p->seqlen_q, t.tokens);
-  const int64_t rows =
-      (p->cu_seqlens_q != nullptr ? (int64_t)p->total_q : (int64_t)p->cache.batch * p->seqlen_q) * p->num_heads_q;
-  t.splits = af::choose_splits_paged(t.work, af::tiles_for(p->seqlen_k, af::kBlockN), rows, p->cache.head_dim,
-                                     af::sm_count(), af::kMaxSplits);
-  if (t.splits > 1) {
-    t.lse_bytes = round256((size_t)t.splits * rows * sizeof(float));
-    t.o_bytes = (size_t)t.splits * rows * p->cache.head_dim * sizeof(float);
+  int64_t token_tiles = (int64_t)c.batch * af::tiles_for(p->seqlen_q, t.tokens);
+  if (p->cu_seqlens_q != nullptr && p->total_q / t.tokens + c.batch < token_tiles)
+    token_tiles = p->total_q / t.tokens + c.batch;
+  t.work = token_tiles * (p->num_heads_q >> t.pack_shift);
+  t.list = af::tiles_for(p->seqlen_k, af::kBlockN) > af::kMinPieceUnits && t.work <= af::kPlanMaxTiles &&
+           c.batch <= af::kPlanMaxBatch;
+  if (t.list) {
+    const int64_t ctas = af::sm_count();
+    t.max_cut = (int)(t.work < 2 * ctas ? t.work : 2 * ctas);
+    t.max_pieces = (int)(2 * ctas);
+    const int64_t slots = t.max_cut + t.max_pieces;
+    t.items = round256((size_t)(t.work + slots) * sizeof(af::PlanItem));
+    t.pieces = round256((size_t)t.max_pieces * sizeof(af::PlanPiece));
+    t.cuts = round256((size_t)t.max_cut * sizeof(af::PlanCut));
+    t.lse = round256((size_t)slots * af::kRowsPerTile * sizeof(float));
+    t.o = (size_t)slots * af::kRowsPerTile * c.head_dim * sizeof(float);
+    t.bytes = 256 + t.items + t.pieces + t.cuts + t.lse + t.o;
   }
   return t;
 }
@@ -211,8 +226,7 @@ StreamPlan plan_stream(const attn_paged_params* p) {
 
 size_t workspace_need(const attn_paged_params* p) {
   if (use_tc05(p)) {
-    const TilePlan t = plan_tiles(p);
-    return ATTN_FWD_WORKSPACE_BYTES + t.lse_bytes + t.o_bytes;
+    return ATTN_FWD_WORKSPACE_BYTES + plan_tiles(p).bytes;
   }
   const StreamPlan s = plan_stream(p);
   return ATTN_FWD_WORKSPACE_BYTES + s.meta_bytes + s.ml_bytes + s.o_bytes;
@@ -267,46 +281,59 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   prm.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   prm.timeout_ns = 2000000000ull;
   prm.schedule = ATTN_SCHEDULE_DYNAMIC;
-  prm.num_splits = plan.splits;
+  prm.num_splits = 1;
   prm.cache = view_of(c);
   prm.seqlens_k = p->seqlens_k;
   prm.max_k = p->seqlen_k;
   prm.pack_shift = plan.pack_shift;
   prm.heads_total = p->num_heads_q;
-  if (plan.splits > 1) {
-    uint8_t* ws = static_cast<uint8_t*>(p->workspace);
-    prm.lse_part = reinterpret_cast<float*>(ws + ATTN_FWD_WORKSPACE_BYTES);
-    prm.o_part = reinterpret_cast<float*>(ws + ATTN_FWD_WORKSPACE_BYTES + plan.lse_bytes);
-  }
-  const int64_t work = plan.work * plan.splits;
   const int sms = af::sm_count();
-  const int grid = (int)(work < sms ? work : sms);
-  prm.dependent_launch = grid < sms ? 1 : 0;
-  const int mask = (p->causal ? af::kMaskCausal : 0) | (plan.splits > 1 ? af::kMaskNoneSplit : 0);
+  const int64_t most = plan.list ? plan.work + plan.max_pieces : plan.work;
+  const int grid = (int)(most < sms ? most : sms);
+  // A full grid gains nothing from starting before the kernel in front of it
+  // ends, but for the plan kernel, which is one block.
+  prm.dependent_launch = plan.list || grid < sms ? 1 : 0;
+  af::PlanParams pp;
+  memset(&pp, 0, sizeof(pp));
+  cudaError_t e = cudaSuccess;
+  if (plan.list) {
+    uint8_t* ws = static_cast<uint8_t*>(p->workspace) + ATTN_FWD_WORKSPACE_BYTES;
+    pp.s = {p->cu_seqlens_q, p->seqlens_k, c.batch, p->seqlen_q, p->total_q, p->seqlen_k};
+    pp.heads_kv = c.num_heads_kv;
+    pp.group = prm.group;
+    pp.kv_chunk = prm.kv_chunk;
+    pp.tokens = plan.tokens;
+    pp.causal = p->causal != 0;
+    pp.ctas = grid;
+    pp.pack_shift = plan.pack_shift;
+    pp.heads_total = p->num_heads_q;
+    pp.max_tiles = (int32_t)plan.work;
+    pp.ws = prm.ws;
+    pp.head = reinterpret_cast<af::PlanHead*>(ws);
+    pp.items = reinterpret_cast<af::PlanItem*>(ws += 256);
+    pp.pieces = reinterpret_cast<af::PlanPiece*>(ws += plan.items);
+    pp.cuts = reinterpret_cast<af::PlanCut*>(ws += plan.pieces);
+    prm.lse_part = reinterpret_cast<float*>(ws += plan.cuts);
+    prm.o_part = reinterpret_cast<float*>(ws += plan.lse);
+    pp.lse_part = prm.lse_part;
+    pp.o_part = prm.o_part;
+    pp.o = prm.o;
+    pp.lse = p->lse;
+    pp.o_b = prm.o_stride_b;
+    pp.o_t = prm.o_stride_t;
+    pp.o_h = prm.o_stride_h;
+    prm.plan = pp.head;
+    prm.items = pp.items;
+    prm.pieces = pp.pieces;
+    e = af::paged_plan_launch(pp, stream);
+    if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged plan launch failed: %s", cudaGetErrorString(e));
+  }
+  const int mask = (p->causal ? af::kMaskCausal : 0) | (plan.list ? af::kMaskNoneSplit : 0);
   const int variant = c.head_dim == 64 ? (fp8 ? af::kVarPaged8D64 : af::kVarPagedD64)
                                        : (fp8 ? af::kVarPaged8D128 : af::kVarPagedD128);
-  cudaError_t e = af::tc05_launch(variant, mask, prm, grid, stream);
+  e = af::tc05_launch(variant, mask, prm, grid, stream);
+  if (e == cudaSuccess && plan.list) e = af::paged_tile_merge_launch(pp, c.head_dim, plan.max_cut, stream);
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
-  if (plan.splits > 1) {
-    af::SplitCombineParams cp;
-    memset(&cp, 0, sizeof(cp));
-    cp.lse_part = prm.lse_part;
-    cp.o_part = prm.o_part;
-    cp.o = prm.o;
-    cp.lse = p->lse;
-    cp.splits = plan.splits;
-    cp.batch = c.batch;
-    cp.seqlen_q = p->seqlen_q;
-    cp.heads_q = p->num_heads_q;
-    cp.packed = prm.packed;
-    cp.total_q = prm.total_q;
-    cp.o_stride_b = prm.o_stride_b;
-    cp.o_stride_t = prm.o_stride_t;
-    cp.o_stride_h = prm.o_stride_h;
-    cp.cu_q = p->cu_seqlens_q;
-    e = af::splitkv_combine_launch(cp, c.head_dim, stream);
-    if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "split-KV merge launch failed: %s", cudaGetErrorString(e));
-  }
   return ATTN_OK;
 }
 

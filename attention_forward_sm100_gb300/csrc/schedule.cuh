@@ -164,29 +164,6 @@ AF_HD inline int32_t choose_splits_causal(int64_t heads, int32_t lq, int32_t lk,
   return best;
 }
 
-// Split count for `work` paged query tiles (the last rows of their sequences,
-// so nearly all of the kv_tiles key tiles are seen by each) on `ctas` CTAs.
-// As choose_splits, in units of one 256-row step over a key tile, plus the
-// merge: its launch (~4 steps) and its traffic (the fp32 partial O of `rows`
-// query rows times heads written and read back at ~6 TB/s, 1.1 us per step).
-AF_HD inline int32_t choose_splits_paged(int64_t work, int32_t kv_tiles, int64_t rows, int32_t dv, int32_t ctas,
-                                         int32_t max_splits) {
-  if (work <= 0 || kv_tiles <= 1 || ctas <= 0) return 1;
-  const int32_t hi = kv_tiles < max_splits ? kv_tiles : max_splits;
-  int32_t best = 1;
-  int64_t best_cost = -1;
-  for (int32_t s = 1; s <= hi; ++s) {
-    const int64_t waves = (work * s + ctas - 1) / ctas;
-    const int64_t merge = s > 1 ? 4 + (int64_t)s * rows * dv * 8 / 6600000 : 0;
-    const int64_t cost = waves * ((kv_tiles + s - 1) / s + 2) + merge;
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  return best;
-}
-
 // KV heads per chunk: as many as keep the chunk's K/V (seqlen_k rows of
 // k_row_bytes + v_row_bytes per head) within l2_budget bytes.
 AF_HD inline int32_t choose_kv_chunk(int64_t seqlen_k, int64_t kv_row_bytes, int32_t heads_kv, int64_t l2_budget) {

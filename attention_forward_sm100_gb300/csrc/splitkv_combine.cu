@@ -40,7 +40,6 @@ __global__ void __launch_bounds__(kCombineWarps * 32) splitkv_combine_kernel(con
   if (row >= rows) return;
   const int h = (int)(row % p.heads_q);
   const int64_t t = row / p.heads_q;
-  if (p.cu_q != nullptr && (t < p.cu_q[0] || t >= p.cu_q[p.batch])) return;
   // Partial LSE: S copies of the LSE layout ([B][Hq][Sq] or [Hq][Tq]);
   // partial O: [S][rows][Hq][Dv].
   int64_t lse_row, o_off;

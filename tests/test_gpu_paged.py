@@ -407,3 +407,31 @@ def test_no_rows(pkg):
     k, v = pkg.cache_read(p.k_cache, p.v_cache, p.table, torch.zeros(2, dtype=torch.int32, device="cuda"), total_k=0)
     assert k.shape == (0, 2, 64) and v.shape == (0, 2, 64)
     pkg.check()
+
+
+def test_overlapping_offsets_are_reported(pkg):
+    """Offsets that go back and forth claim more rows than there are: no list
+    or scratch is overrun, and check() says so."""
+    p = R.make([400] * 6, [0, 0, 0, 0, 0, 240], 4, 2, 64, 16, packed=True, seed=28)
+    cu = torch.tensor([0, 240, 0, 240, 0, 240, 240], dtype=torch.int32, device="cuda")
+    pkg.paged_forward(p.q, *p.cache, cu_seqlens_q=cu, max_seqlen_q=240)
+    _bad(pkg, p)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lens_k,lens_q,hq,hkv,dim,page", [
+    ([9000], [256], 4, 4, 128, 64),                      # few tiles, each cut in many pieces
+    ([5000], [300], 16, 2, 64, 128),                     # pieces across tile borders
+    ([4100, 1300, 2600, 1029], [200, 900, 1, 130], 8, 2, 128, 32),   # ragged, whole tiles and cut ones
+    ([1200] * 40, [70] * 40, 6, 2, 64, 16),              # several waves, heads in pairs
+    ([1500, 0, 1100, 3], [40, 5, 0, 100], 32, 1, 64, 16),
+])
+def test_attend_chunks_that_are_cut(pkg, lens_k, lens_q, hq, hkv, dim, page, fp8):
+    p = R.make(lens_k, lens_q, hq, hkv, dim, page, fp8=fp8, packed=True, seed=29)
+    for causal in (True, False):
+        kw = dict(causal=causal, cu_seqlens_q=p.cu_q, max_seqlen_q=max(lens_q), **p.scales)
+        o, lse = pkg.paged_forward(p.q, *p.cache, **kw)
+        pkg.check()
+        R.check_attend(p, o, lse, causal)
+        o2, lse2 = pkg.paged_forward(p.q, *p.cache, **kw)
+        assert torch.equal(R.bits(o), R.bits(o2)) and torch.equal(R.bits(lse), R.bits(lse2))
