@@ -8,7 +8,10 @@
 
 namespace af {
 
-constexpr int kStreamTile = 64;      // keys per work unit of the streaming attention kernel
+// Keys per work unit of the streaming attention kernel: 16 per warp and step
+// for 256-byte cache rows, 32 for shorter ones (the fixed work of a step then
+// weighs half); a group of several warps shares its keys.
+constexpr int stream_tile(int row_bytes, int group_warps) { return group_warps == 1 && row_bytes < 256 ? 128 : 64; }
 constexpr int kMinPage = 16;         // smallest page: one warp's step of keys lies in one page
 
 // The new rows of each sequence (fixed: b * seqlen_q; packed: cu_q) and the
@@ -86,9 +89,9 @@ cudaError_t paged_tile_merge_launch(const PlanParams& p, int head_dim, int max_c
 
 cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream);
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream);
-// Streaming attention over `grid` CTAs with row tiles of 16 * row_groups rows
-// (1, 2 or 4), then the merge of split segments if p.split.
-cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_groups, int grid,
+// Streaming attention over `grid` CTAs with row tiles of 8, 16, 32 or 64 rows,
+// then the merge of split segments if p.split.
+cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,
                                 cudaStream_t stream);
 
 #ifdef __CUDACC__

@@ -194,24 +194,25 @@ TilePlan plan_tiles(const attn_paged_params* p) {
 }
 
 struct StreamPlan {
-  int row_groups;      // 16-row groups of a row tile
+  int row_tile;
   int split;
   int64_t grid;
   int64_t units;       // upper bound of the work units
   size_t meta_bytes, ml_bytes, o_bytes;
 };
 
-// Row tiles of 16, 32 or 64 rows, the smallest that holds a sequence's rows;
+// Row tiles of 8, 16, 32 or 64 rows, the smallest that holds a sequence's rows;
 // two CTAs per SM. Segments of up to kUnsplitTiles key tiles are not cut: the
 // merge would cost more than the longer CTA.
 constexpr int kUnsplitTiles = 4;
 StreamPlan plan_stream(const attn_paged_params* p) {
   StreamPlan s = {};
   const int64_t rows = shared_rows(p);
-  s.row_groups = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  const int64_t rt = 16 * s.row_groups;
+  s.row_tile = rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+  const int64_t rt = s.row_tile;
+  const int row_bytes = p->cache.head_dim * (p->cache.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2);
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
-  const int64_t tiles = af::tiles_for(p->seqlen_k, af::kStreamTile);
+  const int64_t tiles = af::tiles_for(p->seqlen_k, af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
   s.split = tiles > kUnsplitTiles ? 1 : 0;
   s.units = segments * (s.split ? tiles : 1);
   const int64_t most = s.split ? 2ll * af::sm_count() : s.units;
@@ -453,7 +454,7 @@ attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
   a.part_ml = reinterpret_cast<float2*>(ws + plan.meta_bytes);
   a.part_o = reinterpret_cast<float*>(ws + plan.meta_bytes + plan.ml_bytes);
   const cudaError_t e =
-      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_groups,
+      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
                               (int)plan.grid, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
   return ATTN_OK;

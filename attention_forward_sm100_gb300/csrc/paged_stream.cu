@@ -40,16 +40,19 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kThreads = 128;
+constexpr int min_int(int a, int b) { return a < b ? a : b; }
 
-template <int D_, bool FP8_, int WM_>
+// NT * 8 rows per warp, WM warps to a key group.
+template <int D_, bool FP8_, int NT_, int WM_>
 struct Cfg {
-  static constexpr int D = D_, WM = WM_;
+  static constexpr int D = D_, NT = NT_, WM = WM_;
   static constexpr bool FP8 = FP8_;
   static constexpr int WK = 4 / WM;              // key groups
-  static constexpr int KW = 16 * WM;             // keys of a group per tile
-  static constexpr int RT = 16 * WM;             // rows of a row tile
-  static_assert(WK * KW == kStreamTile, "the groups cover a tile");
+  static constexpr int RT = 8 * NT * WM;         // rows of a row tile
   static constexpr int ROWB = FP8 ? D : 2 * D;   // bytes of a cached row
+  static constexpr int KW = stream_tile(ROWB, WM) / WK;   // keys of a group per tile
+  static constexpr int TILE = KW * WK;
+  static constexpr int BLOCKS = KW / 16;         // 16-key blocks of a group's tile
   static constexpr int CPR = ROWB / 16;          // 16-byte pieces of a row
   static constexpr int GT = 32 * WM;             // threads of a group
   static constexpr int RS = GT / CPR;            // rows a group loads at a time
@@ -57,12 +60,12 @@ struct Cfg {
   static constexpr int KV = KW * ROWB;
   static constexpr int SC = FP8 ? KW * 4 : 0;
   static constexpr int STAGE = 2 * KV + 2 * SC;  // bytes of one group's stage
-  static constexpr int STAGES = ROWB == 256 ? 3 : (ROWB == 128 ? 6 : 8);
+  static constexpr int STAGES = min_int(8, 98304 / (WK * 2 * KV));
   static constexpr int PITCH = D + 8;            // floats of a row in the group merge
   static constexpr int RING = WK * STAGES * STAGE;
   static constexpr int MERGE = WK * RT * (PITCH + 2) * 4;
   static constexpr int SMEM = RING > MERGE ? RING : MERGE;   // the merge reuses the ring
-  static_assert(SMEM <= 113 * 1024, "two CTAs per SM");
+  static_assert(STAGES >= 3 && SMEM <= 113 * 1024, "two CTAs per SM");
   // Position of 16-byte piece `c` of row `r` in a stage (bank conflicts).
   __device__ static int swz_k(int r, int c) {
     return FP8 ? (CPR == 8 ? c ^ ((r & 1) << 2) : c) : c ^ (r & 7);
@@ -81,7 +84,7 @@ __device__ __forceinline__ SeqUnits seq_units(const StreamParams& P, int b) {
   SeqUnits u;
   u.r = load_seq(P.s, b, P.ws);
   u.row_tiles = (int)(((int64_t)u.r.lq * P.group + C::RT - 1) / C::RT);
-  u.tiles = P.split ? max(1, (u.r.lk + kStreamTile - 1) / kStreamTile) : 1;
+  u.tiles = P.split ? max(1, (u.r.lk + C::TILE - 1) / C::TILE) : 1;
   u.units = u.row_tiles * P.c.heads_kv * u.tiles;
   return u;
 }
@@ -167,7 +170,7 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 template <class C>
 __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, uint8_t* smem) {
-  constexpr int D = C::D, WM = C::WM, KW = C::KW;
+  constexpr int D = C::D, WM = C::WM, NT = C::NT, KW = C::KW, NB = C::BLOCKS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int wm = warp % WM, kg = warp / WM;
@@ -175,34 +178,71 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   const int hk = pc.seg % P.c.heads_kv, rt = pc.seg / P.c.heads_kv;
   const int rows = s.lq * P.group;
   const uint32_t ring = ptx::smem_u32(smem) + kg * (C::STAGES * C::STAGE);
-  const int key_tiles = (s.lk + kStreamTile - 1) / kStreamTile;
+  const int key_tiles = (s.lk + C::TILE - 1) / C::TILE;
   const int t0 = P.split ? pc.first : 0;
   const int n = P.split ? min(pc.count, key_tiles - t0) : key_tiles;
+  const int row0 = rt * C::RT + 8 * NT * wm;      // this warp's first row
 
-  // This thread's two rows: fragments of q and the keys each row sees.
-  uint32_t qf[D / 16][4];
-  int lim[2];
+  // Rows r0 + 8 x + 2 t and + 1 are this lane's columns of the score and output
+  // tiles: the keys they see, and (e4m3) the factor of their scaled q.
+  int lim[NT][2], lim_min = s.lk;
+  float qscale[NT][2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = rt * C::RT + 16 * wm + g + 8 * e;
+  for (int x = 0; x < NT; ++x)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = row0 + 8 * x + 2 * t + e;
+      // (rows past the segment's end compute on zeros and are not stored)
+      lim[x][e] = P.causal && r < rows ? min(s.lk, s.lk - s.lq + r / P.group + 1) : s.lk;
+      lim_min = min(lim_min, lim[x][e]);
+    }
+  lim_min = min(lim_min, __shfl_xor_sync(kFull, lim_min, 1));
+  lim_min = min(lim_min, __shfl_xor_sync(kFull, lim_min, 2));
+  // q of row g of each column tile: pairs at depths d and d + step of every 16
+  uint32_t qf[NT][D / 16][2];
+#pragma unroll
+  for (int x = 0; x < NT; ++x) {
+    const int r = row0 + 8 * x + g;
     const bool ok = r < rows;
     const RowAt a = row_at(P, hk, ok ? r : 0);
-    // (rows past the tile's end compute on zeros and are not stored)
-    lim[e] = ok && P.causal ? min(s.lk, s.lk - s.lq + a.i + 1) : s.lk;
     const uint8_t* src = P.q + (P.s.cu_q != nullptr ? 0 : pc.b * P.q_b) + (int64_t)(s.q0 + a.i) * P.q_t + a.h * P.q_h;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      // depths of this lane's fragment: pairs at d and d + step
       const int d = C::FP8 ? 16 * (t + 4 * (kk >> 2)) + 4 * (kk & 3) : 16 * kk + 2 * t;
       const int step = C::FP8 ? 2 : 8;
-      qf[kk][e] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * d)) : 0u;
-      qf[kk][2 + e] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * (d + step))) : 0u;
+      qf[x][kk][0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * d)) : 0u;
+      qf[x][kk][1] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * (d + step))) : 0u;
+    }
+    if constexpr (C::FP8) {
+      // The codes of an e4m3 cache are multiplied as f16 (one conversion for two
+      // of them). q becomes f16 too, times the power of two that brings its
+      // largest magnitude to [2^14, 2^15): exact down to 2^-38 of that.
+      uint32_t top = 0u;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          top = max(top, max(qf[x][kk][e] & 0x7fffu, (qf[x][kk][e] >> 16) & 0x7fffu));
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      // 2^(14 - e) in a float's exponent; e at least -112 keeps it finite, a
+      // row with infinities or NaN ends as NaN whatever the factor
+      const int e = max((int)(top >> 7), 15);
+      const float up = __uint_as_float((uint32_t)min(268 - e, 254) << 23);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t w = qf[x][kk][c];
+          qf[x][kk][c] = ptx::pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+        }
+      const float down = __uint_as_float((uint32_t)max(e - 14, 1) << 23);
+      qscale[x][0] = __shfl_sync(kFull, down, 8 * t) * P.scale_log2;
+      qscale[x][1] = __shfl_sync(kFull, down, 8 * t + 4) * P.scale_log2;
+    } else {
+      qscale[x][0] = qscale[x][1] = P.scale_log2;
     }
   }
-  // keys that every row of this warp sees need no mask
-  int lim_min = min(lim[0], lim[1]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(kFull, lim_min, o));
 
   const uint8_t* kbase = P.c.k + hk * P.c.k_head;
   const uint8_t* vbase = P.c.v + hk * P.c.v_head;
@@ -211,28 +251,34 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
 
   // Pages of the 16-key blocks of a group's tile, fetched one tile ahead of
   // their use (the loads' addresses depend on them).
-  int pages[WM];
+  int pages[NB];
   auto fetch_pages = [&](int j) {
-    const int key0 = (t0 + j) * kStreamTile + kg * KW;
+    const int key0 = (t0 + j) * C::TILE + kg * KW;
 #pragma unroll
-    for (int u = 0; u < WM; ++u)
+    for (int u = 0; u < NB; ++u)
       pages[u] = (j < n && key0 + 16 * u < s.lk) ? load_page(P.c, pc.b, (key0 + 16 * u) >> P.c.page_shift, P.ws) : 0;
   };
   auto load_tile = [&](int j) {
-    const int key0 = (t0 + j) * kStreamTile + kg * KW;
+    const int key0 = (t0 + j) * C::TILE + kg * KW;
     const uint32_t st = ring + (j % C::STAGES) * C::STAGE;
+    constexpr int PER = C::RS <= 16 ? 16 / C::RS : 1;   // loads of a 16-key block per thread
 #pragma unroll
-    for (int i = 0; i < C::NL; ++i) {
-      const int row = lrow + i * C::RS;
-      // rows of one load step lie in one 16-key block, or (RS = 32) in two
-      const int page = C::RS <= 16 ? pages[(i * C::RS) >> 4]
-                                   : (lrow < 16 ? pages[(i * C::RS) >> 4] : pages[((i * C::RS) >> 4) + (C::RS > 16)]);
-      const bool ok = key0 + row < s.lk;
-      const int64_t slot = (key0 + row) & page_mask;
-      const uint8_t* ks = ok ? kbase + page * P.c.k_page + slot * P.c.k_tok + lcol * 16 : P.c.k;
-      const uint8_t* vs = ok ? vbase + page * P.c.v_page + slot * P.c.v_tok + lcol * 16 : P.c.v;
-      ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, ks, ok);
-      ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, vs, ok);
+    for (int i = 0; i < C::NL; i += PER) {
+      // block of these loads' rows (RS = 32: of this thread's row)
+      const int u = C::RS <= 16 ? i / PER : 2 * i;
+      const int page = C::RS <= 16 || lrow < 16 ? pages[u] : pages[u + (C::RS > 16 ? 1 : 0)];
+      const int64_t slot = (key0 + lrow + i * C::RS) & page_mask;
+      const uint8_t* ks = kbase + page * P.c.k_page + slot * P.c.k_tok + lcol * 16;
+      const uint8_t* vs = vbase + page * P.c.v_page + slot * P.c.v_tok + lcol * 16;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int row = lrow + (i + x) * C::RS;
+        const bool ok = key0 + row < s.lk;
+        ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, ok ? ks : P.c.k, ok);
+        ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, ok ? vs : P.c.v, ok);
+        ks += C::RS * P.c.k_tok;
+        vs += C::RS * P.c.v_tok;
+      }
     }
     if constexpr (C::FP8) {
       // scales: 4 keys per 16 bytes; a piece that crosses the end is cut there
@@ -240,7 +286,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
         const int which = gt / (KW / 4), k4 = 4 * (gt % (KW / 4));
         int page = pages[0];
 #pragma unroll
-        for (int u = 1; u < WM; ++u)
+        for (int u = 1; u < NB; ++u)
           if ((k4 >> 4) == u) page = pages[u];
         const int left = s.lk - (key0 + k4);
         const int bytes = left >= 4 ? 16 : (left > 0 ? 4 * left : 0);
@@ -257,12 +303,22 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     else ptx::bar_sync(1 + kg, C::GT);
   };
 
-  float acc[D / 8][4];
+  // O^T: depths by rows, D / 16 tiles of 16 depths
+  float acc[D / 16][NT][4];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
+  for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][x][e] = 0.f;
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int x = 0; x < NT; ++x)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[x][e] = -INFINITY;
+      l[x][e] = 0.f;
+    }
 
   fetch_pages(0);
 #pragma unroll 1
@@ -280,123 +336,140 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     fetch_pages(j + C::STAGES);
 
     const uint32_t st = ring + (j % C::STAGES) * C::STAGE;
-    const int key0 = (t0 + j) * kStreamTile + kg * KW;
-    // ---- S = Q K^T
-    float sc[KW / 8][4];
+    const int key0 = (t0 + j) * C::TILE + kg * KW;
+    // ---- S^T = K Q^T: keys g and g + 8 of each block by rows 2 t, 2 t + 1 of each column tile
+    float sc[NB][NT][4];
 #pragma unroll
-    for (int i = 0; i < KW / 8; ++i)
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[i][x][e] = 0.f;
     if constexpr (!C::FP8) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; kk += 2)
+      for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-        for (int i = 0; i < KW / 8; ++i) {
-          uint32_t b[4];
-          const int row = 8 * i + (lane & 7);
-          ptx::ldmatrix_x4(st + row * C::ROWB + C::swz_k(row, 2 * kk + (lane >> 3)) * 16, b);
-          ptx::mma_16816(sc[i], qf[kk], b[0], b[1]);
-          ptx::mma_16816(sc[i], qf[kk + 1], b[2], b[3]);
+        for (int i = 0; i < NB; ++i) {
+          uint32_t a[4];
+          const int row = 16 * i + (lane & 15);
+          ptx::ldmatrix_x4(st + row * C::ROWB + C::swz_k(row, 2 * kk + (lane >> 4)) * 16, a);
+#pragma unroll
+          for (int x = 0; x < NT; ++x) ptx::mma_16816(sc[i][x], a, qf[x][kk][0], qf[x][kk][1]);
         }
     } else {
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int i = 0; i < KW / 8; ++i) {
-          const int row = 8 * i + g;
-          const uint4 w = ptx::ld_shared_v4(st + row * C::ROWB + C::swz_k(row, t + 4 * c) * 16);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < NB; ++i) {
+          const int row = 16 * i + g;
+          const uint4 w0 = ptx::ld_shared_v4(st + row * C::ROWB + C::swz_k(row, t + 4 * c) * 16);
+          const uint4 w1 = ptx::ld_shared_v4(st + (row + 8) * C::ROWB + C::swz_k(row + 8, t + 4 * c) * 16);
+          const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            ptx::mma_16816(sc[i], qf[4 * c + e], ptx::e4m3x2_to_bf16x2(x[e] & 0xffffu), ptx::e4m3x2_to_bf16x2(x[e] >> 16));
-        }
+          for (int e = 0; e < 4; ++e) {
+            uint32_t a[4];
+            ptx::e4m3x4_to_f16x2(u0[e], a[0], a[2]);
+            ptx::e4m3x4_to_f16x2(u1[e], a[1], a[3]);
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i) {
-        const uint2 k2 = ptx::ld_shared_v2(st + 2 * C::KV + (8 * i + 2 * t) * 4);
-        const float k0 = __uint_as_float(k2.x), k1 = __uint_as_float(k2.y);
-        sc[i][0] *= k0;
-        sc[i][1] *= k1;
-        sc[i][2] *= k0;
-        sc[i][3] *= k1;
-      }
-    }
-    // ---- mask, running maximum
-    if (key0 + KW > lim_min) {
-#pragma unroll
-      for (int i = 0; i < KW / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key0 + 8 * i + 2 * t + (e & 1) >= lim[e >> 1]) sc[i][e] = -INFINITY;
-    }
-    float mx[2] = {sc[0][0], sc[0][2]};
-#pragma unroll
-    for (int i = 0; i < KW / 8; ++i) {
-      mx[0] = fmaxf(mx[0], fmaxf(sc[i][0], sc[i][1]));
-      mx[1] = fmaxf(mx[1], fmaxf(sc[i][2], sc[i][3]));
-    }
-    bool grow = false;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 1));
-      mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 2)) * P.scale_log2;
-      grow = grow || mx[e] > m[e] + 8.f;
-    }
-    if (__any_sync(kFull, grow)) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (mx[e] > m[e] + 8.f) {
-          const float alpha = ptx::ex2(m[e] - mx[e]);   // 0 at the first visible key
-          m[e] = mx[e];
-          l[e] *= alpha;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            acc[i][2 * e] *= alpha;
-            acc[i][2 * e + 1] *= alpha;
+            for (int x = 0; x < NT; ++x) ptx::mma_16816_f16(sc[i][x], a, qf[x][4 * c + e][0], qf[x][4 * c + e][1]);
           }
         }
-      }
     }
-    // ---- weights; a row that has seen no key yet keeps m = -inf and weights 0
-    const float off[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+    // ---- scores in log2 units; mask; running maximum
+    const float* scale_sm = reinterpret_cast<const float*>(smem + (st - ptx::smem_u32(smem)) + 2 * C::KV);
 #pragma unroll
-    for (int i = 0; i < KW / 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sc[i][e] = ptx::ex2(fmaf(sc[i][e], P.scale_log2, -off[e >> 1]));
-        l[e >> 1] += sc[i][e];
+    for (int i = 0; i < NB; ++i) {
+      float k0 = 1.f, k1 = 1.f;
+      if constexpr (C::FP8) {
+        k0 = scale_sm[16 * i + g];
+        k1 = scale_sm[16 * i + g + 8];
       }
-    if constexpr (C::FP8) {
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i) {
-        const uint2 v2 = ptx::ld_shared_v2(st + 2 * C::KV + C::SC + (8 * i + 2 * t) * 4);
-        const float v0 = __uint_as_float(v2.x), v1 = __uint_as_float(v2.y);
-        sc[i][0] *= v0;
-        sc[i][1] *= v1;
-        sc[i][2] *= v0;
-        sc[i][3] *= v1;
-      }
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sc[i][x][e] *= C::FP8 ? qscale[x][e & 1] * (e < 2 ? k0 : k1) : qscale[x][e & 1];
     }
-    // ---- O += P V
+    if (key0 + KW > lim_min) {
 #pragma unroll
-    for (int kb = 0; kb < KW / 16; ++kb) {
-      const uint32_t pf[4] = {
-          ptx::pack_bf16(sc[2 * kb][0], sc[2 * kb][1]), ptx::pack_bf16(sc[2 * kb][2], sc[2 * kb][3]),
-          ptx::pack_bf16(sc[2 * kb + 1][0], sc[2 * kb + 1][1]), ptx::pack_bf16(sc[2 * kb + 1][2], sc[2 * kb + 1][3])};
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + 16 * i + g + 8 * (e >> 1) >= lim[x][e & 1]) sc[i][x][e] = -INFINITY;
+    }
+    float mx[NT][2];
+    bool grow = false;
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = fmaxf(sc[0][x][e], sc[0][x][2 + e]);
+#pragma unroll
+        for (int i = 1; i < NB; ++i) v = fmaxf(v, fmaxf(sc[i][x][e], sc[i][x][2 + e]));
+        grow = grow || v > m[x][e] + 8.f;
+        mx[x][e] = v;
+      }
+    if (__any_sync(kFull, grow)) {   // some row's maximum may have to move (the lanes hold parts of it)
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = mx[x][e];
+          v = fmaxf(v, __shfl_xor_sync(kFull, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(kFull, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(kFull, v, 16));
+          if (v > m[x][e] + 8.f) {
+            const float alpha = ptx::ex2(m[x][e] - v);   // 0 at the first visible key
+            m[x][e] = v;
+            l[x][e] *= alpha;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              acc[i][x][e] *= alpha;
+              acc[i][x][2 + e] *= alpha;
+            }
+          }
+        }
+    }
+    // ---- weights (a row that has seen no key yet keeps m = -inf and weights 0), O^T += V^T P^T
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      uint32_t pf[NT][2];
+      float v0 = 1.f, v1 = 1.f;
+      if constexpr (C::FP8) {
+        v0 = scale_sm[KW + 16 * i + g];
+        v1 = scale_sm[KW + 16 * i + g + 8];
+      }
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float off = m[x][e & 1] == -INFINITY ? 0.f : m[x][e & 1];
+          w[e] = ptx::ex2(sc[i][x][e] - off);
+          l[x][e & 1] += w[e];
+          if constexpr (C::FP8) w[e] *= e < 2 ? v0 : v1;
+        }
+        // (key, rows) pairs to (row, keys) pairs
+        pf[x][0] = ptx::movmatrix_trans(ptx::pack_bf16(w[0], w[1]));
+        pf[x][1] = ptx::movmatrix_trans(ptx::pack_bf16(w[2], w[3]));
+      }
       if constexpr (!C::FP8) {
 #pragma unroll
-        for (int np = 0; np < D / 16; ++np) {
-          uint32_t b[4];
-          const int row = 16 * kb + (lane & 15);
-          ptx::ldmatrix_x4_trans(st + C::KV + row * C::ROWB + C::swz_v(row, 2 * np + (lane >> 4)) * 16, b);
-          ptx::mma_16816(acc[2 * np], pf, b[0], b[1]);
-          ptx::mma_16816(acc[2 * np + 1], pf, b[2], b[3]);
+        for (int q = 0; q < D / 16; ++q) {
+          uint32_t a[4];
+          const int row = 16 * i + (lane & 7) + 8 * (lane >> 4);
+          ptx::ldmatrix_x4_trans(st + C::KV + row * C::ROWB + C::swz_v(row, 2 * q + ((lane >> 3) & 1)) * 16, a);
+#pragma unroll
+          for (int x = 0; x < NT; ++x) ptx::mma_16816(acc[q][x], a, pf[x][0], pf[x][1]);
         }
       } else {
-        // lane (g, t): columns g * D/8 .. + D/8 of keys 2t, 2t+1, 2t+8, 2t+9
+        // lane (g, t): depths g * D/8 .. + D/8 of keys 2t, 2t+1, 2t+8, 2t+9
         uint32_t v[4][D / 32];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int row = 16 * kb + 2 * t + (e & 1) + 8 * (e >> 1);
+          const int row = 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
           const uint32_t at = st + C::KV + row * C::ROWB;
           if constexpr (D == 128) {
             const uint4 w = ptx::ld_shared_v4(at + C::swz_v(row, g) * 16);
@@ -408,21 +481,25 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
         }
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
-          const uint32_t lo01 = __byte_perm(v[0][w], v[1][w], 0x5140), lo23 = __byte_perm(v[0][w], v[1][w], 0x7362);
-          const uint32_t hi01 = __byte_perm(v[2][w], v[3][w], 0x5140), hi23 = __byte_perm(v[2][w], v[3][w], 0x7362);
-          ptx::mma_16816(acc[4 * w], pf, ptx::e4m3x2_to_bf16x2(lo01 & 0xffffu), ptx::e4m3x2_to_bf16x2(hi01 & 0xffffu));
-          ptx::mma_16816(acc[4 * w + 1], pf, ptx::e4m3x2_to_bf16x2(lo01 >> 16), ptx::e4m3x2_to_bf16x2(hi01 >> 16));
-          ptx::mma_16816(acc[4 * w + 2], pf, ptx::e4m3x2_to_bf16x2(lo23 & 0xffffu), ptx::e4m3x2_to_bf16x2(hi23 & 0xffffu));
-          ptx::mma_16816(acc[4 * w + 3], pf, ptx::e4m3x2_to_bf16x2(lo23 >> 16), ptx::e4m3x2_to_bf16x2(hi23 >> 16));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __byte_perm(v[0][w], v[1][w], h ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
+            const uint32_t a[4] = {ptx::e4m3x2_to_bf16x2(lo & 0xffffu), ptx::e4m3x2_to_bf16x2(lo >> 16),
+                                   ptx::e4m3x2_to_bf16x2(hi & 0xffffu), ptx::e4m3x2_to_bf16x2(hi >> 16)};
+#pragma unroll
+            for (int x = 0; x < NT; ++x) ptx::mma_16816(acc[2 * w + h][x], a, pf[x][0], pf[x][1]);
+          }
         }
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    l[e] += __shfl_xor_sync(kFull, l[e], 1);
-    l[e] += __shfl_xor_sync(kFull, l[e], 2);
-  }
+  for (int x = 0; x < NT; ++x)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) l[x][e] += __shfl_xor_sync(kFull, l[x][e], o);
   ptx::cp_async_wait<0>();
 
   // ---- the key groups' results meet in shared memory (over the ring)
@@ -430,24 +507,22 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   float2* ml = reinterpret_cast<float2*>(buf + C::WK * C::RT * C::PITCH);   // [WK][RT]
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = 16 * wm + g + 8 * e;
-    float* dst = buf + (kg * C::RT + r) * C::PITCH;
-    if constexpr (!C::FP8) {
+  for (int x = 0; x < NT; ++x)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(dst + 8 * i + 2 * t) = make_float2(acc[i][2 * e], acc[i][2 * e + 1]);
-    } else {
+    for (int e = 0; e < 2; ++e) {
+      const int r = kg * C::RT + 8 * (NT * wm + x) + 2 * t + e;
+      float* dst = buf + r * C::PITCH;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-          *reinterpret_cast<float4*>(dst + (2 * t + c) * (D / 8) + 4 * i) =
-              make_float4(acc[4 * i][2 * e + c], acc[4 * i + 1][2 * e + c], acc[4 * i + 2][2 * e + c],
-                          acc[4 * i + 3][2 * e + c]);
+      for (int i = 0; i < D / 16; ++i) {
+        if constexpr (C::FP8) {
+          *reinterpret_cast<float2*>(dst + g * (D / 8) + 2 * i) = make_float2(acc[i][x][e], acc[i][x][2 + e]);
+        } else {
+          dst[16 * i + g] = acc[i][x][e];
+          dst[16 * i + g + 8] = acc[i][x][2 + e];
+        }
+      }
+      if (g == 0) ml[r] = make_float2(m[x][e], l[x][e]);
     }
-    if (t == 0) ml[kg * C::RT + r] = make_float2(m[e], l[e]);
-  }
   __syncthreads();
   const bool whole = pc.count == pc.tiles;
   // a part of a segment: slot 2c if it continues an earlier CTA's, 2c + 1 if it starts one
@@ -486,9 +561,9 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   __syncthreads();   // before the next piece loads over the merge buffer
 }
 
-template <int D, bool FP8, int WM>
+template <int D, bool FP8, int NT, int WM>
 __global__ void __launch_bounds__(kThreads, 2) paged_stream_kernel(const __grid_constant__ StreamParams P) {
-  using C = Cfg<D, FP8, WM>;
+  using C = Cfg<D, FP8, NT, WM>;
   extern __shared__ __align__(128) uint8_t smem[];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
@@ -575,10 +650,10 @@ __global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_cons
   if (threadIdx.x == 0 && P.lse != nullptr) P.lse[lse_at(P, s, me.b, a)] = lse_of(m, l);
 }
 
-template <int D, bool FP8, int WM>
+template <int D, bool FP8, int NT, int WM>
 cudaError_t launch_t(const StreamParams& p, int grid, cudaStream_t stream) {
-  using C = Cfg<D, FP8, WM>;
-  constexpr auto kern = paged_stream_kernel<D, FP8, WM>;
+  using C = Cfg<D, FP8, NT, WM>;
+  constexpr auto kern = paged_stream_kernel<D, FP8, NT, WM>;
   cudaError_t e = launch_with_smem<kern>(
       C::SMEM, [&]() { return launch_dependent(kern, p, dim3((unsigned)grid), kThreads, C::SMEM, stream); });
   if (e != cudaSuccess || !p.split) return e;
@@ -588,21 +663,22 @@ cudaError_t launch_t(const StreamParams& p, int grid, cudaStream_t stream) {
 }
 
 template <int D, bool FP8>
-cudaError_t launch_d(const StreamParams& p, int row_groups, int grid, cudaStream_t stream) {
-  switch (row_groups) {
-    case 1: return launch_t<D, FP8, 1>(p, grid, stream);
-    case 2: return launch_t<D, FP8, 2>(p, grid, stream);
-    default: return launch_t<D, FP8, 4>(p, grid, stream);
+cudaError_t launch_d(const StreamParams& p, int row_tile, int grid, cudaStream_t stream) {
+  switch (row_tile) {
+    case 8: return launch_t<D, FP8, 1, 1>(p, grid, stream);
+    case 16: return launch_t<D, FP8, 2, 1>(p, grid, stream);
+    case 32: return launch_t<D, FP8, 2, 2>(p, grid, stream);
+    default: return launch_t<D, FP8, 2, 4>(p, grid, stream);
   }
 }
 
 }  // namespace
 
-cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_groups, int grid,
+cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,
                                 cudaStream_t stream) {
   if (head_dim == 128)
-    return fp8 ? launch_d<128, true>(p, row_groups, grid, stream) : launch_d<128, false>(p, row_groups, grid, stream);
-  return fp8 ? launch_d<64, true>(p, row_groups, grid, stream) : launch_d<64, false>(p, row_groups, grid, stream);
+    return fp8 ? launch_d<128, true>(p, row_tile, grid, stream) : launch_d<128, false>(p, row_tile, grid, stream);
+  return fp8 ? launch_d<64, true>(p, row_tile, grid, stream) : launch_d<64, false>(p, row_tile, grid, stream);
 }
 
 }  // namespace af

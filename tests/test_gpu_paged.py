@@ -382,7 +382,7 @@ def test_two_streams_at_once(pkg):
 
 
 def test_own_workspace(pkg):
-    p = R.make([300, 40], [1, 1], 8, 2, 64, 16, seed=26)
+    p = R.make([1300, 40], [1, 1], 8, 2, 64, 16, seed=26)
     ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
     pkg.cache_append(p.k_new, p.v_new, *p.cache, workspace=ws)
     o, lse = pkg.paged_forward(p.q, *p.cache, workspace=ws)
