@@ -42,14 +42,6 @@ struct ReadParams {
   uint32_t* ws;
 };
 
-// One CTA's segment that continues in later CTAs (streaming kernel to merge).
-struct StreamMeta {
-  int32_t b;      // sequence, or -1: no such segment
-  int32_t seg;    // row tile * Hkv + KV head
-  int32_t last;   // CTA that ends the segment
-  int32_t pad;
-};
-
 struct StreamParams {
   CacheView c;
   NewRows s;
@@ -62,7 +54,7 @@ struct StreamParams {
   int32_t split;             // 1: units are key tiles, segments may span CTAs; 0: units are segments
   float scale_log2;
   uint32_t* ws;
-  StreamMeta* meta;          // [grid]
+  uint32_t* counters;        // [3 * grid], zero between calls
   float2* part_ml;           // [2 * grid][rows]: running maximum (log2 units) and sum
   float* part_o;             // [2 * grid][rows][D], not normalised
 };
@@ -89,8 +81,7 @@ cudaError_t paged_tile_merge_launch(const PlanParams& p, int head_dim, int max_c
 
 cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream);
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream);
-// Streaming attention over `grid` CTAs with row tiles of 8, 16, 32 or 64 rows,
-// then the merge of split segments if p.split.
+// Streaming attention over `grid` CTAs with row tiles of 8, 16 or 32 rows.
 cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,
                                 cudaStream_t stream);
 
@@ -129,13 +120,16 @@ __device__ __forceinline__ SeqRows load_seq(const NewRows& s, int b, uint32_t* w
   return r;
 }
 
-// Page of column `col` of sequence b's table row; a number outside the cache
-// is recorded and replaced by page 0.
-__device__ __forceinline__ int load_page(const CacheView& c, int b, int col, uint32_t* ws) {
-  const int p = __ldg(c.table + (int64_t)b * c.table_stride + col);
-  if ((unsigned)p < (unsigned)c.num_pages) return p;
+// A page number of sequence b's table row; one outside the cache is recorded
+// and replaced by page 0.
+__device__ __forceinline__ int checked_page(const CacheView& c, int page, int b, uint32_t* ws) {
+  if ((unsigned)page < (unsigned)c.num_pages) return page;
   record_bad_cache(ws, b);
   return 0;
+}
+// Page of column `col` of sequence b's table row.
+__device__ __forceinline__ int load_page(const CacheView& c, int b, int col, uint32_t* ws) {
+  return checked_page(c, __ldg(c.table + (int64_t)b * c.table_stride + col), b, ws);
 }
 #endif
 

@@ -142,11 +142,20 @@ attn_status check_paged(const attn_paged_params* p) {
   return ATTN_OK;
 }
 
+// The zeroed head of the workspace: the words every kernel of the library uses,
+// then the streaming kernel's counters, three per CTA.
+constexpr size_t kZeroedBytes = ATTN_PAGED_ZEROED_BYTES;
+constexpr int64_t kMaxStreamCtas = (kZeroedBytes - ATTN_FWD_WORKSPACE_BYTES) / 12;
+
 // Two kernels. R = Lq * Hq / Hkv rows share the keys of a (sequence, KV head).
-// The streaming kernel reads the cache at close to the copy bandwidth but its
-// tensor instructions and its registers give out as R grows; the tcgen05
-// kernel computes 256-row tiles, mostly padding while R is small.
-constexpr int kStreamRows = 64;
+// The streaming kernel reads the cache at close to the copy bandwidth, but its
+// work grows with R; the tcgen05 kernel computes 256-row tiles, mostly padding
+// while R is small. Measured on both (us, streaming / tcgen05; 64 sequences of up
+// to 8192 keys in bf16, 16 of up to 32768 in e4m3, GQA 32/8, d128):
+//   R      4          16         32         48         64         128
+//   bf16   178 / -    193 / 234  212 / 236  306 / 239  320 / 241  610 / 249
+//   e4m3   109 / 342             230 / 344             421 / 347  806 / 354
+constexpr int kStreamRows = 32;
 int64_t shared_rows(const attn_paged_params* p) {
   return (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
 }
@@ -198,27 +207,27 @@ struct StreamPlan {
   int split;
   int64_t grid;
   int64_t units;       // upper bound of the work units
-  size_t meta_bytes, ml_bytes, o_bytes;
+  size_t ml_bytes, o_bytes;
 };
 
-// Row tiles of 8, 16, 32 or 64 rows, the smallest that holds a sequence's rows;
+// Row tiles of 8, 16 or 32 rows, the smallest that holds a sequence's rows;
 // two CTAs per SM. Segments of up to kUnsplitTiles key tiles are not cut: the
 // merge would cost more than the longer CTA.
 constexpr int kUnsplitTiles = 4;
 StreamPlan plan_stream(const attn_paged_params* p) {
   StreamPlan s = {};
   const int64_t rows = shared_rows(p);
-  s.row_tile = rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+  s.row_tile = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
   const int64_t rt = s.row_tile;
   const int row_bytes = p->cache.head_dim * (p->cache.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2);
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
   const int64_t tiles = af::tiles_for(p->seqlen_k, af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
   s.split = tiles > kUnsplitTiles ? 1 : 0;
   s.units = segments * (s.split ? tiles : 1);
-  const int64_t most = s.split ? 2ll * af::sm_count() : s.units;
+  const int64_t ctas = 2ll * af::sm_count();
+  const int64_t most = s.split ? (ctas < kMaxStreamCtas ? ctas : kMaxStreamCtas) : s.units;
   s.grid = s.units < most ? s.units : most;
   if (s.split) {
-    s.meta_bytes = round256((size_t)s.grid * sizeof(af::StreamMeta));
     s.ml_bytes = round256((size_t)(2 * s.grid * rt) * sizeof(float2));
     s.o_bytes = (size_t)(2 * s.grid * rt) * p->cache.head_dim * sizeof(float);
   }
@@ -227,10 +236,10 @@ StreamPlan plan_stream(const attn_paged_params* p) {
 
 size_t workspace_need(const attn_paged_params* p) {
   if (use_tc05(p)) {
-    return ATTN_FWD_WORKSPACE_BYTES + plan_tiles(p).bytes;
+    return kZeroedBytes + plan_tiles(p).bytes;
   }
   const StreamPlan s = plan_stream(p);
-  return ATTN_FWD_WORKSPACE_BYTES + s.meta_bytes + s.ml_bytes + s.o_bytes;
+  return kZeroedBytes + s.ml_bytes + s.o_bytes;
 }
 
 // Stride of a dimension of size 1 (never used, but a tensor map wants a legal one).
@@ -298,7 +307,7 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   memset(&pp, 0, sizeof(pp));
   cudaError_t e = cudaSuccess;
   if (plan.list) {
-    uint8_t* ws = static_cast<uint8_t*>(p->workspace) + ATTN_FWD_WORKSPACE_BYTES;
+    uint8_t* ws = static_cast<uint8_t*>(p->workspace) + kZeroedBytes;
     pp.s = {p->cu_seqlens_q, p->seqlens_k, c.batch, p->seqlen_q, p->total_q, p->seqlen_k};
     pp.heads_kv = c.num_heads_kv;
     pp.group = prm.group;
@@ -407,7 +416,7 @@ attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t strea
 }
 
 size_t attn_paged_workspace_bytes(const attn_paged_params* p) {
-  if (check_paged(p) != ATTN_OK || no_rows(p)) return ATTN_FWD_WORKSPACE_BYTES;
+  if (check_paged(p) != ATTN_OK || no_rows(p)) return kZeroedBytes;
   return workspace_need(p);
 }
 
@@ -449,10 +458,9 @@ attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
   a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
   a.ws = reinterpret_cast<uint32_t*>(ws);
-  ws += ATTN_FWD_WORKSPACE_BYTES;
-  a.meta = reinterpret_cast<af::StreamMeta*>(ws);
-  a.part_ml = reinterpret_cast<float2*>(ws + plan.meta_bytes);
-  a.part_o = reinterpret_cast<float*>(ws + plan.meta_bytes + plan.ml_bytes);
+  a.counters = reinterpret_cast<uint32_t*>(ws + ATTN_FWD_WORKSPACE_BYTES);
+  a.part_ml = reinterpret_cast<float2*>(ws + kZeroedBytes);
+  a.part_o = reinterpret_cast<float*>(ws + kZeroedBytes + plan.ml_bytes);
   const cudaError_t e =
       af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
                               (int)plan.grid, reinterpret_cast<cudaStream_t>(stream));

@@ -1,32 +1,38 @@
 // Attention of a few new tokens over the paged cache: a streaming kernel for
-// problems that HBM bounds, and the merge of its partial results.
+// problems that HBM bounds.
 //
 // The new tokens of one sequence times the query heads that share one KV head
 // are R = Lq * Hq / Hkv rows over the same keys. For few rows the cached K and V
 // are all that matters: they have to cross HBM once, and R flops per byte leave
 // the tensor cores idle. So the kernel is built around the loads:
-//   * the work is the list of all 64-key tiles of all (sequence, KV head, row
-//     tile) segments, cut into equal contiguous parts, one per CTA (two CTAs per
-//     SM). Lengths are read on the device, so ragged batches balance without the
-//     host knowing them and a captured call follows lengths that change;
-//   * a CTA streams its tiles through a ring of cp.async stages (about 96 KB in
-//     flight per CTA). A row tile is 16 * WM rows (WM = 1, 2, 4); the four warps
-//     form 4 / WM key groups of WM warps, each group with its own keys and ring,
-//     so with up to 16 rows every warp streams by itself and no barrier is met
-//     inside a segment;
-//   * one pass with running maximum and sum (fp32, log2 units), m16n8k16 tensor
-//     instructions: the rows are too few for the 128-row instructions of the
-//     tcgen05 kernel, and the loads bound both. The maximum only moves when it
-//     grows by more than 2^8, so the accumulator is rarely rescaled; O and the
-//     sum share it, so their quotient is exact;
-//   * an e4m3 cache is widened to bf16 in registers (exactly; the key scale is
-//     applied to the fp32 score, the value scale to the fp32 weight before its
-//     rounding to bf16). Depth and value columns are dealt to lanes in the order
-//     in which 16-byte reads from shared memory deliver them: a dot product does
-//     not depend on the order of its depth, nor a product on that of its columns;
-//   * a segment that lies in one CTA is finished there; the others leave their
-//     accumulator, maximum and sum in the workspace (at most two per CTA) and a
-//     second small kernel, already resident when the first one ends, merges them.
+//   * the work is the list of all key tiles (64 or 128 keys) of all (sequence,
+//     KV head, row tile) segments, cut into equal contiguous parts, one per CTA
+//     (two CTAs per SM). Lengths are read on the device, so ragged batches
+//     balance without the host knowing them and a captured call follows lengths
+//     that change;
+//   * a CTA streams its tiles through a ring of cp.async stages (about 96 KB),
+//     across segments: while one is finished, the next one's tiles are loading.
+//     A row tile is 8, 16 or 32 rows; the four warps form four key groups, each
+//     with its own keys and ring, so that every warp streams by itself and meets
+//     no barrier inside a segment (with 32 rows two groups of two warps);
+//   * one pass with running maximum and sum (fp32, log2 units) and m16n8k16
+//     tensor instructions, keys (then depths) on the 16-wide side and rows on
+//     the 8-wide one: S^T = K Q^T, O^T = V^T P^T, so up to eight rows cost half
+//     the instructions, exponentials and registers of sixteen. They are too few
+//     for the 128-row instructions of the tcgen05 kernel, and the loads bound
+//     both. The maximum only moves when it grows by more than 2^8, so the
+//     accumulator is rarely rescaled; O and the sum share it, so their quotient
+//     is exact;
+//   * e4m3 keys are multiplied as f16 (exactly; q as f16 too, normalised by a
+//     power of two per row), e4m3 values as bf16; the key scale is applied to the
+//     fp32 score, the value scale to the fp32 weight before its rounding to
+//     bf16. Depth and value columns are dealt to lanes in the order in which
+//     16-byte reads from shared memory deliver them: a dot product does not
+//     depend on the order of its depth, nor a product on that of its columns;
+//   * a segment that lies in one CTA is finished there; the parts of one that
+//     CTA borders cut meet in the workspace, and whichever of its CTAs comes last
+//     joins them (in the order of the CTAs, so the result does not depend on who
+//     it is). A second kernel for that cost 4 to 7 us per call.
 // Slots at or past the sequence's end are not read (their shared memory is
 // zeroed), so whatever they hold cannot reach a result.
 #include <math.h>
@@ -56,16 +62,25 @@ struct Cfg {
   static constexpr int CPR = ROWB / 16;          // 16-byte pieces of a row
   static constexpr int GT = 32 * WM;             // threads of a group
   static constexpr int RS = GT / CPR;            // rows a group loads at a time
+  static_assert(RS <= 16, "the rows of a load lie in one 16-key block");
   static constexpr int NL = KW / RS;             // loads per thread of K (and of V)
   static constexpr int KV = KW * ROWB;
   static constexpr int SC = FP8 ? KW * 4 : 0;
   static constexpr int STAGE = 2 * KV + 2 * SC;  // bytes of one group's stage
-  static constexpr int STAGES = min_int(8, 98304 / (WK * 2 * KV));
-  static constexpr int PITCH = D + 8;            // floats of a row in the group merge
+  // At the end of a segment a group leaves its part of O in the stage that it
+  // has just used up, or, where that is too small, in room of its own.
+  static constexpr int PART = RT * D * 4;
+  static constexpr bool OWN_PART = PART > STAGE;
+  static constexpr int STAGES = min_int(8, (98304 - (OWN_PART ? WK * PART : 0)) / (WK * 2 * KV));
   static constexpr int RING = WK * STAGES * STAGE;
-  static constexpr int MERGE = WK * RT * (PITCH + 2) * 4;
-  static constexpr int SMEM = RING > MERGE ? RING : MERGE;   // the merge reuses the ring
+  static constexpr int OFF_ML = RING + (OWN_PART ? WK * PART : 0);   // [WK][RT] (maximum, sum)
+  static constexpr int SMEM = OFF_ML + WK * RT * 8;
+  static constexpr int ROUNDS = (RT * (D / 4) + 127) / 128;   // 16-byte pieces of a row tile per thread
+  // Byte offset of group k's part, `last` being its stage's in the group's ring.
+  __device__ static int part_at(int k, int last) { return OWN_PART ? RING + k * PART : k * (STAGES * STAGE) + last; }
   static_assert(STAGES >= 3 && SMEM <= 113 * 1024, "two CTAs per SM");
+  // Column of depth d of row r there: rows 2 t and 2 t + 1 shifted by 8 t banks.
+  __device__ static int part_col(int r, int d) { return d ^ (((r >> 1) & 3) << 3); }
   // Position of 16-byte piece `c` of row `r` in a stage (bank conflicts).
   __device__ static int swz_k(int r, int c) {
     return FP8 ? (CPR == 8 ? c ^ ((r & 1) << 2) : c) : c ^ (r & 7);
@@ -96,55 +111,58 @@ struct Piece {
   int tiles;             // units of the segment
 };
 
+// Finds pieces in order. Lane i holds sequence b + i of the current window of 32.
 template <class C>
 struct Walker {
-  int b = 0;             // first sequence of the current window of 32
-  int base = 0;          // units in front of it
-  // Piece that holds unit x, cut at `end`. All lanes of the warp; x increases.
-  __device__ __forceinline__ Piece at(const StreamParams& P, int x, int end, SeqRows& rows) {
+  SeqUnits u;
+  int incl;              // units of the window's sequences up to and including this lane's
+  int b, base;           // first sequence of the window, units in front of it
+
+  __device__ __forceinline__ void window(const StreamParams& P, int first) {
+    b = first;
+    u.r = {0, 0, 0};
+    u.tiles = 1;
+    u.units = 0;
     const int lane = threadIdx.x & 31;
-    while (true) {
-      SeqUnits u;
-      u.units = 0;
-      if (b + lane < P.s.batch) u = seq_units<C>(P, b + lane);
-      int incl = u.units;
+    if (b + lane < P.s.batch) u = seq_units<C>(P, b + lane);
+    incl = u.units;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += n;
-      }
-      const unsigned hit = __ballot_sync(kFull, b + lane < P.s.batch && x < base + incl);
-      if (hit) {
-        const int w = __ffs(hit) - 1;
-        const int local = x - base - __shfl_sync(kFull, incl - u.units, w);
-        Piece p;
-        p.b = b + w;
-        p.tiles = __shfl_sync(kFull, u.tiles, w);
-        rows.lq = __shfl_sync(kFull, u.r.lq, w);
-        rows.lk = __shfl_sync(kFull, u.r.lk, w);
-        rows.q0 = __shfl_sync(kFull, u.r.q0, w);
-        p.seg = local / p.tiles;
-        p.first = local - p.seg * p.tiles;
-        p.count = min(p.tiles - p.first, end - x);
-        return p;
-      }
-      base += __shfl_sync(kFull, incl, 31);
-      b += 32;
-      if (b >= P.s.batch) {   // cannot happen while x < total
-        Piece p = {0, 0, 0, 0, 1};
-        rows = {0, 0, 0};
-        return p;
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += n;
     }
   }
+  // To the first sequence; returns the units of all of them.
+  __device__ __forceinline__ int start(const StreamParams& P) {
+    int n = 0;
+    for (int c = 32 + (threadIdx.x & 31); c < P.s.batch; c += 32) n += seq_units<C>(P, c).units;
+    window(P, 0);
+    base = 0;
+    return __reduce_add_sync(kFull, n + u.units);
+  }
+  // Piece that holds unit x, cut at `end`. All lanes of the warp; x increases
+  // and is in front of the last unit.
+  __device__ __forceinline__ Piece at(const StreamParams& P, int x, int end, SeqRows& rows) {
+    unsigned hit = __ballot_sync(kFull, x < base + incl);
+    while (hit == 0u && b + 32 < P.s.batch) {
+      base += __shfl_sync(kFull, incl, 31);
+      window(P, b + 32);
+      hit = __ballot_sync(kFull, x < base + incl);
+    }
+    const int w = hit ? __ffs(hit) - 1 : 0;
+    const int local = x - base - __shfl_sync(kFull, incl - u.units, w);
+    Piece p;
+    p.b = b + w;
+    p.tiles = __shfl_sync(kFull, u.tiles, w);
+    rows.lq = __shfl_sync(kFull, u.r.lq, w);
+    rows.lk = __shfl_sync(kFull, u.r.lk, w);
+    rows.q0 = __shfl_sync(kFull, u.r.q0, w);
+    p.seg = local / p.tiles;
+    p.first = local - p.seg * p.tiles;
+    p.count = min(p.tiles - p.first, end - x);
+    return p;
+  }
 };
-
-template <class C>
-__device__ __forceinline__ int total_units(const StreamParams& P) {
-  int n = 0;
-  for (int b = threadIdx.x & 31; b < P.s.batch; b += 32) n += seq_units<C>(P, b).units;
-  return __reduce_add_sync(kFull, n);
-}
 
 // Element offsets of row `r` (token-major, the group's heads fastest) of a segment.
 struct RowAt {
@@ -168,8 +186,185 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -INFINITY : fmaf(m, 0.69314718055994531f, logf(l));
 }
 
+// Tiles [first, first + count) of key tiles of a piece (none for an empty sequence).
 template <class C>
-__device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, uint8_t* smem) {
+__device__ __forceinline__ void piece_tiles(const StreamParams& P, const Piece& pc, const SeqRows& s, int& t0, int& n) {
+  const int key_tiles = (s.lk + C::TILE - 1) / C::TILE;
+  t0 = P.split ? pc.first : 0;
+  n = P.split ? min(pc.count, key_tiles - t0) : key_tiles;
+}
+
+// The loads of this CTA's tiles, in order and without regard to pieces: while
+// one piece is finished the next one's tiles are already on their way. One
+// loader per key group; its threads agree on everything but their part of a tile.
+template <class C>
+struct Loader {
+  Walker<C> walk;
+  int x, end;              // units not yet looked at
+  int b, hk, lk;           // the current tile's sequence, KV head, keys
+  int key0, left;          // its first key of this group; tiles left in the piece, this one included (0: none left)
+  int pages[C::BLOCKS];    // of its 16-key blocks, as read from the table
+
+  __device__ __forceinline__ void fetch_pages(const StreamParams& P) {
+    const int32_t* table = P.c.table + (int64_t)b * P.c.table_stride;
+#pragma unroll
+    for (int u = 0; u < C::BLOCKS; ++u)
+      pages[u] = key0 + 16 * u < lk ? ptx::ld_global_pinned(table + ((key0 + 16 * u) >> P.c.page_shift)) : 0;
+  }
+  // Moves to the first tile of the next piece that has any.
+  __device__ __forceinline__ void next_piece(const StreamParams& P, int kg) {
+    left = 0;
+    while (left <= 0 && x < end) {
+      SeqRows s;
+      const Piece pc = walk.at(P, x, end, s);
+      x += max(1, pc.count);
+      int t0;
+      piece_tiles<C>(P, pc, s, t0, left);
+      b = pc.b;
+      hk = pc.seg % P.c.heads_kv;
+      lk = s.lk;
+      key0 = t0 * C::TILE + kg * C::KW;
+    }
+    if (left > 0) fetch_pages(P);
+  }
+  // Copies the current tile into the stage at `st` and moves on: the table is
+  // read a tile ahead of the copies that depend on it.
+  __device__ __forceinline__ void issue(const StreamParams& P, uint32_t st, int gt, int kg) {
+    if (left <= 0) return;
+    const int lrow = gt / C::CPR, lcol = gt % C::CPR;
+    const int page_mask = (1 << P.c.page_shift) - 1;
+#pragma unroll
+    for (int u = 0; u < C::BLOCKS; ++u) pages[u] = checked_page(P.c, pages[u], b, P.ws);
+    constexpr int PER = 16 / C::RS;   // loads of a 16-key block per thread
+#pragma unroll
+    for (int i = 0; i < C::NL; i += PER) {
+      const int page = pages[i / PER];
+      const int64_t slot = (key0 + lrow + i * C::RS) & page_mask;
+      const uint8_t* ks = P.c.k + hk * P.c.k_head + page * P.c.k_page + slot * P.c.k_tok + lcol * 16;
+      const uint8_t* vs = P.c.v + hk * P.c.v_head + page * P.c.v_page + slot * P.c.v_tok + lcol * 16;
+#pragma unroll
+      for (int y = 0; y < PER; ++y) {
+        const int row = lrow + (i + y) * C::RS;
+        const bool ok = key0 + row < lk;
+        ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, ok ? ks : P.c.k, ok);
+        ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, ok ? vs : P.c.v, ok);
+        ks += C::RS * P.c.k_tok;
+        vs += C::RS * P.c.v_tok;
+      }
+    }
+    if constexpr (C::FP8) {
+      // scales: 4 keys per 16 bytes; a piece that crosses the end is cut there
+      if (gt < 2 * C::KW / 4) {
+        const int which = gt / (C::KW / 4), k4 = 4 * (gt % (C::KW / 4));
+        int page = pages[0];
+#pragma unroll
+        for (int u = 1; u < C::BLOCKS; ++u)
+          if ((k4 >> 4) == u) page = pages[u];
+        const int keys = lk - (key0 + k4);
+        const int bytes = keys >= 4 ? 16 : (keys > 0 ? 4 * keys : 0);
+        const float* base = which ? P.c.v_scale : P.c.k_scale;
+        const float* src =
+            bytes ? base + ((((int64_t)page * P.c.heads_kv + hk) << P.c.page_shift) + ((key0 + k4) & page_mask)) : base;
+        ptx::cp_async16_part(st + 2 * C::KV + which * C::SC + k4 * 4, src, bytes);
+      }
+    }
+    key0 += C::TILE;
+    if (--left > 0) fetch_pages(P);
+    else next_piece(P, kg);
+  }
+};
+
+// Joining the parts of a segment that several CTAs hold, CTAs c0 .. last. Each
+// leaves its part (accumulator, maximum, sum) in the workspace and counts
+// itself in; the last of every kJoin neighbours joins theirs into the first
+// one's, the last of those neighbourhoods joins what is left and finishes the
+// rows. Nobody waits, and the parts are summed in the order of their CTAs
+// whoever sums them. Slot 2 c + 1 is the part of the segment that starts in CTA
+// c and goes on, slot 2 c that of the one that comes from an earlier CTA.
+constexpr int kJoin = 16;
+
+// Whether this CTA is the last of `want` to count itself in (and leaves the
+// counter at zero).
+__device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t want) {
+  __shared__ bool is_last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    is_last = atomicAdd(counter, 1u) == want - 1u;
+    if (is_last) *counter = 0u;
+    __threadfence();
+  }
+  __syncthreads();
+  return is_last;
+}
+
+// Sums parts 0 .. n - 1 at slots slot(i) of the segment's `valid` rows; hands
+// (round, row, depth, four sums, maximum, sum) to `put`, whose thread alone
+// holds them (round: of this thread's, a constant after unrolling). Sixteen
+// loads of a thread are in flight: up to four rows, times parts.
+template <class C, class Slot, class Put>
+__device__ __forceinline__ void join_parts(const StreamParams& P, int n, int valid, Slot slot, Put put) {
+  constexpr int D = C::D, ROUNDS = C::ROUNDS, IT = min_int(ROUNDS, 4), PB = 16 / IT;
+#pragma unroll
+  for (int g = 0; g < ROUNDS / IT; ++g) {
+    float mm[IT], ll[IT];
+    float4 o[IT];
+#pragma unroll
+    for (int y = 0; y < IT; ++y) {
+      mm[y] = -INFINITY;
+      ll[y] = 0.f;
+      o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int x0 = threadIdx.x + g * IT * kThreads;
+    if (x0 >= valid * (D / 4)) break;
+    for (int i0 = 0; i0 < n; i0 += PB) {
+      float4 v[IT][PB];
+      float2 ml[IT][PB];
+#pragma unroll
+      for (int i = 0; i < PB; ++i)
+#pragma unroll
+        for (int y = 0; y < IT; ++y) {
+          const int x = x0 + y * kThreads;
+          ml[y][i] = make_float2(-INFINITY, 0.f);
+          v[y][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + i < n && x < valid * (D / 4)) {
+            const int64_t at = slot(i0 + i) * C::RT + x / (D / 4);
+            ml[y][i] = __ldcg(P.part_ml + at);
+            v[y][i] = __ldcg(reinterpret_cast<const float4*>(P.part_o + at * D + 4 * (x % (D / 4))));
+          }
+        }
+#pragma unroll
+      for (int y = 0; y < IT; ++y) {
+        float top = mm[y];
+#pragma unroll
+        for (int i = 0; i < PB; ++i) top = fmaxf(top, ml[y][i].x);
+        const float base = top == -INFINITY ? 0.f : top, w = ptx::ex2(mm[y] - base);
+        mm[y] = top;
+        ll[y] *= w;
+        o[y].x *= w; o[y].y *= w; o[y].z *= w; o[y].w *= w;
+#pragma unroll
+        for (int i = 0; i < PB; ++i) {
+          const float wi = ptx::ex2(ml[y][i].x - base);
+          ll[y] = fmaf(wi, ml[y][i].y, ll[y]);
+          o[y].x = fmaf(wi, v[y][i].x, o[y].x);
+          o[y].y = fmaf(wi, v[y][i].y, o[y].y);
+          o[y].z = fmaf(wi, v[y][i].z, o[y].z);
+          o[y].w = fmaf(wi, v[y][i].w, o[y].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < IT; ++y) {
+      const int x = x0 + y * kThreads;
+      if (x < valid * (D / 4)) put(g * IT + y, x / (D / 4), 4 * (x % (D / 4)), o[y], mm[y], ll[y]);
+    }
+  }
+}
+
+// `first`: the unit at which this CTA's piece starts, `per` the units of a CTA.
+template <class C>
+__device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, uint8_t* smem, Loader<C>& load,
+                          int& count, int first, int per) {
   constexpr int D = C::D, WM = C::WM, NT = C::NT, KW = C::KW, NB = C::BLOCKS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -178,9 +373,8 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   const int hk = pc.seg % P.c.heads_kv, rt = pc.seg / P.c.heads_kv;
   const int rows = s.lq * P.group;
   const uint32_t ring = ptx::smem_u32(smem) + kg * (C::STAGES * C::STAGE);
-  const int key_tiles = (s.lk + C::TILE - 1) / C::TILE;
-  const int t0 = P.split ? pc.first : 0;
-  const int n = P.split ? min(pc.count, key_tiles - t0) : key_tiles;
+  int t0, n;
+  piece_tiles<C>(P, pc, s, t0, n);
   const int row0 = rt * C::RT + 8 * NT * wm;      // this warp's first row
 
   // Rows r0 + 8 x + 2 t and + 1 are this lane's columns of the score and output
@@ -244,60 +438,6 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     }
   }
 
-  const uint8_t* kbase = P.c.k + hk * P.c.k_head;
-  const uint8_t* vbase = P.c.v + hk * P.c.v_head;
-  const int page_mask = (1 << P.c.page_shift) - 1;
-  const int lrow = gt / C::CPR, lcol = gt % C::CPR;
-
-  // Pages of the 16-key blocks of a group's tile, fetched one tile ahead of
-  // their use (the loads' addresses depend on them).
-  int pages[NB];
-  auto fetch_pages = [&](int j) {
-    const int key0 = (t0 + j) * C::TILE + kg * KW;
-#pragma unroll
-    for (int u = 0; u < NB; ++u)
-      pages[u] = (j < n && key0 + 16 * u < s.lk) ? load_page(P.c, pc.b, (key0 + 16 * u) >> P.c.page_shift, P.ws) : 0;
-  };
-  auto load_tile = [&](int j) {
-    const int key0 = (t0 + j) * C::TILE + kg * KW;
-    const uint32_t st = ring + (j % C::STAGES) * C::STAGE;
-    constexpr int PER = C::RS <= 16 ? 16 / C::RS : 1;   // loads of a 16-key block per thread
-#pragma unroll
-    for (int i = 0; i < C::NL; i += PER) {
-      // block of these loads' rows (RS = 32: of this thread's row)
-      const int u = C::RS <= 16 ? i / PER : 2 * i;
-      const int page = C::RS <= 16 || lrow < 16 ? pages[u] : pages[u + (C::RS > 16 ? 1 : 0)];
-      const int64_t slot = (key0 + lrow + i * C::RS) & page_mask;
-      const uint8_t* ks = kbase + page * P.c.k_page + slot * P.c.k_tok + lcol * 16;
-      const uint8_t* vs = vbase + page * P.c.v_page + slot * P.c.v_tok + lcol * 16;
-#pragma unroll
-      for (int x = 0; x < PER; ++x) {
-        const int row = lrow + (i + x) * C::RS;
-        const bool ok = key0 + row < s.lk;
-        ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, ok ? ks : P.c.k, ok);
-        ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, ok ? vs : P.c.v, ok);
-        ks += C::RS * P.c.k_tok;
-        vs += C::RS * P.c.v_tok;
-      }
-    }
-    if constexpr (C::FP8) {
-      // scales: 4 keys per 16 bytes; a piece that crosses the end is cut there
-      if (gt < 2 * KW / 4) {
-        const int which = gt / (KW / 4), k4 = 4 * (gt % (KW / 4));
-        int page = pages[0];
-#pragma unroll
-        for (int u = 1; u < NB; ++u)
-          if ((k4 >> 4) == u) page = pages[u];
-        const int left = s.lk - (key0 + k4);
-        const int bytes = left >= 4 ? 16 : (left > 0 ? 4 * left : 0);
-        const float* base = which ? P.c.v_scale : P.c.k_scale;
-        const float* src =
-            bytes ? base + ((((int64_t)page * P.c.heads_kv + hk) << P.c.page_shift) + ((key0 + k4) & page_mask)) : base;
-        const uint32_t dst = st + 2 * C::KV + which * C::SC + k4 * 4;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-      }
-    }
-  };
   auto group_sync = [&]() {
     if constexpr (WM == 1) __syncwarp();
     else ptx::bar_sync(1 + kg, C::GT);
@@ -320,22 +460,14 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
       l[x][e] = 0.f;
     }
 
-  fetch_pages(0);
 #pragma unroll 1
-  for (int j = 0; j < C::STAGES - 1; ++j) {
-    if (j < n) load_tile(j);
-    ptx::cp_async_commit();
-    fetch_pages(j + 1);
-  }
-#pragma unroll 1
-  for (int j = 0; j < n; ++j) {
+  for (int j = 0; j < n; ++j, ++count) {
     ptx::cp_async_wait<C::STAGES - 2>();
-    group_sync();   // tile j has arrived, and nobody reads tile j - 1's stage any more
-    if (j + C::STAGES - 1 < n) load_tile(j + C::STAGES - 1);
+    group_sync();   // this tile has arrived, and nobody reads the previous one's stage any more
+    load.issue(P, ring + ((count + C::STAGES - 1) % C::STAGES) * C::STAGE, gt, kg);
     ptx::cp_async_commit();
-    fetch_pages(j + C::STAGES);
 
-    const uint32_t st = ring + (j % C::STAGES) * C::STAGE;
+    const uint32_t st = ring + (count % C::STAGES) * C::STAGE;
     const int key0 = (t0 + j) * C::TILE + kg * KW;
     // ---- S^T = K Q^T: keys g and g + 8 of each block by rows 2 t, 2 t + 1 of each column tile
     float sc[NB][NT][4];
@@ -500,37 +632,55 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[x][e] += __shfl_xor_sync(kFull, l[x][e], o);
-  ptx::cp_async_wait<0>();
 
-  // ---- the key groups' results meet in shared memory (over the ring)
-  float* buf = reinterpret_cast<float*>(smem);                          // [WK][RT][PITCH]
-  float2* ml = reinterpret_cast<float2*>(buf + C::WK * C::RT * C::PITCH);   // [WK][RT]
-  __syncthreads();
+  // ---- The key groups' results meet in shared memory, each group's in the
+  // stage it used last (the loader does not fill that one before the next
+  // piece's first tile). Without keys there is no such stage, and only the
+  // (maximum, sum) say so.
+  float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);   // [WK][RT]
+  const int last = ((count + C::STAGES - 1) % C::STAGES) * C::STAGE;
+  group_sync();   // the group is done with its last tile
+  if (n > 0) {
+    float* part = reinterpret_cast<float*>(smem + C::part_at(kg, last));   // [RT][D]
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * (NT * wm + x) + 2 * t + e;
+        float* dst = part + r * D;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          if constexpr (C::FP8) {
+            *reinterpret_cast<float2*>(dst + C::part_col(r, g * (D / 8) + 2 * i)) = make_float2(acc[i][x][e], acc[i][x][2 + e]);
+          } else {
+            dst[C::part_col(r, 16 * i + g)] = acc[i][x][e];
+            dst[C::part_col(r, 16 * i + g + 8)] = acc[i][x][2 + e];
+          }
+        }
+      }
+  }
 #pragma unroll
   for (int x = 0; x < NT; ++x)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = kg * C::RT + 8 * (NT * wm + x) + 2 * t + e;
-      float* dst = buf + r * C::PITCH;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        if constexpr (C::FP8) {
-          *reinterpret_cast<float2*>(dst + g * (D / 8) + 2 * i) = make_float2(acc[i][x][e], acc[i][x][2 + e]);
-        } else {
-          dst[16 * i + g] = acc[i][x][e];
-          dst[16 * i + g + 8] = acc[i][x][2 + e];
-        }
-      }
-      if (g == 0) ml[r] = make_float2(m[x][e], l[x][e]);
-    }
+    for (int e = 0; e < 2; ++e)
+      if (g == 0) ml[kg * C::RT + 8 * (NT * wm + x) + 2 * t + e] = make_float2(m[x][e], l[x][e]);
   __syncthreads();
+  auto finish_row = [&](int, int row, int d, const float4& o, float mm, float ll) {
+    const RowAt a = row_at(P, hk, rt * C::RT + row);
+    const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    *reinterpret_cast<uint2*>(o_at(P, s, pc.b, a) + d) =
+        make_uint2(ptx::pack_bf16(o.x * inv, o.y * inv), ptx::pack_bf16(o.z * inv, o.w * inv));
+    if (d == 0 && P.lse != nullptr) P.lse[lse_at(P, s, pc.b, a)] = lse_of(mm, ll);
+  };
+  auto keep_row = [&](int64_t slot, int row, int d, const float4& o, float mm, float ll) {
+    *reinterpret_cast<float4*>(P.part_o + (slot * C::RT + row) * D + d) = o;
+    if (d == 0) P.part_ml[slot * C::RT + row] = make_float2(mm, ll);
+  };
   const bool whole = pc.count == pc.tiles;
-  // a part of a segment: slot 2c if it continues an earlier CTA's, 2c + 1 if it starts one
-  const int64_t slot = ((int64_t)2 * blockIdx.x + (pc.first == 0 ? 1 : 0)) * C::RT;
-  for (int x = threadIdx.x; x < C::RT * (D / 4); x += kThreads) {
+  const int valid = min(C::RT, rows - rt * C::RT);
+  const int64_t mine = 2 * (int64_t)blockIdx.x + (pc.first == 0 ? 1 : 0);
+  for (int x = threadIdx.x; x < valid * (D / 4); x += kThreads) {
     const int row = x / (D / 4), d = 4 * (x % (D / 4));
-    const int r = rt * C::RT + row;
-    if (r >= rows) break;
     float mm = -INFINITY, ll = 0.f;
 #pragma unroll
     for (int k = 0; k < C::WK; ++k) mm = fmaxf(mm, ml[k * C::RT + row].x);
@@ -540,25 +690,53 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     for (int k = 0; k < C::WK; ++k) {
       const float2 kml = ml[k * C::RT + row];
       const float w = ptx::ex2(kml.x - base);
-      const float4 v = *reinterpret_cast<const float4*>(buf + (k * C::RT + row) * C::PITCH + d);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (n > 0)
+        v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + C::part_at(k, last)) + row * D +
+                                             C::part_col(row, d));
       ll = fmaf(w, kml.y, ll);
       o.x = fmaf(w, v.x, o.x);
       o.y = fmaf(w, v.y, o.y);
       o.z = fmaf(w, v.z, o.z);
       o.w = fmaf(w, v.w, o.w);
     }
-    if (whole) {
-      const RowAt a = row_at(P, hk, r);
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;
-      *reinterpret_cast<uint2*>(o_at(P, s, pc.b, a) + d) =
-          make_uint2(ptx::pack_bf16(o.x * inv, o.y * inv), ptx::pack_bf16(o.z * inv, o.w * inv));
-      if (d == 0 && P.lse != nullptr) P.lse[lse_at(P, s, pc.b, a)] = lse_of(mm, ll);
-    } else {
-      *reinterpret_cast<float4*>(P.part_o + (slot + row) * D + d) = o;
-      if (d == 0) P.part_ml[slot + row] = make_float2(mm, ll);
-    }
+    if (whole) finish_row(0, row, d, o, mm, ll);
+    else keep_row(mine, row, d, o, mm, ll);
   }
-  __syncthreads();   // before the next piece loads over the merge buffer
+  if (whole) {
+    __syncthreads();   // before the next piece loads over the parts
+    return;
+  }
+  const int start = first - pc.first, c0 = start / per, parts = (start + pc.tiles - 1) / per - c0 + 1;
+  const int hood = ((int)blockIdx.x - c0) / kJoin, in_hood = min(kJoin, parts - kJoin * hood);
+  const int hoods = (parts + kJoin - 1) / kJoin;
+  // counters: [0] a segment's first neighbourhood by its first CTA, [1] others
+  // by theirs, [2] neighbourhoods by the segment's first CTA
+  uint32_t* const counters = P.counters;
+  const int grid = gridDim.x;
+  auto slot_in_hood = [&](int i) { return 2 * (int64_t)(c0 + kJoin * hood + i) + (hood == 0 && i == 0 ? 1 : 0); };
+  if (!count_in(counters + (hood == 0 ? c0 : grid + c0 + kJoin * hood), in_hood)) return;
+  if (hoods == 1) {
+    join_parts<C>(P, in_hood, valid, slot_in_hood, finish_row);
+    return;
+  }
+  // The joined part overwrites the first one's: every thread its own columns,
+  // but the (maximum, sum) of a row only once all threads have read them.
+  float2 kept[C::ROUNDS];
+#pragma unroll
+  for (int i = 0; i < C::ROUNDS; ++i) kept[i] = make_float2(0.f, 0.f);
+  join_parts<C>(P, in_hood, valid, slot_in_hood, [&](int round, int row, int d, const float4& o, float mm, float ll) {
+    *reinterpret_cast<float4*>(P.part_o + (slot_in_hood(0) * C::RT + row) * D + d) = o;
+    kept[round] = make_float2(mm, ll);
+  });
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < C::ROUNDS; ++i) {
+    const int x = threadIdx.x + i * kThreads;
+    if (x < valid * (D / 4) && x % (D / 4) == 0) P.part_ml[slot_in_hood(0) * C::RT + x / (D / 4)] = kept[i];
+  }
+  if (!count_in(counters + 2 * grid + c0, hoods)) return;
+  join_parts<C>(P, hoods, valid, [&](int i) { return 2 * (int64_t)(c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish_row);
 }
 
 template <int D, bool FP8, int NT, int WM>
@@ -567,99 +745,41 @@ __global__ void __launch_bounds__(kThreads, 2) paged_stream_kernel(const __grid_
   extern __shared__ __align__(128) uint8_t smem[];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
-  const int total = total_units<C>(P);
+  Loader<C> load;
+  const int total = load.walk.start(P);
   const int per = (total + gridDim.x - 1) / (int)gridDim.x;
   int x = min(total, (int)blockIdx.x * per);
   const int end = min(total, x + per);
-  StreamMeta meta = {-1, 0, 0, 0};
-  Walker<C> walk;
+  if (x >= end) return;
+  // Fill the ring, then run the pieces; the loader stays STAGES - 1 tiles ahead.
+  const int warp = threadIdx.x >> 5, kg = warp / C::WM, gt = (warp % C::WM) * 32 + (threadIdx.x & 31);
+  const uint32_t ring = ptx::smem_u32(smem) + kg * (C::STAGES * C::STAGE);
+  Walker<C> walk = load.walk;
+  load.x = x;
+  load.end = end;
+  load.next_piece(P, kg);
+#pragma unroll 1
+  for (int j = 0; j < C::STAGES - 1; ++j) {
+    load.issue(P, ring + j * C::STAGE, gt, kg);
+    ptx::cp_async_commit();
+  }
+  int count = 0;   // tiles used so far
   while (x < end) {
     SeqRows s;
     const Piece pc = walk.at(P, x, end, s);
     if (pc.count <= 0) break;
-    run_piece<C>(P, pc, s, smem);
-    if (pc.first == 0 && pc.count < pc.tiles) meta = {pc.b, pc.seg, (x + pc.tiles - 1) / per, 0};
+    run_piece<C>(P, pc, s, smem, load, count, x, per);
     x += pc.count;
   }
-  if (P.split && threadIdx.x == 0) P.meta[blockIdx.x] = meta;
-}
-
-// Merges the parts of the segment that starts in CTA blockIdx.x and ends in a
-// later one; one row per block, its warps sharing the parts.
-template <int D, int RT>
-__global__ void __launch_bounds__(kThreads) paged_merge_kernel(const __grid_constant__ StreamParams P) {
-  constexpr int E = D / 32;   // columns per lane
-  __shared__ float part[kThreads / 32][D];
-  ptx::grid_dependency_wait();
-  const StreamMeta me = P.meta[blockIdx.x];
-  if (me.b < 0) return;
-  const int hk = me.seg % P.c.heads_kv, rt = me.seg / P.c.heads_kv;
-  const SeqRows s = load_seq(P.s, me.b, P.ws);
-  const int row = blockIdx.y, r = rt * RT + row;
-  if (r >= s.lq * P.group) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = me.last - (int)blockIdx.x + 1;
-  // part 0 is slot 2c + 1 of the first CTA, the others slot 2c of theirs
-  auto at = [&](int p) { return ((int64_t)2 * (blockIdx.x + p) + (p == 0 ? 1 : 0)) * RT + row; };
-  float m = -INFINITY;
-  for (int p = lane; p < n; p += 32) m = fmaxf(m, P.part_ml[at(p)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  for (int p = lane; p < n; p += 32) {
-    const float2 ml = P.part_ml[at(p)];
-    l = fmaf(ptx::ex2(ml.x - base), ml.y, l);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int p = warp; p < n; p += kThreads / 32) {
-    const float w = ptx::ex2(P.part_ml[at(p)].x - base);
-    const float* v = P.part_o + at(p) * D + E * lane;
-    if constexpr (E == 4) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(v));
-      acc[0] = fmaf(w, x.x, acc[0]);
-      acc[1] = fmaf(w, x.y, acc[1]);
-      acc[2] = fmaf(w, x.z, acc[2]);
-      acc[3] = fmaf(w, x.w, acc[3]);
-    } else {
-      const float2 x = __ldcs(reinterpret_cast<const float2*>(v));
-      acc[0] = fmaf(w, x.x, acc[0]);
-      acc[1] = fmaf(w, x.y, acc[1]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) part[warp][E * lane + e] = acc[e];
-  __syncthreads();
-  const RowAt a = row_at(P, hk, r);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  if (threadIdx.x < D / 2) {
-    const int d = 2 * threadIdx.x;
-    float x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      x += part[w][d];
-      y += part[w][d + 1];
-    }
-    *reinterpret_cast<uint32_t*>(o_at(P, s, me.b, a) + d) = ptx::pack_bf16(x * inv, y * inv);
-  }
-  if (threadIdx.x == 0 && P.lse != nullptr) P.lse[lse_at(P, s, me.b, a)] = lse_of(m, l);
+  ptx::cp_async_wait<0>();
 }
 
 template <int D, bool FP8, int NT, int WM>
 cudaError_t launch_t(const StreamParams& p, int grid, cudaStream_t stream) {
   using C = Cfg<D, FP8, NT, WM>;
   constexpr auto kern = paged_stream_kernel<D, FP8, NT, WM>;
-  cudaError_t e = launch_with_smem<kern>(
+  return launch_with_smem<kern>(
       C::SMEM, [&]() { return launch_dependent(kern, p, dim3((unsigned)grid), kThreads, C::SMEM, stream); });
-  if (e != cudaSuccess || !p.split) return e;
-  const int64_t rows = (int64_t)p.s.seqlen_q * p.group;
-  const unsigned ny = (unsigned)(rows < C::RT ? rows : C::RT);
-  return launch_dependent(paged_merge_kernel<D, C::RT>, p, dim3((unsigned)grid, ny), kThreads, 0, stream);
 }
 
 template <int D, bool FP8>
@@ -667,8 +787,7 @@ cudaError_t launch_d(const StreamParams& p, int row_tile, int grid, cudaStream_t
   switch (row_tile) {
     case 8: return launch_t<D, FP8, 1, 1>(p, grid, stream);
     case 16: return launch_t<D, FP8, 2, 1>(p, grid, stream);
-    case 32: return launch_t<D, FP8, 2, 2>(p, grid, stream);
-    default: return launch_t<D, FP8, 2, 4>(p, grid, stream);
+    default: return launch_t<D, FP8, 2, 2>(p, grid, stream);
   }
 }
 

@@ -18,6 +18,7 @@
 
 #include <cuda_runtime_api.h>
 
+#include <algorithm>
 #include <array>
 #include <cmath>
 #include <cstdarg>
@@ -168,12 +169,13 @@ at::Tensor workspace_for(c10::DeviceIndex device, cudaStream_t stream, int64_t b
       c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
   at::Tensor* kept = capturing ? nullptr : &buffers()[{device, stream}];
   if (kept != nullptr && kept->defined() && kept->numel() >= bytes) return *kept;
-  at::Tensor fresh = at::empty({bytes < ATTN_FWD_WORKSPACE_BYTES ? ATTN_FWD_WORKSPACE_BYTES : bytes}, options);
+  const int64_t zeroed = ATTN_PAGED_ZEROED_BYTES;
+  at::Tensor fresh = at::empty({std::max(bytes, zeroed)}, options);
   cudaError_t e;
   if (kept != nullptr && kept->defined())   // an error that nobody has read yet moves with it
-    e = cudaMemcpyAsync(fresh.data_ptr(), kept->data_ptr(), ATTN_FWD_WORKSPACE_BYTES, cudaMemcpyDeviceToDevice, stream);
+    e = cudaMemcpyAsync(fresh.data_ptr(), kept->data_ptr(), zeroed, cudaMemcpyDeviceToDevice, stream);
   else
-    e = cudaMemsetAsync(fresh.data_ptr(), 0, ATTN_FWD_WORKSPACE_BYTES, stream);
+    e = cudaMemsetAsync(fresh.data_ptr(), 0, zeroed, stream);
   if (e != cudaSuccess) throw std::runtime_error(std::string("workspace: ") + cudaGetErrorString(e));
   if (kept != nullptr) *kept = fresh;
   return fresh;
@@ -237,7 +239,7 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
   at::Tensor own;
-  if (!ws) own = workspace_for(device, stream, ATTN_FWD_WORKSPACE_BYTES);
+  if (!ws) own = workspace_for(device, stream, ATTN_PAGED_ZEROED_BYTES);
   p.k = k.ptr();
   p.v = v.ptr();
   p.seqlens_k = static_cast<const int32_t*>(lens.ptr());
@@ -288,7 +290,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     fresh_v = at::empty({total, heads, dim}, options);
   }
   const Arg k = {"out_k", ok ? ok.t : &fresh_k}, v = {"out_v", ov ? ov.t : &fresh_v};
-  if (!ws) own = workspace_for(device, stream, ATTN_FWD_WORKSPACE_BYTES);
+  if (!ws) own = workspace_for(device, stream, ATTN_PAGED_ZEROED_BYTES);
   p.k = k.ptr();
   p.v = v.ptr();
   for (int i = 0; i < 2; ++i) {

@@ -49,6 +49,10 @@
 extern "C" {
 #endif
 
+/* Bytes at the start of attn_paged_fwd's workspace that are zero before its
+ * first use and after every call (and its least size). */
+#define ATTN_PAGED_ZEROED_BYTES 8192
+
 typedef struct attn_kv_cache {
   void *k;                    /* [P][page_size][Hkv][D], bf16 or e4m3 (dtype), 16-byte aligned */
   void *v;                    /* the same shape and type */
@@ -104,7 +108,7 @@ typedef struct attn_paged_params {
   const int32_t *cu_seqlens_q; /* packed only: [B+1]; rows of o at or past cu_seqlens_q[B] are left
                                   as they are */
   void *workspace;             /* >= attn_paged_workspace_bytes(p), 256-byte aligned; its first
-                                  ATTN_FWD_WORKSPACE_BYTES zero-filled once before its first use
+                                  ATTN_PAGED_ZEROED_BYTES zero-filled once before its first use
                                   (every call leaves them zeroed). Calls that share a workspace
                                   must not overlap. */
   size_t workspace_bytes;
@@ -134,7 +138,7 @@ attn_status attn_cache_read(const attn_cache_read_params *p, attn_stream_t strea
 attn_status attn_paged_fwd(const attn_paged_params *p, attn_stream_t stream);
 
 /* Workspace bytes attn_paged_fwd needs for `p` on the current device (an
- * invalid `p` or NULL gives ATTN_FWD_WORKSPACE_BYTES). Depends on sizes only,
+ * invalid `p` or NULL gives ATTN_PAGED_ZEROED_BYTES). Depends on sizes only,
  * never on device data. */
 size_t attn_paged_workspace_bytes(const attn_paged_params *p);
 

@@ -198,12 +198,12 @@ def test_library_refuses_calls(pkg, change, status):
 def test_workspace_depends_on_sizes_only(pkg):
     L = _library(pkg)
     size = L.attn_paged_workspace_bytes
-    assert size(None) == 256
-    assert size(_paged(pkg, dict(dim=96))) == 256
+    assert size(None) == 8192
+    assert size(_paged(pkg, dict(dim=96))) == 8192
     short, long = dict(max_pages=8), dict(max_pages=4096)
-    assert size(_paged(pkg, short)) == 256                                # nothing is split
+    assert size(_paged(pkg, short)) == 8192                               # nothing is split
     n = size(_paged(pkg, long, seqlen_k=65536))
-    assert n > 256
+    assert n > 8192
     assert n == size(_paged(pkg, long, seqlen_k=65536, ws=0, ws_bytes=0))  # asked before there is one
     assert L.attn_paged_fwd(_paged(pkg, long, seqlen_k=65536, ws_bytes=n - 1), None) == 1
 
