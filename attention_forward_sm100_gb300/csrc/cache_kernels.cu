@@ -1,11 +1,15 @@
 // Writing new K/V rows into the paged cache and reading sequences back.
 //
-// One (token, K or V, head) vector is handled by D / E lanes, each moving E
-// elements: 8 for a bf16 cache (16 bytes either way), 16 for an e4m3 cache
-// (32 bytes of bf16, 16 bytes of codes). Both operations move every byte once
-// and compute next to nothing, so HBM bounds them; what the kernels add is the
-// way from a row to its slot (sequence, position, page), done per vector from
-// L1/L2-resident tables while the vector itself is on its way.
+// A block takes a few whole tokens (their K and V vectors of all heads). Its first
+// warp finds where the tokens live, one lane per token: sequence, position, page.
+// The other warps meanwhile load the rows to write; only the stores (when
+// reading: the loads) wait for it. A (token, K or V, head) vector is moved by
+// D / E lanes, E elements each: 8 for a bf16 cache (16 bytes either way), 16 for
+// an e4m3 cache (32 bytes of bf16, 16 bytes of codes). Every byte is moved once
+// and next to nothing is computed, so HBM bounds both operations, once the way
+// to a vector is short: with the token of each vector found by a 64-bit division
+// and its slot looked up by every lane, 190 instructions per vector took 72 us
+// for 41690 tokens of 8 heads of 128 (341 MB) where this takes TBD.
 //
 // e4m3: scale = the smallest power of two s with amax / s <= 448. The largest
 // finite magnitude is found on the bf16 bit patterns (they order like the
@@ -21,19 +25,45 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBatch = 4;   // vectors a thread has in flight
 
-// Sequence that holds row t: the number of sequences that end at or before t
-// (offsets cu[0..batch]). All threads of the block, with one barrier.
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t t) {
-  int n = 0;
-  for (int b = threadIdx.x; b < batch; b += kThreads) n += (int64_t)cu[b + 1] <= t ? 1 : 0;
-  n = __reduce_add_sync(0xffffffffu, n);
-  __shared__ int part[kThreads / 32];
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = n;
-  __syncthreads();
-  n = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) n += part[w];
-  return n;
+constexpr int kMaxTokens = 32;   // tokens of a block: one lane each
+
+// Where a token's vectors are in the cache, or page < 0: nowhere.
+struct Slot {
+  int page, slot;
+};
+
+// The sequence of row t, for the lanes of one warp with consecutive rows from
+// t0 on (offsets cu[0 .. batch]); `batch` if it lies behind the last one.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t t0, int64_t t) {
+  int b = 0;
+  for (int c = threadIdx.x & 31; c < batch; c += 32) b += (int64_t)cu[c + 1] <= t0 ? 1 : 0;
+  b = __reduce_add_sync(0xffffffffu, b);
+  while (b < batch && (int64_t)cu[b + 1] <= t) ++b;
+  return b;
+}
+
+__device__ __forceinline__ Slot slot_of(const CacheView& c, int b, int pos, uint32_t* ws) {
+  Slot s = {-1, pos & ((1 << c.page_shift) - 1)};
+  if (pos >= 0 && (pos >> c.page_shift) < c.max_pages) {
+    const int page = __ldg(c.table + (int64_t)b * c.table_stride + (pos >> c.page_shift));
+    if ((unsigned)page < (unsigned)c.num_pages) s.page = page;
+  }
+  if (s.page < 0) record_bad_cache(ws, b);
+  return s;
+}
+
+// Vector `idx` of a block: its token and (V behind K) head.
+struct Vector {
+  int token, h;
+  bool v;
+};
+__device__ __forceinline__ Vector vector_at(uint32_t idx, uint32_t per_token, uint32_t magic, int heads) {
+  Vector x;
+  x.token = (int)__umulhi(idx, magic);   // idx / per_token (magic = 2^32 / per_token rounded up, idx < 2^16)
+  x.h = (int)(idx - x.token * per_token);
+  x.v = x.h >= heads;
+  if (x.v) x.h -= heads;
+  return x;
 }
 
 // Largest finite magnitude of two bf16, as 15-bit patterns.
@@ -54,92 +84,113 @@ __device__ __forceinline__ int scale_exponent(uint32_t m) {
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams P) {
   constexpr int E = FP8 ? 16 : 8, L = D / E, PER = kThreads / L;
+  __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
-  const int nv = 2 * P.c.heads_kv;               // vectors of one token
-  const int64_t total = P.tokens * nv;
-  const int64_t first = (int64_t)blockIdx.x * (PER * kBatch);
+  const int64_t t0 = (int64_t)blockIdx.x * P.block_tokens;
+  const int tokens = (int)min((int64_t)P.block_tokens, P.tokens - t0);
+  const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
-  int b0 = 0;
-  if (P.s.cu_q != nullptr) b0 = find_sequence(P.s.cu_q, P.s.batch, first / nv);
-  uint4 x[kBatch][E / 8];
-  uint8_t* dst[kBatch];
-  float* sdst[kBatch];
-#pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    dst[u] = nullptr;
-    sdst[u] = nullptr;
-    const int64_t id = first + u * PER + threadIdx.x / L;
-#pragma unroll
-    for (int e = 0; e < E / 8; ++e) x[u][e] = make_uint4(0u, 0u, 0u, 0u);
-    if (id >= total) continue;
-    const int64_t t = id / nv;
-    const int w = (int)(id - t * nv);
-    const bool is_v = w >= P.c.heads_kv;
-    const int h = is_v ? w - P.c.heads_kv : w;
-    int b, i;
-    if (P.s.cu_q == nullptr) {
-      b = (int)(t / P.s.seqlen_q);
-      i = (int)(t - (int64_t)b * P.s.seqlen_q);
-    } else {
-      b = b0;
-      while (b < P.s.batch && (int64_t)P.s.cu_q[b + 1] <= t) ++b;
-      if (b >= P.s.batch) continue;              // behind the last sequence
-      i = (int)(t - P.s.cu_q[b]);
+  // fixed layout: sequence and index of the first token
+  const bool packed = P.s.cu_q != nullptr;
+  const int b0 = packed ? 0 : (int)((uint32_t)t0 / (uint32_t)P.s.seqlen_q);
+  const int i0 = packed ? 0 : (int)t0 - b0 * P.s.seqlen_q;
+  auto token_at = [&](int token, int& b, int& i) {
+    b = b0;
+    i = i0 + token;
+    while (i >= P.s.seqlen_q) {
+      i -= P.s.seqlen_q;
+      ++b;
     }
-    const uint8_t* src = (is_v ? P.v + (int64_t)h * P.v_h : P.k + (int64_t)h * P.k_h) +
-                         (P.s.cu_q == nullptr ? b * (is_v ? P.v_b : P.k_b) + i * (is_v ? P.v_t : P.k_t)
-                                              : t * (is_v ? P.v_t : P.k_t)) + lane * (E * 2);
+  };
+  for (uint32_t base = 0; base < total; base += PER * kBatch) {
+    uint4 x[kBatch][E / 8];
 #pragma unroll
-    for (int e = 0; e < E / 8; ++e) x[u][e] = __ldcs(reinterpret_cast<const uint4*>(src) + e);
-    // the slot: position, then page
-    const int a = P.s.cu_q == nullptr ? 0 : P.s.cu_q[b];
-    const int lq = P.s.cu_q == nullptr ? P.s.seqlen_q : P.s.cu_q[b + 1] - a;
-    const int lk = P.s.seqlens_k[b];
-    const int pos = lk - lq + i;
-    if (a < 0 || i < 0 || i >= lq || lk > P.s.max_k || pos < 0) {
-      record_bad_cache(P.ws, b);
-      continue;
-    }
-    const int page = __ldg(P.c.table + (int64_t)b * P.c.table_stride + (pos >> P.c.page_shift));
-    if ((unsigned)page >= (unsigned)P.c.num_pages) {
-      record_bad_cache(P.ws, b);
-      continue;
-    }
-    const int slot = pos & ((1 << P.c.page_shift) - 1);
-    dst[u] = (is_v ? P.c.v + page * P.c.v_page + slot * P.c.v_tok + h * P.c.v_head
-                   : P.c.k + page * P.c.k_page + slot * P.c.k_tok + h * P.c.k_head) + lane * 16;
-    if constexpr (FP8)
-      sdst[u] = (is_v ? P.c.v_scale : P.c.k_scale) +
-                ((((int64_t)page * P.c.heads_kv + h) << P.c.page_shift) + slot);
-  }
+    for (int u = 0; u < kBatch; ++u) {
+      const uint32_t id = base + u * PER + threadIdx.x / L;
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    if constexpr (!FP8) {
-      if (dst[u] != nullptr) *reinterpret_cast<uint4*>(dst[u]) = x[u][0];
-    } else {
-      uint32_t m = 0u;
+      for (int e = 0; e < E / 8; ++e) x[u][e] = make_uint4(0u, 0u, 0u, 0u);
+      if (id < total) {
+        const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
+        int64_t at;
+        if (packed) {
+          at = (t0 + w.token) * (w.v ? P.v_t : P.k_t);
+        } else {
+          int b, i;
+          token_at(w.token, b, i);
+          at = b * (w.v ? P.v_b : P.k_b) + i * (w.v ? P.v_t : P.k_t);
+        }
+        const uint8_t* src = (w.v ? P.v + w.h * P.v_h : P.k + w.h * P.k_h) + at + lane * (E * 2);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m = finite_max(x[u][e].x, m);
-        m = finite_max(x[u][e].y, m);
-        m = finite_max(x[u][e].z, m);
-        m = finite_max(x[u][e].w, m);
+        for (int e = 0; e < E / 8; ++e) x[u][e] = __ldcs(reinterpret_cast<const uint4*>(src) + e);
       }
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int se = scale_exponent(m);
-      const float inv = __uint_as_float((uint32_t)(127 - se) << 23);
-      uint32_t out[4];
-      const uint32_t* in = reinterpret_cast<const uint32_t*>(&x[u][0]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = in[2 * j], c = in[2 * j + 1];
-        out[j] = ptx::pack_e4m3x4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
-                                  __uint_as_float(c << 16) * inv, __uint_as_float(c & 0xffff0000u) * inv);
+    }
+    if (base == 0) {
+      if (threadIdx.x < 32) {
+        Slot s = {-1, 0};
+        const int64_t t = t0 + threadIdx.x;
+        int b, i, lq = P.s.seqlen_q;
+        bool ok = (int)threadIdx.x < tokens;
+        if (packed) {
+          b = find_sequence(P.s.cu_q, P.s.batch, t0, t);
+          ok = ok && b < P.s.batch;                // else behind the last sequence
+          if (ok) {
+            const int a = P.s.cu_q[b];
+            i = (int)(t - a);
+            lq = P.s.cu_q[b + 1] - a;
+            if (a < 0 || i < 0) {                  // offsets out of order
+              record_bad_cache(P.ws, b);
+              ok = false;
+            }
+          }
+        } else {
+          token_at(threadIdx.x, b, i);
+        }
+        if (ok) {
+          const int lk = P.s.seqlens_k[b];
+          s = slot_of(P.c, b, lk > P.s.max_k ? -1 : lk - lq + i, P.ws);
+        }
+        slots[threadIdx.x] = s;
       }
-      if (dst[u] != nullptr) {
-        *reinterpret_cast<uint4*>(dst[u]) = make_uint4(out[0], out[1], out[2], out[3]);
-        if (lane == 0) *sdst[u] = __uint_as_float((uint32_t)(127 + se) << 23);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const uint32_t id = base + u * PER + threadIdx.x / L;
+      const bool there = id < total;
+      const Vector w = vector_at(there ? id : 0u, nv, P.magic, P.c.heads_kv);
+      const Slot s = slots[w.token];
+      const bool ok = there && s.page >= 0;
+      uint8_t* dst = (w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
+                          : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head) + lane * 16;
+      if constexpr (!FP8) {
+        if (ok) *reinterpret_cast<uint4*>(dst) = x[u][0];
+      } else {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m = finite_max(x[u][e].x, m);
+          m = finite_max(x[u][e].y, m);
+          m = finite_max(x[u][e].z, m);
+          m = finite_max(x[u][e].w, m);
+        }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int se = scale_exponent(m);
+        const float inv = __uint_as_float((uint32_t)(127 - se) << 23);
+        uint32_t out[4];
+        const uint32_t in[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a = in[2 * j], c = in[2 * j + 1];
+          out[j] = ptx::pack_e4m3x4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
+                                    __uint_as_float(c << 16) * inv, __uint_as_float(c & 0xffff0000u) * inv);
+        }
+        if (ok) {
+          *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+          if (lane == 0)
+            (w.v ? P.c.v_scale : P.c.k_scale)[(((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot] =
+                __uint_as_float((uint32_t)(127 + se) << 23);
+        }
       }
     }
   }
@@ -148,74 +199,79 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams P) {
   constexpr int E = FP8 ? 16 : 8, L = D / E, PER = kThreads / L;
+  __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
-  const int nv = 2 * P.c.heads_kv;
-  const int64_t total = (int64_t)P.total_k * nv;
-  const int64_t first = (int64_t)blockIdx.x * (PER * kBatch);
+  const int64_t t0 = (int64_t)blockIdx.x * P.block_tokens;
+  const int tokens = (int)min((int64_t)P.block_tokens, P.total_k - t0);
+  const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
-  const int b0 = find_sequence(P.cu_k, P.batch, first / nv);
-  uint4 x[kBatch];
-  float scale[kBatch];
-  uint8_t* dst[kBatch];
-#pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    dst[u] = nullptr;
-    const int64_t id = first + u * PER + threadIdx.x / L;
-    if (id >= total) continue;
-    const int64_t t = id / nv;
-    const int w = (int)(id - t * nv);
-    const bool is_v = w >= P.c.heads_kv;
-    const int h = is_v ? w - P.c.heads_kv : w;
-    int b = b0;
-    while (b < P.batch && (int64_t)P.cu_k[b + 1] <= t) ++b;
-    if (b >= P.batch) continue;
-    const int a = P.cu_k[b], pos = (int)(t - a);
-    // offsets that are out of order (or below zero) leave a row in front of
-    // its sequence's start, or past what the table can hold
-    if (a < 0 || pos < 0 || (pos >> P.c.page_shift) >= P.c.max_pages) {
-      record_bad_cache(P.ws, b);
-      continue;
+  if (threadIdx.x < 32) {
+    Slot s = {-1, 0};
+    const int64_t t = t0 + threadIdx.x;
+    const int b = find_sequence(P.cu_k, P.batch, t0, t);
+    if ((int)threadIdx.x < tokens && b < P.batch) {
+      // offsets that are out of order (or below zero) leave a row in front of
+      // its sequence's start, or past what the table can hold
+      const int a = P.cu_k[b];
+      s = slot_of(P.c, b, a < 0 ? -1 : (int)(t - a), P.ws);
     }
-    const int page = __ldg(P.c.table + (int64_t)b * P.c.table_stride + (pos >> P.c.page_shift));
-    if ((unsigned)page >= (unsigned)P.c.num_pages) {
-      record_bad_cache(P.ws, b);
-      continue;
-    }
-    const int slot = pos & ((1 << P.c.page_shift) - 1);
-    const uint8_t* src = (is_v ? P.c.v + page * P.c.v_page + slot * P.c.v_tok + h * P.c.v_head
-                               : P.c.k + page * P.c.k_page + slot * P.c.k_tok + h * P.c.k_head) + lane * 16;
-    x[u] = __ldcs(reinterpret_cast<const uint4*>(src));
-    if constexpr (FP8)
-      scale[u] = __ldg((is_v ? P.c.v_scale : P.c.k_scale) +
-                       ((((int64_t)page * P.c.heads_kv + h) << P.c.page_shift) + slot));
-    dst[u] = (is_v ? P.v + t * P.v_t + h * P.v_h : P.k + t * P.k_t + h * P.k_h) + lane * (E * 2);
+    slots[threadIdx.x] = s;
   }
+  __syncthreads();
+  for (uint32_t base = 0; base < total; base += PER * kBatch) {
+    uint4 x[kBatch];
+    float scale[kBatch];
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
-    if (dst[u] == nullptr) continue;
-    if constexpr (!FP8) {
-      *reinterpret_cast<uint4*>(dst[u]) = x[u];
-    } else {
-      const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      uint32_t out[8];
+    for (int u = 0; u < kBatch; ++u) {
+      const uint32_t id = base + u * PER + threadIdx.x / L;
+      if (id >= total) continue;
+      const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
+      const Slot s = slots[w.token];
+      if (s.page < 0) continue;
+      const uint8_t* src = (w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
+                                : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head) + lane * 16;
+      x[u] = __ldcs(reinterpret_cast<const uint4*>(src));
+      if constexpr (FP8)
+        scale[u] = __ldg((w.v ? P.c.v_scale : P.c.k_scale) +
+                         ((((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot));
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 lo, hi;
-        ptx::e4m3x2_to_float2(in[j] & 0xffffu, lo.x, lo.y);
-        ptx::e4m3x2_to_float2(in[j] >> 16, hi.x, hi.y);
-        out[2 * j] = ptx::pack_bf16(lo.x * scale[u], lo.y * scale[u]);
-        out[2 * j + 1] = ptx::pack_bf16(hi.x * scale[u], hi.y * scale[u]);
+    for (int u = 0; u < kBatch; ++u) {
+      const uint32_t id = base + u * PER + threadIdx.x / L;
+      if (id >= total) continue;
+      const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
+      if (slots[w.token].page < 0) continue;
+      const int64_t t = t0 + w.token;
+      uint8_t* dst = (w.v ? P.v + t * P.v_t + w.h * P.v_h : P.k + t * P.k_t + w.h * P.k_h) + lane * (E * 2);
+      if constexpr (!FP8) {
+        *reinterpret_cast<uint4*>(dst) = x[u];
+      } else {
+        const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t out[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 lo, hi;
+          ptx::e4m3x2_to_float2(in[j] & 0xffffu, lo.x, lo.y);
+          ptx::e4m3x2_to_float2(in[j] >> 16, hi.x, hi.y);
+          out[2 * j] = ptx::pack_bf16(lo.x * scale[u], lo.y * scale[u]);
+          out[2 * j + 1] = ptx::pack_bf16(hi.x * scale[u], hi.y * scale[u]);
+        }
+        uint4* d = reinterpret_cast<uint4*>(dst);
+        d[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        d[1] = make_uint4(out[4], out[5], out[6], out[7]);
       }
-      uint4* d = reinterpret_cast<uint4*>(dst[u]);
-      d[0] = make_uint4(out[0], out[1], out[2], out[3]);
-      d[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
   }
 }
 
+// A block's tokens: as many as fill its batch of vectors once.
 template <class K, class P>
-cudaError_t launch(K kern, const P& p, int64_t vectors, int per_block, cudaStream_t stream) {
-  const int64_t blocks = (vectors + per_block - 1) / per_block;
+cudaError_t launch(K kern, P p, int64_t tokens, int vectors, cudaStream_t stream) {
+  const uint32_t per_token = 2 * p.c.heads_kv;
+  const int fit = vectors / (int)per_token;
+  p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
+  p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
+  const int64_t blocks = (tokens + p.block_tokens - 1) / p.block_tokens;
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   return launch_dependent(kern, p, dim3((unsigned)blocks), kThreads, 0, stream);
@@ -226,7 +282,7 @@ constexpr int per_block(int d, bool fp8) { return kThreads / (d / (fp8 ? 16 : 8)
 }  // namespace
 
 cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream) {
-  const int64_t n = p.tokens * 2 * p.c.heads_kv;
+  const int64_t n = p.tokens;
   const int pb = per_block(head_dim, fp8);
   if (head_dim == 128)
     return fp8 ? launch(cache_append_kernel<128, true>, p, n, pb, stream)
@@ -236,7 +292,7 @@ cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, c
 }
 
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream) {
-  const int64_t n = (int64_t)p.total_k * 2 * p.c.heads_kv;
+  const int64_t n = p.total_k;
   const int pb = per_block(head_dim, fp8);
   if (head_dim == 128)
     return fp8 ? launch(cache_read_kernel<128, true>, p, n, pb, stream)

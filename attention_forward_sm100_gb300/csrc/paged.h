@@ -29,6 +29,8 @@ struct AppendParams {
   const uint8_t* v;
   int64_t k_b, k_t, k_h, v_b, v_t, v_h;   // bytes
   int64_t tokens;
+  int32_t block_tokens;                   // set by the launch, as `magic`
+  uint32_t magic;
   uint32_t* ws;
 };
 
@@ -39,6 +41,8 @@ struct ReadParams {
   uint8_t* v;
   int64_t k_t, k_h, v_t, v_h;   // bytes
   int32_t batch, total_k;
+  int32_t block_tokens;
+  uint32_t magic;
   uint32_t* ws;
 };
 

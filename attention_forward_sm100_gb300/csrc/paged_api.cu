@@ -20,6 +20,7 @@ attn_status check_cache(const attn_kv_cache& c) {
   if (c.batch < 0 || c.max_pages < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative batch or max_pages");
   if (c.num_pages <= 0 || c.num_heads_kv <= 0)
     return report_error(ATTN_ERR_INVALID_ARG, "the cache needs at least one page and one head");
+  if (c.num_heads_kv > 16384) return report_error(ATTN_ERR_UNSUPPORTED, "more than 16384 heads");
   if (c.head_dim != 64 && c.head_dim != 128)
     return report_error(ATTN_ERR_UNSUPPORTED, "head_dim %d: the paged cache supports 64 and 128", c.head_dim);
   if (c.page_size < af::kMinPage || c.page_size > 65536 || (c.page_size & (c.page_size - 1)))

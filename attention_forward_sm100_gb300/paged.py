@@ -50,7 +50,7 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, *, k_scale=None
     """Writes the new tokens' keys and values into the cache, in place.
 
     ``k`` and ``v`` are bf16, [B, Sq, Hkv, D], or packed [T, Hkv, D] with int32
-    ``cu_seqlens_q`` (rows behind the last sequence are not read).
+    ``cu_seqlens_q`` (rows behind the last sequence are ignored).
     ``seqlens_k`` (int32 [B]) counts each sequence's tokens with the new ones:
     token i of Lq goes to position seqlens_k - Lq + i. Into an e4m3 cache each
     (token, head) vector is rounded with its own scale, the smallest power of

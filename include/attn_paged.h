@@ -78,7 +78,7 @@ typedef struct attn_cache_append_params {
   const void *v;
   const int32_t *seqlens_k;    /* [B]: tokens in the cache, the new ones included */
   const int32_t *cu_seqlens_q; /* packed only: [B+1] offsets of the new rows; rows at or past
-                                  cu_seqlens_q[B] are not read */
+                                  cu_seqlens_q[B] are ignored */
   void *workspace;             /* ATTN_FWD_WORKSPACE_BYTES, as attn_fwd_params.workspace: the
                                   device error record */
   int64_t k_stride[3];         /* elements: [0] batch (unused when packed), [1] token, [2] head */
