@@ -55,6 +55,13 @@ attn_status check_rows(const char* what, const void* p, const int64_t* stride, i
   return ATTN_OK;
 }
 
+// Whether rows at `p` with these strides (of bf16) all start on 32-byte boundaries.
+bool wide_rows(const void* p, const int64_t* stride, int first, int n) {
+  bool ok = aligned(p, 32);
+  for (int i = first; i < n; ++i) ok = ok && (stride[i] * 2) % 32 == 0;
+  return ok;
+}
+
 attn_status check_offsets(const char* what, const int32_t* p, bool needed) {
   if ((needed && p == nullptr) || !aligned(p, 4))
     return report_error(ATTN_ERR_INVALID_ARG, "%s must be non-NULL and 4-byte aligned", what);
@@ -384,6 +391,7 @@ attn_status attn_cache_append(const attn_cache_append_params* p, attn_stream_t s
   a.v_b = packed ? 0 : p->v_stride[0] * 2;
   a.v_t = p->v_stride[1] * 2;
   a.v_h = p->v_stride[2] * 2;
+  a.wide = wide_rows(p->k, p->k_stride, packed ? 1 : 0, 3) && wide_rows(p->v, p->v_stride, packed ? 1 : 0, 3);
   a.tokens = packed ? p->total_q : (int64_t)p->cache.batch * p->seqlen_q;
   a.ws = static_cast<uint32_t*>(p->workspace);
   const cudaError_t e = af::cache_append_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3,
@@ -407,6 +415,7 @@ attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t strea
   r.k_h = p->k_stride[1] * 2;
   r.v_t = p->v_stride[0] * 2;
   r.v_h = p->v_stride[1] * 2;
+  r.wide = wide_rows(p->k, p->k_stride, 0, 2) && wide_rows(p->v, p->v_stride, 0, 2);
   r.batch = p->cache.batch;
   r.total_k = p->total_k;
   r.ws = static_cast<uint32_t*>(p->workspace);

@@ -112,6 +112,14 @@ __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* v) {
                : "memory");
 }
 
+// 256-bit global load (sm_100 and later); `src` 32-byte aligned.
+__device__ __forceinline__ void ld_global_v8(const void* src, uint32_t* v) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(src)
+               : "memory");
+}
+
 // Waits until the grid this one programmatically depends on has completed
 // and its memory is visible (returns at once without such a dependency).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

@@ -435,3 +435,32 @@ def test_attend_chunks_that_are_cut(pkg, lens_k, lens_q, hq, hkv, dim, page, fp8
         R.check_attend(p, o, lse, causal)
         o2, lse2 = pkg.paged_forward(p.q, *p.cache, **kw)
         assert torch.equal(R.bits(o), R.bits(o2)) and torch.equal(R.bits(lse), R.bits(lse2))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_rows_on_16_byte_boundaries_only(pkg, fp8):
+    """New rows, outputs and q whose strides are odd multiples of 16 bytes."""
+    p = R.make([90, 40], [30, 30], 4, 2, 64, 16, fp8=fp8, seed=30)
+    wide = torch.full((2, 30, 2, 3 * 72 + 8), 3.0, dtype=torch.bfloat16, device="cuda")[..., 8:]
+    k, v = wide[..., :64], wide[..., 72:136]
+    k.copy_(p.k_new)
+    v.copy_(p.v_new)
+    want = R.append(p)
+    pkg.cache_append(k, v, *p.cache, **p.scales)
+    for g, w in zip((p.k_cache, p.v_cache, p.k_scale, p.v_scale), want):
+        assert g is None or torch.equal(R.bits(g), R.bits(w))
+    cu = torch.tensor([0, 90, 130], dtype=torch.int32, device="cuda")
+    out = torch.full((130, 2, 152), 5.0, dtype=torch.bfloat16, device="cuda")
+    pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, out_k=out[..., 8:72], out_v=out[..., 80:144], **p.scales)
+    both = [torch.cat(x).to(torch.bfloat16) for x in zip(*(R.gather(p, b) for b in range(2)))]
+    assert torch.equal(out[..., 8:72], both[0]) and torch.equal(out[..., 80:144], both[1])
+    assert bool((out[..., :8] == 5.0).all()) and bool((out[..., 72:80] == 5.0).all()) and bool((out[..., 144:] == 5.0).all())
+    for n in (30, 4):   # either attention kernel
+        q = torch.zeros(2, n, 4, 72, dtype=torch.bfloat16, device="cuda")[..., 8:]
+        q.copy_(p.q[:, 30 - n:])
+        o = torch.full((2, n, 4, 88), 5.0, dtype=torch.bfloat16, device="cuda")
+        _, lse = pkg.paged_forward(q, *p.cache, out=o[..., 8:72], **p.scales)
+        p2 = R.Problem(p.k_cache, p.v_cache, p.k_scale, p.v_scale, p.table, p.seqlens, p.lens_k, [n, n], None, q, None, None)
+        R.check_attend(p2, o[..., 8:72], lse, True)
+        assert bool((o[..., :8] == 5.0).all()) and bool((o[..., 72:] == 5.0).all())
+    pkg.check()
