@@ -174,20 +174,23 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       if constexpr (!FP8) {
         if (ok) *reinterpret_cast<uint4*>(dst) = x[u][0];
       } else {
+        const uint32_t in[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+        // magnitudes two at a time; only where that meets an infinity or a NaN
+        // the finite ones are picked out
         uint32_t m = 0u;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          m = finite_max(x[u][e].x, m);
-          m = finite_max(x[u][e].y, m);
-          m = finite_max(x[u][e].z, m);
-          m = finite_max(x[u][e].w, m);
+        for (int e = 0; e < 8; ++e) m = __vmaxu2(m, in[e] & 0x7fff7fffu);
+        m = max(m & 0xffffu, m >> 16);
+        if (__any_sync(0xffffffffu, m >= 0x7f80u)) {
+          m = 0u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = finite_max(in[e], m);
         }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int se = scale_exponent(m);
         const float inv = __uint_as_float((uint32_t)(127 - se) << 23);
         uint32_t out[4];
-        const uint32_t in[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t a = in[2 * j], c = in[2 * j + 1];
