@@ -58,12 +58,18 @@
 //     as scores, V's are zeroed in shared memory before the tile is handed
 //     to the MMAs (a zero weight does not cancel a NaN).
 //   * an e4m3 paged cache (Tc05Traits<..., PAGED, C8 = true>): warpgroup 2 also
-//     fills the K and V stages. Its threads copy 16 codes at a time straight
-//     from the pages into a two-tile ring (cp.async; every thread reads back
-//     only what it copied, so the ring needs no barrier), widen them to bf16 as
-//     code * scale, rounded once (exact for powers of two, which is what
-//     cache_append writes), and store them where TMA would have put a bf16
-//     tile, zeros behind the sequence's end.
+//     fills the V stages. Its threads copy 16 codes at a time straight from the
+//     pages into a two-tile ring (cp.async; every thread reads back only what it
+//     copied, so the ring needs no barrier), widen them to bf16 as code * scale,
+//     rounded once (exact for powers of two, which is what cache_append
+//     writes), and store them where TMA would have put a bf16 tile, zeros
+//     behind the sequence's end. With D = 64 K takes the same way. With
+//     D = 128 (QSPLIT) K stays e4m3, gathered by TMA, and it is Q that changes:
+//     warpgroup 2 writes q = 2^e (q1 + q2) with e4m3 q1 and q2 (a bf16 has
+//     eight significant bits, an e4m3 four: q2 takes what q1 leaves, exactly
+//     for values above 2^-11 of their row's largest, to 2^-19 of it below), and
+//     S = Q1 K^T + Q2 K^T costs what the bf16 product does. The key scales
+//     (copied next to K into a four-tile ring) and 2^e multiply the fp32 scores.
 // Every wait is bounded: on timeout the CTA records an error in the
 // workspace, raises a shared abort flag that all waits poll (and, in a pair,
 // the peer's flag), drains its outstanding copies and MMAs, frees tensor
@@ -108,6 +114,7 @@ enum BarId : int {
   BAR_FIXED = 33         // then K_FULL[NK], K_EMPTY[NK], V_FULL[NV], V_EMPTY[NV]
 };
 
+constexpr int kScaleSlots = 4;   // tiles of key scales in flight (QSPLIT)
 constexpr int kSlotBytes = 48;   // shared-memory bytes of one SchedSlot entry
 
 // Consumers of a scheduler slot: the two MMA lanes, 2 softmax warpgroups, the
@@ -133,6 +140,8 @@ struct Tc05Traits {
   // The paged cache holds e4m3 codes, widened to bf16 on their way to a stage.
   static constexpr bool C8 = C8_;
   static_assert(!C8 || PAGED, "an e4m3 cache is a paged one");
+  // K stays e4m3; each Q tile is two e4m3 tiles, q1 and what it leaves, q2.
+  static constexpr bool QSPLIT = C8 && DQK == 128;
   static constexpr int BM = kBlockM, BN = kBlockN, NQ = 2;
   static constexpr int MMA_M = PAIR ? 2 * kBlockM : kBlockM;   // rows of one MMA tile (both CTAs)
   static constexpr int ROWS_PER_WORK = NQ * MMA_M;              // rows of one work tile
@@ -144,9 +153,9 @@ struct Tc05Traits {
   static constexpr int K_ROWS = PAIR ? kBlockN / 2 : kBlockN;   // keys of a K stage held by this CTA
   static constexpr int K_CHUNK_BYTES = K_ROWS * 128;
   static constexpr int Q_TILE_BYTES = (QK_CHUNKS + R_CHUNKS) * CHUNK_BYTES;
-  static constexpr int K_STAGE_BYTES = (QK_CHUNKS + R_CHUNKS) * K_CHUNK_BYTES;
+  static constexpr int K_STAGE_BYTES = QSPLIT ? K_CHUNK_BYTES : (QK_CHUNKS + R_CHUNKS) * K_CHUNK_BYTES;
   static constexpr int V_STAGE_BYTES = V8 ? DV * 128 : V_CHUNKS * CHUNK_BYTES;
-  static constexpr int NK = PAIR ? (DR > 0 ? 3 : 5) : (DR > 0 ? 2 : (FP8 ? 4 : (DQK == 64 ? 4 : (C8 ? 2 : 3))));
+  static constexpr int NK = PAIR ? (DR > 0 ? 3 : 5) : (DR > 0 ? 2 : (FP8 ? 4 : (DQK == 64 ? 4 : 3)));
   static constexpr int NV = PAIR ? (DR > 0 ? 3 : 4) : (DR > 0 ? 1 : (V8 ? 4 : (FP8 ? 3 : (DQK == 64 ? 4 : 2))));
   // Bytes one phase of a Q / K / V full barrier waits for (a pair's first CTA
   // counts both CTAs' copies).
@@ -158,12 +167,14 @@ struct Tc05Traits {
   static constexpr int OFF_K = NQ * Q_TILE_BYTES;
   static constexpr int OFF_V = OFF_K + NK * K_STAGE_BYTES;
   static constexpr int OFF_RCPL = OFF_V + NV * V_STAGE_BYTES;       // float [NQ][BM]
-  static constexpr int OFF_KS = OFF_RCPL + NQ * BM * 4;             // float [NQ][2][BN] (fp8)
-  static constexpr int KS_BYTES = FP8 ? NQ * 2 * BN * 4 : (C8 ? 2 * (DQK + 4) * BN : 0);   // C8: codes and scales of two tiles
-  static constexpr int OFF_SCHED = OFF_KS + KS_BYTES;               // 2 slots x kSlotBytes
+  static constexpr int OFF_KS = OFF_RCPL + NQ * BM * 4;             // float [NQ][2][BN] (FP8), [slot][BN] (QSPLIT)
+  static constexpr int KS_BYTES = QSPLIT ? kScaleSlots * BN * 4 : (FP8 ? NQ * 2 * BN * 4 : 0);
+  static constexpr int OFF_QS = OFF_KS + KS_BYTES;                  // float [NQ][BM] (QSPLIT): 2^e of the rows
+  static constexpr int OFF_WIDEN = OFF_QS + (QSPLIT ? NQ * BM * 4 : 0);   // C8: codes and scales of two tiles
+  static constexpr int OFF_SCHED = OFF_WIDEN + (C8 ? 2 * (DQK + 4) * BN : 0);               // 2 slots x kSlotBytes
   static constexpr int OFF_WORK = OFF_SCHED + 2 * kSlotBytes;       // CTA pairs: 2 x int64 work index
   static constexpr int OFF_BAR = OFF_WORK + 16;
-  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV + (PAGED ? 1 : 0);
+  static constexpr int NUM_BARS = BAR_FIXED + 2 * NK + 2 * NV + (QSPLIT ? kScaleSlots : (PAGED ? 1 : 0));
   static constexpr int OFF_TMEM_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_TMEM_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 12;
@@ -175,7 +186,9 @@ struct Tc05Traits {
   static constexpr int BAR_V_FULL = BAR_FIXED + 2 * NK;
   static constexpr int BAR_V_EMPTY = BAR_FIXED + 2 * NK + NV;
   static constexpr int BAR_V_TAIL = BAR_FIXED + 2 * NK + 2 * NV;   // paged: copies of a V tile that ends inside
-  static constexpr uint32_t FILL_COUNT = C8 ? 4 : 1;   // arrivals that fill a K or V stage (C8: one per warp)
+  static constexpr int BAR_SCALES = BAR_FIXED + 2 * NK + 2 * NV;   // QSPLIT: +slot, copies of a tile's key scales
+  // Arrivals that fill a stage (one per warp of warpgroup 2 where that brings it).
+  static constexpr uint32_t Q_FILL = QSPLIT ? 4 : 1, K_FILL = C8 && !QSPLIT ? 4 : 1, V_FILL = C8 ? 4 : 1;
 
   static constexpr uint32_t TMEM_COLS = 512;
   // Tensor-memory columns: S_0, S_1 (P_i overwrites the first 64 columns of
@@ -184,7 +197,7 @@ struct Tc05Traits {
   __host__ __device__ static constexpr uint32_t tm_o(int i) { return i ? 384u : 256u; }
 
   static constexpr uint32_t IDESC_S =
-      FP8 ? ptx::idesc_f32acc(0, 0, false, false, 128, 128) : ptx::idesc_f32acc(1, 1, false, false, MMA_M, 128);
+      FP8 || QSPLIT ? ptx::idesc_f32acc(0, 0, false, false, 128, 128) : ptx::idesc_f32acc(1, 1, false, false, MMA_M, 128);
   static constexpr uint32_t IDESC_PV =
       V8 ? ptx::idesc_f32acc(0, 0, false, false, 128, DV) : ptx::idesc_f32acc(1, 1, false, true, MMA_M, DV);
   // P.V instructions per half tile of 64 keys (K = 16 per bf16 instruction, 32 per e4m3).
@@ -203,7 +216,8 @@ struct Tc05Traits {
   // workloads, no change for bf16).
     // With an e4m3 cache the epilogue warpgroup also widens K and V (96), and
   // the single-thread roles, which load only Q, get by with 48.
-  static constexpr int REG_SOFTMAX = FP8 ? 192 : 184, REG_CORR = FP8 ? 64 : (C8 ? 96 : 80), REG_MISC = C8 ? 48 : 64;
+  static constexpr int REG_SOFTMAX = FP8 ? 192 : 184, REG_CORR = FP8 ? 64 : (C8 && !QSPLIT ? 96 : 80),
+                       REG_MISC = C8 && !QSPLIT ? 48 : 64;
   // Softmax turn: 0 = the two softmax warpgroups run freely; 1 / 2 = they
   // take turns, handing over after the first half of P / after the tile.
   // With FP8 Q/K a tile's MMAs take less time than a softmax, and two
@@ -578,19 +592,38 @@ __device__ __forceinline__ int tile_page(const Tc05Params& P, const Ctx& c, int 
 
 // Copies the pages of one K or V tile into a stage (the whole warp; `page` from
 // tile_page), completing on `bar`, whose one arrival this is.
-template <class T>
+template <class T, int CHUNKS>
 __device__ __forceinline__ void load_paged_tile(const Tc05Params& P, const CUtensorMap* map, uint32_t dst,
                                                 uint32_t bar, int hk, int tile, int page) {
   const int lane = threadIdx.x & 31;
   const int rows = min(kBlockN, 1 << P.cache.page_shift);
   const int parts = __popc(__ballot_sync(kFull, page >= 0));
-  if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)(parts * rows * 128 * T::V_CHUNKS));
+  if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)(parts * rows * 128 * CHUNKS));
   __syncwarp();
   if (page >= 0) {
     const int slot = (tile * kBlockN) & ((1 << P.cache.page_shift) - 1);   // 0 unless pages are longer than a tile
 #pragma unroll
-    for (int ch = 0; ch < T::V_CHUNKS; ++ch)
+    for (int ch = 0; ch < CHUNKS; ++ch)
       ptx::tma_load_4d(dst + ch * T::CHUNK_BYTES + lane * rows * 128, map, bar, ch * 64, hk, slot, page);
+  }
+  __syncwarp();
+}
+
+// Copies the key scales of one tile next to it, into ring slot x (QSPLIT; the
+// whole warp, `page` from tile_page). Slot x was last read for tile x - 4: the
+// K stage just filled was released by S(x - 3), which followed that softmax.
+template <class T>
+__device__ __forceinline__ void load_tile_scales(const Tc05Params& P, const Ctx& c, int hk, int tile, int page, uint32_t x) {
+  const int lane = threadIdx.x & 31;
+  const int rows = min(kBlockN, 1 << P.cache.page_shift);
+  const int parts = __popc(__ballot_sync(kFull, page >= 0));
+  const uint32_t bar = c.bar(T::BAR_SCALES + (int)(x % kScaleSlots));
+  if (lane == 0) ptx::mbar_expect_tx(bar, (uint32_t)(parts * rows * 4));
+  __syncwarp();
+  if (page >= 0) {
+    const int slot = (tile * kBlockN) & ((1 << P.cache.page_shift) - 1);
+    const float* src = P.cache.k_scale + ((((int64_t)page * P.cache.heads_kv + hk) << P.cache.page_shift) + slot);
+    ptx::bulk_load(c.sbase + T::OFF_KS + (x % kScaleSlots) * (kBlockN * 4) + lane * rows * 4, src, (uint32_t)(rows * 4), bar);
   }
   __syncwarp();
 }
@@ -630,6 +663,7 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
   for (int s = 0; s < T::NK; ++s) { k_fill_parity[s] = 0; k_used[s] = false; }
   Cursor cur;
   [[maybe_unused]] ListCursor list;
+  [[maybe_unused]] uint32_t sc_tile = 0;   // QSPLIT: key tiles so far
   // The first work index is this CTA's own (a pair's: the cluster's).
   int64_t w = T::PAIR ? (int64_t)ptx::cluster_id_x() : (int64_t)blockIdx.x;
   const int64_t units = T::PAIR ? (int64_t)ptx::nclusters_x() : (int64_t)gridDim.x;
@@ -677,24 +711,31 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
       };
       // Q tile 0, K_0, then Q tile 1: each Q region is refilled as soon as
       // its own last S MMA of the previous work tile is done.
-      if (!wait_warp(c, BAR_Q_EMPTY, q_empty_phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
-      if (lane == 0) load_q(0);
-      q_fill_parity = q_empty_phase;   // parity of the Q_FULL phases these loads complete
-      q_loaded[0] = true;
-      q_loaded[1] = false;
-      if constexpr (T::C8) {   // warpgroup 2 brings K and V
+      if constexpr (!T::QSPLIT) {   // (else warpgroup 2 brings Q)
+        if (!wait_warp(c, BAR_Q_EMPTY, q_empty_phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
+        if (lane == 0) load_q(0);
+        q_fill_parity = q_empty_phase;   // parity of the Q_FULL phases these loads complete
+        q_loaded[0] = true;
+        q_loaded[1] = false;
+      }
+      if constexpr (T::C8 && !T::QSPLIT) {   // warpgroup 2 brings K and V
         if (!wait_warp(c, BAR_Q_EMPTY1, q_empty_phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
         if (lane == 0) load_q(1);
         q_loaded[1] = true;
         q_empty_phase ^= 1u;
       }
       [[maybe_unused]] int page = -1;   // this lane's part of the next K tile
-      if constexpr (T::PAGED && !T::C8) page = tile_page(P, c, s.b, s.lk, s.k_start);
-      for (int j = 0; j < (T::C8 ? 0 : n1); ++j) {
+      constexpr bool kLoadsK = !T::C8 || T::QSPLIT;
+      if constexpr (T::PAGED && kLoadsK) page = tile_page(P, c, s.b, s.lk, s.k_start);
+      for (int j = 0; j < (kLoadsK ? n1 : 0); ++j) {
         if (!wait_warp(c, T::BAR_K_EMPTY + kr.idx, kr.phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
         if constexpr (T::PAGED) {
-          load_paged_tile<T>(P, &P.tm_k, c.sbase + T::OFF_K + kr.idx * T::K_STAGE_BYTES,
+          load_paged_tile<T, T::K_STAGE_BYTES / T::CHUNK_BYTES>(P, &P.tm_k, c.sbase + T::OFF_K + kr.idx * T::K_STAGE_BYTES,
                              c.bar(T::BAR_K_FULL + kr.idx), hk, s.k_start + j, page);
+          if constexpr (T::QSPLIT) {
+            load_tile_scales<T>(P, c, hk, s.k_start + j, page, sc_tile);
+            ++sc_tile;
+          }
           page = tile_page(P, c, s.b, s.lk, s.k_start + j + 1);
         } else if (lane == 0) {
           const uint32_t bar = c.bar(T::BAR_K_FULL + kr.idx);
@@ -710,7 +751,7 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
         k_fill_parity[kr.idx] = kr.phase;
         k_used[kr.idx] = true;
         kr.next();
-        if (j == 0) {
+        if (!T::QSPLIT && j == 0) {
           if (!wait_warp(c, BAR_Q_EMPTY1, q_empty_phase ^ 1u, kRoleLoadQK)) { aborted = true; break; }
           if (lane == 0) load_q(1);
           q_loaded[1] = true;
@@ -763,6 +804,10 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (q_loaded[i]) wait_drain(c, BAR_Q_FULL + i, q_fill_parity);
+      if constexpr (T::QSPLIT) {
+        for (uint32_t x = sc_tile > kScaleSlots ? sc_tile - kScaleSlots : 0; x < sc_tile; ++x)
+          wait_drain(c, T::BAR_SCALES + (int)(x % kScaleSlots), (x / kScaleSlots) & 1u);
+      }
     } else {
       pair_copy_grace();
     }
@@ -803,13 +848,13 @@ __device__ void role_load_v(const Tc05Params& P, const Ctx& c) {
         const uint32_t full = c.bar(T::BAR_V_FULL + vr.idx);
         const int tile = s.k_start + j, keys = s.lk - tile * kBlockN;
         if (keys >= kBlockN) {
-          load_paged_tile<T>(P, &P.tm_v, dst, full, hk, tile, page);
+          load_paged_tile<T, T::V_CHUNKS>(P, &P.tm_v, dst, full, hk, tile, page);
           v_used[vr.idx] = true;
         } else {
           // The sequence ends inside this tile: its copies land on a barrier
           // of their own, then the rows behind the end (parts of a page, or
           // whatever the stage held) become zeros.
-          load_paged_tile<T>(P, &P.tm_v, dst, c.bar(T::BAR_V_TAIL), hk, tile, page);
+          load_paged_tile<T, T::V_CHUNKS>(P, &P.tm_v, dst, c.bar(T::BAR_V_TAIL), hk, tile, page);
           if (!wait_warp(c, T::BAR_V_TAIL, tail_phase, kRoleLoadV)) {
             wait_drain(c, T::BAR_V_TAIL, tail_phase);
             aborted = true;
@@ -883,6 +928,8 @@ __device__ __forceinline__ void issue_s(const Ctx& c, int i, uint32_t kstage) {
   for (int kk = B; kk < E; ++kk) {
     if (T::FP8) {
       ptx::mma_fp8_ss_lo<HI, HI, T::IDESC_S>(d, qa + kk * 2, ka + kk * 2, kk > 0);
+    } else if (T::QSPLIT) {   // q1 against the four 32-depth parts of K, then q2
+      ptx::mma_fp8_ss_lo<HI, HI, T::IDESC_S>(d, qa + (kk >> 2) * (T::CHUNK_BYTES >> 4) + (kk & 3) * 2, ka + (kk & 3) * 2, kk > 0);
     } else {
       // Q chunks are 128 rows, K chunks K_ROWS rows (64 in a pair)
       const bool rope = kk >= T::DQK / 16;
@@ -1058,6 +1105,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
   const int role = i == 0 ? kRoleSoftmax0 : kRoleSoftmax1;
   Ring<2> sched;
   uint32_t s_phase = 0, ks_phase = 0, stats_phase = 0, turn_phase = 0;
+  [[maybe_unused]] uint32_t q_phase = 0, sc_tile = 0;   // QSPLIT (sc_tile: key tiles before this work tile's)
   const uint32_t turn_flip = i == 0 ? 1u : 0u;   // warpgroup 0 takes the first turn
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, role)) return;
@@ -1105,6 +1153,15 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
                          : ((int64_t)s.b * P.heads_kv + hk) * P.seqlen_k + s.k_start;
     }
     float ks_next = 0.f;
+    if constexpr (T::QSPLIT) {
+      if (n > 0) {
+        // Warpgroup 2 wrote this work tile's row factors before it filled Q; it
+        // writes the next ones after this warpgroup's statistics.
+        if (!wait_warp(c, BAR_Q_FULL + i, q_phase, role)) return;
+        c_row *= reinterpret_cast<const float*>(c.smem + T::OFF_QS)[kBlockM * i + tid];
+      }
+      if (g.n[1] > 0) q_phase ^= 1u;
+    }
     if (T::FP8 && n > 0) ks_next = tid < s.lk ? __ldg(P.k_scale + ks_base + tid) : 0.f;
     float m = -INFINITY, l = 0.f;
     for (int j = 0; j < n; ++j) {
@@ -1133,6 +1190,21 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 32; ++e) sv[32 * q + e] = __uint_as_float(r[q][e]);
+      }
+      if constexpr (T::QSPLIT) {
+        // The slot's copies are complete (S needed K, and a slot is refilled only
+        // once the S after next is done): the wait makes them visible here.
+        const uint32_t x = sc_tile + (uint32_t)j;
+        if (!wait_warp(c, T::BAR_SCALES + (int)(x % kScaleSlots), (x / kScaleSlots) & 1u, role)) return;
+        const float4* k4 = reinterpret_cast<const float4*>(c.smem + T::OFF_KS) + (x % kScaleSlots) * (kBlockN / 4);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float4 kv = k4[e];
+          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(sv[4 * e], sv[4 * e + 1]), ptx::f2_pack(kv.x, kv.y)), sv[4 * e],
+                         sv[4 * e + 1]);
+          ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(sv[4 * e + 2], sv[4 * e + 3]), ptx::f2_pack(kv.z, kv.w)),
+                         sv[4 * e + 2], sv[4 * e + 3]);
+        }
       }
       if (T::FP8) {
         const float2* k2 = reinterpret_cast<const float2*>(ks_sm + (j & 1) * kBlockN);
@@ -1247,6 +1319,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
       l = l * alpha + ((s0 + s1) + (s2 + s3));
       m = m_use;
     }
+    if constexpr (T::QSPLIT) sc_tile += (uint32_t)g.n[1];
     if (T::SM_TURN) {
       // K/V tiles only the other Q tile visits: pass the turn on.
       for (int j = n; j < g.n[1]; ++j) {
@@ -1307,8 +1380,8 @@ __device__ __forceinline__ void store_row_chunk_f32(float* dst, const uint32_t (
 }
 
 // ---------------------------------------------------------------------------------------------
-// C8: warpgroup 2 as the K/V producer. A unit is one K or V tile, 128 rows of D
-// codes; warp w brings rows 32 w .. 32 w + 31, D / 16 lanes to a row (16 codes
+// C8: warpgroup 2 as the V producer (QSPLIT; else of K and V). A unit is one K or
+// V tile, 128 rows of D codes; warp w brings rows 32 w .. 32 w + 31, D / 16 lanes to a row (16 codes
 // each), in D / 16 pieces per thread. The pieces of unit u go through half
 // u & 1 of a ring, each refilled with unit u + 2's as soon as it is read: two
 // units (32 KB at D = 128) are in flight, a whole step's bytes. (Registers in
@@ -1322,8 +1395,8 @@ struct Widen {
   static constexpr int RPL = 32 / LPR;           // rows a warp moves at a time
   static constexpr int NP = 32 / RPL;            // pieces per thread
   static constexpr int PB = 16 / RPL;            // of them in a 16-key block
-  static constexpr int RING = T::OFF_KS;         // [2][NP][128 threads][16 bytes]
-  static constexpr int SCALES = T::OFF_KS + 2 * NP * 2048;   // [2][128 rows] fp32
+  static constexpr int RING = T::OFF_WIDEN;      // [2][NP][128 threads][16 bytes]
+  static constexpr int SCALES = T::OFF_WIDEN + 2 * NP * 2048;   // [2][128 rows] fp32
 
   Ring<T::NK> kr;
   Ring<T::NV> vr;
@@ -1387,52 +1460,64 @@ struct Widen {
                        (key & ((1 << cv.page_shift) - 1));
     ptx::cp_async4(c.sbase + SCALES + half * 512 + tid * 4, ok ? scales + at : scales, ok);
   }
-  // All K and V tiles of one work tile: units K_0, V_0, K_1, V_1, ... False: a
-  // wait ran out. One small loop for both kinds, unrolled twice only: with the
-  // code of every piece laid out, this warpgroup and the softmax ones evicted
-  // each other's instructions.
-  __device__ __forceinline__ bool run(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int n) {
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3;
-    const int hk = s.h / P.group;
-    const CacheView& cv = P.cache;
-    auto pages_of = [&](int tile, int (&page)[2]) {
+  // All units of one work tile, the first two on their way since begin():
+  // K_0, V_0, K_1, V_1, ... or, with QSPLIT, V_0, V_1, ... False: a wait ran out.
+  // One small loop, unrolled twice only: with the code of every piece laid out,
+  // this warpgroup and the softmax ones evicted each other's instructions.
+  static constexpr bool BOTH = !T::QSPLIT;
+  __device__ static __forceinline__ bool is_v(int u) { return BOTH ? (u & 1) != 0 : true; }
+  __device__ static __forceinline__ int tile_of(int u) { return BOTH ? u >> 1 : u; }
+  __device__ static __forceinline__ void pages_of(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int tile,
+                                                  int (&page)[2]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int key = tile * kBlockN + 32 * w + 16 * h;
-        page[h] = key < s.lk ? load_page(cv, s.b, key >> cv.page_shift, c.ws) : 0;
-      }
-    };
-    auto source = [&](bool v, int tile, const int (&page)[2]) {
-      return v ? aim(cv, cv.v + hk * cv.v_head, cv.v_page, cv.v_tok, page, tile, s.lk)
-               : aim(cv, cv.k + hk * cv.k_head, cv.k_page, cv.k_tok, page, tile, s.lk);
-    };
-    const uint32_t at0 = c.sbase + lane_offset();
+    for (int h = 0; h < 2; ++h) {
+      const int key = (s.k_start + tile) * kBlockN + 32 * ((threadIdx.x >> 5) & 3) + 16 * h;
+      page[h] = key < s.lk ? load_page(P.cache, s.b, key >> P.cache.page_shift, c.ws) : 0;
+    }
+  }
+  __device__ static __forceinline__ Source source(const Tc05Params& P, const SchedSlot& s, int u, int hk,
+                                                  const int (&page)[2]) {
+    const CacheView& cv = P.cache;
+    return is_v(u) ? aim(cv, cv.v + hk * cv.v_head, cv.v_page, cv.v_tok, page, s.k_start + tile_of(u), s.lk)
+                   : aim(cv, cv.k + hk * cv.k_head, cv.k_page, cv.k_tok, page, s.k_start + tile_of(u), s.lk);
+  }
+  __device__ __forceinline__ void begin(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int n) {
+    const int hk = s.h / P.group;
     const uint32_t ring0 = c.sbase + RING + (threadIdx.x & 127) * 16;
     int page[2];
-    pages_of(s.k_start, page);
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const Source src = source(half != 0, s.k_start, page);
+    for (int u = 0; u < 2; ++u) {
+      if (u == 0 || !BOTH) pages_of(P, c, s, tile_of(u), page);   // (past the end: pages 0, nothing is read)
+      const Source src = source(P, s, u, hk, page);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) copy(cv, src, ring0 + (half * NP + i) * 2048, i);
-      copy_scale(c, cv, half ? cv.v_scale : cv.k_scale, hk, page, s.k_start, s.lk, half);
+      for (int i = 0; i < NP; ++i) copy(P.cache, src, ring0 + (u * NP + i) * 2048, i);
+      copy_scale(c, P.cache, is_v(u) ? P.cache.v_scale : P.cache.k_scale, hk, page, s.k_start + tile_of(u), s.lk, u);
       ptx::cp_async_commit();
     }
-    if (n > 1) pages_of(s.k_start + 1, page);
+  }
+  __device__ __forceinline__ bool run(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int n) {
+    const int lane = threadIdx.x & 31;
+    const int hk = s.h / P.group;
+    const CacheView& cv = P.cache;
+    const int units = BOTH ? 2 * n : n;
+    const uint32_t at0 = c.sbase + lane_offset();
+    const uint32_t ring0 = c.sbase + RING + (threadIdx.x & 127) * 16;
+    int page[2];   // of unit u + 2's tile
+    pages_of(P, c, s, tile_of(2), page);
 #pragma unroll 1
-    for (int u = 0; u < 2 * n; ++u) {
+    for (int u = 0; u < units; ++u) {
       const uint32_t half = u & 1;
-      const int tile = s.k_start + (u >> 1) + 1;   // the tile whose copies replace this one's
-      Source next = source(half != 0, tile, page);
-      if (u + 2 >= 2 * n) next.keys = 0;            // (zeros, read by nobody)
-      const int empty = half ? T::BAR_V_EMPTY + (int)vr.idx : T::BAR_K_EMPTY + (int)kr.idx;
-      if (!wait_warp(c, empty, (half ? vr.phase : kr.phase) ^ 1u, half ? kRoleLoadV : kRoleLoadQK)) {
+      const bool v = is_v(u);
+      Source next = source(P, s, u + 2, hk, page);
+      if (u + 2 >= units) next.keys = 0;            // (zeros, read by nobody)
+      const int empty = v ? T::BAR_V_EMPTY + (int)vr.idx : T::BAR_K_EMPTY + (int)kr.idx;
+      if (!wait_warp(c, empty, (v ? vr.phase : kr.phase) ^ 1u, v ? kRoleLoadV : kRoleLoadQK)) {
         ptx::cp_async_wait<0>();
         return false;
       }
       ptx::cp_async_wait<1>();
       __syncwarp();   // the scales were copied by other lanes
-      const uint32_t at = at0 + (half ? T::OFF_V + vr.idx * T::V_STAGE_BYTES : T::OFF_K + kr.idx * T::K_STAGE_BYTES);
+      const uint32_t at = at0 + (v ? T::OFF_V + vr.idx * T::V_STAGE_BYTES : T::OFF_K + kr.idx * T::K_STAGE_BYTES);
       const uint32_t ring = ring0 + half * NP * 2048;
       const float* sc = reinterpret_cast<const float*>(c.smem + SCALES + half * 512) + row0();
 #pragma unroll 1
@@ -1446,21 +1531,78 @@ struct Widen {
       }
       ptx::fence_async_shared();   // before the MMAs read the stage
       __syncwarp();
-      if (half) {
+      if (v) {
         if (lane == 0) ptx::mbar_arrive(c.bar(T::BAR_V_FULL + vr.idx));
         vr.next();
       } else {
         if (lane == 0) ptx::mbar_arrive(c.bar(T::BAR_K_FULL + kr.idx));
         kr.next();
       }
-      copy_scale(c, cv, half ? cv.v_scale : cv.k_scale, hk, page, tile, u + 2 < 2 * n ? s.lk : 0, half);
+      copy_scale(c, cv, v ? cv.v_scale : cv.k_scale, hk, page, s.k_start + tile_of(u + 2), u + 2 < units ? s.lk : 0, half);
       ptx::cp_async_commit();
-      if (half && u + 4 <= 2 * n) pages_of(tile + 1, page);
+      if (v) pages_of(P, c, s, tile_of(u + 3), page);   // (the same tile's V follows its K)
     }
     ptx::cp_async_wait<0>();
     return true;
   }
 };
+
+// QSPLIT: Q tile i of a work tile from global memory into its two e4m3 tiles, one
+// row per thread (warpgroup 2): with s the smallest power of two that brings the
+// row to 448 or below, q1 = e4m3(q / s), q2 = e4m3(q / s - q1), and s for the
+// softmax. Rows behind the sequence are zeros.
+template <class T>
+__device__ __forceinline__ void split_q(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int first, int i) {
+  const int r = threadIdx.x & 127;
+  const int tok = first + (r >> P.pack_shift), h = (s.h << P.pack_shift) + (r & ((1 << P.pack_shift) - 1));
+  const bool ok = tok < s.lq;
+  const uint4* src = reinterpret_cast<const uint4*>(P.q + (P.packed ? 0 : s.b * P.q_b) + (int64_t)(s.q_start + tok) * P.q_t + h * P.q_h);
+  uint32_t top = 0u;
+#pragma unroll 4
+  for (int e = 0; e < 16; ++e) {
+    const uint4 x = ok ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+    top = __vmaxu2(top, x.x & 0x7fff7fffu);
+    top = __vmaxu2(top, x.y & 0x7fff7fffu);
+    top = __vmaxu2(top, x.z & 0x7fff7fffu);
+    top = __vmaxu2(top, x.w & 0x7fff7fffu);
+  }
+  top = max(top & 0xffffu, top >> 16);
+  // Exponent of s, so that amax / s is in (224, 448]. A row with infinities or
+  // NaN has them as e4m3 NaN: its scores are NaN, as the formula's are.
+  const bool finite = top < 0x7f80u;
+  const int e2 = finite && top ? max(-126, (int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 96u ? 1 : 0)) : 0;
+  const float inv = finite ? __uint_as_float((uint32_t)(127 - e2) << 23) : __uint_as_float(0x7fc00000u);
+  reinterpret_cast<float*>(c.smem + T::OFF_QS)[kBlockM * i + r] = __uint_as_float((uint32_t)(127 + e2) << 23);
+  const uint32_t dst = c.sbase + T::OFF_Q + i * T::Q_TILE_BYTES + r * 128;
+#pragma unroll 1
+  for (int e = 0; e < 8; ++e) {   // 16 depths at a time
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint4 x = ok ? __ldg(src + 2 * e + k) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float f[4], b[4];
+        f[0] = __uint_as_float(w[2 * y] << 16) * inv;
+        f[1] = __uint_as_float(w[2 * y] & 0xffff0000u) * inv;
+        f[2] = __uint_as_float(w[2 * y + 1] << 16) * inv;
+        f[3] = __uint_as_float(w[2 * y + 1] & 0xffff0000u) * inv;
+        const uint32_t q1 = ptx::pack_e4m3x4(f[0], f[1], f[2], f[3]);
+        ptx::e4m3x2_to_float2(q1 & 0xffffu, b[0], b[1]);
+        ptx::e4m3x2_to_float2(q1 >> 16, b[2], b[3]);
+        hi[2 * k + y] = q1;
+        lo[2 * k + y] = ptx::pack_e4m3x4(f[0] - b[0], f[1] - b[1], f[2] - b[2], f[3] - b[3]);
+      }
+    }
+    const uint32_t at = dst + ((e ^ (r & 7)) << 4);
+    ptx::st_shared_v4(at, hi[0], hi[1], hi[2], hi[3]);
+    ptx::st_shared_v4(at + T::CHUNK_BYTES, lo[0], lo[1], lo[2], lo[3]);
+  }
+  ptx::fence_async_shared();   // before the MMAs read the tiles
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(c.bar(BAR_Q_FULL + i));
+}
 
 template <class T, int CAUSAL>
 __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
@@ -1470,6 +1612,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
   Ring<2> sched;
   uint32_t stats_phase[2] = {0, 0}, ofinal_phase[2] = {0, 0};
   [[maybe_unused]] Widen<T> widen;
+  [[maybe_unused]] uint32_t q_empty_phase = 0;   // QSPLIT
   while (true) {
     if (!wait_warp(c, BAR_SCHED_FULL + sched.idx, sched.phase, kRoleCorrection)) return;
     const SchedSlot s = read_slot<CAUSAL, T::PAGED>(c, sched.idx, T::OFF_SCHED);
@@ -1478,7 +1621,17 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
     if (!s.valid) return;
     const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
     if constexpr (T::C8) {
-      if (g.n[1] > 0 && !widen.run(P, c, s, g.n[1])) return;
+      if (g.n[1] > 0) {
+        widen.begin(P, c, s, g.n[1]);
+        if constexpr (T::QSPLIT) {
+          if (!wait_warp(c, BAR_Q_EMPTY, q_empty_phase ^ 1u, kRoleCorrection)) { ptx::cp_async_wait<0>(); return; }
+          split_q<T>(P, c, s, g.row[0], 0);
+          if (!wait_warp(c, BAR_Q_EMPTY1, q_empty_phase ^ 1u, kRoleCorrection)) { ptx::cp_async_wait<0>(); return; }
+          split_q<T>(P, c, s, g.row[1], 1);
+          q_empty_phase ^= 1u;
+        }
+        if (!widen.run(P, c, s, g.n[1])) return;
+      }
     }
 #pragma unroll 1
     for (int i = 0; i < 2; ++i) {
@@ -1575,7 +1728,7 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(c.bar(BAR_Q_FULL + i), 1);
+      ptx::mbar_init(c.bar(BAR_Q_FULL + i), T::Q_FILL);
       ptx::mbar_init(c.bar(BAR_S_FULL + i), 1);
       ptx::mbar_init(c.bar(BAR_P_LO + i), warp_count);
       ptx::mbar_init(c.bar(BAR_STATS + i), 128);
@@ -1597,15 +1750,20 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
     ptx::mbar_init(c.bar(BAR_DRAIN), 2);
 #pragma unroll
     for (int s = 0; s < T::NK; ++s) {
-      ptx::mbar_init(c.bar(T::BAR_K_FULL + s), T::FILL_COUNT);
+      ptx::mbar_init(c.bar(T::BAR_K_FULL + s), T::K_FILL);
       ptx::mbar_init(c.bar(T::BAR_K_EMPTY + s), 2);
     }
 #pragma unroll
     for (int s = 0; s < T::NV; ++s) {
-      ptx::mbar_init(c.bar(T::BAR_V_FULL + s), T::FILL_COUNT);
+      ptx::mbar_init(c.bar(T::BAR_V_FULL + s), T::V_FILL);
       ptx::mbar_init(c.bar(T::BAR_V_EMPTY + s), 2);
     }
-    if constexpr (T::PAGED) ptx::mbar_init(c.bar(T::BAR_V_TAIL), 1);
+    if constexpr (T::QSPLIT) {
+#pragma unroll
+      for (int s = 0; s < kScaleSlots; ++s) ptx::mbar_init(c.bar(T::BAR_SCALES + s), 1);
+    } else if constexpr (T::PAGED) {
+      ptx::mbar_init(c.bar(T::BAR_V_TAIL), 1);
+    }
     *c.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -1619,11 +1777,9 @@ __global__ void __launch_bounds__(512, 1) fa_tc05_kernel(const __grid_constant__
     }
   }
   if (warp == 14 && lane == 0) {
-    ptx::prefetch_tmap(&P.tm_q);
-    if constexpr (!T::C8) {
-      ptx::prefetch_tmap(&P.tm_k);
-      ptx::prefetch_tmap(&P.tm_v);
-    }
+    if constexpr (!T::QSPLIT) ptx::prefetch_tmap(&P.tm_q);
+    if constexpr (!T::C8 || T::QSPLIT) ptx::prefetch_tmap(&P.tm_k);
+    if constexpr (!T::C8) ptx::prefetch_tmap(&P.tm_v);
     if (T::DR > 0) {
       ptx::prefetch_tmap(&P.tm_qr);
       ptx::prefetch_tmap(&P.tm_kr);

@@ -112,6 +112,8 @@ struct Tc05Params {
   int32_t max_k;           // upper bound of them
   int32_t pack_shift;      // log2 of the query heads in a tile
   int32_t heads_total;     // Hq
+  const uint8_t* q;        // e4m3 cache: Q itself (split by the kernel), byte strides
+  int64_t q_b, q_t, q_h;
   const PlanHead* plan;    // work list, or NULL: every query tile whole, in order
   const PlanItem* items;
   const PlanPiece* pieces;

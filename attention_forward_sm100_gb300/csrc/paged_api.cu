@@ -269,13 +269,20 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
       {64, pack, af::kBlockM / pack, 1});
   if (st != ATTN_OK) return st;
   const bool fp8 = c.dtype == ATTN_DTYPE_FP8_E4M3;
-  for (int i = 0; i < 2 && !fp8; ++i) {   // (an e4m3 cache is read without tensor maps)
+  // (of an e4m3 cache only K with D = 128 is read through a map)
+  for (int i = 0; i < (fp8 ? (c.head_dim == 128 ? 1 : 0) : 2); ++i) {
     const int64_t* s = i ? c.v_stride : c.k_stride;
-    st = af::encode_map(i ? &prm.tm_v : &prm.tm_k, bf16, i ? c.v : c.k,
+    const int64_t es = fp8 ? 1 : 2;
+    st = af::encode_map(i ? &prm.tm_v : &prm.tm_k, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : bf16, i ? c.v : c.k,
                         {c.head_dim, c.num_heads_kv, c.page_size, c.num_pages},
-                        {legal(s[2] * 2, c.num_heads_kv), s[1] * 2, legal(s[0] * 2, c.num_pages)}, {64, 1, page_rows, 1});
+                        {legal(s[2] * es, c.num_heads_kv), s[1] * es, legal(s[0] * es, c.num_pages)},
+                        {fp8 ? 128 : 64, 1, page_rows, 1});
     if (st != ATTN_OK) return st;
   }
+  prm.q = static_cast<const uint8_t*>(p->q);
+  prm.q_b = packed ? 0 : p->q_stride[0] * 2;
+  prm.q_t = p->q_stride[1] * 2;
+  prm.q_h = p->q_stride[2] * 2;
   prm.cu_q = p->cu_seqlens_q;
   prm.o = static_cast<uint16_t*>(p->o);
   prm.lse = p->lse;
