@@ -67,7 +67,8 @@ struct PlanHead {
 };
 constexpr int kPlanMaxBatch = 1024;
 constexpr int64_t kPlanMaxTiles = 8192;
-constexpr int kMinPieceUnits = 8;   // key tiles of a piece worth its set-up and its share of the merge
+constexpr int kMinPieceUnits = 4;   // key tiles of a piece worth its set-up and its share of the merge
+constexpr int kListTiles = 16;      // up to so many key tiles every query tile is taken whole, without a list
 
 // Everything the tcgen05 kernel needs, passed as one __grid_constant__ struct.
 struct Tc05Params {

@@ -193,7 +193,7 @@ TilePlan plan_tiles(const attn_paged_params* p) {
   if (p->cu_seqlens_q != nullptr && p->total_q / t.tokens + c.batch < token_tiles)
     token_tiles = p->total_q / t.tokens + c.batch;
   t.work = token_tiles * (p->num_heads_q >> t.pack_shift);
-  t.list = af::tiles_for(p->seqlen_k, af::kBlockN) > af::kMinPieceUnits && t.work <= af::kPlanMaxTiles &&
+  t.list = af::tiles_for(p->seqlen_k, af::kBlockN) > af::kListTiles && t.work <= af::kPlanMaxTiles &&
            c.batch <= af::kPlanMaxBatch;
   if (t.list) {
     const int64_t ctas = af::sm_count();

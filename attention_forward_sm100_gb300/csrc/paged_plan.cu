@@ -14,12 +14,18 @@
 // a piece border cuts leave partial results: 256 tiles of 256 units on 152 CTAs
 // take 2 * 256 units when handed out whole, 449 when each is cut in four (and
 // four partial results of everything), 431 + the merge of 104 tiles this way.
+// Cutting costs about 8 units (of ~1.5 us: the merge's launch) and one for every
+// 18 segments (their set-up and the traffic of the partial results), and is left
+// where it evens out less: 384 tiles of four sequences of 3271 to 12000 keys
+// take 346 us whole, 369 us cut; 256 tiles of one sequence of 32768 keys 782 us
+// whole, 687 us cut.
 // Whole tiles keep the order in which CTAs of one KV head run side by side
 // over the same keys, which L2 then serves; only the cut ones do not.
 //
 // A piece is one entry of the dynamic schedule, its segments run one after
 // the other in one CTA. Segment (piece p, cut tile i) has index and partial
 // slot p + i: unique, because from one segment to the next either p or i grows.
+#include <limits.h>
 #include <math.h>
 
 #include "launch.cuh"
@@ -59,6 +65,16 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums) {
   return v;
 }
 
+// The last thread's inclusive sum.
+__device__ __forceinline__ int block_total(int incl) {
+  __shared__ int total;
+  if (threadIdx.x == blockDim.x - 1) total = incl;
+  __syncthreads();
+  const int t = total;
+  __syncthreads();
+  return t;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PlanParams P) {
   __shared__ SeqRows seq[kPlanMaxBatch];        // sequences, the longest first
   __shared__ int16_t who[kPlanMaxBatch];        // and their numbers
@@ -91,9 +107,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     if (tid == 0) record_bad_cache(P.ws, 0);
     W = 0;
   }
-  const int waves = W / P.ctas - (B > 1 ? 1 : 0);
-  const int whole = waves > 0 ? waves * P.ctas : 0;
-
   // Tile `x` of the list; returns the key tiles it sees.
   auto tile_at = [&](int x, PlanItem& it) {
     int lo = 0, hi = B - 1;                      // the first sequence with ends > x
@@ -117,22 +130,41 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     it.slot = -1;
     return it.j1;
   };
-  for (int x = tid; x < whole; x += kPlanThreads) {
+  // Every tile whole; the units of all of them, of the largest and of the smallest.
+  __shared__ int most_s, least_s;
+  if (tid == 0) {
+    most_s = 0;
+    least_s = INT_MAX;
+  }
+  int sum = 0, most = 0, least = INT_MAX;
+  for (int x = tid; x < W; x += kPlanThreads) {
     PlanItem it;
-    tile_at(x, it);
+    const int n = max(1, tile_at(x, it));
+    sum += n;
+    most = max(most, n);
+    least = min(least, n);
     P.items[x] = it;
   }
+  const int all = block_total(block_scan(sum, sums));
+  atomicMax(&most_s, most);
+  atomicMin(&least_s, least);
+  __syncthreads();
+  // When the last CTA is done, in units, a tile adding two: equal tiles go in
+  // rounds, unequal ones (the longest first) end within half a small one of
+  // each other.
+  const int rounds = (W + P.ctas - 1) / P.ctas, share = (all + P.ctas - 1) / P.ctas;
+  const int uneven = max(most_s + 2, share + least_s / 2 + 2 * rounds);
+  const int uncut = 4 * least_s >= 3 * most_s ? rounds * (most_s + 2) : uneven;
+  const int waves = W / P.ctas - (B > 1 ? 1 : 0), shares = P.ctas * (B > 1 ? 2 : 1);
+  const int even = waves > 0 ? waves * P.ctas : 0;
+  const int whole = uncut <= share + 8 + (W - even + shares) / 18 ? W : even;
   // The cut tiles: fewer than two waves (and than this block's threads).
   const int cut = W - whole;
   PlanItem it;
   int units = 0;
   if (tid < cut) units = max(1, tile_at(whole + tid, it));
   const int u1 = block_scan(units, sums), u0 = u1 - units;
-  __shared__ int total_s;
-  if (tid == kPlanThreads - 1) total_s = u1;
-  __syncthreads();
-  const int total = total_s;
-  const int shares = P.ctas * (B > 1 ? 2 : 1);
+  const int total = block_total(u1);
   const int size = max(kMinPieceUnits, (total + shares - 1) / shares);
   const int pieces = (total + size - 1) / size;
   if (tid < cut) {
