@@ -23,10 +23,11 @@
 //     both. The maximum only moves when it grows by more than 2^8, so the
 //     accumulator is rarely rescaled; O and the sum share it, so their quotient
 //     is exact;
-//   * e4m3 keys are multiplied as f16 (exactly; q as f16 too, normalised by a
-//     power of two per row), e4m3 values as bf16; the key scale is applied to the
-//     fp32 score, the value scale to the fp32 weight before its rounding to
-//     bf16. Depth and value columns are dealt to lanes in the order in which
+//   * e4m3 codes are multiplied as f16, exactly (one conversion for two of them;
+//     to bf16 it takes four): q as f16 too, normalised by a power of two per row,
+//     and the weights in units of the largest value scale (where scales differ
+//     by more than 2^4 weights and values go through bf16). The key scale is
+//     applied to the fp32 score, the value scale to the fp32 weight. Depth and value columns are dealt to lanes in the order in which
 //     16-byte reads from shared memory deliver them: a dot product does not
 //     depend on the order of its depth, nor a product on that of its columns;
 //   * a segment that lies in one CTA is finished there; the parts of one that
@@ -36,6 +37,8 @@
 // Slots at or past the sequence's end are not read (their shared memory is
 // zeroed), so whatever they hold cannot reach a result.
 #include <math.h>
+
+#include <type_traits>
 
 #include "launch.cuh"
 #include "paged.h"
@@ -245,9 +248,10 @@ struct Loader {
 #pragma unroll
       for (int y = 0; y < PER; ++y) {
         const int row = lrow + (i + y) * C::RS;
+        // (behind the end nothing is read; the address is still inside a page)
         const bool ok = key0 + row < lk;
-        ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, ok ? ks : P.c.k, ok);
-        ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, ok ? vs : P.c.v, ok);
+        ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, ks, ok);
+        ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, vs, ok);
         ks += C::RS * P.c.k_tok;
         vs += C::RS * P.c.v_tok;
       }
@@ -451,6 +455,13 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][x][e] = 0.f;
+  // e4m3: the accumulator is in units of vref / 2^7, vref a power of two at
+  // least as large as every value scale so far. While the scales of a step are
+  // within 2^-4 of it, weights (times scale / vref * 2^7, at most 2^15) and codes
+  // are multiplied as f16: its spacing near zero, 2^-24, then costs a key less
+  // than 2^-28 of the largest weight, so 2^20 keys less than bf16's rounding.
+  // Steps with smaller scales go through bf16.
+  float vref = 0.f, vinv = 0.f;
   float m[NT][2], l[NT][2];
 #pragma unroll
   for (int x = 0; x < NT; ++x)
@@ -564,30 +575,27 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
           }
         }
     }
-    // ---- weights (a row that has seen no key yet keeps m = -inf and weights 0), O^T += V^T P^T
+    // ---- weights (a row that has seen no key yet keeps m = -inf and weights 0)
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      uint32_t pf[NT][2];
-      float v0 = 1.f, v1 = 1.f;
-      if constexpr (C::FP8) {
-        v0 = scale_sm[KW + 16 * i + g];
-        v1 = scale_sm[KW + 16 * i + g + 8];
-      }
+    for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        float w[4];
+      for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float off = m[x][e & 1] == -INFINITY ? 0.f : m[x][e & 1];
-          w[e] = ptx::ex2(sc[i][x][e] - off);
-          l[x][e & 1] += w[e];
-          if constexpr (C::FP8) w[e] *= e < 2 ? v0 : v1;
+          sc[i][x][e] = ptx::ex2(sc[i][x][e] - off);
+          l[x][e & 1] += sc[i][x][e];
         }
-        // (key, rows) pairs to (row, keys) pairs
-        pf[x][0] = ptx::movmatrix_trans(ptx::pack_bf16(w[0], w[1]));
-        pf[x][1] = ptx::movmatrix_trans(ptx::pack_bf16(w[2], w[3]));
-      }
-      if constexpr (!C::FP8) {
+    // ---- O^T += V^T P^T
+    if constexpr (!C::FP8) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {   // (key, rows) pairs to (row, keys) pairs
+          pf[x][0] = ptx::movmatrix_trans(ptx::pack_bf16(sc[i][x][0], sc[i][x][1]));
+          pf[x][1] = ptx::movmatrix_trans(ptx::pack_bf16(sc[i][x][2], sc[i][x][3]));
+        }
 #pragma unroll
         for (int q = 0; q < D / 16; ++q) {
           uint32_t a[4];
@@ -596,7 +604,45 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
 #pragma unroll
           for (int x = 0; x < NT; ++x) ptx::mma_16816(acc[q][x], a, pf[x][0], pf[x][1]);
         }
-      } else {
+      }
+    } else {
+      float vs[NB][2], top = 0.f, low = INFINITY;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          vs[i][e] = scale_sm[KW + 16 * i + g + 8 * e];
+          top = fmaxf(top, fabsf(vs[i][e]));
+          // (keys behind the end have scale 0 and weight 0)
+          if (key0 + 16 * i + g + 8 * e < s.lk) low = fminf(low, fabsf(vs[i][e]));
+        }
+      if (__any_sync(kFull, top > vref)) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        // the next power of two (an infinite or huge scale: 2^127; NaN leaves it)
+        const uint32_t up = min(((__float_as_uint(top) + 0x7fffffu) >> 23), 254u) << 23;
+        const float now = fmaxf(vref, __uint_as_float(max(up, 1u << 23)));
+        const float change = vref == 0.f ? 0.f : vref / now;
+        vref = now;
+        vinv = 128.f / now;
+#pragma unroll
+        for (int q = 0; q < D / 16; ++q)
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[q][x][e] *= change;
+      }
+      const bool as_f16 = __all_sync(kFull, low >= vref * 0.0625f);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        const float w0 = vs[i][0] * vinv, w1 = vs[i][1] * vinv;
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          const float a0 = sc[i][x][0] * w0, a1 = sc[i][x][1] * w0, a2 = sc[i][x][2] * w1, a3 = sc[i][x][3] * w1;
+          pf[x][0] = ptx::movmatrix_trans(as_f16 ? ptx::pack_f16(a0, a1) : ptx::pack_bf16(a0, a1));
+          pf[x][1] = ptx::movmatrix_trans(as_f16 ? ptx::pack_f16(a2, a3) : ptx::pack_bf16(a2, a3));
+        }
         // lane (g, t): depths g * D/8 .. + D/8 of keys 2t, 2t+1, 2t+8, 2t+9
         uint32_t v[4][D / 32];
 #pragma unroll
@@ -611,18 +657,32 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
             v[e][0] = w.x; v[e][1] = w.y;
           }
         }
+        // (key, key) pairs of each depth
+        auto product = [&](auto f16) {
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
+          for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __byte_perm(v[0][w], v[1][w], h ? 0x7362 : 0x5140);
-            const uint32_t hi = __byte_perm(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
-            const uint32_t a[4] = {ptx::e4m3x2_to_bf16x2(lo & 0xffffu), ptx::e4m3x2_to_bf16x2(lo >> 16),
-                                   ptx::e4m3x2_to_bf16x2(hi & 0xffffu), ptx::e4m3x2_to_bf16x2(hi >> 16)};
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t lo = __byte_perm(v[0][w], v[1][w], h ? 0x7362 : 0x5140);
+              const uint32_t hi = __byte_perm(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
+              uint32_t a[4];
+              if constexpr (decltype(f16)::value) {
+                ptx::e4m3x4_to_f16x2(lo, a[0], a[1]);
+                ptx::e4m3x4_to_f16x2(hi, a[2], a[3]);
 #pragma unroll
-            for (int x = 0; x < NT; ++x) ptx::mma_16816(acc[2 * w + h][x], a, pf[x][0], pf[x][1]);
-          }
-        }
+                for (int x = 0; x < NT; ++x) ptx::mma_16816_f16(acc[2 * w + h][x], a, pf[x][0], pf[x][1]);
+              } else {
+                a[0] = ptx::e4m3x2_to_bf16x2(lo & 0xffffu);
+                a[1] = ptx::e4m3x2_to_bf16x2(lo >> 16);
+                a[2] = ptx::e4m3x2_to_bf16x2(hi & 0xffffu);
+                a[3] = ptx::e4m3x2_to_bf16x2(hi >> 16);
+#pragma unroll
+                for (int x = 0; x < NT; ++x) ptx::mma_16816(acc[2 * w + h][x], a, pf[x][0], pf[x][1]);
+              }
+            }
+        };
+        if (as_f16) product(std::true_type{});
+        else product(std::false_type{});
       }
     }
   }
@@ -632,6 +692,15 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     for (int e = 0; e < 2; ++e)
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[x][e] += __shfl_xor_sync(kFull, l[x][e], o);
+
+  if constexpr (C::FP8) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][x][e] *= vref * 0.0078125f;
+  }
 
   // ---- The key groups' results meet in shared memory, each group's in the
   // stage it used last (the loader does not fill that one before the next

@@ -464,3 +464,40 @@ def test_rows_on_16_byte_boundaries_only(pkg, fp8):
         R.check_attend(p2, o[..., 8:72], lse, True)
         assert bool((o[..., :8] == 5.0).all()) and bool((o[..., 72:] == 5.0).all())
     pkg.check()
+
+
+@pytest.mark.parametrize("new", [1, 3, 60])
+@pytest.mark.parametrize("spread", ["powers", "any", "growing", "zero_and_negative"])
+def test_attend_e4m3_scales_that_differ(pkg, spread, new):
+    """Value scales over many orders of magnitude, in any order, not only powers
+    of two; zero vectors, zero and negative scales. The chunk kernel (60 rows)
+    may round code * scale to bf16 once more: 2^-8 of every value, and as much
+    of every key, which moves the scores by less than 2^-8 * scale * sum |q k|."""
+    p = R.make([1500, 700], [new] * 2, 4, 1, 64, 16, fp8=True, seed=31)
+    g = torch.Generator().manual_seed(32)
+    for s, c in ((p.k_scale, p.k_cache), (p.v_scale, p.v_cache)):
+        held = ~torch.isnan(s)
+        n = int(held.sum())
+        if spread == "powers":
+            x = torch.exp2(torch.randint(-40, 11, (n,), generator=g).double())
+        elif spread == "any":
+            x = torch.exp2(torch.rand(n, generator=g).double() * 12 - 14) * 1.2345
+        elif spread == "growing":
+            x = torch.exp2(torch.linspace(-30, 5, n).double())
+        else:
+            x = torch.exp2(torch.randint(-8, -4, (n,), generator=g).double()) * torch.randint(-1, 2, (n,), generator=g)
+        if s is p.k_scale:   # scores stay ordinary
+            x = x.sign() * x.abs().clamp(max=2.0 ** -7)
+        s[held] = x.float().cuda()
+    p.v_cache[p.table[0, 3].long(), 5] = 0.0
+    o, lse = pkg.paged_forward(p.q, *p.cache, **p.scales)
+    pkg.check()
+    for b, (ro, rl, ra) in enumerate(R.attend(p, True)):
+        wide = new * 4 > 32 and spread in ("any", "growing")
+        k, _ = R.gather(p, b)
+        q = p.q[b].double()
+        ds = 2.0 ** -8 * 64 ** -0.5 * (q.abs() @ k[:, 0].abs().t()).max().item() if wide else 0.0
+        grow = math.expm1(2 * ds)
+        bound = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14 + (2.0 ** -8 if wide else 0.0) + grow) * ra * (1 + grow) + 1e-6 * ra.max()
+        assert ((o[b].double() - ro).abs() <= bound).all()
+        assert (lse[b].double() - rl).abs().max().item() <= 5e-5 + ds
