@@ -122,7 +122,7 @@ def _link_native(obj: str, force: bool):
     cuda_rt = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "lib64")
     tmp = NATIVE_PATH + ".tmp"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-lattn_fwd", "-Wl,-rpath,$ORIGIN", "-L" + libs,
-           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + libs, "-L" + cuda_rt,
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + libs, "-L" + cuda_rt,
            "-lcudart_static", "-ldl", "-lrt", "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -51,7 +51,7 @@
 //     sequence over its paged cache): a K or V tile is gathered page by page
 //     (one TMA box per page and 64 depth columns, the page numbers looked up
 //     a tile ahead by the producer's lanes), and a 128-row MMA tile packs
-//     2^pack_shift query heads that share the KV head times as many tokens
+//     all (up to 128) query heads that share the KV head times as many tokens
 //     as fill it, so each K/V byte that reaches shared memory serves that many
 //     heads. The causal mask is aligned to the end of the keys. The slots
 //     behind a sequence's last key may hold anything, NaN too: K's are masked
@@ -345,10 +345,10 @@ struct Geo {
 };
 
 template <class T, int CAUSAL>
-__device__ __forceinline__ Geo tile_geo(const SchedSlot& s, uint32_t rank, int pack_shift) {
+__device__ __forceinline__ Geo tile_geo(const SchedSlot& s, uint32_t rank, int pack_tokens) {
   Geo g;
   if constexpr (T::PAGED) {
-    const int tok = kBlockM >> pack_shift;   // tokens of an MMA tile
+    const int tok = pack_tokens;   // tokens of an MMA tile
     g.q0 = s.t * 2 * tok;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -692,7 +692,7 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
     __syncwarp();
     sched.next();
     if (!s.valid) break;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_tokens);
     const int n1 = g.n[1];
     if (n1 > 0) {
       const int hk = s.h / P.group;
@@ -701,9 +701,9 @@ __device__ void role_load_qk(const Tc05Params& P, const Ctx& c) {
         const uint32_t bar = c.bar(BAR_Q_FULL + i);
         const uint32_t dst = c.sbase + T::OFF_Q + i * T::Q_TILE_BYTES;
         const int row = s.q_start + g.row[i];
-        if (lead) ptx::mbar_expect_tx(bar, T::Q_TX);
-        // paged: one box is 2^pack_shift heads of 128 >> pack_shift tokens
-        const int head = T::PAGED ? s.h << P.pack_shift : s.h;
+        // paged: one box is `pack` heads of pack_tokens tokens, 128 rows at most
+        if (lead) ptx::mbar_expect_tx(bar, T::PAGED ? (uint32_t)(P.pack * P.pack_tokens * 128 * T::QK_CHUNKS) : T::Q_TX);
+        const int head = T::PAGED ? s.h * P.pack : s.h;
 #pragma unroll
         for (int ch = 0; ch < T::QK_CHUNKS; ++ch)
           load_box<T>(c, dst + ch * T::CHUNK_BYTES, &P.tm_q, bar, ch * T::QK_CHUNK_ELEMS, head, row, qb);
@@ -834,7 +834,7 @@ __device__ void role_load_v(const Tc05Params& P, const Ctx& c) {
     if (lane == 0) ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) break;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_tokens);
     const int hk = s.h / P.group;
     const int vb = P.packed ? 0 : s.b;
     [[maybe_unused]] int page = -1;
@@ -1015,7 +1015,7 @@ __device__ void role_mma(const Tc05Params& P, const Ctx& c, const int i) {
     ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) break;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_tokens);
     const int n = g.n[i], n1 = g.n[1];
     if (n1 == 0) {
       // No keys: keep the per-tile O-free handshake in step with the epilogue.
@@ -1089,6 +1089,18 @@ __device__ void role_mma(const Tc05Params& P, const Ctx& c, const int i) {
 }
 
 // ---------------------------------------------------------------------------------------------
+// Paged variants: row r of an MMA tile as token and head of the tile; the rows
+// behind pack_tokens * pack belong to nobody.
+struct PackedRow {
+  int tok, h;
+  bool ok;
+  __device__ __forceinline__ PackedRow(const Tc05Params& P, int r) {
+    tok = P.pack > 0 ? r / P.pack : r;
+    h = r - tok * P.pack;
+    ok = tok < P.pack_tokens;
+  }
+};
+
 // Paged variants: LSE element of token qi and query head h.
 __device__ __forceinline__ int64_t paged_lse_index(const Tc05Params& P, const SchedSlot& s, int qi, int h) {
   return P.packed ? (int64_t)h * P.total_q + s.q_start + qi : ((int64_t)s.b * P.heads_total + h) * P.seqlen_q + qi;
@@ -1103,6 +1115,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
   float* rcpl_sm = reinterpret_cast<float*>(c.smem + T::OFF_RCPL) + i * kBlockM;
   float* ks_sm = reinterpret_cast<float*>(c.smem + T::OFF_KS) + i * 2 * kBlockN;
   const int role = i == 0 ? kRoleSoftmax0 : kRoleSoftmax1;
+  [[maybe_unused]] const PackedRow pk(P, tid);
   Ring<2> sched;
   uint32_t s_phase = 0, ks_phase = 0, stats_phase = 0, turn_phase = 0;
   [[maybe_unused]] uint32_t q_phase = 0, sc_tile = 0;   // QSPLIT (sc_tile: key tiles before this work tile's)
@@ -1113,10 +1126,10 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
     ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) return;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_tokens);
     const int n = g.n[i];
-    const int qi = T::PAGED ? g.row[i] + (tid >> P.pack_shift) : g.row[i] + tid;   // row within the sequence
-    const bool row_valid = qi < s.lq;
+    const int qi = T::PAGED ? g.row[i] + pk.tok : g.row[i] + tid;   // row within the sequence
+    const bool row_valid = qi < s.lq && (!T::PAGED || pk.ok);
     // keys of the range visible to this row (causal: keys 0..qi of the
     // sequence, the range starting at key koff of it)
     // (paged: keys 0 .. koff + qi, the range starting at key tile k_start)
@@ -1137,7 +1150,7 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
     const int sp = split_kv ? s.split : 0;
     const bool partial = T::PAGED ? listed<CAUSAL>() && s.split >= 0 : splits_keys<CAUSAL>(P);
     const int64_t lse_idx = T::PAGED ? (partial ? (int64_t)s.split * kRowsPerTile + kBlockM * i + tid
-                                                : paged_lse_index(P, s, qi, (s.h << P.pack_shift) + (tid & ((1 << P.pack_shift) - 1))))
+                                                : paged_lse_index(P, s, qi, s.h * P.pack + pk.h))
                           : P.packed ? ((int64_t)sp * P.heads_q + s.h) * P.total_q + s.q_start + qi
                                      : (((int64_t)sp * P.batch + s.b) * P.heads_q + s.h) * P.seqlen_q + qi;
     float c_row = P.scale_log2;
@@ -1554,8 +1567,9 @@ struct Widen {
 template <class T>
 __device__ __forceinline__ void split_q(const Tc05Params& P, const Ctx& c, const SchedSlot& s, int first, int i) {
   const int r = threadIdx.x & 127;
-  const int tok = first + (r >> P.pack_shift), h = (s.h << P.pack_shift) + (r & ((1 << P.pack_shift) - 1));
-  const bool ok = tok < s.lq;
+  const PackedRow pk(P, r);
+  const int tok = first + pk.tok, h = s.h * P.pack + pk.h;
+  const bool ok = tok < s.lq && pk.ok;
   const uint4* src = reinterpret_cast<const uint4*>(P.q + (P.packed ? 0 : s.b * P.q_b) + (int64_t)(s.q_start + tok) * P.q_t + h * P.q_h);
   uint32_t top = 0u;
 #pragma unroll 4
@@ -1609,6 +1623,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
   const int tid = threadIdx.x - 256;
   const uint32_t lane_base = (uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16;
   const float* rcpl_sm = reinterpret_cast<const float*>(c.smem + T::OFF_RCPL);
+  [[maybe_unused]] const PackedRow pk(P, tid);
   Ring<2> sched;
   uint32_t stats_phase[2] = {0, 0}, ofinal_phase[2] = {0, 0};
   [[maybe_unused]] Widen<T> widen;
@@ -1619,7 +1634,7 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
     ptx::mbar_arrive(c.bar(BAR_SCHED_EMPTY + sched.idx));
     sched.next();
     if (!s.valid) return;
-    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_shift);
+    const Geo g = tile_geo<T, CAUSAL>(s, c.rank, P.pack_tokens);
     if constexpr (T::C8) {
       if (g.n[1] > 0) {
         widen.begin(P, c, s, g.n[1]);
@@ -1640,9 +1655,9 @@ __device__ void role_correction(const Tc05Params& P, const Ctx& c) {
       stats_phase[i] ^= 1u;
       const float rl = rcpl_sm[i * kBlockM + tid];
       ptx::mbar_arrive(c.bar(BAR_STATS_FREE + i));
-      const int qi = T::PAGED ? g.row[i] + (tid >> P.pack_shift) : g.row[i] + tid;
-      const int h = T::PAGED ? (s.h << P.pack_shift) + (tid & ((1 << P.pack_shift) - 1)) : s.h;
-      const bool row_valid = qi < s.lq;
+      const int qi = T::PAGED ? g.row[i] + pk.tok : g.row[i] + tid;
+      const int h = T::PAGED ? s.h * P.pack + pk.h : s.h;
+      const bool row_valid = qi < s.lq && (!T::PAGED || pk.ok);
       const bool partial = T::PAGED ? listed<CAUSAL>() && s.split >= 0 : splits_keys<CAUSAL>(P);
       const int64_t part_at = T::PAGED ? (int64_t)s.split * kRowsPerTile + kBlockM * i + tid : partial_row(P, s, qi);
       uint16_t* orow = P.o + (int64_t)s.b * P.o_stride_b + (int64_t)(s.q_start + qi) * P.o_stride_t +

@@ -105,13 +105,14 @@ struct Tc05Params {
   int32_t kv_tiles;        // split-KV: ceil(seqlen_k / kBlockN)
   float* lse_part;         // split-KV: partial LSE [splits][B][Hq][Sq] / [splits][Hq][Tq]
   float* o_part;           // split-KV: partial O (normalised, fp32) [splits][rows][Hq][Dv]
-  // Paged variants only. heads_q then counts tiles of 2^pack_shift query heads
+  // Paged variants only. heads_q then counts tiles of `pack` query heads
   // that share a KV head, group the tiles of one KV head, rows_per_tile the
   // tokens of a work tile; tm_k / tm_v map (depth, head, slot, page).
   CacheView cache;
   const int32_t* seqlens_k;   // [B] cached keys
   int32_t max_k;           // upper bound of them
-  int32_t pack_shift;      // log2 of the query heads in a tile
+  int32_t pack;            // query heads in a tile (at most 128)
+  int32_t pack_tokens;     // tokens of a 128-row MMA tile, 128 / pack; its rows: token * pack + head
   int32_t heads_total;     // Hq
   const uint8_t* q;        // e4m3 cache: Q itself (split by the kernel), byte strides
   int64_t q_b, q_t, q_h;

@@ -69,7 +69,7 @@ struct StreamParams {
 struct PlanParams {
   NewRows s;
   int32_t heads_kv, group, kv_chunk, tokens, causal, ctas;   // as in Tc05Params (tokens = rows_per_tile)
-  int32_t pack_shift, heads_total;
+  int32_t pack, pack_tokens, heads_total;
   int32_t max_tiles;         // room in the list
   uint32_t* ws;
   PlanHead* head;

@@ -169,13 +169,13 @@ int64_t shared_rows(const attn_paged_params* p) {
 }
 bool use_tc05(const attn_paged_params* p) { return shared_rows(p) > kStreamRows; }
 
-// tcgen05 kernel: query heads packed into a 128-row tile (the largest power of
-// two that divides the group), tokens of a 256-row work tile, and the work
+// tcgen05 kernel: query heads packed into a 128-row tile (the largest divisor of
+// the group up to 128), tokens of such a tile and of a work tile of two, and the work
 // list's memory. Without a list (few keys, where nothing is worth cutting, or
 // so many tiles that their whole number per CTA does not matter) every tile is
 // taken whole.
 struct TilePlan {
-  int pack_shift;
+  int pack, pack_tokens;
   int tokens;
   int64_t work;      // upper bound of the work tiles
   bool list;
@@ -187,12 +187,14 @@ TilePlan plan_tiles(const attn_paged_params* p) {
   TilePlan t = {};
   const attn_kv_cache& c = p->cache;
   const int group = p->num_heads_q / c.num_heads_kv;
-  while (t.pack_shift < 7 && group % (2 << t.pack_shift) == 0) ++t.pack_shift;
-  t.tokens = af::kRowsPerTile >> t.pack_shift;
+  t.pack = group < af::kBlockM ? group : af::kBlockM;
+  while (group % t.pack) --t.pack;
+  t.pack_tokens = af::kBlockM / t.pack;
+  t.tokens = 2 * t.pack_tokens;
   int64_t token_tiles = (int64_t)c.batch * af::tiles_for(p->seqlen_q, t.tokens);
   if (p->cu_seqlens_q != nullptr && p->total_q / t.tokens + c.batch < token_tiles)
     token_tiles = p->total_q / t.tokens + c.batch;
-  t.work = token_tiles * (p->num_heads_q >> t.pack_shift);
+  t.work = token_tiles * (p->num_heads_q / t.pack);
   t.list = af::tiles_for(p->seqlen_k, af::kBlockN) > af::kListTiles && t.work <= af::kPlanMaxTiles &&
            c.batch <= af::kPlanMaxBatch;
   if (t.list) {
@@ -257,7 +259,6 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   const TilePlan plan = plan_tiles(p);
   const attn_kv_cache& c = p->cache;
   const bool packed = p->cu_seqlens_q != nullptr;
-  const int pack = 1 << plan.pack_shift;
   af::Tc05Params prm;
   memset(&prm, 0, sizeof(prm));
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -266,7 +267,7 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   attn_status st = af::encode_map(
       &prm.tm_q, bf16, p->q, {c.head_dim, p->num_heads_q, q_tokens, q_batches},
       {legal(p->q_stride[2] * 2, p->num_heads_q), legal(p->q_stride[1] * 2, q_tokens), legal(p->q_stride[0] * 2, q_batches)},
-      {64, pack, af::kBlockM / pack, 1});
+      {64, plan.pack, plan.pack_tokens, 1});
   if (st != ATTN_OK) return st;
   const bool fp8 = c.dtype == ATTN_DTYPE_FP8_E4M3;
   // (of an e4m3 cache only K with D = 128 is read through a map)
@@ -295,7 +296,7 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   prm.batch = c.batch;
   prm.seqlen_q = p->seqlen_q;
   prm.seqlen_k = p->seqlen_k;
-  prm.heads_q = p->num_heads_q >> plan.pack_shift;
+  prm.heads_q = p->num_heads_q / plan.pack;
   prm.heads_kv = c.num_heads_kv;
   prm.group = prm.heads_q / c.num_heads_kv;
   prm.rows_per_tile = plan.tokens;
@@ -310,7 +311,8 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   prm.cache = view_of(c);
   prm.seqlens_k = p->seqlens_k;
   prm.max_k = p->seqlen_k;
-  prm.pack_shift = plan.pack_shift;
+  prm.pack = plan.pack;
+  prm.pack_tokens = plan.pack_tokens;
   prm.heads_total = p->num_heads_q;
   const int sms = af::sm_count();
   const int64_t most = plan.list ? plan.work + plan.max_pieces : plan.work;
@@ -330,7 +332,8 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
     pp.tokens = plan.tokens;
     pp.causal = p->causal != 0;
     pp.ctas = grid;
-    pp.pack_shift = plan.pack_shift;
+    pp.pack = plan.pack;
+    pp.pack_tokens = plan.pack_tokens;
     pp.heads_total = p->num_heads_q;
     pp.max_tiles = (int32_t)plan.work;
     pp.ws = prm.ws;

@@ -203,9 +203,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_tile_merge_kernel(cons
   const PlanCut c = P.cuts[blockIdx.x];
   if (c.parts < 2) return;
   const int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int tok = c.item.t * P.tokens + (row >> P.pack_shift);
+  const int r = row & (kBlockM - 1), in_tile = r / P.pack;   // row of its MMA tile, its token
+  const int tok = c.item.t * P.tokens + (row / kBlockM) * P.pack_tokens + in_tile;
+  if (in_tile >= P.pack_tokens) return;
   if (tok >= c.item.lq) return;
-  const int h = (c.item.h << P.pack_shift) + (row & ((1 << P.pack_shift) - 1));
+  const int h = c.item.h * P.pack + (r - in_tile * P.pack);
   const int64_t at = (int64_t)c.item.slot * kRowsPerTile + row;
   float mx = -INFINITY;
   for (int p = lane; p < c.parts; p += 32) mx = fmaxf(mx, P.lse_part[at + (int64_t)p * kRowsPerTile]);

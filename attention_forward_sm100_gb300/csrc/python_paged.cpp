@@ -9,7 +9,7 @@
 // int if the call was refused there. Bad arguments raise ValueError before
 // anything is allocated or enqueued.
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -76,6 +76,11 @@ int64_t integer(const char* name, PyObject* o) {
     need_f(false, "%s must be an integer", name);
   }
   return v;
+}
+
+// Uninitialised memory from torch's allocator (not through the dispatcher).
+at::Tensor fresh(at::IntArrayRef sizes, at::ScalarType type, c10::DeviceIndex device) {
+  return at::Tensor(at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, device), c10::nullopt));
 }
 
 bool is(const Arg& a, at::ScalarType t) { return a->scalar_type() == t; }
@@ -164,21 +169,20 @@ Buffers& buffers() {
 // A captured call gets its own from the graph's memory, so that graphs do
 // not share one either.
 at::Tensor workspace_for(c10::DeviceIndex device, cudaStream_t stream, int64_t bytes) {
-  const auto options = at::TensorOptions().dtype(at::kByte).device(c10::Device(c10::kCUDA, device));
   const bool capturing =
       c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
   at::Tensor* kept = capturing ? nullptr : &buffers()[{device, stream}];
   if (kept != nullptr && kept->defined() && kept->numel() >= bytes) return *kept;
   const int64_t zeroed = ATTN_PAGED_ZEROED_BYTES;
-  at::Tensor fresh = at::empty({std::max(bytes, zeroed)}, options);
+  at::Tensor grown = fresh({std::max(bytes, zeroed)}, at::kByte, device);
   cudaError_t e;
   if (kept != nullptr && kept->defined())   // an error that nobody has read yet moves with it
-    e = cudaMemcpyAsync(fresh.data_ptr(), kept->data_ptr(), zeroed, cudaMemcpyDeviceToDevice, stream);
+    e = cudaMemcpyAsync(grown.data_ptr(), kept->data_ptr(), zeroed, cudaMemcpyDeviceToDevice, stream);
   else
-    e = cudaMemsetAsync(fresh.data_ptr(), 0, zeroed, stream);
+    e = cudaMemsetAsync(grown.data_ptr(), 0, zeroed, stream);
   if (e != cudaSuccess) throw std::runtime_error(std::string("workspace: ") + cudaGetErrorString(e));
-  if (kept != nullptr) *kept = fresh;
-  return fresh;
+  if (kept != nullptr) *kept = grown;
+  return grown;
 }
 
 PyObject* status(attn_status st) { return PyLong_FromLong(st); }
@@ -285,9 +289,8 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
   at::Tensor fresh_k, fresh_v, own;
   if (!ok) {
-    const auto options = kc->options().dtype(at::kBFloat16);
-    fresh_k = at::empty({total, heads, dim}, options);
-    fresh_v = at::empty({total, heads, dim}, options);
+    fresh_k = fresh({total, heads, dim}, at::kBFloat16, device);
+    fresh_v = fresh({total, heads, dim}, at::kBFloat16, device);
   }
   const Arg k = {"out_k", ok ? ok.t : &fresh_k}, v = {"out_v", ov ? ov.t : &fresh_v};
   if (!ws) own = workspace_for(device, stream, ATTN_PAGED_ZEROED_BYTES);
@@ -366,8 +369,8 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
   at::Tensor fresh_o, fresh_l, own;
-  if (!out) fresh_o = at::empty(q->sizes(), q->options());
-  if (!lse && want_lse) fresh_l = at::empty(lse_sizes, q->options().dtype(at::kFloat));
+  if (!out) fresh_o = fresh(q->sizes(), at::kBFloat16, device);
+  if (!lse && want_lse) fresh_l = fresh(lse_sizes, at::kFloat, device);
   const Arg o = {"out", out ? out.t : &fresh_o};
   p.q = q.ptr();
   p.o = o.ptr();

@@ -129,6 +129,10 @@ ATTEND = {
     "chunk_late": ([3000], [200], 8, 1, 128, 128, False, False),
     "chunk_more_new_than_cached": ([150, 300, 1], [300] * 3, 4, 2, 128, 16, False, False),
     "many_sequences": ([1 + 13 * b % 700 for b in range(150)], [1] * 150, 4, 2, 64, 16, False, False),
+    "chunk_group_5": ([200, 333], [55, 55], 10, 2, 128, 16, False, False),
+    "chunk_group_7": ([90, 20, 400], [90, 0, 31], 7, 1, 64, 32, True, False),
+    "chunk_group_130": ([150], [3], 130, 1, 128, 64, False, False),
+    "chunk_group_12": ([700, 100], [23, 23], 24, 2, 64, 16, False, True),
     "large_page": ([5000, 1], [2, 2], 8, 8, 128, 4096, False, False),
 }
 
