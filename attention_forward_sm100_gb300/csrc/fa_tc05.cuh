@@ -1431,11 +1431,16 @@ struct Widen {
     uint32_t y[8];
     const uint64_t s2 = ptx::f2_pack(scale, scale);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float lo, hi;
-      ptx::e4m3x2_to_float2((e & 1) ? x[e >> 1] >> 16 : x[e >> 1] & 0xffffu, lo, hi);
-      ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(lo, hi), s2), lo, hi);
-      y[e] = ptx::pack_bf16(lo, hi);
+    for (int e = 0; e < 8; e += 2) {
+      uint32_t h[2];
+      ptx::e4m3x4_to_f16x2(x[e >> 1], h[0], h[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float lo, hi;
+        ptx::f16x2_to_float2(h[k], lo, hi);
+        ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(lo, hi), s2), lo, hi);
+        y[e + k] = ptx::pack_bf16(lo, hi);
+      }
     }
     ptx::st_shared_v4(a, y[0], y[1], y[2], y[3]);
     ptx::st_shared_v4(a ^ 16u, y[4], y[5], y[6], y[7]);

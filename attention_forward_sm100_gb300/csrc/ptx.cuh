@@ -469,6 +469,14 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t four, uint32_t& lo, uin
       : "=r"(lo), "=r"(hi)
       : "r"(four));
 }
+__device__ __forceinline__ void f16x2_to_float2(uint32_t two, float& lo, float& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.f32.f16 %0, a;\n\t"
+      "cvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(two));
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
