@@ -103,6 +103,8 @@ attn_status check_append(const attn_cache_append_params* p) {
   if (st != ATTN_OK) return st;
   if (p->seqlen_q < 0 || p->total_q < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative size");
   const bool packed = p->cu_seqlens_q != nullptr;
+  if (!packed && (int64_t)p->cache.batch * p->seqlen_q > 0x7fffffffll)
+    return report_error(ATTN_ERR_UNSUPPORTED, "more than 2^31 new tokens");
   if (p->cache.batch == 0 || (packed ? p->total_q : p->seqlen_q) == 0) return ATTN_OK;
   if ((st = check_rows("k", p->k, p->k_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
   if ((st = check_rows("v", p->v, p->v_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;

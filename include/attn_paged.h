@@ -25,8 +25,11 @@
  *             O_i   = sum_{j in J_i} exp(s_ij - LSE_i) * V_j     bf16, rounded once
  *           (the causal mask is aligned to the END of the keys: the new
  *           tokens are the last ones cached). The weights are rounded to bf16
- *           before the P.V product, as in attn_fwd; sums and the softmax
- *           statistics are fp32. Rows with an empty J_i get O_i = 0 and
+ *           before the P.V product, as in attn_fwd (to f16 where an e4m3 cache
+ *           allows); sums and the softmax statistics are fp32. From 33 rows
+ *           (Lq_b * Hq / Hkv) on, code * scale of an e4m3 V, and with D = 64 of K
+ *           too, is rounded to bf16 once, which changes nothing when scales are
+ *           powers of two, as append's are. Rows with an empty J_i get O_i = 0 and
  *           LSE_i = -inf. Slots at or past position Lk_b are never used, they
  *           may hold anything; cached values in front of Lk_b that the causal
  *           mask hides must be finite (their weight is zero).
@@ -60,7 +63,8 @@ typedef struct attn_kv_cache {
   float *v_scale;
   const int32_t *block_table; /* [B][max_pages], row stride table_stride, entries contiguous */
   int64_t k_stride[3];        /* elements: [0] page, [1] token, [2] head; depth contiguous;
-                                 multiples of 16 bytes */
+                                 multiples of 16 bytes, positive where the dimension is
+                                 larger than 1 */
   int64_t v_stride[3];
   int64_t table_stride;       /* elements between the rows of block_table */
   int32_t dtype;              /* attn_dtype of k and v */

@@ -383,6 +383,9 @@ def test_two_streams_at_once(pkg):
         assert torch.equal(R.bits(o), R.bits(wo)) and torch.equal(R.bits(l), R.bits(wl))
     for s in streams:
         pkg.check(stream=s)
+    o, l = pkg.paged_forward(ps[0].q, *ps[0].cache, stream=streams[1].cuda_stream)   # a bare handle
+    pkg.check(stream=streams[1])
+    assert torch.equal(R.bits(o), R.bits(want[0][0])) and torch.equal(R.bits(l), R.bits(want[0][1]))
 
 
 def test_own_workspace(pkg):

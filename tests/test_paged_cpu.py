@@ -6,7 +6,9 @@ import ctypes
 import math
 import os
 import re
+import shutil
 import struct
+import subprocess
 
 import pytest
 import torch
@@ -53,6 +55,34 @@ def test_struct_layouts(pkg):
     L = _library(pkg)
     L.attn_paged_params_size.restype = ctypes.c_size_t
     assert [L.attn_paged_params_size(i) for i in range(4)] == [APPEND.size, READ.size, PAGED.size, 0]
+
+
+def test_header_compiles_as_c(pkg, tmp_path):
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, exe = tmp_path / "paged.c", str(tmp_path / "paged")
+    src.write_text("""
+#include "attn_paged.h"
+#include <stdio.h>
+int main(void) {
+  attn_paged_params p = {0};
+  p.cache.page_size = 16;
+  if (attn_paged_fwd(&p, 0) != ATTN_ERR_INVALID_ARG || attn_fwd_last_error()[0] == 0) return 1;
+  if (attn_paged_workspace_bytes(&p) != ATTN_PAGED_ZEROED_BYTES) return 2;
+  if (attn_cache_append(0, 0) != ATTN_ERR_INVALID_ARG || attn_cache_read(0, 0) != ATTN_ERR_INVALID_ARG) return 3;
+  if (attn_paged_params_size(2) != sizeof(attn_paged_params)) return 4;
+  puts("ok");
+  return 0;
+}
+""")
+    lib = os.path.join(ROOT, "attention_forward_sm100_gb300")
+    cmd = [cc, "-std=c99", "-Wall", "-Wextra", "-Wno-missing-field-initializers", "-Wno-missing-braces", "-Werror",
+           "-pedantic", "-I", os.path.join(ROOT, "include"), str(src), "-L", lib, "-lattn_fwd", "-Wl,-rpath," + lib, "-o", exe]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok"
 
 
 def _problem(**kw):
@@ -185,6 +215,12 @@ PAGED_ERRORS = [(dict(q=0), 1), (dict(o=(5 << 20) + 2), 1), (dict(seqlens=0), 1)
                 (dict(ws=0), 1), (dict(ws=(8 << 20) + 16), 1), (dict(ws_bytes=100), 1), (dict(hq=3), 1), (dict(hq=0), 1),
                 (dict(scale=0.0), 1), (dict(scale=math.nan), 1), (dict(seqlen_k=129), 1), (dict(seqlen_q=-1), 1),
                 (dict(q_stride=(256, 250, 64)), 1), (dict(o_stride=(256, 256, 60)), 1), (dict(cu=(9 << 20) + 2, total_q=2), 1)]
+
+
+def test_library_refuses_too_many_new_tokens(pkg):
+    L = _library(pkg)
+    p = APPEND.pack(*_cache(batch=1 << 16), 4 << 20, 5 << 20, 6 << 20, 0, 7 << 20, *(128, 128, 64) * 2, 1 << 16, 0)
+    assert L.attn_cache_append(p, None) == 2
 
 
 @pytest.mark.parametrize("change,status", PAGED_ERRORS, ids=[str(c[0]) for c in PAGED_ERRORS])
