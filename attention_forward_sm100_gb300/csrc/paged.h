@@ -57,6 +57,7 @@ struct StreamParams {
   float* lse;
   int64_t o_b, o_t, o_h;     // elements
   int32_t heads_q, group, causal;
+  int32_t team, team_heads;  // CTAs of a team (the grid is a multiple), KV heads of a member
   int32_t split;             // 1: units are key tiles, segments may span CTAs; 0: units are segments
   float scale_log2;
   uint32_t* ws;

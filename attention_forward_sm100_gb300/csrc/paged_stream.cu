@@ -7,7 +7,8 @@
 // the tensor cores idle. So the kernel is built around the loads:
 //   * the work is the list of all key tiles (64 or 128 keys) of all (sequence,
 //     KV head, row tile) segments, cut into equal contiguous parts, one per CTA
-//     (two CTAs per SM). Lengths are read on the device, so ragged batches
+//     (two CTAs per SM; CTAs of a team share a cut and differ in the head, for
+//     HBM's sake: 182 -> 171 us, e4m3 125 -> 106 at the sizes of kMaxTeam). Lengths are read on the device, so ragged batches
 //     balance without the host knowing them and a captured call follows lengths
 //     that change;
 //   * a CTA streams its tiles through a ring of cp.async stages (about 96 KB),
@@ -91,7 +92,18 @@ struct Cfg {
   __device__ static int swz_v(int r, int c) { return FP8 && CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); }
 };
 
-// Work units of sequence b: row tiles * KV heads * (key tiles, or 1 unsplit).
+// The CTAs work in teams of P.team neighbours, and the cut of the work is one for
+// all members of a team: member i takes KV heads i, i + team, ... (head_of), so
+// the members read the same keys' rows, adjacent in memory, at about the same time.
+__device__ __forceinline__ int head_of(const StreamParams& P, int seg) {
+  return seg % P.team_heads * P.team + (int)blockIdx.x % P.team;
+}
+__device__ __forceinline__ int row_tile_of(const StreamParams& P, int seg) { return seg / P.team_heads; }
+// CTA of this member in team `c`.
+__device__ __forceinline__ int cta_of(const StreamParams& P, int c) { return c * P.team + (int)blockIdx.x % P.team; }
+
+// A member's work units of sequence b: row tiles * its KV heads * (key tiles, or 1
+// unsplit).
 struct SeqUnits {
   SeqRows r;
   int row_tiles, tiles, units;
@@ -103,13 +115,13 @@ __device__ __forceinline__ SeqUnits seq_units(const StreamParams& P, int b) {
   u.r = load_seq(P.s, b, P.ws);
   u.row_tiles = (int)(((int64_t)u.r.lq * P.group + C::RT - 1) / C::RT);
   u.tiles = P.split ? max(1, (u.r.lk + C::TILE - 1) / C::TILE) : 1;
-  u.units = u.row_tiles * P.c.heads_kv * u.tiles;
+  u.units = u.row_tiles * P.team_heads * u.tiles;
   return u;
 }
 
 // One contiguous part of a segment.
 struct Piece {
-  int b, seg;            // seg = row tile * Hkv + KV head
+  int b, seg;            // seg = row tile * team_heads + the member's how-manieth KV head
   int first, count;      // unit range within the segment
   int tiles;             // units of the segment
 };
@@ -224,7 +236,7 @@ struct Loader {
       int t0;
       piece_tiles<C>(P, pc, s, t0, left);
       b = pc.b;
-      hk = pc.seg % P.c.heads_kv;
+      hk = head_of(P, pc.seg);
       lk = s.lk;
       key0 = t0 * C::TILE + kg * C::KW;
     }
@@ -278,13 +290,14 @@ struct Loader {
   }
 };
 
-// Joining the parts of a segment that several CTAs hold, CTAs c0 .. last. Each
+// Joining the parts of a segment that several CTAs hold, the same member of
+// teams c0 .. last. Each
 // leaves its part (accumulator, maximum, sum) in the workspace and counts
 // itself in; the last of every kJoin neighbours joins theirs into the first
 // one's, the last of those neighbourhoods joins what is left and finishes the
 // rows. Nobody waits, and the parts are summed in the order of their CTAs
 // whoever sums them. Slot 2 c + 1 is the part of the segment that starts in CTA
-// c and goes on, slot 2 c that of the one that comes from an earlier CTA.
+// c and goes on, slot 2 c that of the one that comes from an earlier team.
 constexpr int kJoin = 16;
 
 // Whether this CTA is the last of `want` to count itself in (and leaves the
@@ -365,7 +378,7 @@ __device__ __forceinline__ void join_parts(const StreamParams& P, int n, int val
   }
 }
 
-// `first`: the unit at which this CTA's piece starts, `per` the units of a CTA.
+// `first`: the unit at which this CTA's piece starts, `per` the units of every CTA.
 template <class C>
 __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, uint8_t* smem, Loader<C>& load,
                           int& count, int first, int per) {
@@ -374,7 +387,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   const int g = lane >> 2, t = lane & 3;
   const int wm = warp % WM, kg = warp / WM;
   const int gt = wm * 32 + lane;                  // thread within its key group
-  const int hk = pc.seg % P.c.heads_kv, rt = pc.seg / P.c.heads_kv;
+  const int hk = head_of(P, pc.seg), rt = row_tile_of(P, pc.seg);
   const int rows = s.lq * P.group;
   const uint32_t ring = ptx::smem_u32(smem) + kg * (C::STAGES * C::STAGE);
   int t0, n;
@@ -777,14 +790,14 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     return;
   }
   const int start = first - pc.first, c0 = start / per, parts = (start + pc.tiles - 1) / per - c0 + 1;
-  const int hood = ((int)blockIdx.x - c0) / kJoin, in_hood = min(kJoin, parts - kJoin * hood);
+  const int hood = ((int)blockIdx.x / P.team - c0) / kJoin, in_hood = min(kJoin, parts - kJoin * hood);
   const int hoods = (parts + kJoin - 1) / kJoin;
   // counters: [0] a segment's first neighbourhood by its first CTA, [1] others
   // by theirs, [2] neighbourhoods by the segment's first CTA
   uint32_t* const counters = P.counters;
   const int grid = gridDim.x;
-  auto slot_in_hood = [&](int i) { return 2 * (int64_t)(c0 + kJoin * hood + i) + (hood == 0 && i == 0 ? 1 : 0); };
-  if (!count_in(counters + (hood == 0 ? c0 : grid + c0 + kJoin * hood), in_hood)) return;
+  auto slot_in_hood = [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * hood + i) + (hood == 0 && i == 0 ? 1 : 0); };
+  if (!count_in(counters + (hood == 0 ? 0 : grid) + cta_of(P, c0 + kJoin * hood), in_hood)) return;
   if (hoods == 1) {
     join_parts<C>(P, in_hood, valid, slot_in_hood, finish_row);
     return;
@@ -804,8 +817,8 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     const int x = threadIdx.x + i * kThreads;
     if (x < valid * (D / 4) && x % (D / 4) == 0) P.part_ml[slot_in_hood(0) * C::RT + x / (D / 4)] = kept[i];
   }
-  if (!count_in(counters + 2 * grid + c0, hoods)) return;
-  join_parts<C>(P, hoods, valid, [&](int i) { return 2 * (int64_t)(c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish_row);
+  if (!count_in(counters + 2 * grid + cta_of(P, c0), hoods)) return;
+  join_parts<C>(P, hoods, valid, [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish_row);
 }
 
 template <int D, bool FP8, int NT, int WM>
@@ -816,8 +829,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_stream_kernel(const __grid_
   ptx::launch_dependents();
   Loader<C> load;
   const int total = load.walk.start(P);
-  const int per = (total + gridDim.x - 1) / (int)gridDim.x;
-  int x = min(total, (int)blockIdx.x * per);
+  const int teams = (int)gridDim.x / P.team;
+  const int per = (total + teams - 1) / teams;
+  int x = min(total, (int)blockIdx.x / P.team * per);
   const int end = min(total, x + per);
   if (x >= end) return;
   // Fill the ring, then run the pieces; the loader stays STAGES - 1 tiles ahead.

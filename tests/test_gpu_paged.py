@@ -161,6 +161,21 @@ def test_attend_long_context_of_few_rows(pkg, fp8):
     R.check_attend(p, o, lse, True)
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("lens_k,hkv,group,new,dim", [
+    ([9000, 1], 32, 1, 1, 64),              # a CTA has more heads than one
+    ([5000, 700, 2600], 12, 2, 3, 128),     # a grid that the heads do not divide
+    ([4000, 0, 3000], 17, 1, 1, 128),       # no divisor
+    ([40000], 6, 16, 2, 128),               # segments cut into many parts, 32 rows
+    ([30000, 20000], 2, 24, 1, 64)])        # row tiles and heads
+def test_attend_many_kv_heads(pkg, lens_k, hkv, group, new, dim, fp8):
+    """How heads are dealt to CTAs, and who joins the parts of which segment."""
+    p = R.make(lens_k, [min(new, n) for n in lens_k], hkv * group, hkv, dim, 32, fp8=fp8, packed=True, seed=31)
+    o, lse = pkg.paged_forward(p.q, *p.cache, cu_seqlens_q=p.cu_q, max_seqlen_q=new, **p.scales)
+    pkg.check()
+    R.check_attend(p, o, lse, True)
+
+
 def test_attend_large_scores(pkg):
     """Scores of both signs in the thousands: the running maximum has to move
     and no exponential may overflow. (The reference bound for LSE assumes
