@@ -102,17 +102,28 @@ struct SeqRows {
   int lq, lk, q0;   // new rows, cached keys, first row (packed) or 0
 };
 
+struct SeqRaw {
+  int lk, a, e;     // as the tensors have them: cached keys, row offsets (packed)
+};
+__device__ __forceinline__ SeqRaw load_seq_raw(const NewRows& s, int b) {
+  SeqRaw w = {s.seqlens_k[b], 0, 0};
+  if (s.cu_q != nullptr) {
+    w.a = s.cu_q[b];
+    w.e = s.cu_q[b + 1];
+  }
+  return w;
+}
 // Lengths of sequence b; out of range ones are recorded and cut to what the
 // tensors hold.
-__device__ __forceinline__ SeqRows load_seq(const NewRows& s, int b, uint32_t* ws) {
+__device__ __forceinline__ SeqRows checked_seq(const NewRows& s, const SeqRaw& w, int b, uint32_t* ws) {
   SeqRows r;
-  r.lk = s.seqlens_k[b];
+  r.lk = w.lk;
   r.lq = s.seqlen_q;
   r.q0 = 0;
   bool bad = r.lk < 0 || r.lk > s.max_k;
   if (bad) r.lk = r.lk < 0 ? 0 : s.max_k;
   if (s.cu_q != nullptr) {
-    const int a = s.cu_q[b], e = s.cu_q[b + 1];
+    const int a = w.a, e = w.e;
     r.q0 = a;
     r.lq = e - a;
     if (a < 0 || e < a || e > s.total_q) {
@@ -125,6 +136,9 @@ __device__ __forceinline__ SeqRows load_seq(const NewRows& s, int b, uint32_t* w
   }
   if (bad) record_bad_cache(ws, b);
   return r;
+}
+__device__ __forceinline__ SeqRows load_seq(const NewRows& s, int b, uint32_t* ws) {
+  return checked_seq(s, load_seq_raw(s, b), b, ws);
 }
 
 // A page number of sequence b's table row; one outside the cache is recorded

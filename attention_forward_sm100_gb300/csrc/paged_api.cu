@@ -163,8 +163,8 @@ constexpr int64_t kMaxStreamCtas = (kZeroedBytes - ATTN_FWD_WORKSPACE_BYTES) / 1
 // while R is small. Measured on both (us, streaming / tcgen05; 64 sequences of up
 // to 8192 keys in bf16, 16 of up to 32768 in e4m3, GQA 32/8, d128):
 //   R      4          16         32         48         64         128
-//   bf16   178 / -    193 / 234  212 / 236  306 / 239  320 / 241  610 / 249
-//   e4m3   109 / 342             230 / 344             421 / 347  806 / 354
+//   bf16   171 / 218  179 / 220  192 / 220  350 / 222  356 / 224  686 / 228
+//   e4m3   106 / 323  117 / 332  201 / 335  371 / 341  373 / 343  731 / 351
 constexpr int kStreamRows = 32;
 int64_t shared_rows(const attn_paged_params* p) {
   return (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
@@ -225,8 +225,13 @@ struct StreamPlan {
 
 // Row tiles of 8, 16 or 32 rows, the smallest that holds a sequence's rows;
 // two CTAs per SM. Segments of up to kUnsplitTiles key tiles are not cut: the
-// merge would cost more than the longer CTA.
+// join would cost more than the longer CTA. Nor are those of up to kUnsplitKeys
+// keys if they are at least a quarter as many as the CTAs and at most twice. GQA
+// 32/8, d128: 12 sequences of up to 300 keys, bf16: 12.8 us cut, 7.0 whole; 32 sequences of up to 1000 keys, bf16 22.7 us cut, 17.5 whole, e4m3 21.2 and
+// 14.9; 8 sequences 13.7 and 13.6; 75 sequences 36.7 and 34.6; but 3 sequences 9.1
+// and 12.3, 256 sequences 94 and 112.
 constexpr int kUnsplitTiles = 4;
+constexpr int kUnsplitKeys = 1024;
 // Of cut segments, the CTAs of a team take different heads of the same keys, so
 // that what HBM is asked for at one time lies together; unteamed, CTAs read
 // strided rows of one head each. The team is the largest divisor of Hkv up to 16
@@ -244,10 +249,11 @@ StreamPlan plan_stream(const attn_paged_params* p) {
   const int row_bytes = p->cache.head_dim * (p->cache.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2);
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
   const int64_t tiles = af::tiles_for(p->seqlen_k, af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
-  s.split = tiles > kUnsplitTiles ? 1 : 0;
-  s.units = segments * (s.split ? tiles : 1);
   const int64_t ctas = 2ll * af::sm_count();
-  const int64_t most = s.split ? (ctas < kMaxStreamCtas ? ctas : kMaxStreamCtas) : s.units;
+  const bool one_wave = 4 * segments >= ctas && segments <= 2 * ctas;
+  s.split = tiles > kUnsplitTiles && !(one_wave && p->seqlen_k <= kUnsplitKeys) ? 1 : 0;
+  s.units = segments * (s.split ? tiles : 1);
+  const int64_t most = ctas < kMaxStreamCtas ? ctas : kMaxStreamCtas;
   s.grid = s.units < most ? s.units : most;
   s.team = 1;
   if (s.split) {

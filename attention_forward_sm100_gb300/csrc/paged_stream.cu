@@ -11,6 +11,9 @@
 //     HBM's sake: 182 -> 171 us, e4m3 125 -> 106 at the sizes of kMaxTeam). Lengths are read on the device, so ragged batches
 //     balance without the host knowing them and a captured call follows lengths
 //     that change;
+//   * q of the next segment is loaded while one is finished (256 sequences of up
+//     to 250 keys: 40.5 -> 38.9 us; with the lengths' sums below and two CTAs per SM
+//     for short segments too, 59 at first);
 //   * a CTA streams its tiles through a ring of cp.async stages (about 96 KB),
 //     across segments: while one is finished, the next one's tiles are loading.
 //     A row tile is 8, 16 or 32 rows; the four warps form four key groups, each
@@ -110,9 +113,9 @@ struct SeqUnits {
 };
 
 template <class C>
-__device__ __forceinline__ SeqUnits seq_units(const StreamParams& P, int b) {
+__device__ __forceinline__ SeqUnits seq_units(const StreamParams& P, const SeqRaw& raw, int b) {
   SeqUnits u;
-  u.r = load_seq(P.s, b, P.ws);
+  u.r = checked_seq(P.s, raw, b, P.ws);
   u.row_tiles = (int)(((int64_t)u.r.lq * P.group + C::RT - 1) / C::RT);
   u.tiles = P.split ? max(1, (u.r.lk + C::TILE - 1) / C::TILE) : 1;
   u.units = u.row_tiles * P.team_heads * u.tiles;
@@ -126,42 +129,99 @@ struct Piece {
   int tiles;             // units of the segment
 };
 
-// Finds pieces in order. Lane i holds sequence b + i of the current window of 32.
+// Inclusive sums over the lanes.
+__device__ __forceinline__ int scan(int v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(kFull, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += n;
+  }
+  return v;
+}
+
+// Finds pieces in order. Lane i holds sequence b + i of the current window of 32
+// and the sums of up to 32 windows, so that a CTA's first sequence, and the next
+// window, are one load away (one window after another, a CTA at the end of 256
+// sequences spent 4 us to get there).
 template <class C>
 struct Walker {
   SeqUnits u;
   int incl;              // units of the window's sequences up to and including this lane's
   int b, base;           // first sequence of the window, units in front of it
+  int span, span_base;   // first sequence of these windows (1024 sequences), units in front of it
+  int wincl;             // units of their windows up to and including this lane's
 
-  __device__ __forceinline__ void window(const StreamParams& P, int first) {
+  // Sums of the windows from sequence `first` on, the lengths of AHEAD windows
+  // being loaded at once; returns their units.
+  template <int AHEAD>
+  __device__ __forceinline__ int windows(const StreamParams& P, int first) {
+    const int lane = threadIdx.x & 31;
+    int mine = 0;
+    span = first;
+#pragma unroll 1
+    for (int w0 = 0; w0 < 32 && first + 32 * w0 < P.s.batch; w0 += AHEAD) {
+      SeqRaw raw[AHEAD];
+#pragma unroll
+      for (int y = 0; y < AHEAD; ++y) {
+        const int c = first + 32 * (w0 + y) + lane;
+        raw[y] = {0, 0, 0};
+        if (c < P.s.batch) raw[y] = load_seq_raw(P.s, c);
+      }
+#pragma unroll
+      for (int y = 0; y < AHEAD; ++y) {
+        const int c = first + 32 * (w0 + y) + lane;
+        const int n = __reduce_add_sync(kFull, c < P.s.batch ? seq_units<C>(P, raw[y], c).units : 0);
+        if (lane == w0 + y) mine = n;
+      }
+    }
+    wincl = scan(mine);
+    return __shfl_sync(kFull, wincl, 31);
+  }
+  // To the window of sequence `first`, `before` units in front of it.
+  __device__ __forceinline__ void window(const StreamParams& P, int first, int before) {
+    const int c = first + (threadIdx.x & 31);
     b = first;
+    base = before;
     u.r = {0, 0, 0};
     u.tiles = 1;
     u.units = 0;
-    const int lane = threadIdx.x & 31;
-    if (b + lane < P.s.batch) u = seq_units<C>(P, b + lane);
-    incl = u.units;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += n;
-    }
+    if (c < P.s.batch) u = seq_units<C>(P, load_seq_raw(P.s, c), c);
+    incl = scan(u.units);
   }
-  // To the first sequence; returns the units of all of them.
+  // To the beginning; returns the units of all sequences.
   __device__ __forceinline__ int start(const StreamParams& P) {
+    if (P.s.batch <= 32) {   // (one window)
+      window(P, 0, 0);
+      span = span_base = 0;
+      wincl = __shfl_sync(kFull, incl, 31);
+      return wincl;
+    }
     int n = 0;
-    for (int c = 32 + (threadIdx.x & 31); c < P.s.batch; c += 32) n += seq_units<C>(P, c).units;
-    window(P, 0);
-    base = 0;
-    return __reduce_add_sync(kFull, n + u.units);
+#pragma unroll 1
+    for (int c = 1024; c < P.s.batch; c += 1024) n += windows<8>(P, c);
+    n += windows<8>(P, 0);
+    span_base = 0;
+    return n;
+  }
+  // To the window that holds unit x, which is not in front of these windows (at
+  // the end of all units: to the last window).
+  __device__ __forceinline__ void seek(const StreamParams& P, int x) {
+    unsigned hit = __ballot_sync(kFull, x < span_base + wincl);
+    while (hit == 0u && span + 1024 < P.s.batch) {
+      span_base += __shfl_sync(kFull, wincl, 31);
+      windows<1>(P, span + 1024);   // (1: this code is part of the loops)
+      hit = __ballot_sync(kFull, x < span_base + wincl);
+    }
+    const int w = hit ? __ffs(hit) - 1 : 31;
+    const int before = __shfl_sync(kFull, wincl, max(w - 1, 0));
+    window(P, span + 32 * w, span_base + (w ? before : 0));
   }
   // Piece that holds unit x, cut at `end`. All lanes of the warp; x increases
   // and is in front of the last unit.
   __device__ __forceinline__ Piece at(const StreamParams& P, int x, int end, SeqRows& rows) {
     unsigned hit = __ballot_sync(kFull, x < base + incl);
-    while (hit == 0u && b + 32 < P.s.batch) {
-      base += __shfl_sync(kFull, incl, 31);
-      window(P, b + 32);
+    if (hit == 0u) {
+      seek(P, x);
       hit = __ballot_sync(kFull, x < base + incl);
     }
     const int w = hit ? __ffs(hit) - 1 : 0;
@@ -188,6 +248,9 @@ __device__ __forceinline__ RowAt row_at(const StreamParams& P, int hk, int r) {
   a.i = r / P.group;
   a.h = hk * P.group + (r - a.i * P.group);
   return a;
+}
+__device__ __forceinline__ const uint8_t* q_row(const StreamParams& P, const SeqRows& s, int b, const RowAt& a) {
+  return P.q + (P.s.cu_q != nullptr ? 0 : b * P.q_b) + (int64_t)(s.q0 + a.i) * P.q_t + a.h * P.q_h;
 }
 __device__ __forceinline__ int64_t lse_at(const StreamParams& P, const SeqRows& s, int b, const RowAt& a) {
   return P.s.cu_q != nullptr ? (int64_t)a.h * P.s.total_q + s.q0 + a.i
@@ -378,10 +441,35 @@ __device__ __forceinline__ void join_parts(const StreamParams& P, int n, int val
   }
 }
 
-// `first`: the unit at which this CTA's piece starts, `per` the units of every CTA.
+// q of a piece's rows: row g of each of the warp's column tiles, pairs at depths d
+// and d + step of every 16. The loads stay where they are written.
+template <class C>
+__device__ __forceinline__ void load_q(const StreamParams& P, const Piece& pc, const SeqRows& s,
+                                       uint32_t (&qf)[C::NT][C::D / 16][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int row0 = row_tile_of(P, pc.seg) * C::RT + 8 * C::NT * ((int)(threadIdx.x >> 5) % C::WM);
+#pragma unroll
+  for (int x = 0; x < C::NT; ++x) {
+    const int r = row0 + 8 * x + g;
+    const bool ok = r < s.lq * P.group;
+    const uint8_t* src = q_row(P, s, pc.b, row_at(P, head_of(P, pc.seg), ok ? r : 0));
+#pragma unroll
+    for (int kk = 0; kk < C::D / 16; ++kk) {
+      const int d = C::FP8 ? 16 * (t + 4 * (kk >> 2)) + 4 * (kk & 3) : 16 * kk + 2 * t;
+      const int step = C::FP8 ? 2 : 8;
+      qf[x][kk][0] = ok ? (uint32_t)ptx::ld_global_pinned(reinterpret_cast<const int*>(src + 2 * d)) : 0u;
+      qf[x][kk][1] = ok ? (uint32_t)ptx::ld_global_pinned(reinterpret_cast<const int*>(src + 2 * (d + step))) : 0u;
+    }
+  }
+}
+
+// Runs piece `pc`, which starts at unit `first`, of a CTA whose units end at `end`,
+// and finds the next one; `per`: the units of every CTA. `qf` holds q of the piece,
+// then of the next: its loads are on their way while this one is finished.
 template <class C>
 __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, uint8_t* smem, Loader<C>& load,
-                          int& count, int first, int per) {
+                          Walker<C>& walk, uint32_t (&qf)[C::NT][C::D / 16][2], Piece& next, SeqRows& next_rows,
+                          int& count, int first, int end, int per) {
   constexpr int D = C::D, WM = C::WM, NT = C::NT, KW = C::KW, NB = C::BLOCKS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -409,21 +497,8 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     }
   lim_min = min(lim_min, __shfl_xor_sync(kFull, lim_min, 1));
   lim_min = min(lim_min, __shfl_xor_sync(kFull, lim_min, 2));
-  // q of row g of each column tile: pairs at depths d and d + step of every 16
-  uint32_t qf[NT][D / 16][2];
 #pragma unroll
   for (int x = 0; x < NT; ++x) {
-    const int r = row0 + 8 * x + g;
-    const bool ok = r < rows;
-    const RowAt a = row_at(P, hk, ok ? r : 0);
-    const uint8_t* src = P.q + (P.s.cu_q != nullptr ? 0 : pc.b * P.q_b) + (int64_t)(s.q0 + a.i) * P.q_t + a.h * P.q_h;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const int d = C::FP8 ? 16 * (t + 4 * (kk >> 2)) + 4 * (kk & 3) : 16 * kk + 2 * t;
-      const int step = C::FP8 ? 2 : 8;
-      qf[x][kk][0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * d)) : 0u;
-      qf[x][kk][1] = ok ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * (d + step))) : 0u;
-    }
     if constexpr (C::FP8) {
       // The codes of an e4m3 cache are multiplied as f16 (one conversion for two
       // of them). q becomes f16 too, times the power of two that brings its
@@ -715,6 +790,11 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
         for (int e = 0; e < 4; ++e) acc[i][x][e] *= vref * 0.0078125f;
   }
 
+  if (first + pc.count < end) {
+    next = walk.at(P, first + pc.count, end, next_rows);
+    load_q<C>(P, next, next_rows, qf);
+  }
+
   // ---- The key groups' results meet in shared memory, each group's in the
   // stage it used last (the loader does not fill that one before the next
   // piece's first tile). Without keys there is no such stage, and only the
@@ -837,7 +917,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_stream_kernel(const __grid_
   // Fill the ring, then run the pieces; the loader stays STAGES - 1 tiles ahead.
   const int warp = threadIdx.x >> 5, kg = warp / C::WM, gt = (warp % C::WM) * 32 + (threadIdx.x & 31);
   const uint32_t ring = ptx::smem_u32(smem) + kg * (C::STAGES * C::STAGE);
+  if (P.s.batch > 32) load.walk.seek(P, x);
   Walker<C> walk = load.walk;
+  SeqRows s;
+  Piece pc = walk.at(P, x, end, s);
+  uint32_t qf[C::NT][D / 16][2];
+  load_q<C>(P, pc, s, qf);
   load.x = x;
   load.end = end;
   load.next_piece(P, kg);
@@ -847,12 +932,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_stream_kernel(const __grid_
     ptx::cp_async_commit();
   }
   int count = 0;   // tiles used so far
-  while (x < end) {
-    SeqRows s;
-    const Piece pc = walk.at(P, x, end, s);
-    if (pc.count <= 0) break;
-    run_piece<C>(P, pc, s, smem, load, count, x, per);
+  while (x < end && pc.count > 0) {
+    Piece next = pc;
+    SeqRows next_rows = s;
+    run_piece<C>(P, pc, s, smem, load, walk, qf, next, next_rows, count, x, end, per);
     x += pc.count;
+    pc = next;
+    s = next_rows;
   }
   ptx::cp_async_wait<0>();
 }

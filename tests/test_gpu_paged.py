@@ -176,6 +176,23 @@ def test_attend_many_kv_heads(pkg, lens_k, hkv, group, new, dim, fp8):
     R.check_attend(p, o, lse, True)
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("batch,hkv,group,new,longest", [
+    (75, 8, 1, 1, 1000),     # two segments to a CTA, none cut
+    (75, 3, 4, 2, 3000),     # more than one window of 32 lengths, segments cut
+    (300, 2, 2, 1, 90),      # many short ones
+    (1100, 1, 2, 1, 40),     # more than 1024 lengths
+    (2300, 1, 1, 3, 700)])
+def test_attend_many_sequences(pkg, batch, hkv, group, new, longest, fp8):
+    """How the kernel finds its sequences among many, empty ones between them."""
+    lens_k = [0 if b % 5 == 3 or 40 <= b < 80 and batch > 200 else 1 + (b * 7919) % longest for b in range(batch)]
+    lens_k[batch // 2] = longest
+    p = R.make(lens_k, [min(new, n) for n in lens_k], hkv * group, hkv, 64, 16, fp8=fp8, packed=True, seed=32)
+    o, lse = pkg.paged_forward(p.q, *p.cache, cu_seqlens_q=p.cu_q, max_seqlen_q=new, **p.scales)
+    pkg.check()
+    R.check_attend(p, o, lse, True)
+
+
 def test_attend_large_scores(pkg):
     """Scores of both signs in the thousands: the running maximum has to move
     and no exponential may overflow. (The reference bound for LSE assumes
