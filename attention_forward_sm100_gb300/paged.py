@@ -18,7 +18,9 @@ replays of a captured call. What is wrong with them is found there: nothing
 outside the tensors is touched, and ``check`` raises. Scratch memory is kept
 per device and stream, so calls on different streams may overlap; a captured
 call takes its own from the graph's memory, and what its replays find wrong
-is only seen by ``check`` if the call was given a ``workspace``.
+is only seen by ``check`` if the call was given a ``workspace``: a contiguous
+tensor that is zero before its first use and that calls which may overlap do
+not share (what a call needs is in the error that refuses too small a one).
 
 Arguments are checked and marshalled by the extension module _paged_native
 (csrc/python_paged.cpp).
@@ -35,6 +37,8 @@ def _on(stream, tensor):
     """The context that makes ``stream`` (a torch stream or a handle) current."""
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=tensor.device)
+    elif getattr(tensor, "is_cuda", False) and stream.device != tensor.device:
+        raise ValueError("stream is on another device than the tensors")
     return torch.cuda.stream(stream)
 
 

@@ -4,6 +4,7 @@ within the bound its roundings imply), what only the device can refuse, and
 runs of them together. Slots that no sequence holds are NaN throughout, and
 table columns past a sequence's pages hold numbers outside the cache."""
 import math
+import types
 
 import pytest
 import torch
@@ -418,6 +419,15 @@ def test_two_streams_at_once(pkg):
     o, l = pkg.paged_forward(ps[0].q, *ps[0].cache, stream=streams[1].cuda_stream)   # a bare handle
     pkg.check(stream=streams[1])
     assert torch.equal(R.bits(o), R.bits(want[0][0])) and torch.equal(R.bits(l), R.bits(want[0][1]))
+
+
+def test_stream_of_another_device_is_refused(pkg):
+    p = R.make([20], [1], 2, 2, 64, 16, seed=33)
+    other = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
+    with pytest.raises(ValueError, match="another device"):
+        pkg.cache_append(p.k_new, p.v_new, *p.cache, stream=other)
+    with pytest.raises(ValueError, match="another device"):
+        pkg.paged_forward(p.q, *p.cache, stream=other)
 
 
 def test_own_workspace(pkg):
