@@ -12,6 +12,11 @@ namespace af {
 // for 256-byte cache rows, 32 for shorter ones (the fixed work of a step then
 // weighs half); a group of several warps shares its keys.
 constexpr int stream_tile(int row_bytes, int group_warps) { return group_warps == 1 && row_bytes < 256 ? 128 : 64; }
+// CTAs of it per SM. A third one hides the latencies of e4m3 at D = 64 (16 sequences
+// of up to 32768 keys, GQA 32/8: 69.6 -> 64.2 us; a fourth leaves too few registers,
+// 77.6); where two already wait for HBM it does not pay (e4m3, D = 128: 104 -> 118 with
+// the half tiles that it needs).
+constexpr int stream_ctas(int row_bytes, int row_tile) { return row_bytes == 64 && row_tile == 8 ? 3 : 2; }
 constexpr int kMinPage = 16;         // smallest page: one warp's step of keys lies in one page
 
 // The new rows of each sequence (fixed: b * seqlen_q; packed: cu_q) and the

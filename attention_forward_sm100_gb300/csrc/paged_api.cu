@@ -223,13 +223,13 @@ struct StreamPlan {
   size_t ml_bytes, o_bytes;
 };
 
-// Row tiles of 8, 16 or 32 rows, the smallest that holds a sequence's rows;
-// two CTAs per SM. Segments of up to kUnsplitTiles key tiles are not cut: the
+// Row tiles of 8, 16 or 32 rows, the smallest that holds a sequence's rows; two
+// or three CTAs per SM. Segments of up to kUnsplitTiles key tiles are not cut: the
 // join would cost more than the longer CTA. Nor are those of up to kUnsplitKeys
-// keys if they are at least a quarter as many as the CTAs and at most twice. GQA
-// 32/8, d128: 12 sequences of up to 300 keys, bf16: 12.8 us cut, 7.0 whole; 32 sequences of up to 1000 keys, bf16 22.7 us cut, 17.5 whole, e4m3 21.2 and
-// 14.9; 8 sequences 13.7 and 13.6; 75 sequences 36.7 and 34.6; but 3 sequences 9.1
-// and 12.3, 256 sequences 94 and 112.
+// keys if they are at least a quarter as many as the CTAs and at most twice.
+// GQA 32/8, d128, us cut / whole: 12 sequences of up to 300 keys, bf16: 12.8 / 7.0;
+// 32 sequences of up to 1000 keys, bf16 22.7 / 17.5, e4m3 21.2 / 14.9; 8 of them
+// 13.7 / 13.6; 75 of them 36.7 / 34.6; but 3 of them 9.1 / 12.3, 256 of them 94 / 112.
 constexpr int kUnsplitTiles = 4;
 constexpr int kUnsplitKeys = 1024;
 // Of cut segments, the CTAs of a team take different heads of the same keys, so
@@ -249,7 +249,7 @@ StreamPlan plan_stream(const attn_paged_params* p) {
   const int row_bytes = p->cache.head_dim * (p->cache.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2);
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
   const int64_t tiles = af::tiles_for(p->seqlen_k, af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
-  const int64_t ctas = 2ll * af::sm_count();
+  const int64_t ctas = (int64_t)af::stream_ctas(row_bytes, s.row_tile) * af::sm_count();
   const bool one_wave = 4 * segments >= ctas && segments <= 2 * ctas;
   s.split = tiles > kUnsplitTiles && !(one_wave && p->seqlen_k <= kUnsplitKeys) ? 1 : 0;
   s.units = segments * (s.split ? tiles : 1);

@@ -7,14 +7,16 @@
 // the tensor cores idle. So the kernel is built around the loads:
 //   * the work is the list of all key tiles (64 or 128 keys) of all (sequence,
 //     KV head, row tile) segments, cut into equal contiguous parts, one per CTA
-//     (two CTAs per SM; CTAs of a team share a cut and differ in the head, for
-//     HBM's sake: 182 -> 171 us, e4m3 125 -> 106 at the sizes of kMaxTeam). Lengths are read on the device, so ragged batches
-//     balance without the host knowing them and a captured call follows lengths
-//     that change;
-//   * q of the next segment is loaded while one is finished (256 sequences of up
-//     to 250 keys: 40.5 -> 38.9 us; with the lengths' sums below and two CTAs per SM
-//     for short segments too, 59 at first);
-//   * a CTA streams its tiles through a ring of cp.async stages (about 96 KB),
+//     (two or three CTAs per SM). Neighbouring CTAs share a cut and differ in
+//     the head, so that HBM is asked for what lies together (182 -> 171 us, e4m3
+//     125 -> 106 at the sizes given at kMaxTeam). Lengths are read on the device,
+//     so ragged batches balance without the host knowing them and a captured
+//     call follows lengths that change;
+//   * many short segments are bound by what is done once for each: lengths are
+//     summed 256 at a time, q of the next segment is loaded while one is
+//     finished, uncut segments share CTAs as cut ones do (256 sequences of up to
+//     250 keys: 59 -> 39 us);
+//   * a CTA streams its tiles through a ring of cp.async stages (192 KB per SM),
 //     across segments: while one is finished, the next one's tiles are loading.
 //     A row tile is 8, 16 or 32 rows; the four warps form four key groups, each
 //     with its own keys and ring, so that every warp streams by itself and meets
@@ -31,9 +33,10 @@
 //     to bf16 it takes four): q as f16 too, normalised by a power of two per row,
 //     and the weights in units of the largest value scale (where scales differ
 //     by more than 2^4 weights and values go through bf16). The key scale is
-//     applied to the fp32 score, the value scale to the fp32 weight. Depth and value columns are dealt to lanes in the order in which
-//     16-byte reads from shared memory deliver them: a dot product does not
-//     depend on the order of its depth, nor a product on that of its columns;
+//     applied to the fp32 score, the value scale to the fp32 weight. Depth and
+//     value columns are dealt to lanes in the order in which 16-byte reads from
+//     shared memory deliver them: a dot product does not depend on the order of
+//     its depth, nor a product on that of its columns;
 //   * a segment that lies in one CTA is finished there; the parts of one that
 //     CTA borders cut meet in the workspace, and whichever of its CTAs comes last
 //     joins them (in the order of the CTAs, so the result does not depend on who
@@ -60,6 +63,7 @@ template <int D_, bool FP8_, int NT_, int WM_>
 struct Cfg {
   static constexpr int D = D_, NT = NT_, WM = WM_;
   static constexpr bool FP8 = FP8_;
+  static constexpr int CTAS = stream_ctas(FP8 ? D : 2 * D, 8 * NT * WM);
   static constexpr int WK = 4 / WM;              // key groups
   static constexpr int RT = 8 * NT * WM;         // rows of a row tile
   static constexpr int ROWB = FP8 ? D : 2 * D;   // bytes of a cached row
@@ -78,14 +82,14 @@ struct Cfg {
   // has just used up, or, where that is too small, in room of its own.
   static constexpr int PART = RT * D * 4;
   static constexpr bool OWN_PART = PART > STAGE;
-  static constexpr int STAGES = min_int(8, (98304 - (OWN_PART ? WK * PART : 0)) / (WK * 2 * KV));
+  static constexpr int STAGES = min_int(8, (196608 / CTAS - (OWN_PART ? WK * PART : 0)) / (WK * 2 * KV));
   static constexpr int RING = WK * STAGES * STAGE;
   static constexpr int OFF_ML = RING + (OWN_PART ? WK * PART : 0);   // [WK][RT] (maximum, sum)
   static constexpr int SMEM = OFF_ML + WK * RT * 8;
   static constexpr int ROUNDS = (RT * (D / 4) + 127) / 128;   // 16-byte pieces of a row tile per thread
   // Byte offset of group k's part, `last` being its stage's in the group's ring.
   __device__ static int part_at(int k, int last) { return OWN_PART ? RING + k * PART : k * (STAGES * STAGE) + last; }
-  static_assert(STAGES >= 3 && SMEM <= 113 * 1024, "two CTAs per SM");
+  static_assert(STAGES >= 3 && SMEM <= 226 * 1024 / CTAS, "the CTAs per SM");
   // Column of depth d of row r there: rows 2 t and 2 t + 1 shifted by 8 t banks.
   __device__ static int part_col(int r, int d) { return d ^ (((r >> 1) & 3) << 3); }
   // Position of 16-byte piece `c` of row `r` in a stage (bank conflicts).
@@ -282,15 +286,16 @@ struct Loader {
   int b, hk, lk;           // the current tile's sequence, KV head, keys
   int key0, left;          // its first key of this group; tiles left in the piece, this one included (0: none left)
   int pages[C::BLOCKS];    // of its 16-key blocks, as read from the table
+  const uint8_t *ks, *vs;  // the KV head's keys and values, at this thread's row and depth of a block
+  const int32_t* table;    // the sequence's row
 
   __device__ __forceinline__ void fetch_pages(const StreamParams& P) {
-    const int32_t* table = P.c.table + (int64_t)b * P.c.table_stride;
 #pragma unroll
     for (int u = 0; u < C::BLOCKS; ++u)
       pages[u] = key0 + 16 * u < lk ? ptx::ld_global_pinned(table + ((key0 + 16 * u) >> P.c.page_shift)) : 0;
   }
   // Moves to the first tile of the next piece that has any.
-  __device__ __forceinline__ void next_piece(const StreamParams& P, int kg) {
+  __device__ __forceinline__ void next_piece(const StreamParams& P, int gt, int kg) {
     left = 0;
     while (left <= 0 && x < end) {
       SeqRows s;
@@ -303,7 +308,12 @@ struct Loader {
       lk = s.lk;
       key0 = t0 * C::TILE + kg * C::KW;
     }
-    if (left > 0) fetch_pages(P);
+    if (left <= 0) return;
+    const int lrow = gt / C::CPR, lcol = gt % C::CPR;
+    ks = P.c.k + hk * P.c.k_head + lrow * P.c.k_tok + lcol * 16;
+    vs = P.c.v + hk * P.c.v_head + lrow * P.c.v_tok + lcol * 16;
+    table = P.c.table + (int64_t)b * P.c.table_stride;
+    fetch_pages(P);
   }
   // Copies the current tile into the stage at `st` and moves on: the table is
   // read a tile ahead of the copies that depend on it.
@@ -317,18 +327,18 @@ struct Loader {
 #pragma unroll
     for (int i = 0; i < C::NL; i += PER) {
       const int page = pages[i / PER];
-      const int64_t slot = (key0 + lrow + i * C::RS) & page_mask;
-      const uint8_t* ks = P.c.k + hk * P.c.k_head + page * P.c.k_page + slot * P.c.k_tok + lcol * 16;
-      const uint8_t* vs = P.c.v + hk * P.c.v_head + page * P.c.v_page + slot * P.c.v_tok + lcol * 16;
+      const int64_t slot = (key0 + 16 * (i / PER)) & page_mask;
+      const uint8_t* kp = ks + page * P.c.k_page + slot * P.c.k_tok;
+      const uint8_t* vp = vs + page * P.c.v_page + slot * P.c.v_tok;
 #pragma unroll
       for (int y = 0; y < PER; ++y) {
         const int row = lrow + (i + y) * C::RS;
         // (behind the end nothing is read; the address is still inside a page)
         const bool ok = key0 + row < lk;
-        ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, ks, ok);
-        ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, vs, ok);
-        ks += C::RS * P.c.k_tok;
-        vs += C::RS * P.c.v_tok;
+        ptx::cp_async16(st + row * C::ROWB + C::swz_k(row, lcol) * 16, kp, ok);
+        ptx::cp_async16(st + C::KV + row * C::ROWB + C::swz_v(row, lcol) * 16, vp, ok);
+        kp += C::RS * P.c.k_tok;
+        vp += C::RS * P.c.v_tok;
       }
     }
     if constexpr (C::FP8) {
@@ -349,7 +359,7 @@ struct Loader {
     }
     key0 += C::TILE;
     if (--left > 0) fetch_pages(P);
-    else next_piece(P, kg);
+    else next_piece(P, gt, kg);
   }
 };
 
@@ -902,7 +912,8 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
 }
 
 template <int D, bool FP8, int NT, int WM>
-__global__ void __launch_bounds__(kThreads, 2) paged_stream_kernel(const __grid_constant__ StreamParams P) {
+__global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, NT, WM>::CTAS))
+    paged_stream_kernel(const __grid_constant__ StreamParams P) {
   using C = Cfg<D, FP8, NT, WM>;
   extern __shared__ __align__(128) uint8_t smem[];
   ptx::grid_dependency_wait();
@@ -925,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_stream_kernel(const __grid_
   load_q<C>(P, pc, s, qf);
   load.x = x;
   load.end = end;
-  load.next_piece(P, kg);
+  load.next_piece(P, gt, kg);
 #pragma unroll 1
   for (int j = 0; j < C::STAGES - 1; ++j) {
     load.issue(P, ring + j * C::STAGE, gt, kg);
