@@ -377,9 +377,9 @@ constexpr int kJoin = 16;
 // counter at zero).
 __device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t want) {
   __shared__ bool is_last;
-  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
+    __threadfence();   // (of the whole CTA's stores: the barrier above orders them before it)
     is_last = atomicAdd(counter, 1u) == want - 1u;
     if (is_last) *counter = 0u;
     __threadfence();
