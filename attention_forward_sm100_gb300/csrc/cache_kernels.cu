@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         }
         if (ok) {
           const int lk = P.s.seqlens_k[b];
-          s = slot_of(P.c, b, lk > P.s.max_k ? -1 : lk - lq + i, P.ws);
+          s = slot_of(P.c, b, lk < 0 || lk > P.s.max_k ? -1 : lk - lq + i, P.ws);
         }
         slots[threadIdx.x] = s;
       }

@@ -421,6 +421,41 @@ def test_two_streams_at_once(pkg):
     assert torch.equal(R.bits(o), R.bits(want[0][0])) and torch.equal(R.bits(l), R.bits(want[0][1]))
 
 
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 130])
+def test_sequences_that_share_pages(pkg, new, fp8):
+    """A common prefix in the same pages, and a page that a sequence names twice."""
+    p = R.make([2000, 2000], [new] * 2, 4, 2, 64, 16, fp8=fp8, seed=34)
+    p.table[1, :124] = p.table[0, :124]
+    p.table[:, 7] = p.table[:, 3]
+    p.q[1] = p.q[0]
+    o, lse = pkg.paged_forward(p.q, *p.cache, **p.scales)
+    pkg.check()
+    R.check_attend(p, o, lse, True)
+    p.table[1] = p.table[0]
+    o, lse = pkg.paged_forward(p.q, *p.cache, **p.scales)
+    R.check_attend(p, o, lse, True)
+    cu = torch.tensor([0, 2000, 4000], dtype=torch.int32, device="cuda")
+    k, v = pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, total_k=4000, **p.scales)
+    pkg.check()
+    assert torch.equal(R.bits(k[:2000]), R.bits(k[2000:])) and torch.equal(R.bits(v[:2000]), R.bits(v[2000:]))
+    assert torch.equal(R.bits(k[48:64]), R.bits(k[112:128]))
+
+
+def test_append_with_a_length_far_below_zero(pkg):
+    """lk - lq must not wrap around to a position that exists."""
+    page, n = 65536, 70000
+    k_cache = torch.full((1, page, 1, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    v_cache = k_cache.clone()
+    table = torch.zeros(1, 0x7fff0000 // page, dtype=torch.int32, device="cuda")
+    lens = torch.full((1,), -2 ** 31, dtype=torch.int32, device="cuda")
+    new = torch.zeros(1, n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    pkg.cache_append(new, new, k_cache, v_cache, table, lens)
+    with pytest.raises(pkg.AttnError, match="out of range"):
+        pkg.check()
+    assert bool((k_cache == 3.0).all()) and bool((v_cache == 3.0).all())
+
+
 def test_stream_of_another_device_is_refused(pkg):
     p = R.make([20], [1], 2, 2, 64, 16, seed=33)
     other = types.SimpleNamespace(cuda_stream=0, device=torch.device("cuda", 1))
