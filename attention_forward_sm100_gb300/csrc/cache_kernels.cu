@@ -143,10 +143,10 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
           b = find_sequence(P.s.cu_q, P.s.batch, t0, t);
           ok = ok && b < P.s.batch;                // else behind the last sequence
           if (ok) {
-            const int a = P.s.cu_q[b];
+            const int a = P.s.cu_q[b], e = P.s.cu_q[b + 1];
             i = (int)(t - a);
-            lq = P.s.cu_q[b + 1] - a;
-            if (a < 0 || i < 0) {                  // offsets out of order
+            lq = e - a;
+            if (a < 0 || i < 0 || e > P.tokens) {  // offsets out of order or past the rows
               record_bad_cache(P.ws, b);
               ok = false;
             }
@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
   if (threadIdx.x < 32) {
+    if (blockIdx.x == 0 && P.batch > 0 && P.cu_k[P.batch] > P.total_k) record_bad_cache(P.ws, P.batch - 1);
     Slot s = {-1, 0};
     const int64_t t = t0 + threadIdx.x;
     const int b = find_sequence(P.cu_k, P.batch, t0, t);

@@ -442,6 +442,23 @@ def test_sequences_that_share_pages(pkg, new, fp8):
     assert torch.equal(R.bits(k[48:64]), R.bits(k[112:128]))
 
 
+def test_offsets_past_the_rows_are_reported(pkg):
+    """Fewer rows than the offsets claim: what is there of the other sequences is right."""
+    p = R.make([40, 30], [5, 6], 2, 2, 64, 16, packed=True, seed=35)
+    want = R.append(p)
+    before = p.k_cache.clone()
+    pkg.cache_append(p.k_new[:-1], p.v_new[:-1], *p.cache, cu_seqlens_q=p.cu_q)
+    _bad(pkg, p)
+    pages = p.table[0, :3].long()
+    assert torch.equal(R.bits(p.k_cache[pages]), R.bits(want[0][pages]))
+    pages = p.table[1, :2].long()
+    assert torch.equal(R.bits(p.k_cache[pages]), R.bits(before[pages]))
+    cu = torch.tensor([0, 40, 70], dtype=torch.int32, device="cuda")
+    k, _ = pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, total_k=69)
+    _bad(pkg, p)
+    assert torch.equal(k[:40].double(), R.gather(p, 0)[0])
+
+
 def test_append_with_a_length_far_below_zero(pkg):
     """lk - lq must not wrap around to a position that exists."""
     page, n = 65536, 70000
