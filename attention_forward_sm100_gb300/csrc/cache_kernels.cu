@@ -208,6 +208,19 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   }
 }
 
+// Sixteen codes times their scale, rounded once, as 32 bytes of bf16.
+__device__ __forceinline__ void widen(const uint4& x, float scale, uint32_t (&out)[8]) {
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 lo, hi;
+    ptx::e4m3x2_to_float2(in[j] & 0xffffu, lo.x, lo.y);
+    ptx::e4m3x2_to_float2(in[j] >> 16, hi.x, hi.y);
+    out[2 * j] = ptx::pack_bf16(lo.x * scale, lo.y * scale);
+    out[2 * j + 1] = ptx::pack_bf16(hi.x * scale, hi.y * scale);
+  }
+}
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams P) {
   constexpr int E = FP8 ? 16 : 8, L = D / E, PER = kThreads / L;
@@ -259,16 +272,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       if constexpr (!FP8) {
         *reinterpret_cast<uint4*>(dst) = x[u];
       } else {
-        const uint32_t in[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
         uint32_t out[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float2 lo, hi;
-          ptx::e4m3x2_to_float2(in[j] & 0xffffu, lo.x, lo.y);
-          ptx::e4m3x2_to_float2(in[j] >> 16, hi.x, hi.y);
-          out[2 * j] = ptx::pack_bf16(lo.x * scale[u], lo.y * scale[u]);
-          out[2 * j + 1] = ptx::pack_bf16(hi.x * scale[u], hi.y * scale[u]);
-        }
+        widen(x[u], scale[u], out);
         if (P.wide) {
           ptx::st_global_v8(dst, out);
         } else {
@@ -276,6 +281,58 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
           d[0] = make_uint4(out[0], out[1], out[2], out[3]);
           d[1] = make_uint4(out[4], out[5], out[6], out[7]);
         }
+      }
+    }
+  }
+}
+
+// Every sequence's cached tokens as bf16 pages (WidenParams): blocks (x, b) take
+// the token chunks x, x + grid, ... of sequence b. Three bytes of traffic per
+// element, HBM bounds it as it does reading.
+template <int D>
+__global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_constant__ WidenParams P) {
+  constexpr int L = D / 16, PER = kThreads / L;
+  __shared__ Slot slots[kMaxTokens];
+  ptx::grid_dependency_wait();
+  const int b = blockIdx.y, lane = threadIdx.x % L;
+  const int lk = min(max(P.seqlens_k[b], 0), P.max_k);   // (a length out of range is recorded by its attention)
+  const uint32_t nv = 2 * P.c.heads_kv;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < P.pages; i += kThreads) P.table[(int64_t)b * P.pages + i] = b * P.pages + i;
+  const int step = (int)gridDim.x * P.block_tokens;
+  for (int64_t t0 = (int64_t)blockIdx.x * P.block_tokens; t0 < lk; t0 += step) {
+    const int tokens = (int)min((int64_t)P.block_tokens, lk - t0);
+    const uint32_t total = tokens * nv;
+    __syncthreads();   // nobody reads the previous chunk's slots any more
+    if (threadIdx.x < 32 && (int)threadIdx.x < tokens) slots[threadIdx.x] = slot_of(P.c, b, (int)t0 + threadIdx.x, P.ws);
+    __syncthreads();
+    for (uint32_t base = 0; base < total; base += PER * kBatch) {
+      uint4 x[kBatch];
+      float scale[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t id = base + u * PER + threadIdx.x / L;
+        if (id >= total) continue;
+        const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
+        const Slot s = slots[w.token];
+        if (s.page < 0) continue;
+        const uint8_t* src = (w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
+                                  : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head) + lane * 16;
+        x[u] = __ldg(reinterpret_cast<const uint4*>(src));
+        scale[u] = __ldg((w.v ? P.c.v_scale : P.c.k_scale) +
+                         ((((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot));
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const uint32_t id = base + u * PER + threadIdx.x / L;
+        if (id >= total) continue;
+        const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
+        if (slots[w.token].page < 0) continue;
+        const int t = (int)t0 + w.token;
+        const int64_t row = (((int64_t)b * P.pages + t / kBlockN) * P.c.heads_kv + w.h) * kBlockN + t % kBlockN;
+        uint32_t out[8];
+        widen(x[u], scale[u], out);
+        ptx::st_global_v8((w.v ? P.v : P.k) + row * (D * 2) + lane * 32, out);
       }
     }
   }
@@ -306,6 +363,19 @@ cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, c
                : launch(cache_append_kernel<128, false>, p, n, pb, stream);
   return fp8 ? launch(cache_append_kernel<64, true>, p, n, pb, stream)
              : launch(cache_append_kernel<64, false>, p, n, pb, stream);
+}
+
+cudaError_t cache_widen_launch(const WidenParams& params, int head_dim, cudaStream_t stream) {
+  WidenParams p = params;
+  const uint32_t per_token = 2 * p.c.heads_kv;
+  const int fit = per_block(head_dim, true) / (int)per_token;
+  p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
+  p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
+  const int64_t chunks = ((int64_t)p.max_k + p.block_tokens - 1) / p.block_tokens;
+  const int64_t fill = (16ll * sm_count() + p.batch - 1) / p.batch;   // two rounds of eight blocks per SM
+  const dim3 grid((unsigned)(chunks < 1 ? 1 : (chunks < fill ? chunks : fill)), (unsigned)p.batch);
+  return head_dim == 128 ? launch_dependent(cache_widen_kernel<128>, p, grid, kThreads, 0, stream)
+                         : launch_dependent(cache_widen_kernel<64>, p, grid, kThreads, 0, stream);
 }
 
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream) {

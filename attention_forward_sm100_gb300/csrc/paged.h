@@ -53,6 +53,20 @@ struct ReadParams {
   uint32_t* ws;
 };
 
+// Widening an e4m3 cache into bf16 pages of kBlockN tokens, [batch * pages][Hkv][kBlockN][D],
+// sequence b's in order from page b * pages on, and the block table that says so.
+struct WidenParams {
+  CacheView c;
+  const int32_t* seqlens_k;
+  int32_t max_k, batch, pages;
+  uint8_t* k;
+  uint8_t* v;
+  int32_t* table;
+  int32_t block_tokens;
+  uint32_t magic;
+  uint32_t* ws;
+};
+
 struct StreamParams {
   CacheView c;
   NewRows s;
@@ -92,6 +106,7 @@ cudaError_t paged_plan_launch(const PlanParams& p, cudaStream_t stream);
 cudaError_t paged_tile_merge_launch(const PlanParams& p, int head_dim, int max_cut, cudaStream_t stream);
 
 cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream);
+cudaError_t cache_widen_launch(const WidenParams& p, int head_dim, cudaStream_t stream);
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream);
 // Streaming attention over `grid` CTAs with row tiles of 8, 16 or 32 rows.
 cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,

@@ -269,9 +269,39 @@ StreamPlan plan_stream(const attn_paged_params* p) {
   return s;
 }
 
+// Whether an e4m3 cache is widened to bf16 pages in scratch memory first, for the
+// tcgen05 kernel's bf16 form to read: that costs K and V once each way, the e4m3
+// form extra work for every 256 rows. us, widened / e4m3 form, GQA 32/8, d128,
+// 32768 keys: 64 new tokens (R = 256) 79 / 77, 128: 100 / 104, 256: 143 / 157,
+// 512: 230 / 265, 2048: 711 / 897; four ragged sequences of up to 12000 keys and 1023
+// new tokens 372 / 468, d64 316 / 422; with 32 KV heads 485 / 480, of up to 512 new
+// tokens (R about 300 on average) 386 / 342. Not where the scratch memory would
+// pass kWidenBytes.
+constexpr int64_t kWidenRows = 512, kWidenBytes = 1ll << 30;
+struct WidenPlan {
+  bool on;
+  int pages;                 // of kBlockN tokens, per sequence
+  size_t table, rows;        // bytes: block table, K (and V as many)
+};
+WidenPlan plan_widen(const attn_paged_params* p) {
+  WidenPlan w = {};
+  const attn_kv_cache& c = p->cache;
+  if (c.dtype != ATTN_DTYPE_FP8_E4M3 || !use_tc05(p)) return w;
+  const int64_t tokens = p->cu_seqlens_q != nullptr ? p->total_q : (int64_t)c.batch * p->seqlen_q;
+  w.pages = af::tiles_for(p->seqlen_k, af::kBlockN);
+  const int64_t n = (int64_t)c.batch * w.pages, row = (int64_t)c.num_heads_kv * af::kBlockN * c.head_dim * 2;
+  w.on = w.pages > 0 && tokens * (p->num_heads_q / c.num_heads_kv) >= kWidenRows * c.batch &&
+         n <= kWidenBytes / (2 * row);
+  if (!w.on) return w;
+  w.table = round256((size_t)n * sizeof(int32_t));
+  w.rows = (size_t)(n * row);
+  return w;
+}
+
 size_t workspace_need(const attn_paged_params* p) {
   if (use_tc05(p)) {
-    return kZeroedBytes + plan_tiles(p).bytes;
+    const WidenPlan w = plan_widen(p);
+    return kZeroedBytes + round256(plan_tiles(p).bytes) + w.table + 2 * w.rows;
   }
   const StreamPlan s = plan_stream(p);
   return kZeroedBytes + s.ml_bytes + s.o_bytes;
@@ -282,8 +312,38 @@ int64_t legal(int64_t stride, int64_t size) { return size > 1 ? stride : 16; }
 
 attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   const TilePlan plan = plan_tiles(p);
-  const attn_kv_cache& c = p->cache;
+  attn_kv_cache c = p->cache;
   const bool packed = p->cu_seqlens_q != nullptr;
+  if (const WidenPlan w = plan_widen(p); w.on) {
+    af::WidenParams wp;
+    memset(&wp, 0, sizeof(wp));
+    uint8_t* at = static_cast<uint8_t*>(p->workspace) + kZeroedBytes + round256(plan.bytes);
+    wp.c = view_of(c);
+    wp.seqlens_k = p->seqlens_k;
+    wp.max_k = p->seqlen_k;
+    wp.batch = c.batch;
+    wp.pages = w.pages;
+    wp.table = reinterpret_cast<int32_t*>(at);
+    wp.k = at + w.table;
+    wp.v = wp.k + w.rows;
+    wp.ws = static_cast<uint32_t*>(p->workspace);
+    const cudaError_t e = af::cache_widen_launch(wp, c.head_dim, stream);
+    if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "cache widening launch failed: %s", cudaGetErrorString(e));
+    c.k = wp.k;
+    c.v = wp.v;
+    c.k_scale = c.v_scale = nullptr;
+    c.block_table = wp.table;
+    c.dtype = ATTN_DTYPE_BF16;
+    c.page_size = af::kBlockN;
+    c.num_pages = c.batch * w.pages;
+    c.max_pages = w.pages;
+    c.table_stride = w.pages;
+    for (int64_t* s : {c.k_stride, c.v_stride}) {
+      s[0] = (int64_t)c.num_heads_kv * af::kBlockN * c.head_dim;
+      s[1] = c.head_dim;
+      s[2] = (int64_t)af::kBlockN * c.head_dim;
+    }
+  }
   af::Tc05Params prm;
   memset(&prm, 0, sizeof(prm));
   const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -538,6 +538,26 @@ def test_attend_chunks_that_are_cut(pkg, lens_k, lens_q, hq, hkv, dim, page, fp8
         assert torch.equal(R.bits(o), R.bits(o2)) and torch.equal(R.bits(lse), R.bits(lse2))
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("lens_k,lens_q,hq,hkv,dim,page,head_major", [
+    ([700, 0, 129, 1300], [600, 0, 129, 900], 2, 1, 64, 16, True),     # empty, one past a tile, whole prompts
+    ([2500, 333], [200, 333], 12, 3, 128, 32, False),
+    ([65, 1], [65, 1], 32, 1, 128, 128, False),                        # a bare tile
+    ([5000], [1030], 4, 4, 128, 256, False)])
+def test_attend_e4m3_chunks_widened_or_not(pkg, lens_k, lens_q, hq, hkv, dim, page, head_major, causal):
+    """Long chunks read a bf16 copy of the sequences, unless a bound on the
+    lengths asks for too much scratch memory; the exact copy of the writer's
+    values keeps the bound either way."""
+    p = R.make(lens_k, lens_q, hq, hkv, dim, page, fp8=True, packed=True, head_major=head_major, seed=36)
+    wide = torch.full((len(lens_k), (1 << 21) // page), -1, dtype=torch.int32, device="cuda")
+    wide[:, :p.table.shape[1]] = p.table
+    for table in (p.table, wide):
+        o, lse = pkg.paged_forward(p.q, p.k_cache, p.v_cache, table, p.seqlens, causal=causal, cu_seqlens_q=p.cu_q,
+                                   max_seqlen_q=max(lens_q), **p.scales)
+        pkg.check()
+        R.check_attend(p, o, lse, causal)
+
+
 @pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
 def test_rows_on_16_byte_boundaries_only(pkg, fp8):
     """New rows, outputs and q whose strides are odd multiples of 16 bytes."""
