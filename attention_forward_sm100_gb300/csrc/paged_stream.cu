@@ -558,7 +558,9 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   // within 2^-4 of it, weights (times scale / vref * 2^7, at most 2^15) and codes
   // are multiplied as f16: its spacing near zero, 2^-24, then costs a key less
   // than 2^-28 of the largest weight, so 2^20 keys less than bf16's rounding.
-  // Steps with smaller scales go through bf16.
+  // Steps with smaller scales go through bf16. vref is 2^-100 at least: 128 / vref
+  // stays finite, and a weight times the smallest scale, 2^-126, keeps bf16's bits.
+  constexpr float kLeastVref = 0x1p-100f;
   float vref = 0.f, vinv = 0.f;
   float m[NT][2], l[NT][2];
 #pragma unroll
@@ -719,7 +721,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
         for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         // the next power of two (an infinite or huge scale: 2^127; NaN leaves it)
         const uint32_t up = min(((__float_as_uint(top) + 0x7fffffu) >> 23), 254u) << 23;
-        const float now = fmaxf(vref, __uint_as_float(max(up, 1u << 23)));
+        const float now = fmaxf(vref, fmaxf(__uint_as_float(up), kLeastVref));
         const float change = vref == 0.f ? 0.f : vref / now;
         vref = now;
         vinv = 128.f / now;
