@@ -38,11 +38,24 @@ struct Slot {
 };
 
 // The sequence of row t, for the lanes of one warp with consecutive rows from
-// t0 on (offsets cu[0 .. batch]); `batch` if it lies behind the last one.
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t t0, int64_t t) {
-  int b = 0;
-  for (int c = threadIdx.x & 31; c < batch; c += 32) b += (int64_t)cu[c + 1] <= t0 ? 1 : 0;
+// t0 on (offsets cu[0 .. batch] into `rows` rows); `batch` if it lies behind the
+// last one. Every block looks at all offsets: where they decrease, rows cannot
+// be told apart, and none has a sequence. The first block records the first
+// sequence whose offsets are wrong, whether or not it has a row that is there.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t t0, int64_t t, int64_t rows,
+                                             uint32_t* ws) {
+  int b = 0, wrong = batch;
+  bool back = false;
+  for (int c = threadIdx.x & 31; c < batch; c += 32) {
+    const int a = cu[c], e = cu[c + 1];
+    b += (int64_t)e <= t0 ? 1 : 0;
+    back = back || e < a;
+    if (a < 0 || e < a || e > rows) wrong = min(wrong, c);
+  }
   b = __reduce_add_sync(0xffffffffu, b);
+  wrong = __reduce_min_sync(0xffffffffu, wrong);
+  if (wrong < batch && blockIdx.x == 0 && threadIdx.x == 0) record_bad_cache(ws, wrong);
+  if (__any_sync(0xffffffffu, back)) return batch;
   while (b < batch && (int64_t)cu[b + 1] <= t) ++b;
   return b;
 }
@@ -140,13 +153,13 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         int b, i, lq = P.s.seqlen_q;
         bool ok = (int)threadIdx.x < tokens;
         if (packed) {
-          b = find_sequence(P.s.cu_q, P.s.batch, t0, t);
+          b = find_sequence(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws);
           ok = ok && b < P.s.batch;                // else behind the last sequence
           if (ok) {
             const int a = P.s.cu_q[b], e = P.s.cu_q[b + 1];
             i = (int)(t - a);
             lq = e - a;
-            if (a < 0 || i < 0 || e > P.tokens) {  // offsets out of order or past the rows
+            if (a < 0 || i < 0 || e > P.tokens) {  // offsets below zero or past the rows
               record_bad_cache(P.ws, b);
               ok = false;
             }
@@ -231,13 +244,12 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
   if (threadIdx.x < 32) {
-    if (blockIdx.x == 0 && P.batch > 0 && P.cu_k[P.batch] > P.total_k) record_bad_cache(P.ws, P.batch - 1);
     Slot s = {-1, 0};
     const int64_t t = t0 + threadIdx.x;
-    const int b = find_sequence(P.cu_k, P.batch, t0, t);
+    const int b = find_sequence(P.cu_k, P.batch, t0, t, P.total_k, P.ws);
     if ((int)threadIdx.x < tokens && b < P.batch) {
-      // offsets that are out of order (or below zero) leave a row in front of
-      // its sequence's start, or past what the table can hold
+      // an offset below zero: the position is none; a row in front of its
+      // sequence's start has none either
       const int a = P.cu_k[b];
       s = slot_of(P.c, b, a < 0 ? -1 : (int)(t - a), P.ws);
     }

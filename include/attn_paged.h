@@ -40,8 +40,9 @@
  * What only the device can see is checked there and reported through
  * attn_fwd_check(workspace): lengths out of range, offsets out of order, page
  * numbers outside the cache. Such a call touches no memory outside the
- * tensors: append and read skip the rows concerned, attend computes them from
- * other data (nothing of that call's output can be trusted).
+ * tensors: append and read skip the rows concerned (all rows, where offsets
+ * decrease), attend computes them from other data (nothing of that call's output
+ * can be trusted). A call without rows enqueues nothing, and nothing is checked.
  */
 #ifndef ATTN_PAGED_H
 #define ATTN_PAGED_H

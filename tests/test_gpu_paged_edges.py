@@ -69,3 +69,73 @@ def test_attend_to_what_append_wrote_for_tiny_values(pkg, size):
     for b, (ro, rl, ra) in enumerate(R.attend(p, True)):
         bound = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14) * ra + 2.0 ** -134
         assert ((o[b].double() - ro).abs() <= bound).all()
+
+
+# ---------------------------------------------------------------- offsets
+def _reported(pkg):
+    with pytest.raises(pkg.AttnError, match="paged cache"):
+        pkg.check()
+    pkg.check()
+
+
+WRONG = {
+    # offsets, rows there are, sequences that are right all the same
+    "decreasing_inside": ([0, 10, 5, 20], 20, []),
+    "decreasing_at_the_end": ([0, 10, 15, 5], 20, []),
+    "last_wholly_past_the_rows": ([0, 3, 5, 11], 5, [0, 1]),
+    "last_two_past_the_rows": ([0, 5, 9, 11], 5, [0]),
+    "below_zero": ([-5, 0, 4, 10], 10, [1, 2]),
+}
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("name", list(WRONG))
+def test_append_reports_wrong_offsets(pkg, name, fp8):
+    """Out of order: nothing is written. Past the rows or below zero: the
+    sequences concerned are not written, the others are."""
+    cu, rows, right = WRONG[name]
+    lens = [max(0, cu[b + 1] - cu[b]) if b in right else 0 for b in range(3)]
+    p = R.make([40, 30, 50], lens, 2, 2, 64, 16, fp8=fp8, packed=True, seed=44)
+    g = torch.Generator(device="cuda").manual_seed(45)
+    k, v = (torch.randn(rows, 2, 64, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    p.k_new, p.v_new = (torch.cat([x[cu[b]:cu[b + 1]] for b in right] + [x[:0]]) for x in (k, v))
+    want = R.append(p)
+    pkg.cache_append(k, v, *p.cache, cu_seqlens_q=torch.tensor(cu, dtype=torch.int32, device="cuda"), **p.scales)
+    _reported(pkg)
+    for got, w in zip((p.k_cache, p.v_cache, p.k_scale, p.v_scale), want):
+        assert got is None or torch.equal(R.bits(got), R.bits(w))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("name", ["decreasing_inside", "decreasing_at_the_end", "below_zero"])
+def test_read_reports_wrong_offsets(pkg, name, fp8):
+    cu, rows, right = WRONG[name]
+    p = R.make([40, 30, 50], [0] * 3, 2, 2, 64, 16, fp8=fp8, packed=True, seed=46)
+    out = [torch.full((rows, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    want = [x.clone() for x in out]
+    for b in right:
+        for w, x in zip(want, R.gather(p, b)):
+            w[cu[b]:cu[b + 1]] = x[:cu[b + 1] - cu[b]].to(torch.bfloat16)
+    pkg.cache_read(p.k_cache, p.v_cache, p.table, torch.tensor(cu, dtype=torch.int32, device="cuda"), out_k=out[0],
+                   out_v=out[1], **p.scales)
+    _reported(pkg)
+    assert torch.equal(R.bits(out[0]), R.bits(want[0])) and torch.equal(R.bits(out[1]), R.bits(want[1]))
+
+
+def test_wrong_offsets_among_many_sequences(pkg):
+    """Found wherever they are, and by calls whose rows all lie in front of them."""
+    n = 300
+    p = R.make([20] * n, [1] * n, 1, 1, 64, 16, packed=True, seed=47)
+    before = p.k_cache.clone()
+    cu = p.cu_q.clone()
+    cu[277] = 3
+    pkg.cache_append(p.k_new, p.v_new, *p.cache, cu_seqlens_q=cu)
+    with pytest.raises(pkg.AttnError, match="sequence 276"):
+        pkg.check()
+    pkg.cache_append(p.k_new[:7], p.v_new[:7], *p.cache, cu_seqlens_q=cu)
+    _reported(pkg)
+    assert torch.equal(R.bits(p.k_cache), R.bits(before))
+    out = torch.full((n, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, out_k=out, out_v=out.clone())
+    _reported(pkg)
+    assert bool((out == 7.0).all())
