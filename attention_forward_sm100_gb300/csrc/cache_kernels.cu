@@ -159,10 +159,9 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
             const int a = P.s.cu_q[b], e = P.s.cu_q[b + 1];
             i = (int)(t - a);
             lq = e - a;
-            if (a < 0 || i < 0 || e > P.tokens) {  // offsets below zero or past the rows
-              record_bad_cache(P.ws, b);
-              ok = false;
-            }
+            // (rows in front of the first sequence; offsets below zero or past
+            // the rows, which are recorded)
+            ok = a >= 0 && i >= 0 && e <= P.tokens;
           }
         } else {
           token_at(threadIdx.x, b, i);
@@ -248,10 +247,10 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     const int64_t t = t0 + threadIdx.x;
     const int b = find_sequence(P.cu_k, P.batch, t0, t, P.total_k, P.ws);
     if ((int)threadIdx.x < tokens && b < P.batch) {
-      // an offset below zero: the position is none; a row in front of its
-      // sequence's start has none either
       const int a = P.cu_k[b];
-      s = slot_of(P.c, b, a < 0 ? -1 : (int)(t - a), P.ws);
+      // (else an offset below zero, which is recorded, or a row in front of the
+      // first sequence)
+      if (a >= 0 && t >= a) s = slot_of(P.c, b, (int)(t - a), P.ws);
     }
     slots[threadIdx.x] = s;
   }

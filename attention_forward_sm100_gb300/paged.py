@@ -54,7 +54,8 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, *, k_scale=None
     """Writes the new tokens' keys and values into the cache, in place.
 
     ``k`` and ``v`` are bf16, [B, Sq, Hkv, D], or packed [T, Hkv, D] with int32
-    ``cu_seqlens_q`` (rows behind the last sequence are ignored).
+    ``cu_seqlens_q`` (rows in front of the first sequence and behind the last
+    one are ignored).
     ``seqlens_k`` (int32 [B]) counts each sequence's tokens with the new ones:
     token i of Lq goes to position seqlens_k - Lq + i. Into an e4m3 cache each
     (token, head) vector is rounded with its own scale, the smallest power of
@@ -79,8 +80,8 @@ def cache_read(k_cache, v_cache, block_table, cu_seqlens_k, *, total_k=None, k_s
     Rows ``cu_seqlens_k[b]`` to ``cu_seqlens_k[b + 1]`` (int32 [B + 1]) receive
     positions 0, 1, ... of sequence b; an e4m3 cache gives code * scale,
     rounded once. ``total_k`` is the number of rows to allocate; or pass
-    ``out_k`` and ``out_v``, whose rows behind the last sequence stay as they
-    are. A row whose position or page is out of range is not written and
+    ``out_k`` and ``out_v``, whose rows in front of the first sequence and behind
+    the last one stay as they are. A row whose position or page is out of range is not written and
     reported by ``check``. Asynchronous on ``stream`` (default: the current
     torch stream).
     """
@@ -101,8 +102,8 @@ def paged_forward(q, k_cache, v_cache, block_table, seqlens_k, *, causal=True, s
     ``q`` is bf16, [B, Sq, Hq, D] -> O [B, Sq, Hq, D] bf16, LSE [B, Hq, Sq]
     fp32; or packed [T, Hq, D] with int32 ``cu_seqlens_q`` and ``max_seqlen_q``
     (an upper bound of every sequence's new tokens) -> O [T, Hq, D], LSE
-    [Hq, T] (rows behind the last sequence stay as they are). ``seqlens_k``
-    (int32 [B]) counts each sequence's cached tokens, the new ones included
+    [Hq, T] (rows in front of the first sequence and behind the last one stay as
+    they are). ``seqlens_k`` (int32 [B]) counts each sequence's cached tokens, the new ones included
     (append them first). ``causal``: new token i of Lq sees positions up to
     seqlens_k - Lq + i; otherwise all. Rows that see nothing get O = 0 and
     LSE = -inf. ``max_seqlen_k`` bounds the cached lengths (default: what

@@ -82,8 +82,8 @@ typedef struct attn_cache_append_params {
   const void *k;               /* bf16 new rows: fixed [B][Sq][Hkv][D] / packed [Tq][Hkv][D] */
   const void *v;
   const int32_t *seqlens_k;    /* [B]: tokens in the cache, the new ones included */
-  const int32_t *cu_seqlens_q; /* packed only: [B+1] offsets of the new rows; rows at or past
-                                  cu_seqlens_q[B] are ignored */
+  const int32_t *cu_seqlens_q; /* packed only: [B+1] offsets of the new rows; rows in front of
+                                  cu_seqlens_q[0] and from cu_seqlens_q[B] on are ignored */
   void *workspace;             /* ATTN_FWD_WORKSPACE_BYTES, as attn_fwd_params.workspace: the
                                   device error record */
   int64_t k_stride[3];         /* elements: [0] batch (unused when packed), [1] token, [2] head */
@@ -96,8 +96,9 @@ typedef struct attn_cache_read_params {
   attn_kv_cache cache;
   void *k;                     /* bf16 rows, written: [Tk][Hkv][D] */
   void *v;
-  const int32_t *cu_seqlens_k; /* [B+1] offsets of each sequence's rows; rows at or past
-                                  cu_seqlens_k[B] are left as they are */
+  const int32_t *cu_seqlens_k; /* [B+1] offsets of each sequence's rows; rows in front of
+                                  cu_seqlens_k[0] and from cu_seqlens_k[B] on are left as
+                                  they are */
   void *workspace;             /* the device error record, see append */
   int64_t k_stride[2];         /* elements: [0] token, [1] head */
   int64_t v_stride[2];
@@ -110,8 +111,8 @@ typedef struct attn_paged_params {
   void *o;                     /* bf16, the same shape, written */
   float *lse;                  /* fixed [B][Hq][Sq] / packed [Hq][Tq] contiguous, written; may be NULL */
   const int32_t *seqlens_k;    /* [B]: Lk_b */
-  const int32_t *cu_seqlens_q; /* packed only: [B+1]; rows of o at or past cu_seqlens_q[B] are left
-                                  as they are */
+  const int32_t *cu_seqlens_q; /* packed only: [B+1]; rows of o in front of cu_seqlens_q[0] and
+                                  from cu_seqlens_q[B] on are left as they are */
   void *workspace;             /* >= attn_paged_workspace_bytes(p), 256-byte aligned; its first
                                   ATTN_PAGED_ZEROED_BYTES zero-filled once before its first use
                                   (every call leaves them zeroed). Calls that share a workspace

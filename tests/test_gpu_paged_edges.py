@@ -1,4 +1,6 @@
 """Calls of the paged-cache operators at the edges of what they accept."""
+import math
+
 import pytest
 import torch
 
@@ -139,3 +141,33 @@ def test_wrong_offsets_among_many_sequences(pkg):
     pkg.cache_read(p.k_cache, p.v_cache, p.table, cu, out_k=out, out_v=out.clone())
     _reported(pkg)
     assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_rows_in_front_of_the_first_sequence(pkg, fp8):
+    """Offsets that start late (a part of a larger batch): the rows in front of
+    them belong to nobody, as those behind the last sequence."""
+    p = R.make([70, 9, 200], [70, 1, 30], 4, 2, 64, 16, fp8=fp8, packed=True, seed=48)
+    want = R.append(p)
+    pad = torch.full((13, 2, 64), math.nan, dtype=torch.bfloat16, device="cuda")
+    cu = p.cu_q + 13
+    pkg.cache_append(torch.cat([pad, p.k_new]), torch.cat([pad, p.v_new]), *p.cache, cu_seqlens_q=cu, **p.scales)
+    pkg.check()
+    for got, w in zip((p.k_cache, p.v_cache, p.k_scale, p.v_scale), want):
+        assert got is None or torch.equal(R.bits(got), R.bits(w))
+    lens = p.lens_k
+    cu_k = torch.tensor([13 + sum(lens[:b]) for b in range(4)], dtype=torch.int32, device="cuda")
+    out = [torch.full((13 + sum(lens) + 2, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pkg.cache_read(p.k_cache, p.v_cache, p.table, cu_k, out_k=out[0], out_v=out[1], **p.scales)
+    pkg.check()
+    both = [torch.cat(x).to(torch.bfloat16) for x in zip(*(R.gather(p, b) for b in range(3)))]
+    for got, w in zip(out, both):
+        assert torch.equal(got[13:-2], w) and bool((got[:13] == 7.0).all()) and bool((got[-2:] == 7.0).all())
+    q = torch.cat([torch.full((13, 4, 64), math.nan, dtype=torch.bfloat16, device="cuda"), p.q])
+    o = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, q.shape[0]), 7.0, device="cuda")
+    for most in (70, 200):
+        pkg.paged_forward(q, *p.cache, cu_seqlens_q=cu, max_seqlen_q=most, out=o, lse=lse, **p.scales)
+        pkg.check()
+        R.check_attend(p, o[13:], lse[:, 13:], True)
+        assert bool((o[:13] == 7.0).all()) and bool((lse[:, :13] == 7.0).all())
