@@ -126,7 +126,15 @@ attn_status check_read(const attn_cache_read_params* p) {
 }
 
 bool no_rows(const attn_paged_params* p) {
-  return p->cache.batch == 0 || p->seqlen_q == 0 || (p->cu_seqlens_q != nullptr && p->total_q == 0);
+  return p->cache.batch == 0 || (p->cu_seqlens_q != nullptr ? p->total_q : p->seqlen_q) == 0;
+}
+
+// Packed rows under a bound of no new tokens may belong to nobody, or the bound is
+// wrong, which the device finds out: planned as for one token.
+attn_paged_params planned(const attn_paged_params* p) {
+  attn_paged_params q = *p;
+  if (q.cu_seqlens_q != nullptr && q.seqlen_q == 0) q.seqlen_q = 1;
+  return q;
 }
 
 // Everything but the workspace.
@@ -522,14 +530,16 @@ attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t strea
 
 size_t attn_paged_workspace_bytes(const attn_paged_params* p) {
   if (check_paged(p) != ATTN_OK || no_rows(p)) return kZeroedBytes;
-  return workspace_need(p);
+  const attn_paged_params plan = planned(p);
+  return workspace_need(&plan);
 }
 
-attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
+attn_status attn_paged_fwd(const attn_paged_params* params, attn_stream_t stream) {
   report_error(ATTN_OK, "%s", "");
-  attn_status st = check_paged(p);
+  attn_status st = check_paged(params);
   if (st != ATTN_OK) return st;
-  if (no_rows(p)) return ATTN_OK;
+  if (no_rows(params)) return ATTN_OK;
+  const attn_paged_params with_rows = planned(params), *p = &with_rows;
   if ((st = check_workspace(p->workspace)) != ATTN_OK) return st;
   const size_t need = workspace_need(p);
   if (p->workspace_bytes < need)

@@ -171,3 +171,15 @@ def test_rows_in_front_of_the_first_sequence(pkg, fp8):
         pkg.check()
         R.check_attend(p, o[13:], lse[:, 13:], True)
         assert bool((o[:13] == 7.0).all()) and bool((lse[:, :13] == 7.0).all())
+
+
+def test_a_bound_of_no_new_tokens(pkg):
+    """max_seqlen_q = 0 where sequences have new tokens is a wrong bound like any other."""
+    p = R.make([40, 30], [2, 3], 4, 2, 64, 16, packed=True, seed=49)
+    out = torch.full(p.q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    pkg.paged_forward(p.q, *p.cache, cu_seqlens_q=p.cu_q, max_seqlen_q=0, out=out)
+    _reported(pkg)
+    out.fill_(7.0)
+    pkg.paged_forward(p.q, *p.cache, cu_seqlens_q=torch.zeros_like(p.cu_q), max_seqlen_q=0, out=out)
+    pkg.check()
+    assert bool((out == 7.0).all())
