@@ -1344,13 +1344,15 @@ __device__ void role_softmax(const Tc05Params& P, const Ctx& c, const int i) {
     // Row statistics: LSE (natural log) here, 1/l to the epilogue. A split-KV
     // range writes the LSE of its own keys for the merge.
     float* const lse_dst = partial ? P.lse_part : P.lse;
+    // (paged: a row with a NaN score is NaN, not one that sees nothing)
+    const bool some = T::PAGED ? l != 0.f : l > 0.f;
     if (row_valid && lse_dst != nullptr) {
-      const float lse = l > 0.f ? (m + ptx::lg2(l)) * 0.69314718055994531f : -INFINITY;
+      const float lse = some ? (m + ptx::lg2(l)) * 0.69314718055994531f : -INFINITY;
       lse_dst[lse_idx] = lse;
     }
     if (!wait_warp(c, BAR_STATS_FREE + i, stats_phase ^ 1u, role)) return;
     stats_phase ^= 1u;
-    rcpl_sm[tid] = l > 0.f ? 1.f / l : 0.f;
+    rcpl_sm[tid] = some ? 1.f / l : 0.f;
     ptx::mbar_arrive(c.bar(BAR_STATS + i));
   }
 }

@@ -183,3 +183,30 @@ def test_a_bound_of_no_new_tokens(pkg):
     pkg.paged_forward(p.q, *p.cache, cu_seqlens_q=torch.zeros_like(p.cu_q), max_seqlen_q=0, out=out)
     pkg.check()
     assert bool((out == 7.0).all())
+
+
+# ---------------------------------------------------------------- NaN
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("dim,new,lens_k", [(64, 3, [900, 300]), (128, 3, [900, 300]), (64, 130, [900, 300]),
+                                            (128, 130, [900, 300]), (128, 160, [9000, 300]), (64, 600, [2500, 600])])
+def test_nan_stays_in_its_rows(pkg, dim, new, lens_k, fp8):
+    """A NaN in q makes its (token, head) NaN, O and LSE; a NaN among the keys that
+    every row sees makes its KV head's rows NaN. All others are as ever."""
+    hq, hkv = 4, 2
+    p = R.make(lens_k, [new] * 2, hq, hkv, dim, 16, fp8=fp8, seed=50)
+    p.q[0, 1, 2, 5] = math.nan
+    p.q[1, new - 1, 0, 0] = math.nan
+    p.k_cache[p.table[1, 0].long(), 3, 1, 7] = math.nan     # KV head 1: query heads 2 and 3
+    o, lse = pkg.paged_forward(p.q, *p.cache, **p.scales)
+    pkg.check()
+    bad = torch.zeros(2, hq, new, dtype=torch.bool, device="cuda")
+    bad[0, 2, 1] = bad[1, 0, new - 1] = True
+    bad[1, 2:] = (torch.arange(new, device="cuda") + lens_k[1] - new >= 3)
+    assert torch.equal(torch.isnan(lse), bad)
+    assert torch.equal(torch.isnan(o).any(-1).transpose(1, 2), bad) and torch.equal(torch.isnan(o).all(-1).transpose(1, 2), bad)
+    p.q = p.q.nan_to_num(0.0)
+    for b, (ro, rl, ra) in enumerate(R.attend(p, True)):
+        ok = ~bad[b]
+        off = (o[b].double() - ro).abs() / (2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14) * ra + 1e-6)
+        assert (off.transpose(0, 1)[ok] <= 1.0).all()
+        assert ((lse[b].double() - rl)[ok & torch.isfinite(rl)].abs() <= 5e-5).all()
