@@ -94,7 +94,8 @@ def _compile_native(force: bool) -> str:
     obj = os.path.join(BUILD_DIR, "python_paged.o")
     stamp = obj + ".torch"   # the torch it was compiled against
     known = open(stamp).read() if os.path.exists(stamp) else ""
-    headers = glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__), NATIVE_SRC]
+    headers = glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__), NATIVE_SRC,
+                                                                   os.path.join(CSRC, "paged_host.h")]
     if not force and known == torch.__version__ and os.path.exists(obj) and \
             os.path.getmtime(obj) >= max(os.path.getmtime(f) for f in headers):
         return obj

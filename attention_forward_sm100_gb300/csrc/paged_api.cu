@@ -4,6 +4,7 @@
 #include <string.h>
 
 #include "paged.h"
+#include "paged_host.h"
 #include "schedule.cuh"
 
 namespace {
@@ -306,26 +307,27 @@ WidenPlan plan_widen(const attn_paged_params* p) {
   return w;
 }
 
-size_t workspace_need(const attn_paged_params* p) {
+// Bytes behind the zeroed head.
+size_t scratch_need(const attn_paged_params* p) {
   if (use_tc05(p)) {
     const WidenPlan w = plan_widen(p);
-    return kZeroedBytes + round256(plan_tiles(p).bytes) + w.table + 2 * w.rows;
+    return round256(plan_tiles(p).bytes) + w.table + 2 * w.rows;
   }
   const StreamPlan s = plan_stream(p);
-  return kZeroedBytes + s.ml_bytes + s.o_bytes;
+  return s.ml_bytes + s.o_bytes;
 }
 
 // Stride of a dimension of size 1 (never used, but a tensor map wants a legal one).
 int64_t legal(int64_t stride, int64_t size) { return size > 1 ? stride : 16; }
 
-attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
+attn_status launch_tiles(const attn_paged_params* p, uint8_t* scratch, cudaStream_t stream) {
   const TilePlan plan = plan_tiles(p);
   attn_kv_cache c = p->cache;
   const bool packed = p->cu_seqlens_q != nullptr;
   if (const WidenPlan w = plan_widen(p); w.on) {
     af::WidenParams wp;
     memset(&wp, 0, sizeof(wp));
-    uint8_t* at = static_cast<uint8_t*>(p->workspace) + kZeroedBytes + round256(plan.bytes);
+    uint8_t* at = scratch + round256(plan.bytes);
     wp.c = view_of(c);
     wp.seqlens_k = p->seqlens_k;
     wp.max_k = p->seqlen_k;
@@ -417,7 +419,7 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
   memset(&pp, 0, sizeof(pp));
   cudaError_t e = cudaSuccess;
   if (plan.list) {
-    uint8_t* ws = static_cast<uint8_t*>(p->workspace) + kZeroedBytes;
+    uint8_t* ws = scratch;
     pp.s = {p->cu_seqlens_q, p->seqlens_k, c.batch, p->seqlen_q, p->total_q, p->seqlen_k};
     pp.heads_kv = c.num_heads_kv;
     pp.group = prm.group;
@@ -459,6 +461,60 @@ attn_status launch_tiles(const attn_paged_params* p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+attn_status af::paged_fwd(const attn_paged_params* params, void* scratch, size_t scratch_bytes, cudaStream_t stream) {
+  report_error(ATTN_OK, "%s", "");
+  attn_status st = check_paged(params);
+  if (st != ATTN_OK) return st;
+  if (no_rows(params)) return ATTN_OK;
+  const attn_paged_params with_rows = planned(params), *p = &with_rows;
+  if ((st = check_workspace(p->workspace)) != ATTN_OK) return st;
+  const size_t need = scratch_need(p);
+  if (p->workspace_bytes < kZeroedBytes + (scratch != nullptr ? 0 : need))
+    return report_error(ATTN_ERR_INVALID_ARG, "workspace of at least %zu bytes is required", kZeroedBytes + need);
+  if (scratch != nullptr && (scratch_bytes < need || !aligned(scratch, 256)))
+    return report_error(ATTN_ERR_INVALID_ARG, "scratch memory of at least %zu bytes is required", need);
+  uint8_t* ws = static_cast<uint8_t*>(p->workspace);
+  uint8_t* const room = scratch != nullptr ? static_cast<uint8_t*>(scratch) : ws + kZeroedBytes;
+  if (use_tc05(p)) return launch_tiles(p, room, stream);
+  const StreamPlan plan = plan_stream(p);
+  if (plan.units > 0x3fffffffll) return report_error(ATTN_ERR_UNSUPPORTED, "too much work for one call");
+  const bool packed = p->cu_seqlens_q != nullptr;
+  af::StreamParams a;
+  memset(&a, 0, sizeof(a));
+  a.c = view_of(p->cache);
+  a.s.cu_q = p->cu_seqlens_q;
+  a.s.seqlens_k = p->seqlens_k;
+  a.s.batch = p->cache.batch;
+  a.s.seqlen_q = p->seqlen_q;
+  a.s.total_q = p->total_q;
+  a.s.max_k = p->seqlen_k;
+  a.q = static_cast<const uint8_t*>(p->q);
+  a.q_b = packed ? 0 : p->q_stride[0] * 2;
+  a.q_t = p->q_stride[1] * 2;
+  a.q_h = p->q_stride[2] * 2;
+  a.o = static_cast<uint16_t*>(p->o);
+  a.o_b = packed ? 0 : p->o_stride[0];
+  a.o_t = p->o_stride[1];
+  a.o_h = p->o_stride[2];
+  a.lse = p->lse;
+  a.heads_q = p->num_heads_q;
+  a.group = p->num_heads_q / p->cache.num_heads_kv;
+  a.causal = p->causal != 0;
+  a.team = plan.team;
+  a.team_heads = p->cache.num_heads_kv / plan.team;
+  a.split = plan.split;
+  a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
+  a.ws = reinterpret_cast<uint32_t*>(ws);
+  a.counters = reinterpret_cast<uint32_t*>(ws + ATTN_FWD_WORKSPACE_BYTES);
+  a.part_ml = reinterpret_cast<float2*>(room);
+  a.part_o = reinterpret_cast<float*>(room + plan.ml_bytes);
+  const cudaError_t e =
+      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
+                              (int)plan.grid, stream);
+  if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
+  return ATTN_OK;
+}
 
 extern "C" {
 
@@ -531,58 +587,11 @@ attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t strea
 size_t attn_paged_workspace_bytes(const attn_paged_params* p) {
   if (check_paged(p) != ATTN_OK || no_rows(p)) return kZeroedBytes;
   const attn_paged_params plan = planned(p);
-  return workspace_need(&plan);
+  return kZeroedBytes + scratch_need(&plan);
 }
 
-attn_status attn_paged_fwd(const attn_paged_params* params, attn_stream_t stream) {
-  report_error(ATTN_OK, "%s", "");
-  attn_status st = check_paged(params);
-  if (st != ATTN_OK) return st;
-  if (no_rows(params)) return ATTN_OK;
-  const attn_paged_params with_rows = planned(params), *p = &with_rows;
-  if ((st = check_workspace(p->workspace)) != ATTN_OK) return st;
-  const size_t need = workspace_need(p);
-  if (p->workspace_bytes < need)
-    return report_error(ATTN_ERR_INVALID_ARG, "workspace of at least %zu bytes is required", need);
-  if (use_tc05(p)) return launch_tiles(p, reinterpret_cast<cudaStream_t>(stream));
-  const StreamPlan plan = plan_stream(p);
-  if (plan.units > 0x3fffffffll) return report_error(ATTN_ERR_UNSUPPORTED, "too much work for one call");
-  const bool packed = p->cu_seqlens_q != nullptr;
-  af::StreamParams a;
-  memset(&a, 0, sizeof(a));
-  a.c = view_of(p->cache);
-  a.s.cu_q = p->cu_seqlens_q;
-  a.s.seqlens_k = p->seqlens_k;
-  a.s.batch = p->cache.batch;
-  a.s.seqlen_q = p->seqlen_q;
-  a.s.total_q = p->total_q;
-  a.s.max_k = p->seqlen_k;
-  a.q = static_cast<const uint8_t*>(p->q);
-  a.q_b = packed ? 0 : p->q_stride[0] * 2;
-  a.q_t = p->q_stride[1] * 2;
-  a.q_h = p->q_stride[2] * 2;
-  a.o = static_cast<uint16_t*>(p->o);
-  a.o_b = packed ? 0 : p->o_stride[0];
-  a.o_t = p->o_stride[1];
-  a.o_h = p->o_stride[2];
-  a.lse = p->lse;
-  a.heads_q = p->num_heads_q;
-  a.group = p->num_heads_q / p->cache.num_heads_kv;
-  a.causal = p->causal != 0;
-  a.team = plan.team;
-  a.team_heads = p->cache.num_heads_kv / plan.team;
-  a.split = plan.split;
-  a.scale_log2 = p->softmax_scale * 1.4426950408889634f;
-  uint8_t* ws = static_cast<uint8_t*>(p->workspace);
-  a.ws = reinterpret_cast<uint32_t*>(ws);
-  a.counters = reinterpret_cast<uint32_t*>(ws + ATTN_FWD_WORKSPACE_BYTES);
-  a.part_ml = reinterpret_cast<float2*>(ws + kZeroedBytes);
-  a.part_o = reinterpret_cast<float*>(ws + kZeroedBytes + plan.ml_bytes);
-  const cudaError_t e =
-      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
-                              (int)plan.grid, reinterpret_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
-  return ATTN_OK;
+attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
+  return af::paged_fwd(p, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -28,6 +28,7 @@
 #include <string>
 
 #include "../../include/attn_paged.h"
+#include "paged_host.h"
 
 namespace {
 
@@ -164,26 +165,48 @@ Buffers& buffers() {
   return *b;
 }
 
-// Scratch of a call on `stream` (current, as is `device`): the stream's own
+void enqueued(cudaError_t e) {
+  if (e != cudaSuccess) throw std::runtime_error(std::string("workspace: ") + cudaGetErrorString(e));
+}
+
+// Bytes of a stream's buffer at most: the partial results of any call (80 MB on
+// 152 SMs) fit. What needs more, the bf16 copy of long e4m3 sequences (up to 1 GiB),
+// takes memory of torch's allocator for the one call.
+constexpr int64_t kKeptBytes = 128ll << 20;
+
+// Workspace of a call on `stream` (current, as is `device`): the stream's own
 // buffer, which grows with need, so calls on different streams never share one.
 // A captured call gets its own from the graph's memory, so that graphs do
 // not share one either.
-at::Tensor workspace_for(c10::DeviceIndex device, cudaStream_t stream, int64_t bytes) {
-  const bool capturing =
-      c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None;
-  at::Tensor* kept = capturing ? nullptr : &buffers()[{device, stream}];
-  if (kept != nullptr && kept->defined() && kept->numel() >= bytes) return *kept;
-  const int64_t zeroed = ATTN_PAGED_ZEROED_BYTES;
-  at::Tensor grown = fresh({std::max(bytes, zeroed)}, at::kByte, device);
-  cudaError_t e;
-  if (kept != nullptr && kept->defined())   // an error that nobody has read yet moves with it
-    e = cudaMemcpyAsync(grown.data_ptr(), kept->data_ptr(), zeroed, cudaMemcpyDeviceToDevice, stream);
-  else
-    e = cudaMemsetAsync(grown.data_ptr(), 0, zeroed, stream);
-  if (e != cudaSuccess) throw std::runtime_error(std::string("workspace: ") + cudaGetErrorString(e));
-  if (kept != nullptr) *kept = grown;
-  return grown;
-}
+struct Workspace {
+  at::Tensor memory;    // its head, and all of it unless that would be more than is kept
+  at::Tensor scratch;   // else the rest, for this call
+
+  void take(c10::DeviceIndex device, cudaStream_t stream, int64_t bytes) {
+    const int64_t zeroed = ATTN_PAGED_ZEROED_BYTES;
+    auto zero_filled = [&](int64_t n) {
+      const at::Tensor t = fresh({n}, at::kByte, device);
+      enqueued(cudaMemsetAsync(t.data_ptr(), 0, zeroed, stream));
+      return t;
+    };
+    if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+      memory = zero_filled(bytes);
+      return;
+    }
+    at::Tensor& kept = buffers()[{device, stream}];
+    const int64_t keep = bytes <= kKeptBytes ? bytes : zeroed;
+    if (!kept.defined()) {
+      kept = zero_filled(keep);
+    } else if (kept.numel() < keep) {
+      const at::Tensor grown = fresh({keep}, at::kByte, device);
+      // an error that nobody has read yet moves with it
+      enqueued(cudaMemcpyAsync(grown.data_ptr(), kept.data_ptr(), zeroed, cudaMemcpyDeviceToDevice, stream));
+      kept = grown;
+    }
+    memory = kept;
+    if (bytes > kKeptBytes) scratch = fresh({bytes - zeroed}, at::kByte, device);
+  }
+};
 
 PyObject* status(attn_status st) { return PyLong_FromLong(st); }
 
@@ -242,13 +265,13 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const c10::DeviceIndex device = check_device(std::array<Arg, 10>{k, v, kc, vc, table, lens, ks, vs, cu, ws});
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
-  at::Tensor own;
-  if (!ws) own = workspace_for(device, stream, ATTN_PAGED_ZEROED_BYTES);
+  Workspace own;
+  if (!ws) own.take(device, stream, ATTN_PAGED_ZEROED_BYTES);
   p.k = k.ptr();
   p.v = v.ptr();
   p.seqlens_k = static_cast<const int32_t*>(lens.ptr());
   p.cu_seqlens_q = static_cast<const int32_t*>(cu.ptr());
-  p.workspace = ws ? ws.ptr() : own.data_ptr();
+  p.workspace = ws ? ws.ptr() : own.memory.data_ptr();
   return status(attn_cache_append(&p, stream));
   PAGED_END
 }
@@ -287,13 +310,14 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const c10::DeviceIndex device = check_device(std::array<Arg, 9>{kc, vc, table, cu, ks, vs, ok, ov, ws});
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
-  at::Tensor fresh_k, fresh_v, own;
+  at::Tensor fresh_k, fresh_v;
+  Workspace own;
   if (!ok) {
     fresh_k = fresh({total, heads, dim}, at::kBFloat16, device);
     fresh_v = fresh({total, heads, dim}, at::kBFloat16, device);
   }
   const Arg k = {"out_k", ok ? ok.t : &fresh_k}, v = {"out_v", ov ? ov.t : &fresh_v};
-  if (!ws) own = workspace_for(device, stream, ATTN_PAGED_ZEROED_BYTES);
+  if (!ws) own.take(device, stream, ATTN_PAGED_ZEROED_BYTES);
   p.k = k.ptr();
   p.v = v.ptr();
   for (int i = 0; i < 2; ++i) {
@@ -301,7 +325,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.v_stride[i] = stride(v, i);
   }
   p.cu_seqlens_k = static_cast<const int32_t*>(cu.ptr());
-  p.workspace = ws ? ws.ptr() : own.data_ptr();
+  p.workspace = ws ? ws.ptr() : own.memory.data_ptr();
   const attn_status st = attn_cache_read(&p, stream);
   if (st != ATTN_OK) return status(st);
   PyObject* r = PyTuple_New(2);
@@ -368,7 +392,8 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const c10::DeviceIndex device = check_device(std::array<Arg, 11>{q, kc, vc, table, lens, ks, vs, cu, out, lse, ws});
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
-  at::Tensor fresh_o, fresh_l, own;
+  at::Tensor fresh_o, fresh_l;
+  Workspace own;
   if (!out) fresh_o = fresh(q->sizes(), at::kBFloat16, device);
   if (!lse && want_lse) fresh_l = fresh(lse_sizes, at::kFloat, device);
   const Arg o = {"out", out ? out.t : &fresh_o};
@@ -388,11 +413,13 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.workspace = ws.ptr();
     p.workspace_bytes = ws->nbytes();
   } else {
-    own = workspace_for(device, stream, (int64_t)attn_paged_workspace_bytes(&p));
-    p.workspace = own.data_ptr();
-    p.workspace_bytes = own.nbytes();
+    own.take(device, stream, (int64_t)attn_paged_workspace_bytes(&p));
+    p.workspace = own.memory.data_ptr();
+    p.workspace_bytes = own.memory.nbytes();
   }
-  const attn_status st = attn_paged_fwd(&p, stream);
+  const attn_status st = own.scratch.defined()
+                             ? af::paged_fwd(&p, own.scratch.data_ptr(), own.scratch.nbytes(), stream)
+                             : attn_paged_fwd(&p, stream);
   if (st != ATTN_OK) return status(st);
   PyObject* r = PyTuple_New(2);
   if (r == nullptr) return nullptr;

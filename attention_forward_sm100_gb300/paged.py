@@ -16,11 +16,13 @@ value is code * scale.
 Lengths, offsets and page numbers live on the device and may change between
 replays of a captured call. What is wrong with them is found there: nothing
 outside the tensors is touched, and ``check`` raises. Scratch memory is kept
-per device and stream, so calls on different streams may overlap; a captured
-call takes its own from the graph's memory, and what its replays find wrong
-is only seen by ``check`` if the call was given a ``workspace``: a contiguous
-tensor that is zero before its first use and that calls which may overlap do
-not share (what a call needs is in the error that refuses too small a one).
+per device and stream (up to 128 MiB; what a call needs beyond that goes back
+to torch's allocator with the call), so calls on different streams may overlap;
+a captured call takes its own from the graph's memory, and what its replays
+find wrong is only seen by ``check`` if the call was given a ``workspace``: a
+contiguous tensor that is zero before its first use and that calls which may
+overlap do not share (what a call needs is in the error that refuses too small
+a one).
 
 Arguments are checked and marshalled by the extension module _paged_native
 (csrc/python_paged.cpp).
@@ -110,8 +112,8 @@ def paged_forward(q, k_cache, v_cache, block_table, seqlens_k, *, causal=True, s
     block_table can hold); a tighter bound only helps to plan the launch.
     D is 64 or 128; D ** -0.5 is the default ``softmax_scale``. Slots past a
     sequence's length may hold anything. Long chunks over an e4m3 cache take up
-    to 1 GiB of scratch memory (a bf16 copy of the sequences; none if
-    ``max_seqlen_k`` times B needs more). Asynchronous on ``stream`` (default:
+    to 1 GiB of scratch memory while they run (a bf16 copy of the sequences; none
+    if ``max_seqlen_k`` times B needs more). Asynchronous on ``stream`` (default:
     the current torch stream).
     """
     native = _binding.paged_native()

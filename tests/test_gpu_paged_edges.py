@@ -210,3 +210,54 @@ def test_nan_stays_in_its_rows(pkg, dim, new, lens_k, fp8):
         off = (o[b].double() - ro).abs() / (2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14) * ra + 1e-6)
         assert (off.transpose(0, 1)[ok] <= 1.0).all()
         assert ((lse[b].double() - rl)[ok & torch.isfinite(rl)].abs() <= 5e-5).all()
+
+
+# ---------------------------------------------------------------- scratch memory
+def _long_chunk():
+    """e4m3, 600 rows to a KV head, a table of 131072 tokens: a copy of 512 MiB."""
+    p = R.make([3000, 900], [300] * 2, 8, 4, 128, 64, fp8=True, seed=54)
+    table = torch.full((2, 131072 // 64), -1, dtype=torch.int32, device="cuda")
+    table[:, :p.table.shape[1]] = p.table
+    return p, table
+
+
+def test_a_long_chunk_keeps_no_large_scratch(pkg):
+    """Its memory goes back to the allocator with the call; results, and the
+    calls after it, are as ever."""
+    p, table = _long_chunk()
+    small = R.make([700, 90], [1] * 2, 8, 2, 64, 16, seed=55)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        want = pkg.paged_forward(small.q, *small.cache)
+        held = torch.cuda.memory_allocated()
+        o, lse = pkg.paged_forward(p.q, p.k_cache, p.v_cache, table, p.seqlens, **p.scales)
+        grown = torch.cuda.memory_allocated() - held - o.nbytes - lse.nbytes
+        assert torch.cuda.max_memory_allocated() - held > 512 << 20      # (the copy was made)
+        got = pkg.paged_forward(small.q, *small.cache)
+        o2, lse2 = pkg.paged_forward(p.q, p.k_cache, p.v_cache, table, p.seqlens, **p.scales)
+        pkg.check()
+    R.check_attend(p, o, lse, True)
+    assert torch.equal(R.bits(o), R.bits(o2)) and torch.equal(R.bits(lse), R.bits(lse2))
+    for x, y in zip(want, got):
+        assert torch.equal(R.bits(x), R.bits(y))
+    assert grown <= 128 << 20
+
+
+def test_what_a_long_chunk_finds_wrong_is_reported(pkg):
+    """Its own errors, and one that nobody has read when it starts."""
+    p, table = _long_chunk()
+    bad = table.clone()
+    bad[1, 2] = -3
+    pkg.paged_forward(p.q, p.k_cache, p.v_cache, bad, p.seqlens, **p.scales)
+    with pytest.raises(pkg.AttnError, match="sequence 1"):
+        pkg.check()
+    pkg.check()
+    small = R.make([700, 90], [1] * 2, 8, 2, 64, 16, seed=55)
+    small.table[0, 0] = -1
+    pkg.paged_forward(small.q, *small.cache)
+    o, lse = pkg.paged_forward(p.q, p.k_cache, p.v_cache, table, p.seqlens, **p.scales)
+    with pytest.raises(pkg.AttnError, match="sequence 0"):
+        pkg.check()
+    pkg.check()
+    R.check_attend(p, o, lse, True)
