@@ -67,7 +67,8 @@
 //     D = 128 (QSPLIT) K stays e4m3, gathered by TMA, and it is Q that changes:
 //     warpgroup 2 writes q = 2^e (q1 + q2) with e4m3 q1 and q2 (a bf16 has
 //     eight significant bits, an e4m3 four: q2 takes what q1 leaves, exactly
-//     for values above 2^-11 of their row's largest, to 2^-19 of it below), and
+//     for values above 2^-9 of their row's largest, to 2^-17 of it below: a row's
+//     largest is brought to (224, 448], and e4m3's steps end at 2^-9), and
 //     S = Q1 K^T + Q2 K^T costs what the bf16 product does. The key scales
 //     (copied next to K into a four-tile ring) and 2^e multiply the fp32 scores.
 // Every wait is bounded: on timeout the CTA records an error in the

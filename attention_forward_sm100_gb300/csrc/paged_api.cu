@@ -285,7 +285,8 @@ StreamPlan plan_stream(const attn_paged_params* p) {
 // 512: 230 / 265, 2048: 711 / 897; four ragged sequences of up to 12000 keys and 1023
 // new tokens 372 / 468, d64 316 / 422; with 32 KV heads 485 / 480, of up to 512 new
 // tokens (R about 300 on average) 386 / 342. Not where the scratch memory would
-// pass kWidenBytes.
+// pass kWidenBytes. K is rounded to bf16 with it (D = 128: without it not), which
+// scales that are powers of two do not notice.
 constexpr int64_t kWidenRows = 512, kWidenBytes = 1ll << 30;
 struct WidenPlan {
   bool on;

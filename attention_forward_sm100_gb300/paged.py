@@ -111,9 +111,13 @@ def paged_forward(q, k_cache, v_cache, block_table, seqlens_k, *, causal=True, s
     LSE = -inf. ``max_seqlen_k`` bounds the cached lengths (default: what
     block_table can hold); a tighter bound only helps to plan the launch.
     D is 64 or 128; D ** -0.5 is the default ``softmax_scale``. Slots past a
-    sequence's length may hold anything. Long chunks over an e4m3 cache take up
-    to 1 GiB of scratch memory while they run (a bf16 copy of the sequences; none
-    if ``max_seqlen_k`` times B needs more). Asynchronous on ``stream`` (default:
+    sequence's length may hold anything; cached values that the causal mask hides
+    must be finite. Long chunks over an e4m3 cache take up to 1 GiB of scratch
+    memory while they run (a bf16 copy of the sequences; none if ``max_seqlen_k``
+    times B needs more). More than 32 rows (new tokens times Hq / Hkv) round
+    code * scale of an e4m3 V to bf16, and of K too with D = 64 or where that copy
+    is made: without effect for scales that are powers of two, as
+    ``cache_append`` writes them. Asynchronous on ``stream`` (default:
     the current torch stream).
     """
     native = _binding.paged_native()

@@ -26,10 +26,20 @@
  *           (the causal mask is aligned to the END of the keys: the new
  *           tokens are the last ones cached). The weights are rounded to bf16
  *           before the P.V product, as in attn_fwd (to f16 where an e4m3 cache
- *           allows); sums and the softmax statistics are fp32. From 33 rows
- *           (Lq_b * Hq / Hkv) on, code * scale of an e4m3 V, and with D = 64 of K
- *           too, is rounded to bf16 once, which changes nothing when scales are
- *           powers of two, as append's are. Rows with an empty J_i get O_i = 0 and
+ *           allows); sums and the softmax statistics are fp32. Over an e4m3 cache,
+ *           calls of more than 32 rows (seqlen_q * Hq / Hkv) round more:
+ *             V: code * scale, to bf16, once.
+ *             K, D = 64: the same.
+ *             K, D = 128: the same where the sequences have 512 rows or more in the
+ *               mean and the bf16 copy of them that is then made takes 1 GiB at
+ *               most (4 * Hkv * D bytes for each of B * seqlen_k tokens, seqlen_k
+ *               rounded up to 128). Else K is exact, and q is 2^e (q1 + q2) with
+ *               e4m3 q1 and q2: exact for values above 2^-9 of the row's largest,
+ *               within 2^-17 of the largest below.
+ *           Rounding code * scale to bf16 changes nothing when scales are powers of
+ *           two, as append's are (but for products below bf16's subnormals, 2^-133);
+ *           other scales move a score by up to 2^-8 of scale * sum_d |q_id K_jd|.
+ *           Rows with an empty J_i get O_i = 0 and
  *           LSE_i = -inf. Slots at or past position Lk_b are never used, they
  *           may hold anything; cached values in front of Lk_b that the causal
  *           mask hides must be finite (their weight is zero).

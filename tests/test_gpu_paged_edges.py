@@ -261,3 +261,59 @@ def test_what_a_long_chunk_finds_wrong_is_reported(pkg):
         pkg.check()
     pkg.check()
     R.check_attend(p, o, lse, True)
+
+
+# ---------------------------------------------------------------- scales that are no powers of two, in chunks
+def _score_error(p, b, scale, split):
+    """Bound of a score's error: fp32 products and sums in steps of 16 depths (a
+    tensor core may truncate, 2^-23 a step), the exponent's two roundings, and
+    where q is split in two e4m3 parts 2^-17 of a row's largest value on the
+    values below 2^-9 of it."""
+    k, _ = R.gather(p, b)
+    q = R.rows_of(p, p.q, b).double()
+    group = q.shape[1] // k.shape[1]
+    worst = 0.0
+    for h in range(q.shape[1]):
+        kh = k[:, h // group].abs()
+        size = (q[:, h].abs() @ kh.t()).max().item() * scale
+        ds = (q.shape[2] / 16 + 6) * 2.0 ** -23 * size
+        if split:
+            top = q[:, h].abs().amax(-1, keepdim=True)
+            lost = torch.where(q[:, h].abs() < 2.0 ** -9 * top, 2.0 ** -17 * top, 0.0)
+            ds += (lost @ kh.t()).max().item() * scale
+        worst = max(worst, ds)
+    return worst
+
+
+@pytest.mark.parametrize("wide_table", [False, True], ids=["tight", "wide"])
+@pytest.mark.parametrize("dim,new", [(128, 100), (128, 140), (64, 100), (64, 140)])
+def test_chunks_over_scales_of_any_value(pkg, dim, new, wide_table):
+    """Scales as amax / 448 gives them. code * scale of V is rounded to bf16
+    (2^-8 of every value), that of K with D = 64, and with D = 128 where 512 rows
+    or more (four query heads: 128 new tokens) read a bf16 copy, which a bound on
+    the lengths that asks for more than 1 GiB turns off; a score then moves by
+    at most 2^-8 * scale * sum |q k|."""
+    p = R.make([new, 700], [new] * 2, 8, 2, dim, 16, fp8=True, seed=52)
+    g = torch.Generator().manual_seed(53)
+    for s, factor in ((p.k_scale, 2.0 ** -7), (p.v_scale, 2.0 ** -6)):
+        held = ~torch.isnan(s)
+        s[held] = ((torch.rand(int(held.sum()), generator=g) + 0.5) * factor).cuda()
+    table = p.table
+    if wide_table:
+        table = torch.full((2, (1 << 21) // 16), -1, dtype=torch.int32, device="cuda")
+        table[:, :p.table.shape[1]] = p.table
+    o, lse = pkg.paged_forward(p.q, p.k_cache, p.v_cache, table, p.seqlens, **p.scales)
+    pkg.check()
+    rounds_k = dim == 64 or (new * 4 >= 512 and not wide_table)
+    for b, (ro, rl, ra) in enumerate(R.attend(p, True)):
+        ds = 0.0
+        if rounds_k:
+            k, _ = R.gather(p, b)
+            ds = max(2.0 ** -8 * dim ** -0.5 * (p.q[b, :, h].double().abs() @ k[:, h // 4].abs().t()).max().item()
+                     for h in range(8))
+        else:
+            ds = _score_error(p, b, dim ** -0.5, True)
+        grow = math.expm1(2 * ds)
+        bound = 2.0 ** -8 * ro.abs() + (2 * 2.0 ** -8 + 2.0 ** -14 + grow) * ra * (1 + grow) + 1e-6
+        assert ((o[b].double() - ro).abs() <= bound).all()
+        assert (lse[b].double() - rl).abs().max().item() <= 5e-5 + ds
