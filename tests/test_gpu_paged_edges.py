@@ -317,3 +317,25 @@ def test_chunks_over_scales_of_any_value(pkg, dim, new, wide_table):
         bound = 2.0 ** -8 * ro.abs() + (2 * 2.0 ** -8 + 2.0 ** -14 + grow) * ra * (1 + grow) + 1e-6
         assert ((o[b].double() - ro).abs() <= bound).all()
         assert (lse[b].double() - rl).abs().max().item() <= 5e-5 + ds
+
+
+# ---------------------------------------------------------------- large scores
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("dim,new,lens_k", [(64, 3, [700, 90]), (128, 3, [700, 90]), (64, 10, [1700, 90]),
+                                            (64, 130, [700, 130]), (128, 130, [700, 130]), (128, 200, [9000, 200]),
+                                            (64, 600, [2500, 600]), (128, 600, [2500, 600])])
+def test_values_under_large_scores(pkg, dim, new, lens_k, fp8):
+    """Scores in the thousands, in random order: every move of the running
+    maximum has to rescale what is summed so far, by a power of two with hundreds
+    for its exponent. O and LSE within the bound that the score's error (2 ds in
+    the exponent; ds is 0.02, or 0.3 where q is split) and the roundings imply."""
+    p = R.make(lens_k, [new] * 2, 4, 2, dim, 16, fp8=fp8, seed=51)
+    p.q *= 200
+    o, lse = pkg.paged_forward(p.q, *p.cache, softmax_scale=1.0, **p.scales)
+    pkg.check()
+    for b, (ro, rl, ra) in enumerate(R.attend(p, True, 1.0)):
+        ds = _score_error(p, b, 1.0, fp8 and dim == 128)
+        grow = math.expm1(2 * ds)
+        bound = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14 + grow) * ra * (1 + grow) + 1e-6
+        assert ((o[b].double() - ro).abs() <= bound).all()
+        assert ((lse[b].double() - rl).abs() <= ds + 2.0 ** -20 + 2.0 ** -23 * rl.abs()).all()
