@@ -239,8 +239,11 @@ struct StreamPlan {
 // GQA 32/8, d128, us cut / whole: 12 sequences of up to 300 keys, bf16: 12.8 / 7.0;
 // 32 sequences of up to 1000 keys, bf16 22.7 / 17.5, e4m3 21.2 / 14.9; 8 of them
 // 13.7 / 13.6; 75 of them 36.7 / 34.6; but 3 of them 9.1 / 12.3, 256 of them 94 / 112.
+// Where the bound on the lengths allows more key tiles than the device counts (in
+// 32 bits), segments, which are then thousands, are left whole too.
 constexpr int kUnsplitTiles = 4;
 constexpr int kUnsplitKeys = 1024;
+constexpr int64_t kMaxUnits = 0x3fffffff;
 // Of cut segments, the CTAs of a team take different heads of the same keys, so
 // that what HBM is asked for at one time lies together; unteamed, CTAs read
 // strided rows of one head each. The team is the largest divisor of Hkv up to 16
@@ -260,7 +263,7 @@ StreamPlan plan_stream(const attn_paged_params* p) {
   const int64_t tiles = af::tiles_for(p->seqlen_k, af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
   const int64_t ctas = (int64_t)af::stream_ctas(row_bytes, s.row_tile) * af::sm_count();
   const bool one_wave = 4 * segments >= ctas && segments <= 2 * ctas;
-  s.split = tiles > kUnsplitTiles && !(one_wave && p->seqlen_k <= kUnsplitKeys) ? 1 : 0;
+  s.split = tiles > kUnsplitTiles && !(one_wave && p->seqlen_k <= kUnsplitKeys) && segments <= kMaxUnits / tiles ? 1 : 0;
   s.units = segments * (s.split ? tiles : 1);
   const int64_t most = ctas < kMaxStreamCtas ? ctas : kMaxStreamCtas;
   s.grid = s.units < most ? s.units : most;
@@ -479,7 +482,7 @@ attn_status af::paged_fwd(const attn_paged_params* params, void* scratch, size_t
   uint8_t* const room = scratch != nullptr ? static_cast<uint8_t*>(scratch) : ws + kZeroedBytes;
   if (use_tc05(p)) return launch_tiles(p, room, stream);
   const StreamPlan plan = plan_stream(p);
-  if (plan.units > 0x3fffffffll) return report_error(ATTN_ERR_UNSUPPORTED, "too much work for one call");
+  if (plan.units > kMaxUnits) return report_error(ATTN_ERR_UNSUPPORTED, "more than 2^30 sequences times KV heads");
   const bool packed = p->cu_seqlens_q != nullptr;
   af::StreamParams a;
   memset(&a, 0, sizeof(a));

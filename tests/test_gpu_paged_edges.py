@@ -339,3 +339,31 @@ def test_values_under_large_scores(pkg, dim, new, lens_k, fp8):
         bound = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14 + grow) * ra * (1 + grow) + 1e-6
         assert ((o[b].double() - ro).abs() <= bound).all()
         assert ((lse[b].double() - rl).abs() <= ds + 2.0 ** -20 + 2.0 ** -23 * rl.abs()).all()
+
+
+# ---------------------------------------------------------------- many sequences, a wide table
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_many_short_sequences_under_a_wide_table(pkg, fp8):
+    """1100 sequences of 32 KV heads in a table of 2^22 tokens each: more key tiles
+    than 32 bits count, were they full. All share one page."""
+    batch, heads, dim, page, longest = 1100, 32, 64, 65536, 300
+    g = torch.Generator(device="cuda").manual_seed(61)
+    cache = [torch.full((1, page, heads, dim), math.nan, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for x in cache:
+        x[0, :longest] = torch.randn(longest, heads, dim, generator=g, device="cuda").to(torch.bfloat16)
+    scales = {}
+    if fp8:
+        cache = [x.to(R.E4M3) for x in cache]
+        scales = {n: torch.ones(1, heads, page, device="cuda") for n in ("k_scale", "v_scale")}
+    table = torch.zeros(batch, 64, dtype=torch.int32, device="cuda")
+    lens = 1 + torch.arange(batch, dtype=torch.int32, device="cuda") * 7919 % longest
+    q = torch.randn(batch, 1, heads, dim, generator=g, device="cuda").to(torch.bfloat16)
+    o, lse = pkg.paged_forward(q, *cache, table, lens, **scales)
+    pkg.check()
+    k, v = (x[0, :longest].double() for x in cache)
+    s = torch.einsum("bhd,khd->bhk", q[:, 0].double(), k) * dim ** -0.5
+    s = torch.where(torch.arange(longest, device="cuda") < lens[:, None, None], s, -math.inf)
+    w = torch.softmax(s, -1)
+    ro, ra = torch.einsum("bhk,khd->bhd", w, v), torch.einsum("bhk,khd->bhd", w, v.abs())
+    assert ((o[:, 0].double() - ro).abs() <= 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2.0 ** -14) * ra + 1e-6).all()
+    assert ((lse[:, :, 0].double() - torch.logsumexp(s, -1)).abs() <= 5e-5).all()
