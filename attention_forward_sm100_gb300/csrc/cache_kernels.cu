@@ -37,16 +37,24 @@ struct Slot {
   int page, slot;
 };
 
-// The sequence of row t, for the lanes of one warp with consecutive rows from
-// t0 on (offsets cu[0 .. batch] into `rows` rows); `batch` if it lies behind the
-// last one. Every block looks at all offsets: where they decrease, rows cannot
+// The sequence of row t, for the lanes of the first warp with consecutive rows
+// from t0 on (offsets cu[0 .. batch] into `rows` rows); `batch` if it lies behind
+// the last one. Every block looks at all offsets: where they decrease, rows cannot
 // be told apart, and none has a sequence. The first block records the first
 // sequence whose offsets are wrong, whether or not it has a row that is there.
+// The whole block calls it; past kAloneBatch offsets all of its warps search (one
+// token each of 1024 sequences, append: 8.8 us with one warp, 6.9 with all).
+constexpr int kAloneBatch = 256;
 __device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t t0, int64_t t, int64_t rows,
                                              uint32_t* ws) {
+  constexpr int WARPS = kThreads / 32;
+  __shared__ int part_b[WARPS], part_wrong[WARPS], part_back[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool alone = batch <= kAloneBatch;
+  if (alone && warp > 0) return batch;
   int b = 0, wrong = batch;
   bool back = false;
-  for (int c = threadIdx.x & 31; c < batch; c += 32) {
+  for (int c = threadIdx.x; c < batch; c += alone ? 32 : kThreads) {
     const int a = cu[c], e = cu[c + 1];
     b += (int64_t)e <= t0 ? 1 : 0;
     back = back || e < a;
@@ -54,8 +62,21 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64
   }
   b = __reduce_add_sync(0xffffffffu, b);
   wrong = __reduce_min_sync(0xffffffffu, wrong);
-  if (wrong < batch && blockIdx.x == 0 && threadIdx.x == 0) record_bad_cache(ws, wrong);
-  if (__any_sync(0xffffffffu, back)) return batch;
+  back = __any_sync(0xffffffffu, back);
+  if (!alone) {
+    if (lane == 0) {
+      part_b[warp] = b;
+      part_wrong[warp] = wrong;
+      part_back[warp] = back;
+    }
+    __syncthreads();
+    if (warp > 0) return batch;
+    b = __reduce_add_sync(0xffffffffu, lane < WARPS ? part_b[lane] : 0);
+    wrong = __reduce_min_sync(0xffffffffu, lane < WARPS ? part_wrong[lane] : batch);
+    back = __any_sync(0xffffffffu, lane < WARPS && part_back[lane] != 0);
+  }
+  if (wrong < batch && blockIdx.x == 0 && lane == 0) record_bad_cache(ws, wrong);
+  if (back) return batch;
   while (b < batch && (int64_t)cu[b + 1] <= t) ++b;
   return b;
 }
@@ -147,13 +168,14 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       }
     }
     if (base == 0) {
+      const int64_t t = t0 + (threadIdx.x & 31);
+      const int found = packed ? find_sequence(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws) : 0;
       if (threadIdx.x < 32) {
         Slot s = {-1, 0};
-        const int64_t t = t0 + threadIdx.x;
         int b, i, lq = P.s.seqlen_q;
         bool ok = (int)threadIdx.x < tokens;
         if (packed) {
-          b = find_sequence(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws);
+          b = found;
           ok = ok && b < P.s.batch;                // else behind the last sequence
           if (ok) {
             const int a = P.s.cu_q[b], e = P.s.cu_q[b + 1];
@@ -242,15 +264,15 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   const int tokens = (int)min((int64_t)P.block_tokens, P.total_k - t0);
   const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
+  const int64_t row = t0 + (threadIdx.x & 31);
+  const int b = find_sequence(P.cu_k, P.batch, t0, row, P.total_k, P.ws);
   if (threadIdx.x < 32) {
     Slot s = {-1, 0};
-    const int64_t t = t0 + threadIdx.x;
-    const int b = find_sequence(P.cu_k, P.batch, t0, t, P.total_k, P.ws);
     if ((int)threadIdx.x < tokens && b < P.batch) {
       const int a = P.cu_k[b];
       // (else an offset below zero, which is recorded, or a row in front of the
       // first sequence)
-      if (a >= 0 && t >= a) s = slot_of(P.c, b, (int)(t - a), P.ws);
+      if (a >= 0 && row >= a) s = slot_of(P.c, b, (int)(row - a), P.ws);
     }
     slots[threadIdx.x] = s;
   }
