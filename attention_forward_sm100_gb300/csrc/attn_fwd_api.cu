@@ -574,6 +574,9 @@ attn_status attn_fwd_check(void* workspace, attn_stream_t stream) {
     if (w[af::kWsErrorCode] == af::kDevErrBadCache)
       return fail(ATTN_ERR_INVALID_ARG, "paged cache: a length, offset or page number of sequence %u is out of range "
                   "(nothing of that call's output can be trusted)", info);
+    if (w[af::kWsErrorCode] == af::kDevErrBadPosition)
+      return fail(ATTN_ERR_INVALID_ARG, "rotary: an offset, length or position of sequence %u is out of range "
+                  "(rows concerned are not written)", info);
     return fail(ATTN_ERR_DEVICE_TIMEOUT, "device wait timed out (code %u, block %u, role %u, barrier %u)",
                 w[af::kWsErrorCode], info >> 16, (info >> 8) & 0xffu, info & 0xffu);
   }

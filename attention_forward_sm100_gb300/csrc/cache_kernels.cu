@@ -20,9 +20,18 @@
 // finite magnitude is found on the bf16 bit patterns (they order like the
 // values) with shuffles inside the vector's lanes; multiplying by 1 / s is
 // exact, so the only rounding is the one to e4m3.
+//
+// e2m1: a lane's sixteen values are one block of the format. s is the smallest
+// power of two with amax / s <= 6 * 448, the block's scale e4m3(amax_block / 6 s),
+// and a code the rounded quotient x / (s * scale).
+//
+// With a rotation (ROT) the keys are turned on their way, in fp32, and the new
+// tokens' queries are vectors behind the values, turned and written as bf16.
 #include "launch.cuh"
 #include "paged.h"
 #include "ptx.cuh"
+#include "rotary.cuh"
+#include "rows.cuh"
 
 namespace af {
 namespace {
@@ -32,57 +41,14 @@ constexpr int kBatch = 4;   // vectors a thread has in flight
 
 constexpr int kMaxTokens = 32;   // tokens of a block: one lane each
 
-// Where a token's vectors are in the cache, or page < 0: nowhere.
+// Where a token's vectors are in the cache, or page < 0: nowhere. `angle`: its line
+// of the rotary table.
 struct Slot {
-  int page, slot;
+  int page, slot, angle;
 };
 
-// The sequence of row t, for the lanes of the first warp with consecutive rows
-// from t0 on (offsets cu[0 .. batch] into `rows` rows); `batch` if it lies behind
-// the last one. Every block looks at all offsets: where they decrease, rows cannot
-// be told apart, and none has a sequence. The first block records the first
-// sequence whose offsets are wrong, whether or not it has a row that is there.
-// The whole block calls it; past kAloneBatch offsets all of its warps search (one
-// token each of 1024 sequences, append: 8.8 us with one warp, 6.9 with all).
-constexpr int kAloneBatch = 256;
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int batch, int64_t t0, int64_t t, int64_t rows,
-                                             uint32_t* ws) {
-  constexpr int WARPS = kThreads / 32;
-  __shared__ int part_b[WARPS], part_wrong[WARPS], part_back[WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool alone = batch <= kAloneBatch;
-  if (alone && warp > 0) return batch;
-  int b = 0, wrong = batch;
-  bool back = false;
-  for (int c = threadIdx.x; c < batch; c += alone ? 32 : kThreads) {
-    const int a = cu[c], e = cu[c + 1];
-    b += (int64_t)e <= t0 ? 1 : 0;
-    back = back || e < a;
-    if (a < 0 || e < a || e > rows) wrong = min(wrong, c);
-  }
-  b = __reduce_add_sync(0xffffffffu, b);
-  wrong = __reduce_min_sync(0xffffffffu, wrong);
-  back = __any_sync(0xffffffffu, back);
-  if (!alone) {
-    if (lane == 0) {
-      part_b[warp] = b;
-      part_wrong[warp] = wrong;
-      part_back[warp] = back;
-    }
-    __syncthreads();
-    if (warp > 0) return batch;
-    b = __reduce_add_sync(0xffffffffu, lane < WARPS ? part_b[lane] : 0);
-    wrong = __reduce_min_sync(0xffffffffu, lane < WARPS ? part_wrong[lane] : batch);
-    back = __any_sync(0xffffffffu, lane < WARPS && part_back[lane] != 0);
-  }
-  if (wrong < batch && blockIdx.x == 0 && lane == 0) record_bad_cache(ws, wrong);
-  if (back) return batch;
-  while (b < batch && (int64_t)cu[b + 1] <= t) ++b;
-  return b;
-}
-
 __device__ __forceinline__ Slot slot_of(const CacheView& c, int b, int pos, uint32_t* ws) {
-  Slot s = {-1, pos & ((1 << c.page_shift) - 1)};
+  Slot s = {-1, pos & ((1 << c.page_shift) - 1), pos};
   if (pos >= 0 && (pos >> c.page_shift) < c.max_pages) {
     const int page = __ldg(c.table + (int64_t)b * c.table_stride + (pos >> c.page_shift));
     if ((unsigned)page < (unsigned)c.num_pages) s.page = page;
@@ -91,17 +57,24 @@ __device__ __forceinline__ Slot slot_of(const CacheView& c, int b, int pos, uint
   return s;
 }
 
-// Vector `idx` of a block: its token and (V behind K) head.
+// Vector `idx` of a block: its token and (V behind K, queries to be turned behind
+// both) head.
 struct Vector {
   int token, h;
-  bool v;
+  bool v, q;
 };
+template <bool Q = false>
 __device__ __forceinline__ Vector vector_at(uint32_t idx, uint32_t per_token, uint32_t magic, int heads) {
   Vector x;
   x.token = (int)__umulhi(idx, magic);   // idx / per_token (magic = 2^32 / per_token rounded up, idx < 2^16)
   x.h = (int)(idx - x.token * per_token);
   x.v = x.h >= heads;
   if (x.v) x.h -= heads;
+  x.q = Q && x.v && x.h >= heads;
+  if (x.q) {
+    x.h -= heads;
+    x.v = false;
+  }
   return x;
 }
 
@@ -120,14 +93,61 @@ __device__ __forceinline__ int scale_exponent(uint32_t m) {
   return max(-126, e - 8 + ((m & 0x7fu) > 96u ? 1 : 0));   // 1.75 * 2^8 = 448
 }
 
-template <int D, bool FP8>
+// Exponent of the e2m1 scale for a largest magnitude: of the smallest power of two s
+// with m / s <= 6 * 448 = 1.3125 * 2^11.
+__device__ __forceinline__ int scale_exponent4(float m) {
+  if (m == 0.f) return 0;
+  const uint32_t bits = __float_as_uint(m);
+  return max(-126, (int)(bits >> 23) - 127 - 11 + ((bits & 0x7fffffu) > 0x280000u ? 1 : 0));
+}
+// Of the e4m3 scale, for fp32 values.
+__device__ __forceinline__ int scale_exponent8(float m) {
+  if (m == 0.f) return 0;
+  const uint32_t bits = __float_as_uint(m);
+  return max(-126, (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0));   // 1.75 * 2^8 = 448
+}
+__device__ __forceinline__ float finite_max(float x, float m) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? fmaxf(a, m) : m;   // (not infinities and NaN)
+}
+
+// A block of sixteen values as e2m1 codes (even ones in the low halves) and its
+// e4m3 scale, in units of 1 / inv, the vector's. `top`: the block's largest finite
+// magnitude.
+__device__ __forceinline__ void quantise_block(const float (&f)[16], float top, float inv, uint2& codes, uint32_t& scale) {
+  scale = ptx::pack_e4m3x4(__fdiv_rn(top * inv, 6.f), 0.f, 0.f, 0.f) & 0xffu;
+  float size, unused;
+  ptx::e4m3x2_to_float2(scale, size, unused);
+  // y / size, correctly rounded, by Markstein's theorem: r = 1 / size and a first
+  // quotient t, then t + r (y - t size), the remainder being exact.
+  const float r = size == 0.f ? 0.f : __frcp_rn(size);
+  uint32_t out[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = fminf(fmaxf(f[8 * j + i] * inv, -2688.f), 2688.f);   // (infinities; 2688 / size is in range)
+      t[i] = y * r;
+      t[i] = fmaf(fmaf(-t[i], size, y), r, t[i]);
+    }
+    out[j] = ptx::pack_e2m1x8(t);
+  }
+  codes = size == 0.f ? make_uint2(0u, 0u) : make_uint2(out[0], out[1]);
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) nan = nan || f[i] != f[i];
+  if (nan) scale = 0x7fu;   // a NaN takes its block with it
+}
+
+template <int D, int KIND, bool ROT>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams P) {
-  constexpr int E = FP8 ? 16 : 8, L = D / E, PER = kThreads / L;
+  constexpr int E = KIND == kBf16 ? 8 : 16, L = D / E, PER = kThreads / L;
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
   const int64_t t0 = (int64_t)blockIdx.x * P.block_tokens;
   const int tokens = (int)min((int64_t)P.block_tokens, P.tokens - t0);
-  const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
+  const uint32_t nv = 2 * P.c.heads_kv + (ROT ? P.r.heads_q : 0), total = tokens * nv;
   const int lane = threadIdx.x % L;
   // fixed layout: sequence and index of the first token
   const bool packed = P.s.cu_q != nullptr;
@@ -141,6 +161,13 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       ++b;
     }
   };
+  // offset of a token's rows with batch and token strides sb, st
+  auto row_at = [&](int token, int64_t sb, int64_t st) -> int64_t {
+    if (packed) return (t0 + token) * st;
+    int b, i;
+    token_at(token, b, i);
+    return b * sb + i * st;
+  };
   for (uint32_t base = 0; base < total; base += PER * kBatch) {
     uint4 x[kBatch][E / 8];
 #pragma unroll
@@ -149,17 +176,16 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < E / 8; ++e) x[u][e] = make_uint4(0u, 0u, 0u, 0u);
       if (id < total) {
-        const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
-        int64_t at;
-        if (packed) {
-          at = (t0 + w.token) * (w.v ? P.v_t : P.k_t);
-        } else {
-          int b, i;
-          token_at(w.token, b, i);
-          at = b * (w.v ? P.v_b : P.k_b) + i * (w.v ? P.v_t : P.k_t);
+        const Vector w = vector_at<ROT>(id, nv, P.magic, P.c.heads_kv);
+        const uint8_t* src = w.v ? P.v + w.h * P.v_h : P.k + w.h * P.k_h;
+        int64_t sb = w.v ? P.v_b : P.k_b, st = w.v ? P.v_t : P.k_t;
+        if (ROT && w.q) {
+          src = P.r.q + w.h * P.r.q_h;
+          sb = P.r.q_b;
+          st = P.r.q_t;
         }
-        const uint8_t* src = (w.v ? P.v + w.h * P.v_h : P.k + w.h * P.k_h) + at + lane * (E * 2);
-        if (FP8 && P.wide) {
+        src += row_at(w.token, sb, st) + lane * (E * 2);
+        if (KIND != kBf16 && P.wide) {
           ptx::ld_global_v8(src, reinterpret_cast<uint32_t*>(&x[u][0]));
         } else {
 #pragma unroll
@@ -169,9 +195,10 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     }
     if (base == 0) {
       const int64_t t = t0 + (threadIdx.x & 31);
-      const int found = packed ? find_sequence(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws) : 0;
+      const int found =
+          packed ? find_sequence<kThreads>(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws, kDevErrBadCache) : 0;
       if (threadIdx.x < 32) {
-        Slot s = {-1, 0};
+        Slot s = {-1, 0, 0};
         int b, i, lq = P.s.seqlen_q;
         bool ok = (int)threadIdx.x < tokens;
         if (packed) {
@@ -191,6 +218,13 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         if (ok) {
           const int lk = P.s.seqlens_k[b];
           s = slot_of(P.c, b, lk < 0 || lk > P.s.max_k ? -1 : lk - lq + i, P.ws);
+          if constexpr (ROT) {
+            if (P.r.positions != nullptr) s.angle = P.r.positions[t];
+            if (s.page >= 0 && (s.angle < 0 || s.angle >= P.r.num_positions)) {
+              s.page = -1;
+              record_error(P.ws, kDevErrBadPosition, b);
+            }
+          }
         }
         slots[threadIdx.x] = s;
       }
@@ -200,42 +234,99 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     for (int u = 0; u < kBatch; ++u) {
       const uint32_t id = base + u * PER + threadIdx.x / L;
       const bool there = id < total;
-      const Vector w = vector_at(there ? id : 0u, nv, P.magic, P.c.heads_kv);
+      const Vector w = vector_at<ROT>(there ? id : 0u, nv, P.magic, P.c.heads_kv);
       const Slot s = slots[w.token];
       const bool ok = there && s.page >= 0;
-      uint8_t* dst = (w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
-                          : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head) + lane * 16;
-      if constexpr (!FP8) {
-        if (ok) *reinterpret_cast<uint4*>(dst) = x[u][0];
-      } else {
-        const uint32_t in[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-        // magnitudes two at a time; only where that meets an infinity or a NaN
-        // the finite ones are picked out
-        uint32_t m = 0u;
+      uint32_t in[E / 2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = __vmaxu2(m, in[e] & 0x7fff7fffu);
-        m = max(m & 0xffffu, m >> 16);
-        if (__any_sync(0xffffffffu, m >= 0x7f80u)) {
-          m = 0u;
+      for (int e = 0; e < E / 8; ++e) {
+        in[4 * e] = x[u][e].x;
+        in[4 * e + 1] = x[u][e].y;
+        in[4 * e + 2] = x[u][e].z;
+        in[4 * e + 3] = x[u][e].w;
+      }
+      float f[E];
+      if constexpr (ROT)
+        rotate_lanes<E, L>(in, f, P.r.table + (int64_t)s.angle * P.r.rot, P.r.rot, P.r.interleaved != 0, ok && !w.v);
+      if (ROT && w.q && ok) {
+        uint8_t* dst = P.r.q_out + w.h * P.r.out_h + row_at(w.token, P.r.out_b, P.r.out_t) + lane * (E * 2);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) m = finite_max(in[e], m);
+        for (int e = 0; e < E / 8; ++e)
+          reinterpret_cast<uint4*>(dst)[e] =
+              make_uint4(ptx::pack_bf16(f[8 * e], f[8 * e + 1]), ptx::pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                         ptx::pack_bf16(f[8 * e + 4], f[8 * e + 5]), ptx::pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+      }
+      const bool cached = ok && !w.q;
+      uint8_t* dst = w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
+                         : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head;
+      const int64_t at = (((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot;   // of its scales
+      if constexpr (KIND == kBf16) {
+        uint4 out = x[u][0];
+        if (ROT && !w.v)
+          out = make_uint4(ptx::pack_bf16(f[0], f[1]), ptx::pack_bf16(f[2], f[3]), ptx::pack_bf16(f[4], f[5]),
+                           ptx::pack_bf16(f[6], f[7]));
+        if (cached) *reinterpret_cast<uint4*>(dst + lane * 16) = out;
+      } else if constexpr (KIND == kE4m3) {
+        int se;
+        if constexpr (ROT) {
+          float m = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) m = finite_max(f[e], m);
+#pragma unroll
+          for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          se = scale_exponent8(m);
+        } else {
+          // magnitudes two at a time; only where that meets an infinity or a NaN
+          // the finite ones are picked out
+          uint32_t m = 0u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = __vmaxu2(m, in[e] & 0x7fff7fffu);
+          m = max(m & 0xffffu, m >> 16);
+          if (__any_sync(0xffffffffu, m >= 0x7f80u)) {
+            m = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = finite_max(in[e], m);
+          }
+#pragma unroll
+          for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          se = scale_exponent(m);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            f[2 * e] = bf16_lo(in[e]);
+            f[2 * e + 1] = bf16_hi(in[e]);
+          }
         }
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int se = scale_exponent(m);
         const float inv = __uint_as_float((uint32_t)(127 - se) << 23);
         uint32_t out[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t a = in[2 * j], c = in[2 * j + 1];
-          out[j] = ptx::pack_e4m3x4(__uint_as_float(a << 16) * inv, __uint_as_float(a & 0xffff0000u) * inv,
-                                    __uint_as_float(c << 16) * inv, __uint_as_float(c & 0xffff0000u) * inv);
+        for (int j = 0; j < 4; ++j)
+          out[j] = ptx::pack_e4m3x4(f[4 * j] * inv, f[4 * j + 1] * inv, f[4 * j + 2] * inv, f[4 * j + 3] * inv);
+        if (cached) {
+          *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+          if (lane == 0) (w.v ? P.c.v_scale : P.c.k_scale)[at] = __uint_as_float((uint32_t)(127 + se) << 23);
         }
-        if (ok) {
-          *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-          if (lane == 0)
-            (w.v ? P.c.v_scale : P.c.k_scale)[(((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot] =
-                __uint_as_float((uint32_t)(127 + se) << 23);
+      } else {
+        if constexpr (!ROT) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            f[2 * e] = bf16_lo(in[e]);
+            f[2 * e + 1] = bf16_hi(in[e]);
+          }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = finite_max(f[e], top);
+        float m = top;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int se = scale_exponent4(m);
+        uint2 codes;
+        uint32_t scale;
+        quantise_block(f, top, __uint_as_float((uint32_t)(127 - se) << 23), codes, scale);
+        if (cached) {
+          *reinterpret_cast<uint2*>(dst + lane * 8) = codes;
+          (w.v ? P.blocks.v : P.blocks.k)[at * L + lane] = (uint8_t)scale;
+          if (lane == 0) (w.v ? P.c.v_scale : P.c.k_scale)[at] = __uint_as_float((uint32_t)(127 + se) << 23);
         }
       }
     }
@@ -255,9 +346,52 @@ __device__ __forceinline__ void widen(const uint4& x, float scale, uint32_t (&ou
   }
 }
 
-template <int D, bool FP8>
+// Sixteen values of an e2m1 cache: codes times the block's scale, which is exact,
+// times the vector's scale, rounded once.
+__device__ __forceinline__ void widen4(const uint2& x, uint32_t block, float scale, uint32_t (&out)[8]) {
+  float size, unused;
+  ptx::e4m3x2_to_float2(block, size, unused);
+  const uint32_t in[2] = {x.x, x.y};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t h[4];
+    ptx::e2m1x8_to_f16x2(in[j], h);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      ptx::f16x2_to_float2(h[i], lo, hi);
+      out[4 * j + i] = ptx::pack_bf16(lo * size * scale, hi * size * scale);
+    }
+  }
+}
+// What a lane holds of a quantised vector: sixteen codes and their scales.
+template <int KIND>
+struct Codes {
+  uint4 x;
+  uint32_t block;
+  float scale;
+  // `src`: the vector's first byte, `at` the index of its scales
+  __device__ __forceinline__ void load(const uint8_t* src, const float* scales, const uint8_t* blocks, int64_t at,
+                                       int lane, int lanes) {
+    if constexpr (KIND == kE2m1) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + lane * 8));
+      x.x = v.x;
+      x.y = v.y;
+      block = __ldg(blocks + at * lanes + lane);
+    } else {
+      x = __ldcs(reinterpret_cast<const uint4*>(src + lane * 16));
+    }
+    scale = __ldg(scales + at);
+  }
+  __device__ __forceinline__ void widened(uint32_t (&out)[8]) const {
+    if constexpr (KIND == kE2m1) widen4(make_uint2(x.x, x.y), block, scale, out);
+    else widen(x, scale, out);
+  }
+};
+
+template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams P) {
-  constexpr int E = FP8 ? 16 : 8, L = D / E, PER = kThreads / L;
+  constexpr int E = KIND == kBf16 ? 8 : 16, L = D / E, PER = kThreads / L;
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
   const int64_t t0 = (int64_t)blockIdx.x * P.block_tokens;
@@ -265,9 +399,9 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
   const int64_t row = t0 + (threadIdx.x & 31);
-  const int b = find_sequence(P.cu_k, P.batch, t0, row, P.total_k, P.ws);
+  const int b = find_sequence<kThreads>(P.cu_k, P.batch, t0, row, P.total_k, P.ws, kDevErrBadCache);
   if (threadIdx.x < 32) {
-    Slot s = {-1, 0};
+    Slot s = {-1, 0, 0};
     if ((int)threadIdx.x < tokens && b < P.batch) {
       const int a = P.cu_k[b];
       // (else an offset below zero, which is recorded, or a row in front of the
@@ -278,8 +412,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   }
   __syncthreads();
   for (uint32_t base = 0; base < total; base += PER * kBatch) {
-    uint4 x[kBatch];
-    float scale[kBatch];
+    Codes<KIND> x[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const uint32_t id = base + u * PER + threadIdx.x / L;
@@ -287,12 +420,13 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
       const Slot s = slots[w.token];
       if (s.page < 0) continue;
-      const uint8_t* src = (w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
-                                : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head) + lane * 16;
-      x[u] = __ldcs(reinterpret_cast<const uint4*>(src));
-      if constexpr (FP8)
-        scale[u] = __ldg((w.v ? P.c.v_scale : P.c.k_scale) +
-                         ((((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot));
+      const uint8_t* src = w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
+                               : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head;
+      if constexpr (KIND == kBf16)
+        x[u].x = __ldcs(reinterpret_cast<const uint4*>(src + lane * 16));
+      else
+        x[u].load(src, w.v ? P.c.v_scale : P.c.k_scale, w.v ? P.blocks.v : P.blocks.k,
+                  (((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot, lane, L);
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -302,11 +436,11 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       if (slots[w.token].page < 0) continue;
       const int64_t t = t0 + w.token;
       uint8_t* dst = (w.v ? P.v + t * P.v_t + w.h * P.v_h : P.k + t * P.k_t + w.h * P.k_h) + lane * (E * 2);
-      if constexpr (!FP8) {
-        *reinterpret_cast<uint4*>(dst) = x[u];
+      if constexpr (KIND == kBf16) {
+        *reinterpret_cast<uint4*>(dst) = x[u].x;
       } else {
         uint32_t out[8];
-        widen(x[u], scale[u], out);
+        x[u].widened(out);
         if (P.wide) {
           ptx::st_global_v8(dst, out);
         } else {
@@ -322,7 +456,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 // Every sequence's cached tokens as bf16 pages (WidenParams): blocks (x, b) take
 // the token chunks x, x + grid, ... of sequence b. Three bytes of traffic per
 // element, HBM bounds it as it does reading.
-template <int D>
+template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_constant__ WidenParams P) {
   constexpr int L = D / 16, PER = kThreads / L;
   __shared__ Slot slots[kMaxTokens];
@@ -340,8 +474,7 @@ __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_cons
     if (threadIdx.x < 32 && (int)threadIdx.x < tokens) slots[threadIdx.x] = slot_of(P.c, b, (int)t0 + threadIdx.x, P.ws);
     __syncthreads();
     for (uint32_t base = 0; base < total; base += PER * kBatch) {
-      uint4 x[kBatch];
-      float scale[kBatch];
+      Codes<KIND> x[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const uint32_t id = base + u * PER + threadIdx.x / L;
@@ -349,11 +482,10 @@ __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_cons
         const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
         const Slot s = slots[w.token];
         if (s.page < 0) continue;
-        const uint8_t* src = (w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
-                                  : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head) + lane * 16;
-        x[u] = __ldg(reinterpret_cast<const uint4*>(src));
-        scale[u] = __ldg((w.v ? P.c.v_scale : P.c.k_scale) +
-                         ((((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot));
+        const uint8_t* src = w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
+                                 : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head;
+        x[u].load(src, w.v ? P.c.v_scale : P.c.k_scale, w.v ? P.blocks.v : P.blocks.k,
+                  (((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot, lane, L);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
@@ -364,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_cons
         const int t = (int)t0 + w.token;
         const int64_t row = (((int64_t)b * P.pages + t / kBlockN) * P.c.heads_kv + w.h) * kBlockN + t % kBlockN;
         uint32_t out[8];
-        widen(x[u], scale[u], out);
+        x[u].widened(out);
         ptx::st_global_v8((w.v ? P.v : P.k) + row * (D * 2) + lane * 32, out);
       }
     }
@@ -373,8 +505,7 @@ __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_cons
 
 // A block's tokens: as many as fill its batch of vectors once.
 template <class K, class P>
-cudaError_t launch(K kern, P p, int64_t tokens, int vectors, cudaStream_t stream) {
-  const uint32_t per_token = 2 * p.c.heads_kv;
+cudaError_t launch(K kern, P p, int64_t tokens, uint32_t per_token, int vectors, cudaStream_t stream) {
   const int fit = vectors / (int)per_token;
   p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
   p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
@@ -384,41 +515,54 @@ cudaError_t launch(K kern, P p, int64_t tokens, int vectors, cudaStream_t stream
   return launch_dependent(kern, p, dim3((unsigned)blocks), kThreads, 0, stream);
 }
 
-constexpr int per_block(int d, bool fp8) { return kThreads / (d / (fp8 ? 16 : 8)) * kBatch; }
+constexpr int per_block(int d, int kind) { return kThreads / (d / (kind == kBf16 ? 8 : 16)) * kBatch; }
+
+template <int D, int KIND>
+cudaError_t append_t(const AppendParams& p, cudaStream_t stream) {
+  const uint32_t per_token = 2 * p.c.heads_kv;
+  if (p.r.table == nullptr)
+    return launch(cache_append_kernel<D, KIND, false>, p, p.tokens, per_token, per_block(D, KIND), stream);
+  return launch(cache_append_kernel<D, KIND, true>, p, p.tokens, per_token + p.r.heads_q, per_block(D, KIND), stream);
+}
+template <int D>
+cudaError_t append_d(const AppendParams& p, int kind, cudaStream_t stream) {
+  return kind == kBf16 ? append_t<D, kBf16>(p, stream)
+                       : (kind == kE4m3 ? append_t<D, kE4m3>(p, stream) : append_t<D, kE2m1>(p, stream));
+}
+template <int D>
+cudaError_t read_d(const ReadParams& p, int kind, cudaStream_t stream) {
+  const uint32_t n = 2 * p.c.heads_kv;
+  const int pb = per_block(D, kind);
+  return kind == kBf16 ? launch(cache_read_kernel<D, kBf16>, p, p.total_k, n, pb, stream)
+                       : (kind == kE4m3 ? launch(cache_read_kernel<D, kE4m3>, p, p.total_k, n, pb, stream)
+                                        : launch(cache_read_kernel<D, kE2m1>, p, p.total_k, n, pb, stream));
+}
+template <int D>
+cudaError_t widen_d(const WidenParams& p, int kind, dim3 grid, cudaStream_t stream) {
+  return kind == kE4m3 ? launch_dependent(cache_widen_kernel<D, kE4m3>, p, grid, kThreads, 0, stream)
+                       : launch_dependent(cache_widen_kernel<D, kE2m1>, p, grid, kThreads, 0, stream);
+}
 
 }  // namespace
 
-cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream) {
-  const int64_t n = p.tokens;
-  const int pb = per_block(head_dim, fp8);
-  if (head_dim == 128)
-    return fp8 ? launch(cache_append_kernel<128, true>, p, n, pb, stream)
-               : launch(cache_append_kernel<128, false>, p, n, pb, stream);
-  return fp8 ? launch(cache_append_kernel<64, true>, p, n, pb, stream)
-             : launch(cache_append_kernel<64, false>, p, n, pb, stream);
+cudaError_t cache_append_launch(const AppendParams& p, int head_dim, int kind, cudaStream_t stream) {
+  return head_dim == 128 ? append_d<128>(p, kind, stream) : append_d<64>(p, kind, stream);
 }
 
-cudaError_t cache_widen_launch(const WidenParams& params, int head_dim, cudaStream_t stream) {
+cudaError_t cache_widen_launch(const WidenParams& params, int head_dim, int kind, cudaStream_t stream) {
   WidenParams p = params;
   const uint32_t per_token = 2 * p.c.heads_kv;
-  const int fit = per_block(head_dim, true) / (int)per_token;
+  const int fit = per_block(head_dim, kind) / (int)per_token;
   p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
   p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
   const int64_t chunks = ((int64_t)p.max_k + p.block_tokens - 1) / p.block_tokens;
   const int64_t fill = (16ll * sm_count() + p.batch - 1) / p.batch;   // two rounds of eight blocks per SM
   const dim3 grid((unsigned)(chunks < 1 ? 1 : (chunks < fill ? chunks : fill)), (unsigned)p.batch);
-  return head_dim == 128 ? launch_dependent(cache_widen_kernel<128>, p, grid, kThreads, 0, stream)
-                         : launch_dependent(cache_widen_kernel<64>, p, grid, kThreads, 0, stream);
+  return head_dim == 128 ? widen_d<128>(p, kind, grid, stream) : widen_d<64>(p, kind, grid, stream);
 }
 
-cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream) {
-  const int64_t n = p.total_k;
-  const int pb = per_block(head_dim, fp8);
-  if (head_dim == 128)
-    return fp8 ? launch(cache_read_kernel<128, true>, p, n, pb, stream)
-               : launch(cache_read_kernel<128, false>, p, n, pb, stream);
-  return fp8 ? launch(cache_read_kernel<64, true>, p, n, pb, stream)
-             : launch(cache_read_kernel<64, false>, p, n, pb, stream);
+cudaError_t cache_read_launch(const ReadParams& p, int head_dim, int kind, cudaStream_t stream) {
+  return head_dim == 128 ? read_d<128>(p, kind, stream) : read_d<64>(p, kind, stream);
 }
 
 }  // namespace af

@@ -31,6 +31,7 @@ enum DeviceError : uint32_t {
   kDevErrTimeout = 1,
   kDevErrBadSeqlens = 3,   // packed offsets out of order or past total_q / total_k (info: sequence)
   kDevErrBadCache = 4,     // paged cache: a length, offset or page number out of range (info: sequence)
+  kDevErrBadPosition = 5,  // rotary: an offset out of order or a position outside the table (info: sequence, or row)
 };
 
 // The cache as the kernels see it; strides in bytes.

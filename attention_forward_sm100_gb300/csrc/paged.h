@@ -5,6 +5,7 @@
 
 #include "../../include/attn_paged.h"
 #include "internal.h"
+#include "rows.cuh"
 
 namespace af {
 
@@ -27,14 +28,35 @@ struct NewRows {
   int32_t batch, seqlen_q, total_q, max_k;
 };
 
+// What a cache holds.
+enum CacheKind : int { kBf16 = 0, kE4m3 = 1, kE2m1 = 2 };
+
+// e2m1: the e4m3 scales of blocks of 16, [pages][Hkv][page_size][D / 16].
+struct BlockScales {
+  uint8_t* k;
+  uint8_t* v;
+};
+
+// Rotation on the way into the cache; table NULL: none.
+struct AppendRotary {
+  const float* table;          // [num_positions][rot]
+  const int32_t* positions;    // of the rows, or NULL: the cache's
+  const uint8_t* q;
+  uint8_t* q_out;
+  int64_t q_b, q_t, q_h, out_b, out_t, out_h;   // bytes
+  int32_t heads_q, num_positions, rot, interleaved;
+};
+
 struct AppendParams {
   CacheView c;
+  BlockScales blocks;
+  AppendRotary r;
   NewRows s;
   const uint8_t* k;
   const uint8_t* v;
   int64_t k_b, k_t, k_h, v_b, v_t, v_h;   // bytes
   int64_t tokens;
-  int32_t wide;                           // 1: k, v and their strides are multiples of 32 bytes
+  int32_t wide;                           // 1: k, v, q and their strides are multiples of 32 bytes
   int32_t block_tokens;                   // set by the launch, as `magic`
   uint32_t magic;
   uint32_t* ws;
@@ -42,6 +64,7 @@ struct AppendParams {
 
 struct ReadParams {
   CacheView c;
+  BlockScales blocks;
   const int32_t* cu_k;
   uint8_t* k;
   uint8_t* v;
@@ -53,10 +76,11 @@ struct ReadParams {
   uint32_t* ws;
 };
 
-// Widening an e4m3 cache into bf16 pages of kBlockN tokens, [batch * pages][Hkv][kBlockN][D],
+// Widening an e4m3 or e2m1 cache into bf16 pages of kBlockN tokens, [batch * pages][Hkv][kBlockN][D],
 // sequence b's in order from page b * pages on, and the block table that says so.
 struct WidenParams {
   CacheView c;
+  BlockScales blocks;
   const int32_t* seqlens_k;
   int32_t max_k, batch, pages;
   uint8_t* k;
@@ -69,6 +93,7 @@ struct WidenParams {
 
 struct StreamParams {
   CacheView c;
+  BlockScales blocks;
   NewRows s;
   const uint8_t* q;
   int64_t q_b, q_t, q_h;     // bytes
@@ -105,17 +130,17 @@ struct PlanParams {
 cudaError_t paged_plan_launch(const PlanParams& p, cudaStream_t stream);
 cudaError_t paged_tile_merge_launch(const PlanParams& p, int head_dim, int max_cut, cudaStream_t stream);
 
-cudaError_t cache_append_launch(const AppendParams& p, int head_dim, bool fp8, cudaStream_t stream);
-cudaError_t cache_widen_launch(const WidenParams& p, int head_dim, cudaStream_t stream);
-cudaError_t cache_read_launch(const ReadParams& p, int head_dim, bool fp8, cudaStream_t stream);
+// kind: CacheKind (to widen: not bf16).
+cudaError_t cache_append_launch(const AppendParams& p, int head_dim, int kind, cudaStream_t stream);
+cudaError_t cache_widen_launch(const WidenParams& p, int head_dim, int kind, cudaStream_t stream);
+cudaError_t cache_read_launch(const ReadParams& p, int head_dim, int kind, cudaStream_t stream);
 // Streaming attention over `grid` CTAs with row tiles of 8, 16 or 32 rows.
-cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,
+cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, int kind, int row_tile, int grid,
                                 cudaStream_t stream);
 
 #ifdef __CUDACC__
-// Records the first invalid length, offset or page of a call.
 __device__ __forceinline__ void record_bad_cache(uint32_t* ws, int b) {
-  if (atomicCAS(&ws[kWsErrorCode], 0u, (uint32_t)kDevErrBadCache) == 0u) atomicExch(&ws[kWsErrorInfo], (uint32_t)b);
+  record_error(ws, kDevErrBadCache, b);
 }
 
 struct SeqRows {

@@ -15,8 +15,26 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+static_assert(af::kBf16 == ATTN_DTYPE_BF16 && af::kE4m3 == ATTN_DTYPE_FP8_E4M3 && af::kE2m1 == ATTN_DTYPE_FP4_E2M1);
+
+// Bytes of `n` values of a cached row.
+int64_t code_bytes(int dtype, int64_t n) { return dtype == af::kBf16 ? 2 * n : (dtype == af::kE4m3 ? n : n / 2); }
+
+attn_status check_blocks(const attn_kv_cache& c, const attn_block_scales* blocks) {
+  if (c.dtype != ATTN_DTYPE_FP4_E2M1)
+    return blocks == nullptr ? ATTN_OK : report_error(ATTN_ERR_INVALID_ARG, "only an e2m1 cache has block scales");
+  if (blocks == nullptr || blocks->k == nullptr || blocks->v == nullptr || !aligned(blocks->k, 16) ||
+      !aligned(blocks->v, 16))
+    return report_error(ATTN_ERR_INVALID_ARG, "an e2m1 cache needs 16-byte aligned block scales of K and V");
+  return ATTN_OK;
+}
+af::BlockScales blocks_of(const attn_block_scales* b) {
+  if (b == nullptr) return {nullptr, nullptr};
+  return {static_cast<uint8_t*>(b->k), static_cast<uint8_t*>(b->v)};
+}
+
 attn_status check_cache(const attn_kv_cache& c) {
-  if (c.dtype != ATTN_DTYPE_BF16 && c.dtype != ATTN_DTYPE_FP8_E4M3)
+  if (c.dtype != ATTN_DTYPE_BF16 && c.dtype != ATTN_DTYPE_FP8_E4M3 && c.dtype != ATTN_DTYPE_FP4_E2M1)
     return report_error(ATTN_ERR_INVALID_ARG, "unknown cache dtype %d", c.dtype);
   if (c.batch < 0 || c.max_pages < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative batch or max_pages");
   if (c.num_pages <= 0 || c.num_heads_kv <= 0)
@@ -34,15 +52,15 @@ attn_status check_cache(const attn_kv_cache& c) {
   if (c.batch > 0 && c.max_pages > 0 && (c.block_table == nullptr || !aligned(c.block_table, 4)))
     return report_error(ATTN_ERR_INVALID_ARG, "block_table must be non-NULL and 4-byte aligned");
   if (c.table_stride < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative table_stride");
-  const int es = c.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2;
+  const int es = c.dtype == ATTN_DTYPE_BF16 ? 2 : 1;
   for (int i = 0; i < 3; ++i) {
     if (c.k_stride[i] < 0 || c.v_stride[i] < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative cache stride");
     if ((c.k_stride[i] * es) % 16 || (c.v_stride[i] * es) % 16)
       return report_error(ATTN_ERR_INVALID_ARG, "cache strides must be multiples of 16 bytes");
   }
-  if (c.dtype == ATTN_DTYPE_FP8_E4M3) {
+  if (c.dtype != ATTN_DTYPE_BF16) {
     if (c.k_scale == nullptr || c.v_scale == nullptr || !aligned(c.k_scale, 16) || !aligned(c.v_scale, 16))
-      return report_error(ATTN_ERR_INVALID_ARG, "an e4m3 cache needs 16-byte aligned k_scale and v_scale");
+      return report_error(ATTN_ERR_INVALID_ARG, "an e4m3 or e2m1 cache needs 16-byte aligned k_scale and v_scale");
   }
   return ATTN_OK;
 }
@@ -76,7 +94,7 @@ attn_status check_workspace(const void* ws) {
 }
 
 af::CacheView view_of(const attn_kv_cache& c) {
-  const int es = c.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2;
+  const int es = c.dtype == ATTN_DTYPE_BF16 ? 2 : 1;
   af::CacheView v;
   v.k = static_cast<uint8_t*>(c.k);
   v.v = static_cast<uint8_t*>(c.v);
@@ -98,15 +116,33 @@ af::CacheView view_of(const attn_kv_cache& c) {
   return v;
 }
 
-attn_status check_append(const attn_cache_append_params* p) {
+attn_status check_rotary(const attn_cache_append_params* p, const attn_cache_rotary* r, bool rows) {
+  if (r->num_heads_q < 0 || r->num_positions < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative size");
+  if (r->num_heads_q > 16384) return report_error(ATTN_ERR_UNSUPPORTED, "more than 16384 heads");
+  if (r->rotary_dim < 16 || r->rotary_dim > p->cache.head_dim || r->rotary_dim % 16)
+    return report_error(ATTN_ERR_UNSUPPORTED, "rotary_dim %d is not a multiple of 16 up to head_dim", r->rotary_dim);
+  if (!rows) return ATTN_OK;
+  if (r->table == nullptr || !aligned(r->table, 16))
+    return report_error(ATTN_ERR_INVALID_ARG, "rotary table must be non-NULL and 16-byte aligned");
+  attn_status st = check_offsets("positions", r->positions, false);
+  if (st != ATTN_OK || r->num_heads_q == 0) return st;
+  const int first = p->cu_seqlens_q != nullptr ? 1 : 0;
+  if ((st = check_rows("q", r->q, r->q_stride, first, 3)) != ATTN_OK) return st;
+  return check_rows("q_out", r->q_out, r->q_out_stride, first, 3);
+}
+
+attn_status check_append(const attn_cache_append_params* p, const attn_block_scales* blocks, const attn_cache_rotary* r) {
   if (p == nullptr) return report_error(ATTN_ERR_INVALID_ARG, "params is NULL");
   attn_status st = check_cache(p->cache);
   if (st != ATTN_OK) return st;
+  if ((st = check_blocks(p->cache, blocks)) != ATTN_OK) return st;
   if (p->seqlen_q < 0 || p->total_q < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative size");
   const bool packed = p->cu_seqlens_q != nullptr;
   if (!packed && (int64_t)p->cache.batch * p->seqlen_q > 0x7fffffffll)
     return report_error(ATTN_ERR_UNSUPPORTED, "more than 2^31 new tokens");
-  if (p->cache.batch == 0 || (packed ? p->total_q : p->seqlen_q) == 0) return ATTN_OK;
+  const bool rows = p->cache.batch != 0 && (packed ? p->total_q : p->seqlen_q) != 0;
+  if (r != nullptr && (st = check_rotary(p, r, rows)) != ATTN_OK) return st;
+  if (!rows) return ATTN_OK;
   if ((st = check_rows("k", p->k, p->k_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
   if ((st = check_rows("v", p->v, p->v_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
   if ((st = check_offsets("seqlens_k", p->seqlens_k, true)) != ATTN_OK) return st;
@@ -114,10 +150,11 @@ attn_status check_append(const attn_cache_append_params* p) {
   return check_workspace(p->workspace);
 }
 
-attn_status check_read(const attn_cache_read_params* p) {
+attn_status check_read(const attn_cache_read_params* p, const attn_block_scales* blocks) {
   if (p == nullptr) return report_error(ATTN_ERR_INVALID_ARG, "params is NULL");
   attn_status st = check_cache(p->cache);
   if (st != ATTN_OK) return st;
+  if ((st = check_blocks(p->cache, blocks)) != ATTN_OK) return st;
   if (p->total_k < 0) return report_error(ATTN_ERR_INVALID_ARG, "negative size");
   if (p->cache.batch == 0 || p->total_k == 0) return ATTN_OK;
   if ((st = check_rows("k", p->k, p->k_stride, 0, 2)) != ATTN_OK) return st;
@@ -178,7 +215,18 @@ constexpr int kStreamRows = 32;
 int64_t shared_rows(const attn_paged_params* p) {
   return (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
 }
-bool use_tc05(const attn_paged_params* p) { return shared_rows(p) > kStreamRows; }
+constexpr int64_t kWidenRows = 512, kWidenBytes = 1ll << 30;
+// Whether a bf16 copy of the sequences (of `pages` pages of kBlockN tokens each) stays
+// below the bound.
+bool copy_fits(const attn_paged_params* p) {
+  const attn_kv_cache& c = p->cache;
+  const int64_t n = (int64_t)c.batch * af::tiles_for(p->seqlen_k, af::kBlockN);
+  return n > 0 && n <= kWidenBytes / (2 * (int64_t)c.num_heads_kv * af::kBlockN * c.head_dim * 2);
+}
+// An e2m1 cache has no form on the tcgen05 kernel but the one over a bf16 copy.
+bool use_tc05(const attn_paged_params* p) {
+  return shared_rows(p) > kStreamRows && (p->cache.dtype != ATTN_DTYPE_FP4_E2M1 || copy_fits(p));
+}
 
 // tcgen05 kernel: query heads packed into a 128-row tile (the largest divisor of
 // the group up to 128), tokens of such a tile and of a work tile of two, and the work
@@ -258,7 +306,7 @@ StreamPlan plan_stream(const attn_paged_params* p) {
   const int64_t rows = shared_rows(p);
   s.row_tile = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
   const int64_t rt = s.row_tile;
-  const int row_bytes = p->cache.head_dim * (p->cache.dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2);
+  const int row_bytes = (int)code_bytes(p->cache.dtype, p->cache.head_dim);
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
   const int64_t tiles = af::tiles_for(p->seqlen_k, af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
   const int64_t ctas = (int64_t)af::stream_ctas(row_bytes, s.row_tile) * af::sm_count();
@@ -290,7 +338,6 @@ StreamPlan plan_stream(const attn_paged_params* p) {
 // tokens (R about 300 on average) 386 / 342. Not where the scratch memory would
 // pass kWidenBytes. K is rounded to bf16 with it (D = 128: without it not), which
 // scales that are powers of two do not notice.
-constexpr int64_t kWidenRows = 512, kWidenBytes = 1ll << 30;
 struct WidenPlan {
   bool on;
   int pages;                 // of kBlockN tokens, per sequence
@@ -299,12 +346,12 @@ struct WidenPlan {
 WidenPlan plan_widen(const attn_paged_params* p) {
   WidenPlan w = {};
   const attn_kv_cache& c = p->cache;
-  if (c.dtype != ATTN_DTYPE_FP8_E4M3 || !use_tc05(p)) return w;
+  if (c.dtype == ATTN_DTYPE_BF16 || !use_tc05(p)) return w;
   const int64_t tokens = p->cu_seqlens_q != nullptr ? p->total_q : (int64_t)c.batch * p->seqlen_q;
   w.pages = af::tiles_for(p->seqlen_k, af::kBlockN);
   const int64_t n = (int64_t)c.batch * w.pages, row = (int64_t)c.num_heads_kv * af::kBlockN * c.head_dim * 2;
-  w.on = w.pages > 0 && tokens * (p->num_heads_q / c.num_heads_kv) >= kWidenRows * c.batch &&
-         n <= kWidenBytes / (2 * row);
+  w.on = copy_fits(p) && (c.dtype == ATTN_DTYPE_FP4_E2M1 ||
+                          tokens * (p->num_heads_q / c.num_heads_kv) >= kWidenRows * c.batch);
   if (!w.on) return w;
   w.table = round256((size_t)n * sizeof(int32_t));
   w.rows = (size_t)(n * row);
@@ -324,7 +371,8 @@ size_t scratch_need(const attn_paged_params* p) {
 // Stride of a dimension of size 1 (never used, but a tensor map wants a legal one).
 int64_t legal(int64_t stride, int64_t size) { return size > 1 ? stride : 16; }
 
-attn_status launch_tiles(const attn_paged_params* p, uint8_t* scratch, cudaStream_t stream) {
+attn_status launch_tiles(const attn_paged_params* p, const attn_block_scales* blocks, uint8_t* scratch,
+                         cudaStream_t stream) {
   const TilePlan plan = plan_tiles(p);
   attn_kv_cache c = p->cache;
   const bool packed = p->cu_seqlens_q != nullptr;
@@ -341,7 +389,8 @@ attn_status launch_tiles(const attn_paged_params* p, uint8_t* scratch, cudaStrea
     wp.k = at + w.table;
     wp.v = wp.k + w.rows;
     wp.ws = static_cast<uint32_t*>(p->workspace);
-    const cudaError_t e = af::cache_widen_launch(wp, c.head_dim, stream);
+    wp.blocks = blocks_of(blocks);
+    const cudaError_t e = af::cache_widen_launch(wp, c.head_dim, c.dtype, stream);
     if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "cache widening launch failed: %s", cudaGetErrorString(e));
     c.k = wp.k;
     c.v = wp.v;
@@ -466,10 +515,12 @@ attn_status launch_tiles(const attn_paged_params* p, uint8_t* scratch, cudaStrea
 
 }  // namespace
 
-attn_status af::paged_fwd(const attn_paged_params* params, void* scratch, size_t scratch_bytes, cudaStream_t stream) {
+attn_status af::paged_fwd(const attn_paged_params* params, const attn_block_scales* blocks, void* scratch,
+                          size_t scratch_bytes, cudaStream_t stream) {
   report_error(ATTN_OK, "%s", "");
   attn_status st = check_paged(params);
   if (st != ATTN_OK) return st;
+  if ((st = check_blocks(params->cache, blocks)) != ATTN_OK) return st;
   if (no_rows(params)) return ATTN_OK;
   const attn_paged_params with_rows = planned(params), *p = &with_rows;
   if ((st = check_workspace(p->workspace)) != ATTN_OK) return st;
@@ -480,13 +531,14 @@ attn_status af::paged_fwd(const attn_paged_params* params, void* scratch, size_t
     return report_error(ATTN_ERR_INVALID_ARG, "scratch memory of at least %zu bytes is required", need);
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
   uint8_t* const room = scratch != nullptr ? static_cast<uint8_t*>(scratch) : ws + kZeroedBytes;
-  if (use_tc05(p)) return launch_tiles(p, room, stream);
+  if (use_tc05(p)) return launch_tiles(p, blocks, room, stream);
   const StreamPlan plan = plan_stream(p);
   if (plan.units > kMaxUnits) return report_error(ATTN_ERR_UNSUPPORTED, "more than 2^30 sequences times KV heads");
   const bool packed = p->cu_seqlens_q != nullptr;
   af::StreamParams a;
   memset(&a, 0, sizeof(a));
   a.c = view_of(p->cache);
+  a.blocks = blocks_of(blocks);
   a.s.cu_q = p->cu_seqlens_q;
   a.s.seqlens_k = p->seqlens_k;
   a.s.batch = p->cache.batch;
@@ -514,8 +566,7 @@ attn_status af::paged_fwd(const attn_paged_params* params, void* scratch, size_t
   a.part_ml = reinterpret_cast<float2*>(room);
   a.part_o = reinterpret_cast<float*>(room + plan.ml_bytes);
   const cudaError_t e =
-      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
-                              (int)plan.grid, stream);
+      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype, plan.row_tile, (int)plan.grid, stream);
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
@@ -531,9 +582,22 @@ size_t attn_paged_params_size(int32_t which) {
   return 0;
 }
 
+size_t attn_cache_blocks_params_size(int32_t which) {
+  switch (which) {
+    case 0: return sizeof(attn_block_scales);
+    case 1: return sizeof(attn_cache_rotary);
+  }
+  return 0;
+}
+
 attn_status attn_cache_append(const attn_cache_append_params* p, attn_stream_t stream) {
+  return attn_cache_append_blocks(p, nullptr, nullptr, stream);
+}
+
+attn_status attn_cache_append_blocks(const attn_cache_append_params* p, const attn_block_scales* blocks,
+                                     const attn_cache_rotary* rotary, attn_stream_t stream) {
   report_error(ATTN_OK, "%s", "");
-  const attn_status st = check_append(p);
+  const attn_status st = check_append(p, blocks, rotary);
   if (st != ATTN_OK) return st;
   const bool packed = p->cu_seqlens_q != nullptr;
   if (p->cache.batch == 0 || (packed ? p->total_q : p->seqlen_q) == 0) return ATTN_OK;
@@ -555,17 +619,41 @@ attn_status attn_cache_append(const attn_cache_append_params* p, attn_stream_t s
   a.v_t = p->v_stride[1] * 2;
   a.v_h = p->v_stride[2] * 2;
   a.wide = wide_rows(p->k, p->k_stride, packed ? 1 : 0, 3) && wide_rows(p->v, p->v_stride, packed ? 1 : 0, 3);
+  a.blocks = blocks_of(blocks);
+  if (rotary != nullptr) {
+    const bool q = rotary->num_heads_q > 0;
+    a.wide = a.wide && (!q || wide_rows(rotary->q, rotary->q_stride, packed ? 1 : 0, 3));
+    a.r.table = rotary->table;
+    a.r.positions = rotary->positions;
+    a.r.q = static_cast<const uint8_t*>(rotary->q);
+    a.r.q_out = static_cast<uint8_t*>(rotary->q_out);
+    a.r.q_b = packed ? 0 : rotary->q_stride[0] * 2;
+    a.r.q_t = rotary->q_stride[1] * 2;
+    a.r.q_h = rotary->q_stride[2] * 2;
+    a.r.out_b = packed ? 0 : rotary->q_out_stride[0] * 2;
+    a.r.out_t = rotary->q_out_stride[1] * 2;
+    a.r.out_h = rotary->q_out_stride[2] * 2;
+    a.r.heads_q = rotary->num_heads_q;
+    a.r.num_positions = rotary->num_positions;
+    a.r.rot = rotary->rotary_dim;
+    a.r.interleaved = rotary->interleaved != 0;
+  }
   a.tokens = packed ? p->total_q : (int64_t)p->cache.batch * p->seqlen_q;
   a.ws = static_cast<uint32_t*>(p->workspace);
-  const cudaError_t e = af::cache_append_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3,
-                                                reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e =
+      af::cache_append_launch(a, p->cache.head_dim, p->cache.dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "cache append launch failed: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
 
 attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t stream) {
+  return attn_cache_read_blocks(p, nullptr, stream);
+}
+
+attn_status attn_cache_read_blocks(const attn_cache_read_params* p, const attn_block_scales* blocks,
+                                   attn_stream_t stream) {
   report_error(ATTN_OK, "%s", "");
-  const attn_status st = check_read(p);
+  const attn_status st = check_read(p, blocks);
   if (st != ATTN_OK) return st;
   if (p->cache.batch == 0 || p->total_k == 0) return ATTN_OK;
   af::ReadParams r;
@@ -579,11 +667,12 @@ attn_status attn_cache_read(const attn_cache_read_params* p, attn_stream_t strea
   r.v_t = p->v_stride[0] * 2;
   r.v_h = p->v_stride[1] * 2;
   r.wide = wide_rows(p->k, p->k_stride, 0, 2) && wide_rows(p->v, p->v_stride, 0, 2);
+  r.blocks = blocks_of(blocks);
   r.batch = p->cache.batch;
   r.total_k = p->total_k;
   r.ws = static_cast<uint32_t*>(p->workspace);
-  const cudaError_t e = af::cache_read_launch(r, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3,
-                                              reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e =
+      af::cache_read_launch(r, p->cache.head_dim, p->cache.dtype, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "cache read launch failed: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
@@ -595,7 +684,11 @@ size_t attn_paged_workspace_bytes(const attn_paged_params* p) {
 }
 
 attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
-  return af::paged_fwd(p, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
+  return attn_paged_fwd_blocks(p, nullptr, stream);
+}
+
+attn_status attn_paged_fwd_blocks(const attn_paged_params* p, const attn_block_scales* blocks, attn_stream_t stream) {
+  return af::paged_fwd(p, blocks, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -7,10 +7,11 @@
 
 namespace af {
 
-// attn_paged_fwd with what it needs behind the workspace's first
+// attn_paged_fwd_blocks with what it needs behind the workspace's first
 // ATTN_PAGED_ZEROED_BYTES in memory of its own: at least
 // attn_paged_workspace_bytes(p) - ATTN_PAGED_ZEROED_BYTES bytes, 256-byte aligned
 // (NULL: behind them, as there).
-attn_status paged_fwd(const attn_paged_params* p, void* scratch, size_t scratch_bytes, cudaStream_t stream);
+attn_status paged_fwd(const attn_paged_params* p, const attn_block_scales* blocks, void* scratch, size_t scratch_bytes,
+                      cudaStream_t stream);
 
 }  // namespace af

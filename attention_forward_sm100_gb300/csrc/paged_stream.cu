@@ -59,30 +59,35 @@ constexpr int kThreads = 128;
 constexpr int min_int(int a, int b) { return a < b ? a : b; }
 
 // NT * 8 rows per warp, WM warps to a key group.
-template <int D_, bool FP8_, int NT_, int WM_>
+template <int D_, int KIND_, int NT_, int WM_>
 struct Cfg {
-  static constexpr int D = D_, NT = NT_, WM = WM_;
-  static constexpr bool FP8 = FP8_;
-  static constexpr int CTAS = stream_ctas(FP8 ? D : 2 * D, 8 * NT * WM);
+  static constexpr int D = D_, NT = NT_, WM = WM_, KIND = KIND_;
+  static constexpr bool FP8 = KIND == kE4m3, FP4 = KIND == kE2m1;
+  static constexpr bool CODES = FP8 || FP4;      // codes with scales, multiplied as f16
+  static constexpr int ROWB = FP4 ? D / 2 : (FP8 ? D : 2 * D);   // bytes of a cached row
+  static constexpr int CTAS = stream_ctas(ROWB, 8 * NT * WM);
   static constexpr int WK = 4 / WM;              // key groups
   static constexpr int RT = 8 * NT * WM;         // rows of a row tile
-  static constexpr int ROWB = FP8 ? D : 2 * D;   // bytes of a cached row
   static constexpr int KW = stream_tile(ROWB, WM) / WK;   // keys of a group per tile
   static constexpr int TILE = KW * WK;
   static constexpr int BLOCKS = KW / 16;         // 16-key blocks of a group's tile
   static constexpr int CPR = ROWB / 16;          // 16-byte pieces of a row
   static constexpr int GT = 32 * WM;             // threads of a group
-  static constexpr int RS = GT / CPR;            // rows a group loads at a time
+  static constexpr int LT = min_int(GT, 16 * CPR);   // of them, those that load rows
+  static constexpr int RS = LT / CPR;            // rows a group loads at a time
   static_assert(RS <= 16, "the rows of a load lie in one 16-key block");
   static constexpr int NL = KW / RS;             // loads per thread of K (and of V)
   static constexpr int KV = KW * ROWB;
-  static constexpr int SC = FP8 ? KW * 4 : 0;
-  static constexpr int STAGE = 2 * KV + 2 * SC;  // bytes of one group's stage
+  static constexpr int SC = CODES ? KW * 4 : 0;      // a scale for every key
+  static constexpr int BK = D / 16;                  // block scales of a key
+  static constexpr int BL = FP4 ? KW * BK : 0;
+  static constexpr int STAGE = 2 * (KV + SC + BL);   // bytes of one group's stage
   // At the end of a segment a group leaves its part of O in the stage that it
   // has just used up, or, where that is too small, in room of its own.
   static constexpr int PART = RT * D * 4;
   static constexpr bool OWN_PART = PART > STAGE;
-  static constexpr int STAGES = min_int(8, (196608 / CTAS - (OWN_PART ? WK * PART : 0)) / (WK * 2 * KV));
+  static constexpr int STAGES = FP4 ? min_int(8, (225280 / CTAS - (OWN_PART ? WK * PART : 0)) / (WK * STAGE))
+                                    : min_int(8, (196608 / CTAS - (OWN_PART ? WK * PART : 0)) / (WK * 2 * KV));
   static constexpr int RING = WK * STAGES * STAGE;
   static constexpr int OFF_ML = RING + (OWN_PART ? WK * PART : 0);   // [WK][RT] (maximum, sum)
   static constexpr int SMEM = OFF_ML + WK * RT * 8;
@@ -94,9 +99,17 @@ struct Cfg {
   __device__ static int part_col(int r, int d) { return d ^ (((r >> 1) & 3) << 3); }
   // Position of 16-byte piece `c` of row `r` in a stage (bank conflicts).
   __device__ static int swz_k(int r, int c) {
+    if (FP4) return CPR == 4 ? c ^ ((r >> 1) & 2) : c;
     return FP8 ? (CPR == 8 ? c ^ ((r & 1) << 2) : c) : c ^ (r & 7);
   }
-  __device__ static int swz_v(int r, int c) { return FP8 && CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & 7); }
+  __device__ static int swz_v(int r, int c) {
+    if (FP4) return swz_k(r, c);
+    return FP8 && CPR == 4 ? c ^ ((r >> 1) & 3) : c ^ (r & 7);
+  }
+  // Which row of an 8-key group is key m of the instructions (any order will do, as
+  // long as K and V agree): e2m1 rows are so short that the four rows 2 t that the
+  // lanes of a product with V read would lie in the same banks.
+  __device__ static int key_row(int m) { return !FP4 ? m : (CPR == 4 ? m ^ ((m >> 1) & 1) : m ^ ((m >> 2) & 1)); }
 };
 
 // The CTAs work in teams of P.team neighbours, and the cut of the work is one for
@@ -326,6 +339,7 @@ struct Loader {
     constexpr int PER = 16 / C::RS;   // loads of a 16-key block per thread
 #pragma unroll
     for (int i = 0; i < C::NL; i += PER) {
+      if (C::LT < C::GT && gt >= C::LT) break;
       const int page = pages[i / PER];
       const int64_t slot = (key0 + 16 * (i / PER)) & page_mask;
       const uint8_t* kp = ks + page * P.c.k_page + slot * P.c.k_tok;
@@ -341,7 +355,25 @@ struct Loader {
         vp += C::RS * P.c.v_tok;
       }
     }
-    if constexpr (C::FP8) {
+    if constexpr (C::FP4) {
+      // block scales: 16 / BK keys per 16 bytes, cut at the end as the others
+      constexpr int KP = 16 / C::BK, NP = C::KW / KP;
+      static_assert(2 * NP <= C::GT, "one piece per thread");
+      if (gt < 2 * NP) {
+        const int which = gt / NP, k = KP * (gt % NP);
+        int page = pages[0];
+#pragma unroll
+        for (int u = 1; u < C::BLOCKS; ++u)
+          if ((k >> 4) == u) page = pages[u];
+        const int bytes = min(16, max(0, lk - (key0 + k)) * C::BK);
+        const uint8_t* base = which ? P.blocks.v : P.blocks.k;
+        const uint8_t* src =
+            bytes ? base + ((((int64_t)page * P.c.heads_kv + hk) << P.c.page_shift) + ((key0 + k) & page_mask)) * C::BK
+                  : base;
+        ptx::cp_async16_part(st + 2 * (C::KV + C::SC) + which * C::BL + k * C::BK, src, bytes);
+      }
+    }
+    if constexpr (C::CODES) {
       // scales: 4 keys per 16 bytes; a piece that crosses the end is cut there
       if (gt < 2 * C::KW / 4) {
         const int which = gt / (C::KW / 4), k4 = 4 * (gt % (C::KW / 4));
@@ -465,8 +497,9 @@ __device__ __forceinline__ void load_q(const StreamParams& P, const Piece& pc, c
     const uint8_t* src = q_row(P, s, pc.b, row_at(P, head_of(P, pc.seg), ok ? r : 0));
 #pragma unroll
     for (int kk = 0; kk < C::D / 16; ++kk) {
-      const int d = C::FP8 ? 16 * (t + 4 * (kk >> 2)) + 4 * (kk & 3) : 16 * kk + 2 * t;
-      const int step = C::FP8 ? 2 : 8;
+      const int d = C::FP4 ? C::D / 4 * t + 4 * kk
+                           : (C::FP8 ? 16 * (t + 4 * (kk >> 2)) + 4 * (kk & 3) : 16 * kk + 2 * t);
+      const int step = C::CODES ? 2 : 8;
       qf[x][kk][0] = ok ? (uint32_t)ptx::ld_global_pinned(reinterpret_cast<const int*>(src + 2 * d)) : 0u;
       qf[x][kk][1] = ok ? (uint32_t)ptx::ld_global_pinned(reinterpret_cast<const int*>(src + 2 * (d + step))) : 0u;
     }
@@ -483,6 +516,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   constexpr int D = C::D, WM = C::WM, NT = C::NT, KW = C::KW, NB = C::BLOCKS;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
+  const int gk = C::key_row(g);                   // row of this lane's key among eight
   const int wm = warp % WM, kg = warp / WM;
   const int gt = wm * 32 + lane;                  // thread within its key group
   const int hk = head_of(P, pc.seg), rt = row_tile_of(P, pc.seg);
@@ -509,8 +543,8 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   lim_min = min(lim_min, __shfl_xor_sync(kFull, lim_min, 2));
 #pragma unroll
   for (int x = 0; x < NT; ++x) {
-    if constexpr (C::FP8) {
-      // The codes of an e4m3 cache are multiplied as f16 (one conversion for two
+    if constexpr (C::CODES) {
+      // The codes of an e4m3 or e2m1 cache are multiplied as f16 (one conversion for two
       // of them). q becomes f16 too, times the power of two that brings its
       // largest magnitude to [2^14, 2^15): exact down to 2^-38 of that.
       uint32_t top = 0u;
@@ -553,7 +587,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][x][e] = 0.f;
-  // e4m3: the accumulator is in units of vref / 2^7, vref a power of two at
+  // Codes: the accumulator is in units of vref / 2^7, vref a power of two at
   // least as large as every value scale so far. While the scales of a step are
   // within 2^-4 of it, weights (times scale / vref * 2^7, at most 2^15) and codes
   // are multiplied as f16: its spacing near zero, 2^-24, then costs a key less
@@ -588,7 +622,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[i][x][e] = 0.f;
-    if constexpr (!C::FP8) {
+    if constexpr (!C::CODES) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -599,6 +633,45 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
 #pragma unroll
           for (int x = 0; x < NT; ++x) ptx::mma_16816(sc[i][x], a, qf[x][kk][0], qf[x][kk][1]);
         }
+    } else if constexpr (C::FP4) {
+      // lane t holds depths t D/4 .. of its two keys, one or two blocks of them; codes
+      // times block scales are exact in f16
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        uint32_t w[2][D / 32], s2[2][D / 64];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = 16 * i + gk + 8 * e;
+          const uint32_t bl = st + 2 * (C::KV + C::SC) + row * C::BK;
+          if constexpr (D == 128) {
+            const uint4 v = ptx::ld_shared_v4(st + row * C::ROWB + C::swz_k(row, t) * 16);
+            w[e][0] = v.x; w[e][1] = v.y; w[e][2] = v.z; w[e][3] = v.w;
+            const uint32_t b = ptx::e4m3x2_to_f16x2(ptx::ld_shared_u16(bl + 2 * t));
+            s2[e][0] = __byte_perm(b, b, 0x1010);
+            s2[e][1] = __byte_perm(b, b, 0x3232);
+          } else {
+            const uint2 v = ptx::ld_shared_v2(st + row * C::ROWB + 8 * t);
+            w[e][0] = v.x; w[e][1] = v.y;
+            s2[e][0] = ptx::e4m3x2_to_f16x2(ptx::ld_shared_u8(bl + t) * 0x101u);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t h[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            ptx::e2m1x8_to_f16x2(w[e][c], h[e]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) h[e][y] = ptx::mul_f16x2(h[e][y], s2[e][c / 2]);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t a[4] = {h[0][2 * y], h[1][2 * y], h[0][2 * y + 1], h[1][2 * y + 1]};
+#pragma unroll
+            for (int x = 0; x < NT; ++x) ptx::mma_16816_f16(sc[i][x], a, qf[x][2 * c + y][0], qf[x][2 * c + y][1]);
+          }
+        }
+      }
     } else {
 #pragma unroll
       for (int c = 0; c < D / 64; ++c)
@@ -623,15 +696,15 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       float k0 = 1.f, k1 = 1.f;
-      if constexpr (C::FP8) {
-        k0 = scale_sm[16 * i + g];
-        k1 = scale_sm[16 * i + g + 8];
+      if constexpr (C::CODES) {
+        k0 = scale_sm[16 * i + gk];
+        k1 = scale_sm[16 * i + gk + 8];
       }
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          sc[i][x][e] *= C::FP8 ? qscale[x][e & 1] * (e < 2 ? k0 : k1) : qscale[x][e & 1];
+          sc[i][x][e] *= C::CODES ? qscale[x][e & 1] * (e < 2 ? k0 : k1) : qscale[x][e & 1];
     }
     if (key0 + KW > lim_min) {
 #pragma unroll
@@ -640,7 +713,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (key0 + 16 * i + g + 8 * (e >> 1) >= lim[x][e & 1]) sc[i][x][e] = -INFINITY;
+            if (key0 + 16 * i + gk + 8 * (e >> 1) >= lim[x][e & 1]) sc[i][x][e] = -INFINITY;
     }
     float mx[NT][2];
     bool grow = false;
@@ -687,7 +760,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
           l[x][e & 1] += sc[i][x][e];
         }
     // ---- O^T += V^T P^T
-    if constexpr (!C::FP8) {
+    if constexpr (!C::CODES) {
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         uint32_t pf[NT][2];
@@ -711,10 +784,10 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
       for (int i = 0; i < NB; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          vs[i][e] = scale_sm[KW + 16 * i + g + 8 * e];
+          vs[i][e] = scale_sm[KW + 16 * i + gk + 8 * e];
           top = fmaxf(top, fabsf(vs[i][e]));
           // (keys behind the end have scale 0 and weight 0)
-          if (key0 + 16 * i + g + 8 * e < s.lk) low = fminf(low, fabsf(vs[i][e]));
+          if (key0 + 16 * i + gk + 8 * e < s.lk) low = fminf(low, fabsf(vs[i][e]));
         }
       if (__any_sync(kFull, top > vref)) {
 #pragma unroll
@@ -744,12 +817,25 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
           pf[x][1] = ptx::movmatrix_trans(as_f16 ? ptx::pack_f16(a2, a3) : ptx::pack_bf16(a2, a3));
         }
         // lane (g, t): depths g * D/8 .. + D/8 of keys 2t, 2t+1, 2t+8, 2t+9
-        uint32_t v[4][D / 32];
+        constexpr int VW = C::FP4 ? D / 64 : D / 32;
+        uint32_t v[4][VW];
+        uint32_t s01 = 0u, s23 = 0u;   // e2m1: block scales of the keys' depths, as f16
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int row = 16 * i + 2 * t + (e & 1) + 8 * (e >> 1);
+          const int row = 16 * i + C::key_row(2 * t + (e & 1)) + 8 * (e >> 1);
           const uint32_t at = st + C::KV + row * C::ROWB;
-          if constexpr (D == 128) {
+          if constexpr (C::FP4) {
+            if constexpr (D == 128) {
+              const uint2 w = ptx::ld_shared_v2(at + C::swz_v(row, g >> 1) * 16 + (g & 1) * 8);
+              v[e][0] = w.x; v[e][1] = w.y;
+            } else {
+              v[e][0] = ptx::ld_shared_u32(at + 4 * g);
+            }
+            const uint32_t b =
+                ptx::ld_shared_u8(st + 2 * (C::KV + C::SC) + C::BL + row * C::BK + (D == 128 ? g : g >> 1)) << (8 * (e & 1));
+            if (e < 2) s01 |= b;
+            else s23 |= b;
+          } else if constexpr (D == 128) {
             const uint4 w = ptx::ld_shared_v4(at + C::swz_v(row, g) * 16);
             v[e][0] = w.x; v[e][1] = w.y; v[e][2] = w.z; v[e][3] = w.w;
           } else {
@@ -757,8 +843,42 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
             v[e][0] = w.x; v[e][1] = w.y;
           }
         }
+        if constexpr (C::FP4) {
+          s01 = ptx::e4m3x2_to_f16x2(s01);
+          s23 = ptx::e4m3x2_to_f16x2(s23);
+        }
         // (key, key) pairs of each depth
+        auto product4 = [&](auto f16) {
+          constexpr uint32_t LOW = 0x0f0f0f0fu;
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            uint32_t h[4][4];   // even depths of keys 0 and 1, odd ones, the same of keys 2 and 3
+            ptx::e2m1x8_to_f16x2((v[0][w] & LOW) | ((v[1][w] << 4) & ~LOW), h[0]);
+            ptx::e2m1x8_to_f16x2(((v[0][w] >> 4) & LOW) | (v[1][w] & ~LOW), h[1]);
+            ptx::e2m1x8_to_f16x2((v[2][w] & LOW) | ((v[3][w] << 4) & ~LOW), h[2]);
+            ptx::e2m1x8_to_f16x2(((v[2][w] >> 4) & LOW) | (v[3][w] & ~LOW), h[3]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t a[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                a[c] = ptx::mul_f16x2(h[c][y], c < 2 ? s01 : s23);
+                if constexpr (!decltype(f16)::value) a[c] = ptx::f16x2_to_bf16x2(a[c]);
+              }
+#pragma unroll
+              for (int x = 0; x < NT; ++x) {
+                if constexpr (decltype(f16)::value) ptx::mma_16816_f16(acc[4 * w + y][x], a, pf[x][0], pf[x][1]);
+                else ptx::mma_16816(acc[4 * w + y][x], a, pf[x][0], pf[x][1]);
+              }
+            }
+          }
+        };
         auto product = [&](auto f16) {
+          if constexpr (C::FP4) {
+            product4(f16);
+            return;
+          }
+          if constexpr (!C::FP4) {
 #pragma unroll
           for (int w = 0; w < D / 32; ++w)
 #pragma unroll
@@ -780,6 +900,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
                 for (int x = 0; x < NT; ++x) ptx::mma_16816(acc[2 * w + h][x], a, pf[x][0], pf[x][1]);
               }
             }
+          }
         };
         if (as_f16) product(std::true_type{});
         else product(std::false_type{});
@@ -793,7 +914,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[x][e] += __shfl_xor_sync(kFull, l[x][e], o);
 
-  if constexpr (C::FP8) {
+  if constexpr (C::CODES) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
@@ -824,7 +945,7 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
         float* dst = part + r * D;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          if constexpr (C::FP8) {
+          if constexpr (C::CODES) {
             *reinterpret_cast<float2*>(dst + C::part_col(r, g * (D / 8) + 2 * i)) = make_float2(acc[i][x][e], acc[i][x][2 + e]);
           } else {
             dst[C::part_col(r, 16 * i + g)] = acc[i][x][e];
@@ -913,10 +1034,10 @@ __device__ void run_piece(const StreamParams& P, const Piece& pc, const SeqRows&
   join_parts<C>(P, hoods, valid, [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish_row);
 }
 
-template <int D, bool FP8, int NT, int WM>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, NT, WM>::CTAS))
+template <int D, int KIND, int NT, int WM>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, KIND, NT, WM>::CTAS))
     paged_stream_kernel(const __grid_constant__ StreamParams P) {
-  using C = Cfg<D, FP8, NT, WM>;
+  using C = Cfg<D, KIND, NT, WM>;
   extern __shared__ __align__(128) uint8_t smem[];
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
@@ -956,30 +1077,35 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, NT, WM>::CTAS))
   ptx::cp_async_wait<0>();
 }
 
-template <int D, bool FP8, int NT, int WM>
+template <int D, int KIND, int NT, int WM>
 cudaError_t launch_t(const StreamParams& p, int grid, cudaStream_t stream) {
-  using C = Cfg<D, FP8, NT, WM>;
-  constexpr auto kern = paged_stream_kernel<D, FP8, NT, WM>;
+  using C = Cfg<D, KIND, NT, WM>;
+  constexpr auto kern = paged_stream_kernel<D, KIND, NT, WM>;
   return launch_with_smem<kern>(
       C::SMEM, [&]() { return launch_dependent(kern, p, dim3((unsigned)grid), kThreads, C::SMEM, stream); });
 }
 
-template <int D, bool FP8>
+template <int D, int KIND>
 cudaError_t launch_d(const StreamParams& p, int row_tile, int grid, cudaStream_t stream) {
   switch (row_tile) {
-    case 8: return launch_t<D, FP8, 1, 1>(p, grid, stream);
-    case 16: return launch_t<D, FP8, 2, 1>(p, grid, stream);
-    default: return launch_t<D, FP8, 2, 2>(p, grid, stream);
+    case 8: return launch_t<D, KIND, 1, 1>(p, grid, stream);
+    case 16: return launch_t<D, KIND, 2, 1>(p, grid, stream);
+    default: return launch_t<D, KIND, 2, 2>(p, grid, stream);
   }
+}
+
+template <int D>
+cudaError_t launch_k(const StreamParams& p, int kind, int row_tile, int grid, cudaStream_t stream) {
+  return kind == kBf16 ? launch_d<D, kBf16>(p, row_tile, grid, stream)
+                       : (kind == kE4m3 ? launch_d<D, kE4m3>(p, row_tile, grid, stream)
+                                        : launch_d<D, kE2m1>(p, row_tile, grid, stream));
 }
 
 }  // namespace
 
-cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,
+cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, int kind, int row_tile, int grid,
                                 cudaStream_t stream) {
-  if (head_dim == 128)
-    return fp8 ? launch_d<128, true>(p, row_tile, grid, stream) : launch_d<128, false>(p, row_tile, grid, stream);
-  return fp8 ? launch_d<64, true>(p, row_tile, grid, stream) : launch_d<64, false>(p, row_tile, grid, stream);
+  return head_dim == 128 ? launch_k<128>(p, kind, row_tile, grid, stream) : launch_k<64>(p, kind, row_tile, grid, stream);
 }
 
 }  // namespace af

@@ -1,10 +1,10 @@
-// Python side of the paged-cache operators (attn_paged.h): argument checks,
+// Python side of the paged-cache and rotary operators (attn_paged.h, attn_rotary.h): argument checks,
 // output and workspace allocation, and the call into the library. Compiled
 // code instead of ctypes because a decoding step is a few microseconds of GPU
 // work: with the checks in Python one paged_forward call cost 28 us of host
 // time on GB300's CPU, an append 15 us.
 //
-// Functions take positional arguments (paged.py has the public signatures and
+// Functions take positional arguments (paged.py and rope.py have the public signatures and
 // their documentation) and return the outputs, or the library's status as an
 // int if the call was refused there. Bad arguments raise ValueError before
 // anything is allocated or enqueued.
@@ -28,6 +28,7 @@
 #include <string>
 
 #include "../../include/attn_paged.h"
+#include "../../include/attn_rotary.h"
 #include "paged_host.h"
 
 namespace {
@@ -99,25 +100,47 @@ void check_int32(const Arg& a, int64_t n) {
   need_f(a->dim() == 1 && a->size(0) == n, "%s must have %lld entries", a.name, (long long)n);
 }
 
-attn_kv_cache check_cache(const Arg& k, const Arg& v, const Arg& table, const Arg& k_scale, const Arg& v_scale) {
+// The cache, and (e2m1) its block scales, which are all nothing or all there.
+struct Cache {
+  attn_kv_cache c;
+  attn_block_scales blocks;
+  const attn_block_scales* blocks_or_none() const { return c.dtype == ATTN_DTYPE_FP4_E2M1 ? &blocks : nullptr; }
+};
+
+Cache check_cache(const Arg& k, const Arg& v, const Arg& table, const Arg& k_scale, const Arg& v_scale,
+                  const Arg& k_block, const Arg& v_block) {
   need(k->dim() == 4 && k->sizes() == v->sizes(), "k_cache and v_cache must be [pages, page_size, Hkv, D] of one shape");
-  need(is(k, at::kBFloat16) || is(k, at::kFloat8_e4m3fn), "unsupported cache dtype (bf16 or float8_e4m3fn)");
+  const bool fp4 = is(k, at::kByte) || is(k, at::kFloat4_e2m1fn_x2);
+  need(fp4 || is(k, at::kBFloat16) || is(k, at::kFloat8_e4m3fn),
+       "unsupported cache dtype (bf16, float8_e4m3fn, or e2m1 as uint8 or float4_e2m1fn_x2)");
   need(k->scalar_type() == v->scalar_type(), "k_cache and v_cache must have one dtype");
   need(k->stride(3) == 1 && v->stride(3) == 1, "the cache's depth must be contiguous");
   need(table->dim() == 2 && is(table, at::kInt), "block_table must be an int32 [B, max_pages] tensor");
   need(table->size(1) <= 1 || table->stride(1) == 1, "the rows of block_table must be contiguous");
-  attn_kv_cache c = {};
+  Cache r = {};
+  attn_kv_cache& c = r.c;
   const bool fp8 = is(k, at::kFloat8_e4m3fn);
   c.num_pages = int32("pages", k->size(0));
   c.page_size = int32("page_size", k->size(1));
   c.num_heads_kv = int32("Hkv", k->size(2));
-  c.head_dim = int32("D", k->size(3));
+  c.head_dim = int32("D", k->size(3) * (fp4 ? 2 : 1));
+  for (const Arg* s : {&k_block, &v_block}) {
+    if (!fp4) {
+      need_f(!*s, "only an e2m1 cache takes %s", s->name);
+      continue;
+    }
+    need_f(bool(*s), "an e2m1 cache needs %s", s->name);
+    need_f(is(*s, at::kFloat8_e4m3fn) && (*s)->is_contiguous() && (*s)->dim() == 4 && (*s)->size(0) == c.num_pages &&
+               (*s)->size(1) == c.num_heads_kv && (*s)->size(2) == c.page_size && (*s)->size(3) * 16 == c.head_dim,
+           "%s must be a contiguous float8_e4m3fn [pages, Hkv, page_size, D / 16] tensor", s->name);
+  }
+  r.blocks = {k_block.ptr(), v_block.ptr()};
   for (const Arg* s : {&k_scale, &v_scale}) {
-    if (!fp8) {
+    if (!fp8 && !fp4) {
       need(!*s, "a bf16 cache takes no scales");
       continue;
     }
-    need_f(bool(*s), "an e4m3 cache needs %s", s->name);
+    need_f(bool(*s), "an %s cache needs %s", fp4 ? "e2m1" : "e4m3", s->name);
     need_f(is(*s, at::kFloat) && (*s)->is_contiguous() && (*s)->dim() == 3 && (*s)->size(0) == c.num_pages &&
                (*s)->size(1) == c.num_heads_kv && (*s)->size(2) == c.page_size,
            "%s must be a contiguous fp32 [pages, Hkv, page_size] tensor", s->name);
@@ -132,10 +155,23 @@ attn_kv_cache check_cache(const Arg& k, const Arg& v, const Arg& table, const Ar
     c.v_stride[i] = stride(v, i);
   }
   c.table_stride = stride(table, 0);
-  c.dtype = fp8 ? ATTN_DTYPE_FP8_E4M3 : ATTN_DTYPE_BF16;
+  c.dtype = fp4 ? ATTN_DTYPE_FP4_E2M1 : (fp8 ? ATTN_DTYPE_FP8_E4M3 : ATTN_DTYPE_BF16);
   c.max_pages = int32("max_pages", table->size(1));
   c.batch = int32("B", table->size(0));
-  return c;
+  return r;
+}
+
+// [positions, R] cosines and sines; the number of positions and R.
+void check_table(const Arg& t, int32_t& positions, int32_t& dim) {
+  need_f(is(t, at::kFloat) && t->dim() == 2 && t->is_contiguous(), "%s must be a contiguous fp32 [positions, R] tensor",
+         t.name);
+  positions = int32("positions", t->size(0));
+  dim = int32("R", t->size(1));
+}
+// int32, one for every row of [B, Sq] / [T].
+void check_positions(const Arg& p, at::IntArrayRef rows) {
+  need_f(!p || (is(p, at::kInt) && p->is_contiguous() && p->sizes() == rows),
+         "%s must be a contiguous int32 tensor with an entry for every row", p.name);
 }
 
 // The device all of them are on.
@@ -232,16 +268,21 @@ bool arity(Py_ssize_t got, Py_ssize_t want) {
   return false;
 }
 
-// (k, v, k_cache, v_cache, block_table, seqlens_k, k_scale, v_scale, cu_seqlens_q, workspace)
+// (k, v, k_cache, v_cache, block_table, seqlens_k, k_scale, v_scale, cu_seqlens_q, workspace, k_block, v_block,
+//  rotary_table, positions, interleaved, q, out_q)
 PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!arity(n, 10)) return nullptr;
+  if (!arity(n, 17)) return nullptr;
   PAGED_BEGIN
   const Arg k = tensor("k", a[0]), v = tensor("v", a[1]), kc = tensor("k_cache", a[2]), vc = tensor("v_cache", a[3]),
             table = tensor("block_table", a[4]), lens = tensor("seqlens_k", a[5]),
             ks = tensor_or_none("k_scale", a[6]), vs = tensor_or_none("v_scale", a[7]),
-            cu = tensor_or_none("cu_seqlens_q", a[8]), ws = tensor_or_none("workspace", a[9]);
+            cu = tensor_or_none("cu_seqlens_q", a[8]), ws = tensor_or_none("workspace", a[9]),
+            kb = tensor_or_none("k_block", a[10]), vb = tensor_or_none("v_block", a[11]),
+            turn = tensor_or_none("rotary_table", a[12]), pos = tensor_or_none("positions", a[13]),
+            q = tensor_or_none("q", a[15]), oq = tensor_or_none("out_q", a[16]);
   attn_cache_append_params p = {};
-  p.cache = check_cache(kc, vc, table, ks, vs);
+  const Cache cache = check_cache(kc, vc, table, ks, vs, kb, vb);
+  p.cache = cache.c;
   const int lead = cu ? 1 : 2;
   need(is(k, at::kBFloat16) && is(v, at::kBFloat16), "new keys and values must be bf16");
   need(k->dim() == lead + 2 && k->sizes() == v->sizes(),
@@ -261,10 +302,31 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.k_stride[i + 2 - lead] = stride(k, i);
     p.v_stride[i + 2 - lead] = stride(v, i);
   }
+  attn_cache_rotary r = {};
+  const int interleaved = PyObject_IsTrue(a[14]);
+  if (interleaved < 0) return nullptr;
+  need(bool(turn) || (!pos && !q && !oq && !interleaved), "positions, interleaved, q and out_q go with rotary_table");
+  need(bool(q) || !oq, "out_q goes with q");
+  if (turn) {
+    check_table(turn, r.num_positions, r.rotary_dim);
+    check_positions(pos, k->sizes().slice(0, lead));
+    r.interleaved = interleaved;
+  }
+  if (q) {
+    need(is(q, at::kBFloat16) && q->dim() == lead + 2 && q->sizes().slice(0, lead) == k->sizes().slice(0, lead) &&
+             q->size(lead + 1) == p.cache.head_dim && q->stride(lead + 1) == 1,
+         "q must be bf16 with k's rows and the cache's contiguous depth");
+    need(!oq || (is(oq, at::kBFloat16) && oq->sizes() == q->sizes() && oq->stride(lead + 1) == 1),
+         "out_q must be a bf16 tensor of q's shape with contiguous depth");
+    r.num_heads_q = int32("Hq", q->size(lead));
+  }
   check_workspace(ws);
-  const c10::DeviceIndex device = check_device(std::array<Arg, 10>{k, v, kc, vc, table, lens, ks, vs, cu, ws});
+  const c10::DeviceIndex device =
+      check_device(std::array<Arg, 16>{k, v, kc, vc, table, lens, ks, vs, cu, ws, kb, vb, turn, pos, q, oq});
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
+  at::Tensor fresh_q;
+  if (q && !oq) fresh_q = fresh(q->sizes(), at::kBFloat16, device);
   Workspace own;
   if (!ws) own.take(device, stream, ATTN_PAGED_ZEROED_BYTES);
   p.k = k.ptr();
@@ -272,20 +334,37 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.seqlens_k = static_cast<const int32_t*>(lens.ptr());
   p.cu_seqlens_q = static_cast<const int32_t*>(cu.ptr());
   p.workspace = ws ? ws.ptr() : own.memory.data_ptr();
-  return status(attn_cache_append(&p, stream));
+  if (turn) {
+    r.table = static_cast<const float*>(turn.ptr());
+    r.positions = static_cast<const int32_t*>(pos.ptr());
+    if (q) {
+      const Arg o = {"out_q", oq ? oq.t : &fresh_q};
+      r.q = q.ptr();
+      r.q_out = o.ptr();
+      for (int i = 0; i <= lead; ++i) {
+        r.q_stride[i + 2 - lead] = stride(q, i);
+        r.q_out_stride[i + 2 - lead] = stride(o, i);
+      }
+    }
+  }
+  const attn_status st = attn_cache_append_blocks(&p, cache.blocks_or_none(), turn ? &r : nullptr, stream);
+  if (st != ATTN_OK || !q) return status(st);
+  return oq ? same(a[16]) : THPVariable_Wrap(std::move(fresh_q));
   PAGED_END
 }
 
-// (k_cache, v_cache, block_table, cu_seqlens_k, total_k, k_scale, v_scale, out_k, out_v, workspace)
+// (k_cache, v_cache, block_table, cu_seqlens_k, total_k, k_scale, v_scale, out_k, out_v, workspace, k_block, v_block)
 PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!arity(n, 10)) return nullptr;
+  if (!arity(n, 12)) return nullptr;
   PAGED_BEGIN
   const Arg kc = tensor("k_cache", a[0]), vc = tensor("v_cache", a[1]), table = tensor("block_table", a[2]),
             cu = tensor("cu_seqlens_k", a[3]), ks = tensor_or_none("k_scale", a[5]),
             vs = tensor_or_none("v_scale", a[6]), ok = tensor_or_none("out_k", a[7]),
-            ov = tensor_or_none("out_v", a[8]), ws = tensor_or_none("workspace", a[9]);
+            ov = tensor_or_none("out_v", a[8]), ws = tensor_or_none("workspace", a[9]),
+            kb = tensor_or_none("k_block", a[10]), vb = tensor_or_none("v_block", a[11]);
   attn_cache_read_params p = {};
-  p.cache = check_cache(kc, vc, table, ks, vs);
+  const Cache cache = check_cache(kc, vc, table, ks, vs, kb, vb);
+  p.cache = cache.c;
   const int64_t heads = p.cache.num_heads_kv, dim = p.cache.head_dim;
   check_int32(cu, p.cache.batch + 1ll);
   need(bool(ok) == bool(ov), "out_k and out_v go together");
@@ -307,7 +386,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   p.total_k = int32("total_k", total);
   check_workspace(ws);
-  const c10::DeviceIndex device = check_device(std::array<Arg, 9>{kc, vc, table, cu, ks, vs, ok, ov, ws});
+  const c10::DeviceIndex device = check_device(std::array<Arg, 11>{kc, vc, table, cu, ks, vs, ok, ov, ws, kb, vb});
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
   at::Tensor fresh_k, fresh_v;
@@ -326,7 +405,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   p.cu_seqlens_k = static_cast<const int32_t*>(cu.ptr());
   p.workspace = ws ? ws.ptr() : own.memory.data_ptr();
-  const attn_status st = attn_cache_read(&p, stream);
+  const attn_status st = attn_cache_read_blocks(&p, cache.blocks_or_none(), stream);
   if (st != ATTN_OK) return status(st);
   PyObject* r = PyTuple_New(2);
   if (r == nullptr) return nullptr;
@@ -337,17 +416,19 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (q, k_cache, v_cache, block_table, seqlens_k, causal, softmax_scale, k_scale, v_scale, cu_seqlens_q, max_seqlen_q,
-//  max_seqlen_k, out, lse, return_lse, workspace)
+//  max_seqlen_k, out, lse, return_lse, workspace, k_block, v_block)
 PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!arity(n, 16)) return nullptr;
+  if (!arity(n, 18)) return nullptr;
   PAGED_BEGIN
   const Arg q = tensor("q", a[0]), kc = tensor("k_cache", a[1]), vc = tensor("v_cache", a[2]),
             table = tensor("block_table", a[3]), lens = tensor("seqlens_k", a[4]),
             ks = tensor_or_none("k_scale", a[7]), vs = tensor_or_none("v_scale", a[8]),
             cu = tensor_or_none("cu_seqlens_q", a[9]), out = tensor_or_none("out", a[12]),
-            lse = tensor_or_none("lse", a[13]), ws = tensor_or_none("workspace", a[15]);
+            lse = tensor_or_none("lse", a[13]), ws = tensor_or_none("workspace", a[15]),
+            kb = tensor_or_none("k_block", a[16]), vb = tensor_or_none("v_block", a[17]);
   attn_paged_params p = {};
-  p.cache = check_cache(kc, vc, table, ks, vs);
+  const Cache cache = check_cache(kc, vc, table, ks, vs, kb, vb);
+  p.cache = cache.c;
   const int lead = cu ? 1 : 2;
   need(is(q, at::kBFloat16), "q must be bf16");
   need(q->dim() == lead + 2, "q must be [B, Sq, Hq, D], or [T, Hq, D] with cu_seqlens_q");
@@ -389,7 +470,8 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int causal = PyObject_IsTrue(a[5]), want_lse = PyObject_IsTrue(a[14]);
   if (causal < 0 || want_lse < 0) return nullptr;
   check_workspace(ws);
-  const c10::DeviceIndex device = check_device(std::array<Arg, 11>{q, kc, vc, table, lens, ks, vs, cu, out, lse, ws});
+  const c10::DeviceIndex device =
+      check_device(std::array<Arg, 13>{q, kc, vc, table, lens, ks, vs, cu, out, lse, ws, kb, vb});
   const c10::cuda::CUDAGuard guard(device);
   const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
   at::Tensor fresh_o, fresh_l;
@@ -418,13 +500,92 @@ PyObject* paged_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.workspace_bytes = own.memory.nbytes();
   }
   const attn_status st = own.scratch.defined()
-                             ? af::paged_fwd(&p, own.scratch.data_ptr(), own.scratch.nbytes(), stream)
-                             : attn_paged_fwd(&p, stream);
+                             ? af::paged_fwd(&p, cache.blocks_or_none(), own.scratch.data_ptr(), own.scratch.nbytes(),
+                                             stream)
+                             : attn_paged_fwd_blocks(&p, cache.blocks_or_none(), stream);
   if (st != ATTN_OK) return status(st);
   PyObject* r = PyTuple_New(2);
   if (r == nullptr) return nullptr;
   PyTuple_SET_ITEM(r, 0, out ? same(a[12]) : THPVariable_Wrap(std::move(fresh_o)));
   PyTuple_SET_ITEM(r, 1, lse ? same(a[13]) : (want_lse ? THPVariable_Wrap(std::move(fresh_l)) : same(Py_None)));
+  return r;
+  PAGED_END
+}
+
+// (q, k, table, positions, seqlens, cu_seqlens, interleaved, inverse, out_q, out_k, workspace)
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity(n, 11)) return nullptr;
+  PAGED_BEGIN
+  const Arg q = tensor("q", a[0]), k = tensor_or_none("k", a[1]), table = tensor("table", a[2]),
+            pos = tensor_or_none("positions", a[3]), lens = tensor_or_none("seqlens", a[4]),
+            cu = tensor_or_none("cu_seqlens", a[5]), oq = tensor_or_none("out_q", a[8]),
+            ok = tensor_or_none("out_k", a[9]), ws = tensor_or_none("workspace", a[10]);
+  attn_rotary_params p = {};
+  // rows without offsets may come as [T, H, D] too: one sequence
+  need(q->dim() == 3 || (q->dim() == 4 && !cu), "q must be [B, S, H, D], or [T, H, D]");
+  const int lead = (int)q->dim() - 2;
+  const int64_t dim = q->size(lead + 1);
+  for (const Arg* x : {&q, &k, &oq, &ok}) {
+    if (!*x) continue;
+    need_f(is(*x, at::kBFloat16), "%s must be bf16", x->name);
+    need_f((*x)->dim() == lead + 2 && (*x)->sizes().slice(0, lead) == q->sizes().slice(0, lead) &&
+               (*x)->size(lead + 1) == dim,
+           "%s must have q's rows and depth", x->name);
+    need_f((*x)->stride(lead + 1) == 1 || dim == 1, "the depth of %s must be contiguous", x->name);
+  }
+  need(!oq || oq->size(lead) == q->size(lead), "out_q must have q's shape");
+  need(!ok || (k && ok->size(lead) == k->size(lead)), "out_k must have k's shape");
+  check_table(table, p.num_positions, p.rotary_dim);
+  check_positions(pos, q->sizes().slice(0, lead));
+  const int64_t batch = cu ? (cu->dim() == 1 && cu->size(0) > 0 ? cu->size(0) - 1 : 0) : (lead == 2 ? q->size(0) : 1);
+  if (cu) check_int32(cu, batch + 1);
+  need(!pos || !lens, "positions and seqlens exclude each other");
+  if (lens) check_int32(lens, batch);
+  const int interleaved = PyObject_IsTrue(a[6]), inverse = PyObject_IsTrue(a[7]);
+  if (interleaved < 0 || inverse < 0) return nullptr;
+  check_workspace(ws);
+  const c10::DeviceIndex device = check_device(std::array<Arg, 9>{q, k, table, pos, lens, cu, oq, ok, ws});
+  const c10::cuda::CUDAGuard guard(device);
+  const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(device).stream();
+  at::Tensor fresh_q, fresh_k;
+  Workspace own;
+  if (!oq) fresh_q = fresh(q->sizes(), at::kBFloat16, device);
+  if (k && !ok) fresh_k = fresh(k->sizes(), at::kBFloat16, device);
+  const Arg to_q = {"out_q", oq ? oq.t : &fresh_q}, to_k = {"out_k", ok ? ok.t : &fresh_k};
+  if (!ws) own.take(device, stream, ATTN_PAGED_ZEROED_BYTES);
+  p.q = q.ptr();
+  p.q_out = to_q.ptr();
+  p.num_heads_q = int32("Hq", q->size(lead));
+  for (int i = 0; i <= lead; ++i) {
+    p.q_stride[i + 2 - lead] = stride(q, i);
+    p.q_out_stride[i + 2 - lead] = stride(to_q, i);
+  }
+  if (k) {
+    p.k = k.ptr();
+    p.k_out = to_k.ptr();
+    p.num_heads_k = int32("Hk", k->size(lead));
+    for (int i = 0; i <= lead; ++i) {
+      p.k_stride[i + 2 - lead] = stride(k, i);
+      p.k_out_stride[i + 2 - lead] = stride(to_k, i);
+    }
+  }
+  p.table = static_cast<const float*>(table.ptr());
+  p.positions = static_cast<const int32_t*>(pos.ptr());
+  p.seqlens = static_cast<const int32_t*>(lens.ptr());
+  p.cu_seqlens = static_cast<const int32_t*>(cu.ptr());
+  p.workspace = ws ? ws.ptr() : own.memory.data_ptr();
+  p.batch = int32("B", batch);
+  p.seqlen = cu ? 0 : int32("S", q->size(lead - 1));
+  p.total = cu ? int32("T", q->size(0)) : 0;
+  p.head_dim = int32("D", dim);
+  p.interleaved = interleaved;
+  p.inverse = inverse;
+  const attn_status st = attn_rotary(&p, stream);
+  if (st != ATTN_OK) return status(st);
+  PyObject* r = PyTuple_New(2);
+  if (r == nullptr) return nullptr;
+  PyTuple_SET_ITEM(r, 0, oq ? same(a[8]) : THPVariable_Wrap(std::move(fresh_q)));
+  PyTuple_SET_ITEM(r, 1, ok ? same(a[9]) : (k ? THPVariable_Wrap(std::move(fresh_k)) : same(Py_None)));
   return r;
   PAGED_END
 }
@@ -441,7 +602,8 @@ PyObject* workspace_address(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr }
-PyMethodDef methods[] = {FAST(cache_append), FAST(cache_read), FAST(paged_forward), FAST(workspace_address),
+PyMethodDef methods[] = {FAST(cache_append), FAST(cache_read), FAST(paged_forward), FAST(rotary),
+                         FAST(workspace_address),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -11,7 +11,11 @@ The cache of many sequences is two tensors ``[pages, page_size, Hkv, D]``
 transposed view), bf16 or float8_e4m3fn. Position j of sequence b is slot
 ``j % page_size`` of page ``block_table[b, j // page_size]``. An e4m3 cache
 has an fp32 scale per (token, head), ``[pages, Hkv, page_size]``; the cached
-value is code * scale.
+value is code * scale. A 4-bit cache holds e2m1 codes, two to a byte: uint8 (or
+float4_e2m1fn_x2) ``[pages, page_size, Hkv, D // 2]``, even depths in the low
+half. Besides such scales it has a block scale for every 16 depths, ``k_block``
+and ``v_block``, float8_e4m3fn ``[pages, Hkv, page_size, D // 16]``; the cached
+value is code * block scale * scale (76 bytes for 128 depths).
 
 Lengths, offsets and page numbers live on the device and may change between
 replays of a captured call. What is wrong with them is found there: nothing
@@ -51,8 +55,9 @@ def _result(r):
     return r
 
 
-def cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, *, k_scale=None, v_scale=None, cu_seqlens_q=None,
-                 workspace=None, stream=None):
+def cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, *, k_scale=None, v_scale=None, k_block=None,
+                 v_block=None, cu_seqlens_q=None, rotary_table=None, positions=None, interleaved=False, q=None,
+                 out_q=None, workspace=None, stream=None):
     """Writes the new tokens' keys and values into the cache, in place.
 
     ``k`` and ``v`` are bf16, [B, Sq, Hkv, D], or packed [T, Hkv, D] with int32
@@ -61,27 +66,38 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, *, k_scale=None
     ``seqlens_k`` (int32 [B]) counts each sequence's tokens with the new ones:
     token i of Lq goes to position seqlens_k - Lq + i. Into an e4m3 cache each
     (token, head) vector is rounded with its own scale, the smallest power of
-    two s with amax / s <= 448, which goes to ``k_scale`` / ``v_scale``. Two
+    two s with amax / s <= 448, which goes to ``k_scale`` / ``v_scale``. Into a
+    4-bit cache: s the smallest power of two with amax / s <= 6 * 448, a block's
+    scale its amax / (6 s) rounded to e4m3, and the codes x / (s * block scale)
+    rounded (a NaN makes its block NaN). Two
     new tokens must not share a slot. A token whose position or page is out
-    of range is not written and reported by ``check``. Asynchronous on
-    ``stream`` (default: the current torch stream).
+    of range is not written and reported by ``check``.
+
+    With ``rotary_table`` (fp32 [positions, R], see ``rotary``; R a multiple of
+    16) the keys are turned on their way, in fp32, by their position in the cache
+    or by ``positions`` (int32, one for every row); ``q``, bf16 queries of the
+    same rows, are turned too and returned (into ``out_q``, which may be ``q``).
+
+    Asynchronous on ``stream`` (default: the current torch stream).
     """
     native = _binding.paged_native()
     if stream is not None:
         with _on(stream, k_cache):
             return cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, k_scale=k_scale, v_scale=v_scale,
-                                cu_seqlens_q=cu_seqlens_q, workspace=workspace)
-    _result(native.cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, k_scale, v_scale, cu_seqlens_q,
-                                workspace))
+                                k_block=k_block, v_block=v_block, cu_seqlens_q=cu_seqlens_q, rotary_table=rotary_table,
+                                positions=positions, interleaved=interleaved, q=q, out_q=out_q, workspace=workspace)
+    r = _result(native.cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, k_scale, v_scale, cu_seqlens_q,
+                                    workspace, k_block, v_block, rotary_table, positions, interleaved, q, out_q))
+    return None if q is None else r
 
 
-def cache_read(k_cache, v_cache, block_table, cu_seqlens_k, *, total_k=None, k_scale=None, v_scale=None, out_k=None,
-               out_v=None, workspace=None, stream=None):
+def cache_read(k_cache, v_cache, block_table, cu_seqlens_k, *, total_k=None, k_scale=None, v_scale=None, k_block=None,
+               v_block=None, out_k=None, out_v=None, workspace=None, stream=None):
     """Reads sequences out of the cache; returns packed bf16 (k, v), [Tk, Hkv, D].
 
     Rows ``cu_seqlens_k[b]`` to ``cu_seqlens_k[b + 1]`` (int32 [B + 1]) receive
-    positions 0, 1, ... of sequence b; an e4m3 cache gives code * scale,
-    rounded once. ``total_k`` is the number of rows to allocate; or pass
+    positions 0, 1, ... of sequence b; an e4m3 cache gives code * scale, a 4-bit
+    one code * block scale * scale, rounded once. ``total_k`` is the number of rows to allocate; or pass
     ``out_k`` and ``out_v``, whose rows in front of the first sequence and behind
     the last one stay as they are. A row whose position or page is out of range is not written and
     reported by ``check``. Asynchronous on ``stream`` (default: the current
@@ -91,14 +107,15 @@ def cache_read(k_cache, v_cache, block_table, cu_seqlens_k, *, total_k=None, k_s
     if stream is not None:
         with _on(stream, k_cache):
             return cache_read(k_cache, v_cache, block_table, cu_seqlens_k, total_k=total_k, k_scale=k_scale,
-                              v_scale=v_scale, out_k=out_k, out_v=out_v, workspace=workspace)
+                              v_scale=v_scale, k_block=k_block, v_block=v_block, out_k=out_k, out_v=out_v,
+                              workspace=workspace)
     return _result(native.cache_read(k_cache, v_cache, block_table, cu_seqlens_k, total_k, k_scale, v_scale, out_k,
-                                     out_v, workspace))
+                                     out_v, workspace, k_block, v_block))
 
 
 def paged_forward(q, k_cache, v_cache, block_table, seqlens_k, *, causal=True, softmax_scale=None, k_scale=None,
-                  v_scale=None, cu_seqlens_q=None, max_seqlen_q=None, max_seqlen_k=None, out=None, lse=None,
-                  return_lse=True, workspace=None, stream=None):
+                  v_scale=None, k_block=None, v_block=None, cu_seqlens_q=None, max_seqlen_q=None, max_seqlen_k=None,
+                  out=None, lse=None, return_lse=True, workspace=None, stream=None):
     """Attention of new tokens over the paged cache; returns (O, LSE).
 
     ``q`` is bf16, [B, Sq, Hq, D] -> O [B, Sq, Hq, D] bf16, LSE [B, Hq, Sq]
@@ -123,15 +140,21 @@ def paged_forward(q, k_cache, v_cache, block_table, seqlens_k, *, causal=True, s
     memory (4 * Hkv * D bytes times B times ``max_seqlen_k``): without effect for
     scales that are powers of two, as ``cache_append`` writes them.
 
+    A 4-bit cache is read exactly by up to 32 rows. More of them take a bf16 copy of
+    the sequences in scratch memory, as above (code * block scale * scale rounded to
+    bf16: without effect for scales that are powers of two), where that fits 1 GiB;
+    elsewhere rows go through the cache 32 at a time, so that a tight
+    ``max_seqlen_k`` matters there.
+
     Asynchronous on ``stream`` (default: the current torch stream).
     """
     native = _binding.paged_native()
     if stream is not None:
         with _on(stream, k_cache):
             return paged_forward(q, k_cache, v_cache, block_table, seqlens_k, causal=causal,
-                                 softmax_scale=softmax_scale, k_scale=k_scale, v_scale=v_scale,
-                                 cu_seqlens_q=cu_seqlens_q, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
+                                 softmax_scale=softmax_scale, k_scale=k_scale, v_scale=v_scale, k_block=k_block,
+                                 v_block=v_block, cu_seqlens_q=cu_seqlens_q, max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
                                  out=out, lse=lse, return_lse=return_lse, workspace=workspace)
     return _result(native.paged_forward(q, k_cache, v_cache, block_table, seqlens_k, causal, softmax_scale, k_scale,
                                         v_scale, cu_seqlens_q, max_seqlen_q, max_seqlen_k, out, lse, return_lse,
-                                        workspace))
+                                        workspace, k_block, v_block))

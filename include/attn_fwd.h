@@ -49,7 +49,8 @@ typedef struct CUstream_st *attn_stream_t;
 
 typedef enum attn_dtype {
   ATTN_DTYPE_BF16 = 0,      /* Q and K bf16 */
-  ATTN_DTYPE_FP8_E4M3 = 1   /* Q and K float8_e4m3fn with per-token fp32 scales */
+  ATTN_DTYPE_FP8_E4M3 = 1,  /* Q and K float8_e4m3fn with per-token fp32 scales */
+  ATTN_DTYPE_FP4_E2M1 = 2   /* paged caches only (attn_paged.h): e2m1 codes, two to a byte */
 } attn_dtype;
 
 typedef enum attn_status {

@@ -6,7 +6,11 @@
  * The cache keeps K and V of many sequences in pages of page_size tokens:
  * position j of sequence b is slot j % page_size of page
  * block_table[b][j / page_size]. It holds bf16, or float8_e4m3fn with one fp32
- * scale per (token, head): the cached value is code * scale.
+ * scale per (token, head): the cached value is code * scale. Or it holds e2m1
+ * codes (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) with an e4m3 scale for
+ * every block of 16 depths and an fp32 scale per (token, head): the value is
+ * code * block scale * scale. Such a cache is passed with its block scales to
+ * the calls that end in _blocks.
  *
  *   append  token i of the Lq_b new tokens of sequence b goes to position
  *           seqlens_k[b] - Lq_b + i (seqlens_k counts the new tokens too).
@@ -16,8 +20,17 @@
  *           power of two makes x / s exact and costs no accuracy (a floating
  *           code has the same relative error at any scale). Infinities become
  *           +-448 s, NaN stays NaN.
+ *           e2m1: scale = the smallest power of two s >= 2^-126 with a / s <= 2688
+ *           (6 * 448; 1 if a = 0), a block's scale b = its largest finite
+ *           |x_d| / (6 s) rounded to nearest even, code_d = x_d / (s b) rounded to
+ *           nearest even and cut at +-6 (0 if b = 0), each quotient in fp32. A NaN
+ *           makes its block's scale NaN.
+ *           With a rotation (attn_cache_append_blocks) the keys are turned by
+ *           their positions first, in fp32 (attn_rotary.h), and rounded only
+ *           once, to what the cache holds.
  *   read    positions 0 .. cu_seqlens_k[b+1] - cu_seqlens_k[b] - 1 of sequence
- *           b, as packed bf16 rows (e4m3: code * scale, rounded once).
+ *           b, as packed bf16 rows (e4m3: code * scale, rounded once; e2m1: code *
+ *           block scale, which is exact, * scale, rounded once).
  *   attend  for new token i of sequence b and query head h, hk = h / (Hq / Hkv):
  *             J_i   = { j < Lk_b : !causal || j <= Lk_b - Lq_b + i }
  *             s_ij  = scale * (q_i . K_j)
@@ -68,14 +81,16 @@ extern "C" {
 #define ATTN_PAGED_ZEROED_BYTES 8192
 
 typedef struct attn_kv_cache {
-  void *k;                    /* [P][page_size][Hkv][D], bf16 or e4m3 (dtype), 16-byte aligned */
+  void *k;                    /* [P][page_size][Hkv][D], bf16 or e4m3 (dtype), 16-byte aligned;
+                                 e2m1: [P][page_size][Hkv][D / 2] bytes, depth 2 i in the low
+                                 half of byte i, depth 2 i + 1 in the high half */
   void *v;                    /* the same shape and type */
-  float *k_scale;             /* e4m3 only: [P][Hkv][page_size] contiguous, 16-byte aligned */
+  float *k_scale;             /* not bf16: [P][Hkv][page_size] contiguous, 16-byte aligned */
   float *v_scale;
   const int32_t *block_table; /* [B][max_pages], row stride table_stride, entries contiguous */
-  int64_t k_stride[3];        /* elements: [0] page, [1] token, [2] head; depth contiguous;
-                                 multiples of 16 bytes, positive where the dimension is
-                                 larger than 1 */
+  int64_t k_stride[3];        /* elements (e2m1: bytes): [0] page, [1] token, [2] head; depth
+                                 contiguous; multiples of 16 bytes, positive where the
+                                 dimension is larger than 1 */
   int64_t v_stride[3];
   int64_t table_stride;       /* elements between the rows of block_table */
   int32_t dtype;              /* attn_dtype of k and v */
@@ -152,6 +167,45 @@ attn_status attn_cache_read(const attn_cache_read_params *p, attn_stream_t strea
 
 /* Validates `p` and enqueues the attention. */
 attn_status attn_paged_fwd(const attn_paged_params *p, attn_stream_t stream);
+
+/* Block scales of an e2m1 cache: e4m3, [P][Hkv][page_size][D / 16] contiguous,
+ * 16-byte aligned. */
+typedef struct attn_block_scales {
+  void *k;
+  void *v;
+} attn_block_scales;
+
+/* Rotation of new keys on their way into a cache, and of the same tokens'
+ * queries: attn_rotary.h's definition. A token at a position outside the table
+ * is not written, and reported like a page number outside the cache. */
+typedef struct attn_cache_rotary {
+  const float *table;          /* [num_positions][rotary_dim] contiguous, 16-byte aligned: cosines,
+                                  then sines */
+  const int32_t *positions;    /* of the new rows, fixed [B][Sq] / packed [Tq]; NULL: where the
+                                  token goes in the cache */
+  const void *q;               /* bf16, fixed [B][Sq][Hq][D] / packed [Tq][Hq][D]; NULL: none
+                                  (num_heads_q = 0) */
+  void *q_out;                 /* bf16, q's shape, written; may be q itself with q's strides */
+  int64_t q_stride[3];         /* elements: [0] batch (unused when packed), [1] token, [2] head;
+                                  multiples of 16 bytes */
+  int64_t q_out_stride[3];
+  int32_t num_heads_q;
+  int32_t num_positions;
+  int32_t rotary_dim;          /* a multiple of 16, up to D */
+  int32_t interleaved;
+} attn_cache_rotary;
+
+/* sizeof of those structs (binding check): which = 0 attn_block_scales,
+ * 1 attn_cache_rotary. */
+size_t attn_cache_blocks_params_size(int32_t which);
+
+/* The three calls for caches of any kind: `blocks` is NULL unless the cache is
+ * e2m1, `rotary` NULL unless keys are to be turned. */
+attn_status attn_cache_append_blocks(const attn_cache_append_params *p, const attn_block_scales *blocks,
+                                     const attn_cache_rotary *rotary, attn_stream_t stream);
+attn_status attn_cache_read_blocks(const attn_cache_read_params *p, const attn_block_scales *blocks,
+                                   attn_stream_t stream);
+attn_status attn_paged_fwd_blocks(const attn_paged_params *p, const attn_block_scales *blocks, attn_stream_t stream);
 
 /* Workspace bytes attn_paged_fwd needs for `p` on the current device (an
  * invalid `p` or NULL gives ATTN_PAGED_ZEROED_BYTES). Depends on sizes only,
