@@ -25,8 +25,10 @@
 // power of two with amax / s <= 6 * 448, the block's scale e4m3(amax_block / 6 s),
 // and a code the rounded quotient x / (s * scale).
 //
-// With a rotation (ROT) the keys are turned on their way, in fp32, and the new
-// tokens' queries are vectors behind the values, turned and written as bf16.
+// With a rotation the keys are turned on their way, in fp32, and the queries of the
+// same tokens. Into a bf16 cache all of it is whole rows (append_rows, rotary.cuh);
+// where keys are quantised (ROT), a vector's lanes have to meet, and the queries are
+// other blocks' work.
 #include "launch.cuh"
 #include "paged.h"
 #include "ptx.cuh"
@@ -57,24 +59,17 @@ __device__ __forceinline__ Slot slot_of(const CacheView& c, int b, int pos, uint
   return s;
 }
 
-// Vector `idx` of a block: its token and (V behind K, queries to be turned behind
-// both) head.
+// Vector `idx` of a block: its token and (V behind K) head.
 struct Vector {
   int token, h;
-  bool v, q;
+  bool v;
 };
-template <bool Q = false>
 __device__ __forceinline__ Vector vector_at(uint32_t idx, uint32_t per_token, uint32_t magic, int heads) {
   Vector x;
   x.token = (int)__umulhi(idx, magic);   // idx / per_token (magic = 2^32 / per_token rounded up, idx < 2^16)
   x.h = (int)(idx - x.token * per_token);
   x.v = x.h >= heads;
   if (x.v) x.h -= heads;
-  x.q = Q && x.v && x.h >= heads;
-  if (x.q) {
-    x.h -= heads;
-    x.v = false;
-  }
   return x;
 }
 
@@ -111,15 +106,38 @@ __device__ __forceinline__ float finite_max(float x, float m) {
   return a <= 3.402823466e38f ? fmaxf(a, m) : m;   // (not infinities and NaN)
 }
 
-// A block of sixteen values as e2m1 codes (even ones in the low halves) and its
-// e4m3 scale, in units of 1 / inv, the vector's. `top`: the block's largest finite
-// magnitude.
-__device__ __forceinline__ void quantise_block(const float (&f)[16], float top, float inv, uint2& codes, uint32_t& scale) {
-  scale = ptx::pack_e4m3x4(__fdiv_rn(top * inv, 6.f), 0.f, 0.f, 0.f) & 0xffu;
-  float size, unused;
-  ptx::e4m3x2_to_float2(scale, size, unused);
-  // y / size, correctly rounded, by Markstein's theorem: r = 1 / size and a first
-  // quotient t, then t + r (y - t size), the remainder being exact.
+// e4m3 scale of a block whose largest finite magnitude is `top`, in units of 1 / inv, the
+// vector's scale: as its code, and its value.
+__device__ __forceinline__ uint32_t block_scale(float top, float inv, float& size) {
+  const uint32_t code = ptx::pack_e4m3x4(__fdiv_rn(top * inv, 6.f), 0.f, 0.f, 0.f) & 0xffu;
+  float unused;
+  ptx::e4m3x2_to_float2(code, size, unused);
+  return code;
+}
+// Sixteen values over a block's scale as e2m1 codes, even ones in the low halves. The
+// quotients are correctly rounded, by Markstein's theorem: with r = 1 / size rounded and a
+// first quotient t = x r, they are t + r (x - t size), the remainder being exact. Here
+// with `size` and r times the vector's scale, 2^se, -100 at least, which changes no
+// rounding; two values at a time (57 % of the instructions, 18.4 us for 5000 tokens).
+__device__ __forceinline__ uint2 quantise_block(const uint64_t (&x)[8], float size, int se) {
+  const float r = size == 0.f ? 0.f : __frcp_rn(size);
+  const float up = __uint_as_float((uint32_t)(127 - se) << 23) * r, down = -__uint_as_float((uint32_t)(127 + se) << 23) * size;
+  const uint64_t r2 = ptx::f2_pack(up, up), s2 = ptx::f2_pack(down, down);
+  uint32_t out[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t first = ptx::f2_mul(x[4 * j + i], r2);
+      ptx::f2_unpack(ptx::f2_fma(ptx::f2_fma(first, s2, x[4 * j + i]), r2, first), t[2 * i], t[2 * i + 1]);
+    }
+    out[j] = ptx::pack_e2m1x8(t);
+  }
+  return size == 0.f ? make_uint2(0u, 0u) : make_uint2(out[0], out[1]);
+}
+// The same for any values (infinities, NaN, the smallest scales), one at a time.
+__device__ __noinline__ uint2 quantise_any(const float* f, float size, float inv, uint32_t& code) {
   const float r = size == 0.f ? 0.f : __frcp_rn(size);
   uint32_t out[2];
 #pragma unroll
@@ -127,17 +145,119 @@ __device__ __forceinline__ void quantise_block(const float (&f)[16], float top, 
     float t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float y = fminf(fmaxf(f[8 * j + i] * inv, -2688.f), 2688.f);   // (infinities; 2688 / size is in range)
+      const float x = f[8 * j + i], y = fminf(fmaxf(x * inv, -2688.f), 2688.f);   // (2688 / size is in range)
+      if (x != x) code = 0x7fu;   // a NaN takes its block with it
       t[i] = y * r;
       t[i] = fmaf(fmaf(-t[i], size, y), r, t[i]);
     }
     out[j] = ptx::pack_e2m1x8(t);
   }
-  codes = size == 0.f ? make_uint2(0u, 0u) : make_uint2(out[0], out[1]);
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) nan = nan || f[i] != f[i];
-  if (nan) scale = 0x7fu;   // a NaN takes its block with it
+  return size == 0.f ? make_uint2(0u, 0u) : make_uint2(out[0], out[1]);
+}
+
+// Sequence and index of token t0 + token of rows of a fixed length.
+__device__ __forceinline__ void fixed_token(const AppendParams& P, int64_t t0, int token, int& b, int& i) {
+  const uint32_t t = (uint32_t)t0 + (uint32_t)token, len = (uint32_t)P.s.seqlen_q;
+  b = (int)(t / len);
+  i = (int)(t - (uint32_t)b * len);
+}
+
+// Where each of a block's tokens goes (and, ROT, its angle), one lane of the first warp a
+// token; ends with a barrier. The whole block calls it.
+template <bool ROT>
+__device__ __forceinline__ void find_slots(const AppendParams& P, int64_t t0, int tokens, Slot* slots) {
+  const int64_t t = t0 + (threadIdx.x & 31);
+  const bool packed = P.s.cu_q != nullptr;
+  const int found = packed ? find_sequence<kThreads>(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws, kDevErrBadCache) : 0;
+  if (threadIdx.x < 32) {
+    Slot s = {-1, 0, 0};
+    int b, i, lq = P.s.seqlen_q;
+    bool ok = (int)threadIdx.x < tokens;
+    if (packed) {
+      b = found;
+      ok = ok && b < P.s.batch;                // else behind the last sequence
+      if (ok) {
+        const int a = P.s.cu_q[b], e = P.s.cu_q[b + 1];
+        i = (int)(t - a);
+        lq = e - a;
+        // (rows in front of the first sequence; offsets below zero or past
+        // the rows, which are recorded)
+        ok = a >= 0 && i >= 0 && e <= P.tokens;
+      }
+    } else {
+      fixed_token(P, t0, threadIdx.x, b, i);
+    }
+    if (ok) {
+      const int lk = P.s.seqlens_k[b];
+      s = slot_of(P.c, b, lk < 0 || lk > P.s.max_k ? -1 : lk - lq + i, P.ws);
+      if constexpr (ROT) {
+        if (P.r.positions != nullptr) s.angle = P.r.positions[t];
+        if (s.page >= 0 && (s.angle < 0 || s.angle >= P.r.num_positions)) {
+          s.page = -1;
+          record_error(P.ws, kDevErrBadPosition, b);
+        }
+      }
+    }
+    slots[threadIdx.x] = s;
+  }
+  __syncthreads();
+}
+
+// Offset of a token's rows with batch and token strides sb, st.
+__device__ __forceinline__ int64_t row_offset(const AppendParams& P, int64_t t0, int token, int64_t sb, int64_t st) {
+  if (P.s.cu_q != nullptr) return (t0 + token) * st;
+  int b, i;
+  fixed_token(P, t0, token, b, i);
+  return b * sb + i * st;
+}
+
+// The part of an append that moves whole rows, turning keys and queries: the queries of
+// any cache, and (KV) keys and values on their way into a bf16 one. Heads are those of
+// q, then K's, then V's.
+template <bool KV, bool APART>
+__device__ __forceinline__ void append_rows(const AppendParams& P, int block, Slot* slots) {
+  const int64_t t0 = (int64_t)block * P.r.block_tokens;
+  const int tokens = (int)min((int64_t)P.r.block_tokens, P.tokens - t0);
+  const int hq = P.r.heads_q, hkv = P.c.heads_kv;
+  turn_rows<8, APART, kThreads>(
+      P.r.shape, tokens,
+      [&](int token, int h, TurnHead& head) {
+        const uint8_t* base = P.r.q;
+        int64_t sb = P.r.q_b, st = P.r.q_t, sh = P.r.q_h;
+        if (KV && h >= hq) {
+          const bool v = h >= hq + hkv;
+          h -= v ? hq + hkv : hq;
+          base = v ? P.v : P.k;
+          sb = v ? P.v_b : P.k_b;
+          st = v ? P.v_t : P.k_t;
+          sh = v ? P.v_h : P.k_h;
+        }
+        head.src = base + row_offset(P, t0, token, sb, st) + h * sh;
+        head.src_next = sh;
+      },
+      [&]() { find_slots<true>(P, t0, tokens, slots); },
+      [&](int token, int h, TurnHead& head) {
+        const Slot s = slots[token];
+        if (s.page < 0) return -1;
+        if (KV && h >= hq) {
+          const bool v = h >= hq + hkv;
+          h -= v ? hq + hkv : hq;
+          head.dst = v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + h * P.c.v_head
+                       : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + h * P.c.k_head;
+          head.dst_next = v ? P.c.v_head : P.c.k_head;
+        } else {
+          head.dst = P.r.q_out + row_offset(P, t0, token, P.r.out_b, P.r.out_t) + h * P.r.out_h;
+          head.dst_next = P.r.out_h;
+        }
+        return s.angle;
+      });
+}
+// An append with rotation into a bf16 cache.
+template <bool APART>
+__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ AppendParams P) {
+  __shared__ Slot slots[kMaxTokens];
+  ptx::grid_dependency_wait();
+  append_rows<true, APART>(P, blockIdx.x, slots);
 }
 
 template <int D, int KIND, bool ROT>
@@ -145,29 +265,15 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   constexpr int E = KIND == kBf16 ? 8 : 16, L = D / E, PER = kThreads / L;
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
+  if (ROT && (int)blockIdx.x >= P.blocks_kv) {   // (the queries')
+    if (P.r.interleaved) append_rows<false, false>(P, (int)blockIdx.x - P.blocks_kv, slots);
+    else append_rows<false, true>(P, (int)blockIdx.x - P.blocks_kv, slots);
+    return;
+  }
   const int64_t t0 = (int64_t)blockIdx.x * P.block_tokens;
   const int tokens = (int)min((int64_t)P.block_tokens, P.tokens - t0);
-  const uint32_t nv = 2 * P.c.heads_kv + (ROT ? P.r.heads_q : 0), total = tokens * nv;
+  const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
-  // fixed layout: sequence and index of the first token
-  const bool packed = P.s.cu_q != nullptr;
-  const int b0 = packed ? 0 : (int)((uint32_t)t0 / (uint32_t)P.s.seqlen_q);
-  const int i0 = packed ? 0 : (int)t0 - b0 * P.s.seqlen_q;
-  auto token_at = [&](int token, int& b, int& i) {
-    b = b0;
-    i = i0 + token;
-    while (i >= P.s.seqlen_q) {
-      i -= P.s.seqlen_q;
-      ++b;
-    }
-  };
-  // offset of a token's rows with batch and token strides sb, st
-  auto row_at = [&](int token, int64_t sb, int64_t st) -> int64_t {
-    if (packed) return (t0 + token) * st;
-    int b, i;
-    token_at(token, b, i);
-    return b * sb + i * st;
-  };
   for (uint32_t base = 0; base < total; base += PER * kBatch) {
     uint4 x[kBatch][E / 8];
 #pragma unroll
@@ -176,15 +282,9 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < E / 8; ++e) x[u][e] = make_uint4(0u, 0u, 0u, 0u);
       if (id < total) {
-        const Vector w = vector_at<ROT>(id, nv, P.magic, P.c.heads_kv);
-        const uint8_t* src = w.v ? P.v + w.h * P.v_h : P.k + w.h * P.k_h;
-        int64_t sb = w.v ? P.v_b : P.k_b, st = w.v ? P.v_t : P.k_t;
-        if (ROT && w.q) {
-          src = P.r.q + w.h * P.r.q_h;
-          sb = P.r.q_b;
-          st = P.r.q_t;
-        }
-        src += row_at(w.token, sb, st) + lane * (E * 2);
+        const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
+        const uint8_t* src = (w.v ? P.v + w.h * P.v_h : P.k + w.h * P.k_h) + lane * (E * 2) +
+                             row_offset(P, t0, w.token, w.v ? P.v_b : P.k_b, w.v ? P.v_t : P.k_t);
         if (KIND != kBf16 && P.wide) {
           ptx::ld_global_v8(src, reinterpret_cast<uint32_t*>(&x[u][0]));
         } else {
@@ -193,48 +293,12 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         }
       }
     }
-    if (base == 0) {
-      const int64_t t = t0 + (threadIdx.x & 31);
-      const int found =
-          packed ? find_sequence<kThreads>(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws, kDevErrBadCache) : 0;
-      if (threadIdx.x < 32) {
-        Slot s = {-1, 0, 0};
-        int b, i, lq = P.s.seqlen_q;
-        bool ok = (int)threadIdx.x < tokens;
-        if (packed) {
-          b = found;
-          ok = ok && b < P.s.batch;                // else behind the last sequence
-          if (ok) {
-            const int a = P.s.cu_q[b], e = P.s.cu_q[b + 1];
-            i = (int)(t - a);
-            lq = e - a;
-            // (rows in front of the first sequence; offsets below zero or past
-            // the rows, which are recorded)
-            ok = a >= 0 && i >= 0 && e <= P.tokens;
-          }
-        } else {
-          token_at(threadIdx.x, b, i);
-        }
-        if (ok) {
-          const int lk = P.s.seqlens_k[b];
-          s = slot_of(P.c, b, lk < 0 || lk > P.s.max_k ? -1 : lk - lq + i, P.ws);
-          if constexpr (ROT) {
-            if (P.r.positions != nullptr) s.angle = P.r.positions[t];
-            if (s.page >= 0 && (s.angle < 0 || s.angle >= P.r.num_positions)) {
-              s.page = -1;
-              record_error(P.ws, kDevErrBadPosition, b);
-            }
-          }
-        }
-        slots[threadIdx.x] = s;
-      }
-      __syncthreads();
-    }
+    if (base == 0) find_slots<ROT>(P, t0, tokens, slots);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const uint32_t id = base + u * PER + threadIdx.x / L;
       const bool there = id < total;
-      const Vector w = vector_at<ROT>(there ? id : 0u, nv, P.magic, P.c.heads_kv);
+      const Vector w = vector_at(there ? id : 0u, nv, P.magic, P.c.heads_kv);
       const Slot s = slots[w.token];
       const bool ok = there && s.page >= 0;
       uint32_t in[E / 2];
@@ -248,24 +312,11 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       float f[E];
       if constexpr (ROT)
         rotate_lanes<E, L>(in, f, P.r.table + (int64_t)s.angle * P.r.rot, P.r.rot, P.r.interleaved != 0, ok && !w.v);
-      if (ROT && w.q && ok) {
-        uint8_t* dst = P.r.q_out + w.h * P.r.out_h + row_at(w.token, P.r.out_b, P.r.out_t) + lane * (E * 2);
-#pragma unroll
-        for (int e = 0; e < E / 8; ++e)
-          reinterpret_cast<uint4*>(dst)[e] =
-              make_uint4(ptx::pack_bf16(f[8 * e], f[8 * e + 1]), ptx::pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                         ptx::pack_bf16(f[8 * e + 4], f[8 * e + 5]), ptx::pack_bf16(f[8 * e + 6], f[8 * e + 7]));
-      }
-      const bool cached = ok && !w.q;
       uint8_t* dst = w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
                          : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head;
       const int64_t at = (((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot;   // of its scales
       if constexpr (KIND == kBf16) {
-        uint4 out = x[u][0];
-        if (ROT && !w.v)
-          out = make_uint4(ptx::pack_bf16(f[0], f[1]), ptx::pack_bf16(f[2], f[3]), ptx::pack_bf16(f[4], f[5]),
-                           ptx::pack_bf16(f[6], f[7]));
-        if (cached) *reinterpret_cast<uint4*>(dst + lane * 16) = out;
+        if (ok) *reinterpret_cast<uint4*>(dst + lane * 16) = x[u][0];
       } else if constexpr (KIND == kE4m3) {
         int se;
         if constexpr (ROT) {
@@ -301,29 +352,60 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           out[j] = ptx::pack_e4m3x4(f[4 * j] * inv, f[4 * j + 1] * inv, f[4 * j + 2] * inv, f[4 * j + 3] * inv);
-        if (cached) {
+        if (ok) {
           *reinterpret_cast<uint4*>(dst + lane * 16) = make_uint4(out[0], out[1], out[2], out[3]);
           if (lane == 0) (w.v ? P.c.v_scale : P.c.k_scale)[at] = __uint_as_float((uint32_t)(127 + se) << 23);
         }
       } else {
-        if constexpr (!ROT) {
+        // the block's largest magnitude, and whether something in it is not finite
+        uint64_t pair[8];
+        float top = 0.f;
+        bool odd;
+        if constexpr (ROT) {
+          float zero = 0.f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            f[2 * e] = bf16_lo(in[e]);
-            f[2 * e + 1] = bf16_hi(in[e]);
+            pair[e] = ptx::f2_pack(f[2 * e], f[2 * e + 1]);
+            top = ptx::max3(top, fabsf(f[2 * e]), fabsf(f[2 * e + 1]));
+            zero = fmaf(f[2 * e], 0.f, fmaf(f[2 * e + 1], 0.f, zero));
+          }
+          odd = zero != 0.f;
+        } else {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            pair[e] = f2_of(in[e]);
+            m = __vmaxu2(m, in[e] & 0x7fff7fffu);
+          }
+          m = max(m & 0xffffu, m >> 16);
+          odd = m >= 0x7f80u;
+          top = __uint_as_float(m << 16);
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            ptx::f2_unpack(pair[e], f[2 * e], f[2 * e + 1]);
+            top = finite_max(f[2 * e], finite_max(f[2 * e + 1], top));
           }
         }
-        float top = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) top = finite_max(f[e], top);
         float m = top;
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const int se = scale_exponent4(m);
+        const float inv = __uint_as_float((uint32_t)(127 - se) << 23);
+        float size;
+        uint32_t scale = block_scale(top, inv, size);
         uint2 codes;
-        uint32_t scale;
-        quantise_block(f, top, __uint_as_float((uint32_t)(127 - se) << 23), codes, scale);
-        if (cached) {
+        if (odd || se < -100) {
+          float any[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ptx::f2_unpack(pair[e], any[2 * e], any[2 * e + 1]);
+          codes = quantise_any(any, size, inv, scale);
+        } else {
+          codes = quantise_block(pair, size, se);
+        }
+        if (ok) {
           *reinterpret_cast<uint2*>(dst + lane * 8) = codes;
           (w.v ? P.blocks.v : P.blocks.k)[at * L + lane] = (uint8_t)scale;
           if (lane == 0) (w.v ? P.c.v_scale : P.c.k_scale)[at] = __uint_as_float((uint32_t)(127 + se) << 23);
@@ -349,9 +431,8 @@ __device__ __forceinline__ void widen(const uint4& x, float scale, uint32_t (&ou
 // Sixteen values of an e2m1 cache: codes times the block's scale, which is exact,
 // times the vector's scale, rounded once.
 __device__ __forceinline__ void widen4(const uint2& x, uint32_t block, float scale, uint32_t (&out)[8]) {
-  float size, unused;
-  ptx::e4m3x2_to_float2(block, size, unused);
-  const uint32_t in[2] = {x.x, x.y};
+  const uint32_t size = ptx::e4m3x2_to_f16x2(block * 0x101u), in[2] = {x.x, x.y};
+  const uint64_t s2 = ptx::f2_pack(scale, scale);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     uint32_t h[4];
@@ -359,8 +440,9 @@ __device__ __forceinline__ void widen4(const uint2& x, uint32_t block, float sca
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float lo, hi;
-      ptx::f16x2_to_float2(h[i], lo, hi);
-      out[4 * j + i] = ptx::pack_bf16(lo * size * scale, hi * size * scale);
+      ptx::f16x2_to_float2(ptx::mul_f16x2(h[i], size), lo, hi);
+      ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(lo, hi), s2), lo, hi);
+      out[4 * j + i] = ptx::pack_bf16(lo, hi);
     }
   }
 }
@@ -517,12 +599,36 @@ cudaError_t launch(K kern, P p, int64_t tokens, uint32_t per_token, int vectors,
 
 constexpr int per_block(int d, int kind) { return kThreads / (d / (kind == kBf16 ? 8 : 16)) * kBatch; }
 
+// Rows to be turned: blocks of them, with their sizes in `p`.
+int64_t turn_blocks(AppendParams& p, int head_dim, const int (&heads)[3], int turned) {
+  AppendRotary& r = p.r;
+  r.shape = turn_shape(r.table, head_dim, r.rot, r.interleaved != 0, false, heads, turned);
+  r.block_tokens = turn_tokens(r.shape, p.tokens, kThreads, kMaxTokens, sm_count());
+  return (p.tokens + r.block_tokens - 1) / r.block_tokens;
+}
+
 template <int D, int KIND>
-cudaError_t append_t(const AppendParams& p, cudaStream_t stream) {
+cudaError_t append_t(const AppendParams& params, cudaStream_t stream) {
+  AppendParams p = params;
   const uint32_t per_token = 2 * p.c.heads_kv;
+  const int vectors = per_block(D, KIND), fit = vectors / (int)per_token;
   if (p.r.table == nullptr)
-    return launch(cache_append_kernel<D, KIND, false>, p, p.tokens, per_token, per_block(D, KIND), stream);
-  return launch(cache_append_kernel<D, KIND, true>, p, p.tokens, per_token + p.r.heads_q, per_block(D, KIND), stream);
+    return launch(cache_append_kernel<D, KIND, false>, p, p.tokens, per_token, vectors, stream);
+  if constexpr (KIND == kBf16) {
+    const int64_t blocks = turn_blocks(p, D, {p.r.heads_q, p.c.heads_kv, p.c.heads_kv}, 2);
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks);
+    return turn_apart(p.r.shape) ? launch_dependent(append_rows_kernel<true>, p, grid, kThreads, 0, stream)
+                                 : launch_dependent(append_rows_kernel<false>, p, grid, kThreads, 0, stream);
+  } else {
+    const int64_t rows = p.r.heads_q > 0 ? turn_blocks(p, D, {p.r.heads_q, 0, 0}, 1) : 0;
+    p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
+    p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
+    const int64_t blocks = (p.tokens + p.block_tokens - 1) / p.block_tokens;
+    if (blocks + rows > 0x7fffffffll) return cudaErrorInvalidValue;
+    p.blocks_kv = (int32_t)blocks;
+    return launch_dependent(cache_append_kernel<D, KIND, true>, p, dim3((unsigned)(blocks + rows)), kThreads, 0, stream);
+  }
 }
 template <int D>
 cudaError_t append_d(const AppendParams& p, int kind, cudaStream_t stream) {

@@ -5,6 +5,7 @@
 
 #include "../../include/attn_paged.h"
 #include "internal.h"
+#include "rotary.cuh"
 #include "rows.cuh"
 
 namespace af {
@@ -18,6 +19,8 @@ constexpr int stream_tile(int row_bytes, int group_warps) { return group_warps =
 // 77.6); where two already wait for HBM it does not pay (e4m3, D = 128: 104 -> 118 with
 // the half tiles that it needs).
 constexpr int stream_ctas(int row_bytes, int row_tile) { return row_bytes == 64 && row_tile == 8 ? 3 : 2; }
+// Keys per work unit of the streaming kernel over e2m1 codes, whose CTAs have an SM each.
+constexpr int stream4_tile = 128;
 constexpr int kMinPage = 16;         // smallest page: one warp's step of keys lies in one page
 
 // The new rows of each sequence (fixed: b * seqlen_q; packed: cu_q) and the
@@ -39,6 +42,8 @@ struct BlockScales {
 
 // Rotation on the way into the cache; table NULL: none.
 struct AppendRotary {
+  TurnShape shape;             // set by the launch, as block_tokens
+  int32_t block_tokens;
   const float* table;          // [num_positions][rot]
   const int32_t* positions;    // of the rows, or NULL: the cache's
   const uint8_t* q;
@@ -57,8 +62,9 @@ struct AppendParams {
   int64_t k_b, k_t, k_h, v_b, v_t, v_h;   // bytes
   int64_t tokens;
   int32_t wide;                           // 1: k, v, q and their strides are multiples of 32 bytes
-  int32_t block_tokens;                   // set by the launch, as `magic`
+  int32_t block_tokens;                   // set by the launch, as `magic` and
   uint32_t magic;
+  int32_t blocks_kv;                      // the blocks of keys and values, in front of those of queries
   uint32_t* ws;
 };
 
@@ -135,8 +141,10 @@ cudaError_t cache_append_launch(const AppendParams& p, int head_dim, int kind, c
 cudaError_t cache_widen_launch(const WidenParams& p, int head_dim, int kind, cudaStream_t stream);
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, int kind, cudaStream_t stream);
 // Streaming attention over `grid` CTAs with row tiles of 8, 16 or 32 rows.
-cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, int kind, int row_tile, int grid,
+cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,
                                 cudaStream_t stream);
+// The same over an e2m1 cache.
+cudaError_t paged_stream4_launch(const StreamParams& p, int head_dim, int row_tile, int grid, cudaStream_t stream);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void record_bad_cache(uint32_t* ws, int b) {

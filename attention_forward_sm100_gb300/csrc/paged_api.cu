@@ -308,8 +308,10 @@ StreamPlan plan_stream(const attn_paged_params* p) {
   const int64_t rt = s.row_tile;
   const int row_bytes = (int)code_bytes(p->cache.dtype, p->cache.head_dim);
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
-  const int64_t tiles = af::tiles_for(p->seqlen_k, af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
-  const int64_t ctas = (int64_t)af::stream_ctas(row_bytes, s.row_tile) * af::sm_count();
+  const bool fp4 = p->cache.dtype == ATTN_DTYPE_FP4_E2M1;
+  const int64_t tiles = af::tiles_for(
+      p->seqlen_k, fp4 ? af::stream4_tile : af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
+  const int64_t ctas = (int64_t)(fp4 ? 1 : af::stream_ctas(row_bytes, s.row_tile)) * af::sm_count();
   const bool one_wave = 4 * segments >= ctas && segments <= 2 * ctas;
   s.split = tiles > kUnsplitTiles && !(one_wave && p->seqlen_k <= kUnsplitKeys) && segments <= kMaxUnits / tiles ? 1 : 0;
   s.units = segments * (s.split ? tiles : 1);
@@ -320,6 +322,11 @@ StreamPlan plan_stream(const attn_paged_params* p) {
     const int heads = p->cache.num_heads_kv;
     s.team = heads < kMaxTeam ? heads : kMaxTeam;
     while (heads % s.team) --s.team;
+    // (one CTA per SM: sixteen of 152 would idle eight)
+    while (fp4 && s.grid >= ctas && s.team > 1 && (s.grid % s.team) * 50 > s.grid) {
+      --s.team;
+      while (heads % s.team) --s.team;
+    }
     s.grid -= s.grid % s.team;
   }
   if (s.split) {
@@ -566,7 +573,10 @@ attn_status af::paged_fwd(const attn_paged_params* params, const attn_block_scal
   a.part_ml = reinterpret_cast<float2*>(room);
   a.part_o = reinterpret_cast<float*>(room + plan.ml_bytes);
   const cudaError_t e =
-      af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype, plan.row_tile, (int)plan.grid, stream);
+      p->cache.dtype == ATTN_DTYPE_FP4_E2M1
+          ? af::paged_stream4_launch(a, p->cache.head_dim, plan.row_tile, (int)plan.grid, stream)
+          : af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
+                                    (int)plan.grid, stream);
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }

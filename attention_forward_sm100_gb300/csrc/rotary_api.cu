@@ -82,7 +82,6 @@ attn_status attn_rotary(const attn_rotary_params* p, attn_stream_t stream) {
     a.out_t[i] = out[i][1] * 2;
     a.out_h[i] = out[i][2] * 2;
   }
-  a.table = p->table;
   a.positions = p->positions;
   a.seqlens = p->seqlens;
   a.cu = p->cu_seqlens;
@@ -92,12 +91,9 @@ attn_status attn_rotary(const attn_rotary_params* p, attn_stream_t stream) {
   a.heads[1] = p->num_heads_k;
   a.batch = p->batch;
   a.seqlen = p->seqlen;
-  a.dim = p->head_dim;
-  a.rot = p->rotary_dim;
   a.num_positions = p->num_positions;
-  a.interleaved = p->interleaved != 0;
-  a.inverse = p->inverse != 0;
-  const cudaError_t e = af::rotary_launch(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = af::rotary_launch(a, p->head_dim, p->rotary_dim, p->interleaved != 0, p->inverse != 0, p->table,
+                                          reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "rotary launch failed: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
