@@ -503,7 +503,7 @@ attn_status af::report_error(attn_status st, const char* fmt, ...) {
 int af::sm_count() { return sm_count_cached(); }
 
 attn_status af::encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, const int64_t (&dims)[4],
-                           const int64_t (&strides)[3], const int (&box)[4]) {
+                           const int64_t (&strides)[3], const int (&box)[4], CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
   cuuint64_t d[4], st[3];
@@ -513,9 +513,8 @@ attn_status af::encode_map(CUtensorMap* map, CUtensorMapDataType type, const voi
     bx[i] = (cuuint32_t)box[i];
     if (i < 3) st[i] = (cuuint64_t)strides[i];
   }
-  const CUresult r = fn(map, type, 4, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(map, type, 4, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(ATTN_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for a %lldx%lldx%lldx%lld tensor", (int)r,
                 (long long)dims[0], (long long)dims[1], (long long)dims[2], (long long)dims[3]);

@@ -161,10 +161,11 @@ struct Tc05Config {
 // returns `st`.
 attn_status report_error(attn_status st, const char* fmt, ...);
 
-// 4-D tensor map of a 128-byte-swizzled box (strides of dimensions 1 to 3 in
+// 4-D tensor map of a swizzled box (strides of dimensions 1 to 3 in
 // bytes); the calling thread's last error says why it failed.
 attn_status encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, const int64_t (&dims)[4],
-                       const int64_t (&strides)[3], const int (&box)[4]);
+                       const int64_t (&strides)[3], const int (&box)[4],
+                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 // SMs of the current device (148 when it cannot be asked).
 int sm_count();
 

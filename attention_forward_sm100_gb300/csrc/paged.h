@@ -19,8 +19,10 @@ constexpr int stream_tile(int row_bytes, int group_warps) { return group_warps =
 // 77.6); where two already wait for HBM it does not pay (e4m3, D = 128: 104 -> 118 with
 // the half tiles that it needs).
 constexpr int stream_ctas(int row_bytes, int row_tile) { return row_bytes == 64 && row_tile == 8 ? 3 : 2; }
-// Keys per work unit of the streaming kernel over e2m1 codes, whose CTAs have an SM each.
-constexpr int stream4_tile = 128;
+// The streaming kernel over e2m1 codes, for row tiles of so many rows: its keys per
+// work unit and CTAs per SM.
+constexpr int stream4_tile(int row_tile) { return row_tile <= 16 ? 128 : 64; }
+constexpr int stream4_ctas(int row_tile) { return row_tile == 8 ? 3 : 2; }
 constexpr int kMinPage = 16;         // smallest page: one warp's step of keys lies in one page
 
 // The new rows of each sequence (fixed: b * seqlen_q; packed: cu_q) and the
@@ -116,6 +118,12 @@ struct StreamParams {
   float* part_o;             // [2 * grid][rows][D], not normalised
 };
 
+// Over an e2m1 cache, with maps of its codes: (byte, head, slot, page), boxes of one
+// head's rows of up to a tile's slots of a page.
+struct Stream4Params : StreamParams {
+  CUtensorMap tm_k, tm_v;
+};
+
 // Arguments of the plan and merge kernels of a paged problem on the tcgen05 kernel.
 struct PlanParams {
   NewRows s;
@@ -144,7 +152,7 @@ cudaError_t cache_read_launch(const ReadParams& p, int head_dim, int kind, cudaS
 cudaError_t paged_stream_launch(const StreamParams& p, int head_dim, bool fp8, int row_tile, int grid,
                                 cudaStream_t stream);
 // The same over an e2m1 cache.
-cudaError_t paged_stream4_launch(const StreamParams& p, int head_dim, int row_tile, int grid, cudaStream_t stream);
+cudaError_t paged_stream4_launch(const Stream4Params& p, int head_dim, int row_tile, int grid, cudaStream_t stream);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ void record_bad_cache(uint32_t* ws, int b) {

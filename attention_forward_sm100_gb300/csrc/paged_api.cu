@@ -310,8 +310,9 @@ StreamPlan plan_stream(const attn_paged_params* p) {
   const int64_t segments = (int64_t)p->cache.batch * p->cache.num_heads_kv * ((rows + rt - 1) / rt);
   const bool fp4 = p->cache.dtype == ATTN_DTYPE_FP4_E2M1;
   const int64_t tiles = af::tiles_for(
-      p->seqlen_k, fp4 ? af::stream4_tile : af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
-  const int64_t ctas = (int64_t)(fp4 ? 1 : af::stream_ctas(row_bytes, s.row_tile)) * af::sm_count();
+      p->seqlen_k, fp4 ? af::stream4_tile(s.row_tile) : af::stream_tile(row_bytes, s.row_tile <= 16 ? 1 : s.row_tile / 16));
+  const int64_t ctas =
+      (int64_t)(fp4 ? af::stream4_ctas(s.row_tile) : af::stream_ctas(row_bytes, s.row_tile)) * af::sm_count();
   const bool one_wave = 4 * segments >= ctas && segments <= 2 * ctas;
   s.split = tiles > kUnsplitTiles && !(one_wave && p->seqlen_k <= kUnsplitKeys) && segments <= kMaxUnits / tiles ? 1 : 0;
   s.units = segments * (s.split ? tiles : 1);
@@ -322,11 +323,6 @@ StreamPlan plan_stream(const attn_paged_params* p) {
     const int heads = p->cache.num_heads_kv;
     s.team = heads < kMaxTeam ? heads : kMaxTeam;
     while (heads % s.team) --s.team;
-    // (one CTA per SM: sixteen of 152 would idle eight)
-    while (fp4 && s.grid >= ctas && s.team > 1 && (s.grid % s.team) * 50 > s.grid) {
-      --s.team;
-      while (heads % s.team) --s.team;
-    }
     s.grid -= s.grid % s.team;
   }
   if (s.split) {
@@ -572,11 +568,26 @@ attn_status af::paged_fwd(const attn_paged_params* params, const attn_block_scal
   a.counters = reinterpret_cast<uint32_t*>(ws + ATTN_FWD_WORKSPACE_BYTES);
   a.part_ml = reinterpret_cast<float2*>(room);
   a.part_o = reinterpret_cast<float*>(room + plan.ml_bytes);
-  const cudaError_t e =
-      p->cache.dtype == ATTN_DTYPE_FP4_E2M1
-          ? af::paged_stream4_launch(a, p->cache.head_dim, plan.row_tile, (int)plan.grid, stream)
-          : af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
-                                    (int)plan.grid, stream);
+  cudaError_t e;
+  if (p->cache.dtype == ATTN_DTYPE_FP4_E2M1) {
+    af::Stream4Params a4;
+    static_cast<af::StreamParams&>(a4) = a;
+    const attn_kv_cache& c = p->cache;
+    const int tile = af::stream4_tile(plan.row_tile), rows = c.page_size < tile ? c.page_size : tile;
+    for (int i = 0; i < 2; ++i) {
+      const int64_t* s = i ? c.v_stride : c.k_stride;
+      st = af::encode_map(i ? &a4.tm_v : &a4.tm_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, i ? c.v : c.k,
+                          {c.head_dim / 2, c.num_heads_kv, c.page_size, c.num_pages},
+                          {legal(s[2], c.num_heads_kv), legal(s[1], c.page_size), legal(s[0], c.num_pages)},
+                          {c.head_dim / 2, 1, rows, 1},
+                          c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+      if (st != ATTN_OK) return st;
+    }
+    e = af::paged_stream4_launch(a4, c.head_dim, plan.row_tile, (int)plan.grid, stream);
+  } else {
+    e = af::paged_stream_launch(a, p->cache.head_dim, p->cache.dtype == ATTN_DTYPE_FP8_E4M3, plan.row_tile,
+                                (int)plan.grid, stream);
+  }
   if (e != cudaSuccess) return report_error(ATTN_ERR_CUDA, "paged attention launch failed: %s", cudaGetErrorString(e));
   return ATTN_OK;
 }
