@@ -252,9 +252,11 @@ __device__ __forceinline__ void append_rows(const AppendParams& P, int block, Sl
         return s.angle;
       });
 }
-// An append with rotation into a bf16 cache.
+// An append with rotation into a bf16 cache. With four blocks to an SM (64 registers, a few
+// of them spilled) 41690 tokens, 32 query heads and 8 of 128 in the cache, take 169 us of a
+// floor of 152; with three 180.
 template <bool APART>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kThreads, 4) append_rows_kernel(const __grid_constant__ AppendParams P) {
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
   append_rows<true, APART>(P, blockIdx.x, slots);
@@ -296,6 +298,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
     if (base == 0) find_slots<ROT>(P, t0, tokens, slots);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
+      if (base + u * PER >= total) break;
       const uint32_t id = base + u * PER + threadIdx.x / L;
       const bool there = id < total;
       const Vector w = vector_at(there ? id : 0u, nv, P.magic, P.c.heads_kv);
@@ -446,34 +449,35 @@ __device__ __forceinline__ void widen4(const uint2& x, uint32_t block, float sca
     }
   }
 }
-// What a lane holds of a quantised vector: sixteen codes and their scales.
+// Values of a vector that a lane reads: 16 bytes of the cache (e2m1: of 8 bytes a lane,
+// finding a vector's place took more instructions than its values: an append of 6360 and
+// a read of 38100 tokens, 8 heads of 128, 47.7 us where this takes 45.6).
+constexpr int read_width(int kind) { return kind == kBf16 ? 8 : (kind == kE4m3 ? 16 : 32); }
+
+// What a lane holds of a quantised vector: its codes and their scales.
 template <int KIND>
 struct Codes {
+  static constexpr int PARTS = KIND == kE2m1 ? 2 : 1;   // of sixteen values
   uint4 x;
   uint32_t block;
   float scale;
   // `src`: the vector's first byte, `at` the index of its scales
   __device__ __forceinline__ void load(const uint8_t* src, const float* scales, const uint8_t* blocks, int64_t at,
                                        int lane, int lanes) {
-    if constexpr (KIND == kE2m1) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + lane * 8));
-      x.x = v.x;
-      x.y = v.y;
-      block = __ldg(blocks + at * lanes + lane);
-    } else {
-      x = __ldcs(reinterpret_cast<const uint4*>(src + lane * 16));
-    }
+    x = __ldcs(reinterpret_cast<const uint4*>(src + lane * 16));
+    if constexpr (KIND == kE2m1) block = __ldg(reinterpret_cast<const uint16_t*>(blocks) + at * lanes + lane);
     scale = __ldg(scales + at);
   }
-  __device__ __forceinline__ void widened(uint32_t (&out)[8]) const {
-    if constexpr (KIND == kE2m1) widen4(make_uint2(x.x, x.y), block, scale, out);
+  __device__ __forceinline__ void widened(int part, uint32_t (&out)[8]) const {
+    if constexpr (KIND == kE2m1)
+      widen4(part ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y), part ? block >> 8 : block & 0xffu, scale, out);
     else widen(x, scale, out);
   }
 };
 
 template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams P) {
-  constexpr int E = KIND == kBf16 ? 8 : 16, L = D / E, PER = kThreads / L;
+  constexpr int E = read_width(KIND), L = D / E, PER = kThreads / L;
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
   const int64_t t0 = (int64_t)blockIdx.x * P.block_tokens;
@@ -521,14 +525,17 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
       if constexpr (KIND == kBf16) {
         *reinterpret_cast<uint4*>(dst) = x[u].x;
       } else {
-        uint32_t out[8];
-        x[u].widened(out);
-        if (P.wide) {
-          ptx::st_global_v8(dst, out);
-        } else {
-          uint4* d = reinterpret_cast<uint4*>(dst);
-          d[0] = make_uint4(out[0], out[1], out[2], out[3]);
-          d[1] = make_uint4(out[4], out[5], out[6], out[7]);
+#pragma unroll
+        for (int part = 0; part < Codes<KIND>::PARTS; ++part) {
+          uint32_t out[8];
+          x[u].widened(part, out);
+          if (P.wide) {
+            ptx::st_global_v8(dst + part * 32, out);
+          } else {
+            uint4* d = reinterpret_cast<uint4*>(dst) + part * 2;
+            d[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            d[1] = make_uint4(out[4], out[5], out[6], out[7]);
+          }
         }
       }
     }
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 // element, HBM bounds it as it does reading.
 template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_constant__ WidenParams P) {
-  constexpr int L = D / 16, PER = kThreads / L;
+  constexpr int L = D / read_width(KIND), PER = kThreads / L;
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
   const int b = blockIdx.y, lane = threadIdx.x % L;
@@ -577,19 +584,29 @@ __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_cons
         if (slots[w.token].page < 0) continue;
         const int t = (int)t0 + w.token;
         const int64_t row = (((int64_t)b * P.pages + t / kBlockN) * P.c.heads_kv + w.h) * kBlockN + t % kBlockN;
-        uint32_t out[8];
-        x[u].widened(out);
-        ptx::st_global_v8((w.v ? P.v : P.k) + row * (D * 2) + lane * 32, out);
+#pragma unroll
+        for (int part = 0; part < Codes<KIND>::PARTS; ++part) {
+          uint32_t out[8];
+          x[u].widened(part, out);
+          ptx::st_global_v8((w.v ? P.v : P.k) + row * (D * 2) + (lane * Codes<KIND>::PARTS + part) * 32, out);
+        }
       }
     }
   }
 }
 
-// A block's tokens: as many as fill its batch of vectors once.
+// A block's tokens: as many as fill its batch of vectors once. Where that leaves SMs
+// without a block, fewer: values to quantise are one vector's after another's in a thread.
+// (32 tokens, 32 query heads and 8 of 128 in the cache, e2m1 with rotation: 13 us with
+// eight tokens to a block, 6 with one.)
+int tokens_of_block(int64_t tokens, uint32_t per_token, int vectors) {
+  const int64_t fit = vectors / (int)per_token, few = tokens / sm_count();
+  const int64_t n = fit < few ? fit : few;
+  return n < 1 ? 1 : (n < kMaxTokens ? (int)n : kMaxTokens);
+}
 template <class K, class P>
 cudaError_t launch(K kern, P p, int64_t tokens, uint32_t per_token, int vectors, cudaStream_t stream) {
-  const int fit = vectors / (int)per_token;
-  p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
+  p.block_tokens = tokens_of_block(tokens, per_token, vectors);
   p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
   const int64_t blocks = (tokens + p.block_tokens - 1) / p.block_tokens;
   if (blocks <= 0) return cudaSuccess;
@@ -598,6 +615,7 @@ cudaError_t launch(K kern, P p, int64_t tokens, uint32_t per_token, int vectors,
 }
 
 constexpr int per_block(int d, int kind) { return kThreads / (d / (kind == kBf16 ? 8 : 16)) * kBatch; }
+constexpr int read_block(int d, int kind) { return kThreads / (d / read_width(kind)) * kBatch; }
 
 // Rows to be turned: blocks of them, with their sizes in `p`.
 int64_t turn_blocks(AppendParams& p, int head_dim, const int (&heads)[3], int turned) {
@@ -611,7 +629,7 @@ template <int D, int KIND>
 cudaError_t append_t(const AppendParams& params, cudaStream_t stream) {
   AppendParams p = params;
   const uint32_t per_token = 2 * p.c.heads_kv;
-  const int vectors = per_block(D, KIND), fit = vectors / (int)per_token;
+  const int vectors = per_block(D, KIND);
   if (p.r.table == nullptr)
     return launch(cache_append_kernel<D, KIND, false>, p, p.tokens, per_token, vectors, stream);
   if constexpr (KIND == kBf16) {
@@ -622,7 +640,7 @@ cudaError_t append_t(const AppendParams& params, cudaStream_t stream) {
                                  : launch_dependent(append_rows_kernel<false>, p, grid, kThreads, 0, stream);
   } else {
     const int64_t rows = p.r.heads_q > 0 ? turn_blocks(p, D, {p.r.heads_q, 0, 0}, 1) : 0;
-    p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
+    p.block_tokens = tokens_of_block(p.tokens, per_token, vectors);
     p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
     const int64_t blocks = (p.tokens + p.block_tokens - 1) / p.block_tokens;
     if (blocks + rows > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -638,7 +656,7 @@ cudaError_t append_d(const AppendParams& p, int kind, cudaStream_t stream) {
 template <int D>
 cudaError_t read_d(const ReadParams& p, int kind, cudaStream_t stream) {
   const uint32_t n = 2 * p.c.heads_kv;
-  const int pb = per_block(D, kind);
+  const int pb = read_block(D, kind);
   return kind == kBf16 ? launch(cache_read_kernel<D, kBf16>, p, p.total_k, n, pb, stream)
                        : (kind == kE4m3 ? launch(cache_read_kernel<D, kE4m3>, p, p.total_k, n, pb, stream)
                                         : launch(cache_read_kernel<D, kE2m1>, p, p.total_k, n, pb, stream));
@@ -658,7 +676,7 @@ cudaError_t cache_append_launch(const AppendParams& p, int head_dim, int kind, c
 cudaError_t cache_widen_launch(const WidenParams& params, int head_dim, int kind, cudaStream_t stream) {
   WidenParams p = params;
   const uint32_t per_token = 2 * p.c.heads_kv;
-  const int fit = per_block(head_dim, kind) / (int)per_token;
+  const int fit = read_block(head_dim, kind) / (int)per_token;
   p.block_tokens = fit < 1 ? 1 : (fit < kMaxTokens ? fit : kMaxTokens);
   p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
   const int64_t chunks = ((int64_t)p.max_k + p.block_tokens - 1) / p.block_tokens;

@@ -18,11 +18,12 @@
 // Measured, GQA 32/8, 128 depths: 16 sequences of up to 32768 keys 84 us (floor 54, the
 // loads alone 68), 64 of up to 8192 88 (50), one of 777 10.4; 24 of up to 4097, five new
 // tokens, 16 heads of 64 depths, pages of 16 slots, 45 (11; the loads alone 31).
-// With each thread copying its own 16-byte pieces (cp.async): 96, 97, 9.7 and 42. With one CTA of 16 warps per SM, of which two or
-// three load and two join and store results: 82, 91, 13 and 40, and a step of 32 sequences
-// of up to 4096, rotation and append included, 59 instead of 53. Shares of the units by the order in which an SM's CTAs
-// start (the first has its instructions issued first, and is done 15 % earlier): 83, 88,
-// but 47 and 57.
+// With each thread copying its own 16-byte pieces (cp.async): 96, 97, 9.7 and 42. With
+// one CTA of 16 warps per SM, of which two or three load and two join and store results:
+// 82, 91, 13 and 40, and a step of 32 sequences of up to 4096, rotation and append
+// included, 59 instead of 53. With shares of the units by the order in which an SM's CTAs
+// start (the first has its instructions issued first and ends 15 % earlier): 83, 88, 11
+// and 47, the step 57.
 // Slots at or past the sequence's end are loaded with the rest of their page but
 // their scales are set to zero, so whatever they hold cannot reach a result (codes
 // are always finite).

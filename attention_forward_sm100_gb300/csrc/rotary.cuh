@@ -46,21 +46,21 @@ struct TurnWord<1> {
   __device__ static __forceinline__ uint16_t load(const uint8_t* p) { return *reinterpret_cast<const uint16_t*>(p); }
 };
 
-// Sums of packed products. The products are packed, two to an instruction, the sums are
-// not: packed additions of packed products are contracted to fused ones, whatever
-// rounding they ask for.
+// Sums (differences) of packed products. The products are packed, two to an instruction,
+// the sums are not: packed additions of packed products are contracted to fused ones,
+// whatever rounding they ask for.
+template <bool MINUS = false>
 __device__ __forceinline__ void sum2(uint64_t a, uint64_t b, float& lo, float& hi) {
   float a0, a1, b0, b1;
   ptx::f2_unpack(a, a0, a1);
   ptx::f2_unpack(b, b0, b1);
-  lo = __fadd_rn(a0, b0);
-  hi = __fadd_rn(a1, b1);
+  lo = MINUS ? __fsub_rn(a0, b0) : __fadd_rn(a0, b0);
+  hi = MINUS ? __fsub_rn(a1, b1) : __fadd_rn(a1, b1);
 }
 // Two pairs at once, as bf16: (a c - b s, b c + a s) of packed values.
-__device__ __forceinline__ void turned2(uint64_t a, uint64_t b, uint64_t c, uint64_t s, uint64_t minus_s, uint32_t& y1,
-                                        uint32_t& y2) {
+__device__ __forceinline__ void turned2(uint64_t a, uint64_t b, uint64_t c, uint64_t s, uint32_t& y1, uint32_t& y2) {
   float lo, hi;
-  sum2(ptx::f2_mul(a, c), ptx::f2_mul(b, minus_s), lo, hi);
+  sum2<true>(ptx::f2_mul(a, c), ptx::f2_mul(b, s), lo, hi);
   y1 = ptx::pack_bf16(lo, hi);
   sum2(ptx::f2_mul(b, c), ptx::f2_mul(a, s), lo, hi);
   y2 = ptx::pack_bf16(lo, hi);
@@ -74,9 +74,10 @@ __device__ __forceinline__ uint64_t f2_of(uint32_t two) { return ptx::f2_pack(bf
 // the 16 bytes R / 2 behind them (or 16 bytes that are only copied). It keeps the item's
 // cosines and sines and goes through up to four (eight) neighbouring heads, whose loads are
 // all in flight, those of a thread's first item before anything is known about its token.
-// (Heads looked up one by one, values turned one by one, tokens found before the first
-// load, 62 % of the threads busy: 16.9 million rows of 40 heads took 139 us of a floor of
-// 72; rotated appends of 41690 tokens by shuffles among a head's lanes 303 of 152.)
+// Packed rows of 23700 tokens, 40 heads of 128, 64 values of each turned, take 74 us of a
+// floor of 72. (Heads looked up one by one, values turned one by one, tokens found before
+// the first load, 62 % of the threads busy: 139. Appends of 41690 tokens with 48 heads, by
+// shuffles among a head's lanes: 303 of 152, by this 169.)
 constexpr int turn_heads(bool apart) { return apart ? 4 : 8; }   // 128 bytes of a thread on their way
 
 struct TurnShape {
@@ -179,22 +180,19 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
           float c[8], s[8];
           load_angles<8>(row, u.d, c);
           load_angles<8>(row, T.rot / 2 + u.d, s);
-          uint64_t c2[4], s2[4], m2[4];
+          uint64_t c2[4], s2[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float s0 = T.inverse ? -s[2 * i] : s[2 * i], s1 = T.inverse ? -s[2 * i + 1] : s[2 * i + 1];
             c2[i] = ptx::f2_pack(c[2 * i], c[2 * i + 1]);
             s2[i] = ptx::f2_pack(s0, s1);
-            m2[i] = ptx::f2_pack(-s0, -s1);
           }
 #pragma unroll
           for (int y = 0; y < HEADS; ++y) {
             if (y < T.group) {
               uint32_t p[4] = {a[y].x, a[y].y, a[y].z, a[y].w}, q[4] = {b[y].x, b[y].y, b[y].z, b[y].w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                turned2(f2_of(p[i]), f2_of(q[i]), c2[i], s2[i], m2[i], p[i], q[i]);
-              }
+              for (int i = 0; i < 4; ++i) turned2(f2_of(p[i]), f2_of(q[i]), c2[i], s2[i], p[i], q[i]);
               a[y] = make_uint4(p[0], p[1], p[2], p[3]);
               b[y] = make_uint4(q[0], q[1], q[2], q[3]);
             }
