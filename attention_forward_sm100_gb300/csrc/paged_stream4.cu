@@ -67,9 +67,9 @@ struct Cfg {
   static constexpr int STAGES = min_int(8, (232448 / CTAS - 1024 - REST) / STAGE);
   static constexpr int AT_PART = STAGES * STAGE, AT_Q = AT_PART, AT_ML = AT_PART + WK * PART,
                        AT_PIECE = AT_ML + WK * RT * 8,
-                       AT_BAR = AT_PIECE + PIECES * 48, SMEM = STAGES * STAGE + REST;
+                       AT_BAR = AT_PIECE + (PIECES + 1) * 48, SMEM = STAGES * STAGE + REST;
   static_assert(STAGES >= 3, "loads in flight");
-  static_assert(PIECES * 48 + 16 * (STAGES + PIECES) <= 512, "room for pieces and barriers");
+  static_assert((PIECES + 1) * 48 + 16 * (STAGES + PIECES) <= 512, "room for pieces and barriers");
   static constexpr int FT = kThreads;   // those that compute finish a piece
   __device__ static int ftid() { return threadIdx.x; }
   __device__ static void fsync() { ptx::bar_sync(0, kThreads); }
@@ -139,12 +139,13 @@ __device__ __forceinline__ bool hand_over(const Pipe& pipe, int k, const Job& j)
   __syncwarp();
   return true;
 }
-template <class C>
-__device__ __forceinline__ Job job_at(const Pipe& pipe, int k) {
-  const int4* from = reinterpret_cast<const int4*>(pipe.pieces + 12 * (k % C::PIECES));
+__device__ __forceinline__ Job job_in(const Pipe& pipe, int place) {
+  const int4* from = reinterpret_cast<const int4*>(pipe.pieces + 12 * place);
   const int4 a = from[0], b = from[1];
   return {{a.x, a.y, a.z, a.w, b.x}, {b.y, b.z, b.w}, from[2].x};
 }
+template <class C>
+__device__ __forceinline__ Job job_at(const Pipe& pipe, int k) { return job_in(pipe, k % C::PIECES); }
 
 // The warp that loads: every tile of this CTA's pieces, in order.
 template <class C>
@@ -212,7 +213,7 @@ __device__ __forceinline__ void load_tiles(const Stream4Params& P, Walker<C> wal
 // next: its loads are on their way while this one is finished. False after the last.
 template <class C>
 __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem, const Pipe& pipe, int k,
-                                          uint32_t (&qf)[C::NT][C::D / 16][2], int& count, int per) {
+                                          uint32_t (&qf)[C::NT][C::D / 16][2], int& count, int per, bool& waits, uint32_t& early) {
   constexpr int D = C::D, WM = C::WM, NT = C::NT, KW = C::KW, NB = C::NB;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3, gk = C::key_row(g);
@@ -584,9 +585,30 @@ __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem,
   ptx::bar_sync(0, kThreads);
   const Job job = job_at<C>(pipe, k);
   auto part_of = [&](int i) { return n > 0 ? reinterpret_cast<const float*>(smem + C::AT_PART + i * C::PART) : nullptr; };
-  finish_piece<C>(P, job.pc, job.s, ml, part_of, job.first, per);
+  leave_piece<C>(P, job.pc, job.s, ml, part_of);
+  const bool whole = job.pc.count == job.pc.tiles;
+  if (more) {
+    ptx::bar_sync(0, kThreads);   // (before the next piece's q is where the parts are)
+    if (!whole && threadIdx.x == 0) {   // (k is 0)
+      // counted in now, looked at in the end
+      __threadfence();
+      early = atomicAdd(PartOf(P, job.pc, job.first, per).counter(P), 1u);
+      int4* to = reinterpret_cast<int4*>(pipe.pieces + 12 * C::PIECES);
+      const int4* from = reinterpret_cast<const int4*>(pipe.pieces);
+      to[0] = from[0]; to[1] = from[1]; to[2] = from[2];
+    }
+  }
+  if (k == 0) waits = more && !whole;
   __syncwarp();
-  if (lane == 0) ptx::mbar_arrive(pipe.taken + 8 * (k % C::PIECES));
+  if (lane == 0 && more) ptx::mbar_arrive(pipe.taken + 8 * (k % C::PIECES));
+  if (!more) {
+    if (!whole) join_piece<C>(P, job.pc, job.s, job.first, per);
+    if (waits) {
+      ptx::bar_sync(0, kThreads);
+      const Job kept = job_in(pipe, C::PIECES);
+      join_piece<C>(P, kept.pc, kept.s, kept.first, per, true, early);
+    }
+  }
   return more;
 }
 
@@ -643,7 +665,10 @@ __global__ void __launch_bounds__(kAll, (Cfg<D, NT, WM>::CTAS))
     load_q<C>(P, job.pc, job.s, (int)(threadIdx.x >> 5) % C::WM, qf);
   }
   int count = 0;   // tiles used so far
-  for (int k = 0; run_piece<C>(P, smem, pipe, k, qf, count, per); ++k) {
+  // a first piece that is a part, counted in as this one from 0
+  bool waits = false;
+  uint32_t early = 0u;
+  for (int k = 0; run_piece<C>(P, smem, pipe, k, qf, count, per, waits, early); ++k) {
   }
 }
 

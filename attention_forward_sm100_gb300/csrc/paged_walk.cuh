@@ -205,20 +205,42 @@ __device__ __forceinline__ void piece_tiles(const StreamParams& P, const Piece& 
 constexpr int kJoin = 16;
 
 // Whether this CTA is the last of `want` to count itself in (and leaves the
-// counter at zero).
+// counter at zero). `counted`: thread 0 has done so already, being the n-th from 0.
 template <class C>
-__device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t want) {
+__device__ __forceinline__ bool count_in(uint32_t* counter, uint32_t want, bool counted = false, uint32_t n = 0u) {
   __shared__ bool is_last;
   C::fsync();
   if (C::ftid() == 0) {
-    __threadfence();   // (of the whole CTA's stores: the barrier above orders them before it)
-    is_last = atomicAdd(counter, 1u) == want - 1u;
+    if (!counted) {
+      __threadfence();   // (of the whole CTA's stores: the barrier above orders them before it)
+      n = atomicAdd(counter, 1u);
+    }
+    is_last = n == want - 1u;
     if (is_last) *counter = 0u;
     __threadfence();
   }
   C::fsync();
   return is_last;
 }
+// Which of a segment's parts a CTA has, the piece's first unit being `first` among all
+// and `per` the units of every CTA: the parts, from team c0 on, this one's neighbourhood,
+// how many are in there, and neighbourhoods.
+struct PartOf {
+  int c0, parts, hood, in_hood, hoods;
+  __device__ __forceinline__ PartOf(const StreamParams& P, const Piece& pc, int first, int per) {
+    const int start = first - pc.first;
+    c0 = start / per;
+    parts = (start + pc.tiles - 1) / per - c0 + 1;
+    hood = ((int)blockIdx.x / P.team - c0) / kJoin;
+    in_hood = min(kJoin, parts - kJoin * hood);
+    hoods = (parts + kJoin - 1) / kJoin;
+  }
+  // Counters: [0] a segment's first neighbourhood by its first CTA, [1] others by theirs,
+  // [2] neighbourhoods by the segment's first CTA.
+  __device__ __forceinline__ uint32_t* counter(const StreamParams& P) const {
+    return P.counters + (hood == 0 ? 0 : (int)gridDim.x) + cta_of(P, c0 + kJoin * hood);
+  }
+};
 
 // 16-byte pieces of a row tile per thread.
 template <class C>
@@ -309,29 +331,31 @@ __device__ __forceinline__ void load_q(const StreamParams& P, const Piece& pc, c
   }
 }
 
-// Finishes a piece whose key groups have left their results in shared memory
+// Writes the row piece (row, d .. d + 3) of a segment: its sums over l, and lse.
+template <class C>
+__device__ __forceinline__ void finish_row(const StreamParams& P, const Piece& pc, const SeqRows& s, int row, int d,
+                                           const float4& o, float mm, float ll) {
+  const RowAt a = row_at(P, head_of(P, pc.seg), row_tile_of(P, pc.seg) * C::RT + row);
+  const float inv = ll == 0.f ? 0.f : 1.f / ll;
+  *reinterpret_cast<uint2*>(o_at(P, s, pc.b, a) + d) =
+      make_uint2(ptx::pack_bf16(o.x * inv, o.y * inv), ptx::pack_bf16(o.z * inv, o.w * inv));
+  if (d == 0 && P.lse != nullptr) P.lse[lse_at(P, s, pc.b, a)] = lse_of(mm, ll);
+}
+template <class C>
+__device__ __forceinline__ int rows_of_piece(const StreamParams& P, const Piece& pc, const SeqRows& s) {
+  return min(C::RT, s.lq * P.group - row_tile_of(P, pc.seg) * C::RT);
+}
+
+// Sums the key groups of a piece, whose results have been left in shared memory
 // (a barrier ago): `ml` [WK][RT] maxima and sums, part(k) group k's [RT][D]
-// accumulators, or NULL where it had no keys. Rows of a segment that
-// lies in this CTA are written, others joined by whichever CTA comes last. `first`:
-// the piece's first unit among all; `per`: the units of every CTA.
+// accumulators, or NULL where it had no keys. Rows of a segment that lies in this
+// CTA are written, others left as a part of it.
 template <class C, class Part>
-__device__ __forceinline__ void finish_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, const float2* ml,
-                                             Part part, int first, int per) {
+__device__ __forceinline__ void leave_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, const float2* ml,
+                                            Part part) {
   constexpr int D = C::D;
-  const int hk = head_of(P, pc.seg), rt = row_tile_of(P, pc.seg), rows = s.lq * P.group;
-  auto finish_row = [&](int, int row, int d, const float4& o, float mm, float ll) {
-    const RowAt a = row_at(P, hk, rt * C::RT + row);
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    *reinterpret_cast<uint2*>(o_at(P, s, pc.b, a) + d) =
-        make_uint2(ptx::pack_bf16(o.x * inv, o.y * inv), ptx::pack_bf16(o.z * inv, o.w * inv));
-    if (d == 0 && P.lse != nullptr) P.lse[lse_at(P, s, pc.b, a)] = lse_of(mm, ll);
-  };
-  auto keep_row = [&](int64_t slot, int row, int d, const float4& o, float mm, float ll) {
-    *reinterpret_cast<float4*>(P.part_o + (slot * C::RT + row) * D + d) = o;
-    if (d == 0) P.part_ml[slot * C::RT + row] = make_float2(mm, ll);
-  };
   const bool whole = pc.count == pc.tiles;
-  const int valid = min(C::RT, rows - rt * C::RT);
+  const int valid = rows_of_piece<C>(P, pc, s);
   const int64_t mine = 2 * (int64_t)blockIdx.x + (pc.first == 0 ? 1 : 0);
   for (int x = C::ftid(); x < valid * (D / 4); x += C::FT) {
     const int row = x / (D / 4), d = 4 * (x % (D / 4));
@@ -353,24 +377,29 @@ __device__ __forceinline__ void finish_piece(const StreamParams& P, const Piece&
       o.z = fmaf(w, v.z, o.z);
       o.w = fmaf(w, v.w, o.w);
     }
-    if (whole) finish_row(0, row, d, o, mm, ll);
-    else keep_row(mine, row, d, o, mm, ll);
+    if (whole) {
+      finish_row<C>(P, pc, s, row, d, o, mm, ll);
+    } else {
+      *reinterpret_cast<float4*>(P.part_o + (mine * C::RT + row) * D + d) = o;
+      if (d == 0) P.part_ml[mine * C::RT + row] = make_float2(mm, ll);
+    }
   }
-  if (whole) {
-    C::fsync();   // before the next piece loads over the parts
-    return;
-  }
-  const int start = first - pc.first, c0 = start / per, parts = (start + pc.tiles - 1) / per - c0 + 1;
-  const int hood = ((int)blockIdx.x / P.team - c0) / kJoin, in_hood = min(kJoin, parts - kJoin * hood);
-  const int hoods = (parts + kJoin - 1) / kJoin;
-  // counters: [0] a segment's first neighbourhood by its first CTA, [1] others
-  // by theirs, [2] neighbourhoods by the segment's first CTA
-  uint32_t* const counters = P.counters;
-  const int grid = gridDim.x;
+}
+
+// Joins the parts of a piece's segment if this CTA is the last to count itself in
+// (`counted`, `n`: as count_in).
+template <class C>
+__device__ __forceinline__ void join_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, int first, int per,
+                                           bool counted = false, uint32_t n = 0u) {
+  constexpr int D = C::D;
+  const int valid = rows_of_piece<C>(P, pc, s);
+  const PartOf at(P, pc, first, per);
+  const int c0 = at.c0, hood = at.hood, in_hood = at.in_hood, hoods = at.hoods;
+  auto finish = [&](int, int row, int d, const float4& o, float mm, float ll) { finish_row<C>(P, pc, s, row, d, o, mm, ll); };
   auto slot_in_hood = [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * hood + i) + (hood == 0 && i == 0 ? 1 : 0); };
-  if (!count_in<C>(counters + (hood == 0 ? 0 : grid) + cta_of(P, c0 + kJoin * hood), in_hood)) return;
+  if (!count_in<C>(at.counter(P), in_hood, counted, n)) return;
   if (hoods == 1) {
-    join_parts<C>(P, in_hood, valid, slot_in_hood, finish_row);
+    join_parts<C>(P, in_hood, valid, slot_in_hood, finish);
     return;
   }
   // The joined part overwrites the first one's: every thread its own columns,
@@ -388,9 +417,17 @@ __device__ __forceinline__ void finish_piece(const StreamParams& P, const Piece&
     const int x = C::ftid() + i * C::FT;
     if (x < valid * (D / 4) && x % (D / 4) == 0) P.part_ml[slot_in_hood(0) * C::RT + x / (D / 4)] = kept[i];
   }
-  if (!count_in<C>(counters + 2 * grid + cta_of(P, c0), hoods)) return;
-  join_parts<C>(P, hoods, valid, [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish_row);
+  if (!count_in<C>(P.counters + 2 * (int)gridDim.x + cta_of(P, c0), hoods)) return;
+  join_parts<C>(P, hoods, valid, [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish);
 }
 
+// Both: rows of a segment of several CTAs are finished by whichever comes last.
+template <class C, class Part>
+__device__ __forceinline__ void finish_piece(const StreamParams& P, const Piece& pc, const SeqRows& s, const float2* ml,
+                                             Part part, int first, int per) {
+  leave_piece<C>(P, pc, s, ml, part);
+  if (pc.count == pc.tiles) C::fsync();   // before the next piece loads over the parts
+  else join_piece<C>(P, pc, s, first, per);
+}
 
 }  // namespace af
