@@ -29,6 +29,8 @@
 // same tokens. Into a bf16 cache all of it is whole rows (append_rows, rotary.cuh);
 // where keys are quantised (ROT), a vector's lanes have to meet, and the queries are
 // other blocks' work.
+#include <type_traits>
+
 #include "launch.cuh"
 #include "paged.h"
 #include "ptx.cuh"
@@ -155,17 +157,39 @@ __device__ __noinline__ uint2 quantise_any(const float* f, float size, float inv
   return size == 0.f ? make_uint2(0u, 0u) : make_uint2(out[0], out[1]);
 }
 
-// Sequence and index of token t0 + token of rows of a fixed length.
-__device__ __forceinline__ void fixed_token(const AppendParams& P, int64_t t0, int token, int& b, int& i) {
-  const uint32_t t = (uint32_t)t0 + (uint32_t)token, len = (uint32_t)P.s.seqlen_q;
-  b = (int)(t / len);
-  i = (int)(t - (uint32_t)b * len);
-}
+// Sequence and index of a block's token, of rows of a fixed length: by a division of
+// its own, or counted from the block's first one.
+struct TokenByDivision {
+  uint32_t t0, len;
+  __device__ __forceinline__ TokenByDivision(const AppendParams& P, int64_t t0_)
+      : t0((uint32_t)t0_), len((uint32_t)P.s.seqlen_q) {}
+  __device__ __forceinline__ void at(int token, int& b, int& i) const {
+    const uint32_t t = t0 + (uint32_t)token;
+    b = (int)(t / len);
+    i = (int)(t - (uint32_t)b * len);
+  }
+};
+struct TokenByCount {
+  int b0, i0, len;
+  __device__ __forceinline__ TokenByCount(const AppendParams& P, int64_t t0) : b0(0), i0(0), len(P.s.seqlen_q) {
+    if (P.s.cu_q != nullptr) return;
+    b0 = (int)((uint32_t)t0 / (uint32_t)len);
+    i0 = (int)t0 - b0 * len;
+  }
+  __device__ __forceinline__ void at(int token, int& b, int& i) const {
+    b = b0;
+    i = i0 + token;
+    while (i >= len) {
+      i -= len;
+      ++b;
+    }
+  }
+};
 
 // Where each of a block's tokens goes (and, ROT, its angle), one lane of the first warp a
 // token; ends with a barrier. The whole block calls it.
-template <bool ROT>
-__device__ __forceinline__ void find_slots(const AppendParams& P, int64_t t0, int tokens, Slot* slots) {
+template <bool ROT, class Params, class Token>
+__device__ __forceinline__ void find_slots(const Params& P, int64_t t0, int tokens, const Token& token_of, Slot* slots) {
   const int64_t t = t0 + (threadIdx.x & 31);
   const bool packed = P.s.cu_q != nullptr;
   const int found = packed ? find_sequence<kThreads>(P.s.cu_q, P.s.batch, t0, t, P.tokens, P.ws, kDevErrBadCache) : 0;
@@ -185,7 +209,7 @@ __device__ __forceinline__ void find_slots(const AppendParams& P, int64_t t0, in
         ok = a >= 0 && i >= 0 && e <= P.tokens;
       }
     } else {
-      fixed_token(P, t0, threadIdx.x, b, i);
+      token_of.at(threadIdx.x, b, i);
     }
     if (ok) {
       const int lk = P.s.seqlens_k[b];
@@ -204,10 +228,12 @@ __device__ __forceinline__ void find_slots(const AppendParams& P, int64_t t0, in
 }
 
 // Offset of a token's rows with batch and token strides sb, st.
-__device__ __forceinline__ int64_t row_offset(const AppendParams& P, int64_t t0, int token, int64_t sb, int64_t st) {
+template <class Token>
+__device__ __forceinline__ int64_t row_offset(const AppendParams& P, int64_t t0, const Token& token_of, int token, int64_t sb,
+                                              int64_t st) {
   if (P.s.cu_q != nullptr) return (t0 + token) * st;
   int b, i;
-  fixed_token(P, t0, token, b, i);
+  token_of.at(token, b, i);
   return b * sb + i * st;
 }
 
@@ -215,10 +241,11 @@ __device__ __forceinline__ int64_t row_offset(const AppendParams& P, int64_t t0,
 // any cache, and (KV) keys and values on their way into a bf16 one. Heads are those of
 // q, then K's, then V's.
 template <bool KV, bool APART>
-__device__ __forceinline__ void append_rows(const AppendParams& P, int block, Slot* slots) {
+__device__ __forceinline__ void append_rows(const TurnedAppendParams& P, int block, Slot* slots) {
   const int64_t t0 = (int64_t)block * P.r.block_tokens;
   const int tokens = (int)min((int64_t)P.r.block_tokens, P.tokens - t0);
   const int hq = P.r.heads_q, hkv = P.c.heads_kv;
+  const TokenByDivision token_of(P, t0);
   turn_rows<8, APART, kThreads>(
       P.r.shape, tokens,
       [&](int token, int h, TurnHead& head) {
@@ -232,10 +259,10 @@ __device__ __forceinline__ void append_rows(const AppendParams& P, int block, Sl
           st = v ? P.v_t : P.k_t;
           sh = v ? P.v_h : P.k_h;
         }
-        head.src = base + row_offset(P, t0, token, sb, st) + h * sh;
+        head.src = base + row_offset(P, t0, token_of, token, sb, st) + h * sh;
         head.src_next = sh;
       },
-      [&]() { find_slots<true>(P, t0, tokens, slots); },
+      [&]() { find_slots<true>(P, t0, tokens, token_of, slots); },
       [&](int token, int h, TurnHead& head) {
         const Slot s = slots[token];
         if (s.page < 0) return -1;
@@ -246,7 +273,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& P, int block, Sl
                        : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + h * P.c.k_head;
           head.dst_next = v ? P.c.v_head : P.c.k_head;
         } else {
-          head.dst = P.r.q_out + row_offset(P, t0, token, P.r.out_b, P.r.out_t) + h * P.r.out_h;
+          head.dst = P.r.q_out + row_offset(P, t0, token_of, token, P.r.out_b, P.r.out_t) + h * P.r.out_h;
           head.dst_next = P.r.out_h;
         }
         return s.angle;
@@ -256,26 +283,30 @@ __device__ __forceinline__ void append_rows(const AppendParams& P, int block, Sl
 // of them spilled) 41690 tokens, 32 query heads and 8 of 128 in the cache, take 169 us of a
 // floor of 152; with three 180.
 template <bool APART>
-__global__ void __launch_bounds__(kThreads, 4) append_rows_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kThreads, 4) append_rows_kernel(const __grid_constant__ TurnedAppendParams P) {
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
   append_rows<true, APART>(P, blockIdx.x, slots);
 }
 
 template <int D, int KIND, bool ROT>
-__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ AppendParams P) {
+__global__ void __launch_bounds__(kThreads)
+    cache_append_kernel(const __grid_constant__ std::conditional_t<ROT, TurnedAppendParams, AppendParams> P) {
   constexpr int E = KIND == kBf16 ? 8 : 16, L = D / E, PER = kThreads / L;
   __shared__ Slot slots[kMaxTokens];
   ptx::grid_dependency_wait();
-  if (ROT && (int)blockIdx.x >= P.blocks_kv) {   // (the queries')
-    if (P.r.interleaved) append_rows<false, false>(P, (int)blockIdx.x - P.blocks_kv, slots);
-    else append_rows<false, true>(P, (int)blockIdx.x - P.blocks_kv, slots);
-    return;
+  if constexpr (ROT) {
+    if ((int)blockIdx.x >= P.blocks_kv) {   // (the queries')
+      if (P.r.interleaved) append_rows<false, false>(P, (int)blockIdx.x - P.blocks_kv, slots);
+      else append_rows<false, true>(P, (int)blockIdx.x - P.blocks_kv, slots);
+      return;
+    }
   }
   const int64_t t0 = (int64_t)blockIdx.x * P.block_tokens;
   const int tokens = (int)min((int64_t)P.block_tokens, P.tokens - t0);
   const uint32_t nv = 2 * P.c.heads_kv, total = tokens * nv;
   const int lane = threadIdx.x % L;
+  const TokenByCount token_of(P, t0);
   for (uint32_t base = 0; base < total; base += PER * kBatch) {
     uint4 x[kBatch][E / 8];
 #pragma unroll
@@ -286,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       if (id < total) {
         const Vector w = vector_at(id, nv, P.magic, P.c.heads_kv);
         const uint8_t* src = (w.v ? P.v + w.h * P.v_h : P.k + w.h * P.k_h) + lane * (E * 2) +
-                             row_offset(P, t0, w.token, w.v ? P.v_b : P.k_b, w.v ? P.v_t : P.k_t);
+                             row_offset(P, t0, token_of, w.token, w.v ? P.v_b : P.k_b, w.v ? P.v_t : P.k_t);
         if (KIND != kBf16 && P.wide) {
           ptx::ld_global_v8(src, reinterpret_cast<uint32_t*>(&x[u][0]));
         } else {
@@ -295,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
         }
       }
     }
-    if (base == 0) find_slots<ROT>(P, t0, tokens, slots);
+    if (base == 0) find_slots<ROT>(P, t0, tokens, token_of, slots);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (base + u * PER >= total) break;
@@ -453,11 +484,11 @@ __device__ __forceinline__ void widen4(const uint2& x, uint32_t block, float sca
 // finding a vector's place took more instructions than its values: an append of 6360 and
 // a read of 38100 tokens, 8 heads of 128, 47.7 us where this takes 45.6).
 constexpr int read_width(int kind) { return kind == kBf16 ? 8 : (kind == kE4m3 ? 16 : 32); }
+constexpr int read_parts(int kind) { return kind == kE2m1 ? 2 : 1; }   // of sixteen, of a lane's quantised values
 
 // What a lane holds of a quantised vector: its codes and their scales.
 template <int KIND>
 struct Codes {
-  static constexpr int PARTS = KIND == kE2m1 ? 2 : 1;   // of sixteen values
   uint4 x;
   uint32_t block;
   float scale;
@@ -526,7 +557,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         *reinterpret_cast<uint4*>(dst) = x[u].x;
       } else {
 #pragma unroll
-        for (int part = 0; part < Codes<KIND>::PARTS; ++part) {
+        for (int part = 0; part < read_parts(KIND); ++part) {
           uint32_t out[8];
           x[u].widened(part, out);
           if (P.wide) {
@@ -585,28 +616,30 @@ __global__ void __launch_bounds__(kThreads) cache_widen_kernel(const __grid_cons
         const int t = (int)t0 + w.token;
         const int64_t row = (((int64_t)b * P.pages + t / kBlockN) * P.c.heads_kv + w.h) * kBlockN + t % kBlockN;
 #pragma unroll
-        for (int part = 0; part < Codes<KIND>::PARTS; ++part) {
+        for (int part = 0; part < read_parts(KIND); ++part) {
           uint32_t out[8];
           x[u].widened(part, out);
-          ptx::st_global_v8((w.v ? P.v : P.k) + row * (D * 2) + (lane * Codes<KIND>::PARTS + part) * 32, out);
+          ptx::st_global_v8((w.v ? P.v : P.k) + row * (D * 2) + (lane * read_parts(KIND) + part) * 32, out);
         }
       }
     }
   }
 }
 
-// A block's tokens: as many as fill its batch of vectors once. Where that leaves SMs
-// without a block, fewer: values to quantise are one vector's after another's in a thread.
+// A block's tokens: as many as fill its batch of vectors once, at most (FEW) as leave
+// no SM without a block: values to quantise are one vector's after another's in a thread.
 // (32 tokens, 32 query heads and 8 of 128 in the cache, e2m1 with rotation: 13 us with
-// eight tokens to a block, 6 with one.)
+// eight tokens to a block, 6 with one. What is only moved is not faster in smaller blocks:
+// 96 tokens of 8 heads, bf16, 3.6 us with four, 3.7 with one.)
+template <bool FEW>
 int tokens_of_block(int64_t tokens, uint32_t per_token, int vectors) {
-  const int64_t fit = vectors / (int)per_token, few = tokens / sm_count();
+  const int64_t fit = vectors / (int)per_token, few = FEW ? tokens / sm_count() : fit;
   const int64_t n = fit < few ? fit : few;
   return n < 1 ? 1 : (n < kMaxTokens ? (int)n : kMaxTokens);
 }
-template <class K, class P>
+template <bool FEW = false, class K, class P>
 cudaError_t launch(K kern, P p, int64_t tokens, uint32_t per_token, int vectors, cudaStream_t stream) {
-  p.block_tokens = tokens_of_block(tokens, per_token, vectors);
+  p.block_tokens = tokens_of_block<FEW>(tokens, per_token, vectors);
   p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
   const int64_t blocks = (tokens + p.block_tokens - 1) / p.block_tokens;
   if (blocks <= 0) return cudaSuccess;
@@ -618,7 +651,7 @@ constexpr int per_block(int d, int kind) { return kThreads / (d / (kind == kBf16
 constexpr int read_block(int d, int kind) { return kThreads / (d / read_width(kind)) * kBatch; }
 
 // Rows to be turned: blocks of them, with their sizes in `p`.
-int64_t turn_blocks(AppendParams& p, int head_dim, const int (&heads)[3], int turned) {
+int64_t turn_blocks(TurnedAppendParams& p, int head_dim, const int (&heads)[3], int turned) {
   AppendRotary& r = p.r;
   r.shape = turn_shape(r.table, head_dim, r.rot, r.interleaved != 0, false, heads, turned);
   r.block_tokens = turn_tokens(r.shape, p.tokens, kThreads, kMaxTokens, sm_count());
@@ -626,12 +659,13 @@ int64_t turn_blocks(AppendParams& p, int head_dim, const int (&heads)[3], int tu
 }
 
 template <int D, int KIND>
-cudaError_t append_t(const AppendParams& params, cudaStream_t stream) {
-  AppendParams p = params;
+cudaError_t append_t(const TurnedAppendParams& params, cudaStream_t stream) {
+  TurnedAppendParams p = params;
   const uint32_t per_token = 2 * p.c.heads_kv;
   const int vectors = per_block(D, KIND);
   if (p.r.table == nullptr)
-    return launch(cache_append_kernel<D, KIND, false>, p, p.tokens, per_token, vectors, stream);
+    return launch<KIND == kE2m1>(cache_append_kernel<D, KIND, false>, static_cast<const AppendParams&>(params), p.tokens,
+                                 per_token, vectors, stream);
   if constexpr (KIND == kBf16) {
     const int64_t blocks = turn_blocks(p, D, {p.r.heads_q, p.c.heads_kv, p.c.heads_kv}, 2);
     if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -640,7 +674,7 @@ cudaError_t append_t(const AppendParams& params, cudaStream_t stream) {
                                  : launch_dependent(append_rows_kernel<false>, p, grid, kThreads, 0, stream);
   } else {
     const int64_t rows = p.r.heads_q > 0 ? turn_blocks(p, D, {p.r.heads_q, 0, 0}, 1) : 0;
-    p.block_tokens = tokens_of_block(p.tokens, per_token, vectors);
+    p.block_tokens = tokens_of_block<true>(p.tokens, per_token, vectors);
     p.magic = (uint32_t)((((uint64_t)1 << 32) + per_token - 1) / per_token);
     const int64_t blocks = (p.tokens + p.block_tokens - 1) / p.block_tokens;
     if (blocks + rows > 0x7fffffffll) return cudaErrorInvalidValue;
@@ -649,7 +683,7 @@ cudaError_t append_t(const AppendParams& params, cudaStream_t stream) {
   }
 }
 template <int D>
-cudaError_t append_d(const AppendParams& p, int kind, cudaStream_t stream) {
+cudaError_t append_d(const TurnedAppendParams& p, int kind, cudaStream_t stream) {
   return kind == kBf16 ? append_t<D, kBf16>(p, stream)
                        : (kind == kE4m3 ? append_t<D, kE4m3>(p, stream) : append_t<D, kE2m1>(p, stream));
 }
@@ -669,7 +703,7 @@ cudaError_t widen_d(const WidenParams& p, int kind, dim3 grid, cudaStream_t stre
 
 }  // namespace
 
-cudaError_t cache_append_launch(const AppendParams& p, int head_dim, int kind, cudaStream_t stream) {
+cudaError_t cache_append_launch(const TurnedAppendParams& p, int head_dim, int kind, cudaStream_t stream) {
   return head_dim == 128 ? append_d<128>(p, kind, stream) : append_d<64>(p, kind, stream);
 }
 

@@ -57,7 +57,6 @@ struct AppendRotary {
 struct AppendParams {
   CacheView c;
   BlockScales blocks;
-  AppendRotary r;
   NewRows s;
   const uint8_t* k;
   const uint8_t* v;
@@ -66,8 +65,11 @@ struct AppendParams {
   int32_t wide;                           // 1: k, v, q and their strides are multiples of 32 bytes
   int32_t block_tokens;                   // set by the launch, as `magic` and
   uint32_t magic;
-  int32_t blocks_kv;                      // the blocks of keys and values, in front of those of queries
   uint32_t* ws;
+};
+struct TurnedAppendParams : AppendParams {
+  AppendRotary r;
+  int32_t blocks_kv;                      // the blocks of keys and values, in front of those of queries
 };
 
 struct ReadParams {
@@ -145,7 +147,7 @@ cudaError_t paged_plan_launch(const PlanParams& p, cudaStream_t stream);
 cudaError_t paged_tile_merge_launch(const PlanParams& p, int head_dim, int max_cut, cudaStream_t stream);
 
 // kind: CacheKind (to widen: not bf16).
-cudaError_t cache_append_launch(const AppendParams& p, int head_dim, int kind, cudaStream_t stream);
+cudaError_t cache_append_launch(const TurnedAppendParams& p, int head_dim, int kind, cudaStream_t stream);
 cudaError_t cache_widen_launch(const WidenParams& p, int head_dim, int kind, cudaStream_t stream);
 cudaError_t cache_read_launch(const ReadParams& p, int head_dim, int kind, cudaStream_t stream);
 // Streaming attention over `grid` CTAs with row tiles of 8, 16 or 32 rows.

@@ -211,10 +211,20 @@ constexpr int64_t kMaxStreamCtas = (kZeroedBytes - ATTN_FWD_WORKSPACE_BYTES) / 1
 //   R      4          16         32         48         64         128
 //   bf16   171 / 218  179 / 220  192 / 220  350 / 222  356 / 224  686 / 228
 //   e4m3   106 / 323  117 / 332  201 / 335  371 / 341  373 / 343  731 / 351
-constexpr int kStreamRows = 32;
+// An e2m1 cache goes to the tcgen05 kernel as a bf16 copy, which has to be written first,
+// so that two passes of the streaming kernel are worth while (8 sequences of up to 16384
+// keys; 2 of up to 2000):
+//   R            32        48         64         96         128
+//   d128        84 / -   125 / 160  127 / 160  181 / 162  225 / 165
+//   d64         49 / -    75 / 112   77 / 112  109 / 113  138 / 114
+//   d128, 2     47 / -    37 / 36    54 / 36    42 / 37    41 / 37
+//   d64, 2      28 / -    28 / 33    31 / 33    24 / 33    25 / 33
+constexpr int kStreamRows = 32, kStreamRows4 = 64;
 int64_t shared_rows(const attn_paged_params* p) {
   return (int64_t)p->seqlen_q * (p->num_heads_q / p->cache.num_heads_kv);
 }
+// Bytes of a bf16 copy of the sequences at most, and rows of a sequence from which an
+// e4m3 cache gets one (plan_widen).
 constexpr int64_t kWidenRows = 512, kWidenBytes = 1ll << 30;
 // Whether a bf16 copy of the sequences (of `pages` pages of kBlockN tokens each) stays
 // below the bound.
@@ -225,7 +235,8 @@ bool copy_fits(const attn_paged_params* p) {
 }
 // An e2m1 cache has no form on the tcgen05 kernel but the one over a bf16 copy.
 bool use_tc05(const attn_paged_params* p) {
-  return shared_rows(p) > kStreamRows && (p->cache.dtype != ATTN_DTYPE_FP4_E2M1 || copy_fits(p));
+  if (p->cache.dtype == ATTN_DTYPE_FP4_E2M1) return shared_rows(p) > kStreamRows4 && copy_fits(p);
+  return shared_rows(p) > kStreamRows;
 }
 
 // tcgen05 kernel: query heads packed into a 128-row tile (the largest divisor of
@@ -287,6 +298,8 @@ struct StreamPlan {
 // GQA 32/8, d128, us cut / whole: 12 sequences of up to 300 keys, bf16: 12.8 / 7.0;
 // 32 sequences of up to 1000 keys, bf16 22.7 / 17.5, e4m3 21.2 / 14.9; 8 of them
 // 13.7 / 13.6; 75 of them 36.7 / 34.6; but 3 of them 9.1 / 12.3, 256 of them 94 / 112.
+// e2m1: 32 of up to 600 19.5 / 12.1, of up to 1000 21.8 / 14.9; 75 of them 32.0 / 28.2;
+// 114 of them 40.3 / 33.4; 12 of them with 16 rows 34.3 / 18.6.
 // Where the bound on the lengths allows more key tiles than the device counts (in
 // 32 bits), segments, which are then thousands, are left whole too.
 constexpr int kUnsplitTiles = 4;
@@ -622,7 +635,7 @@ attn_status attn_cache_append_blocks(const attn_cache_append_params* p, const at
   if (st != ATTN_OK) return st;
   const bool packed = p->cu_seqlens_q != nullptr;
   if (p->cache.batch == 0 || (packed ? p->total_q : p->seqlen_q) == 0) return ATTN_OK;
-  af::AppendParams a;
+  af::TurnedAppendParams a;
   memset(&a, 0, sizeof(a));
   a.c = view_of(p->cache);
   a.s.cu_q = p->cu_seqlens_q;

@@ -602,11 +602,21 @@ __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem,
   __syncwarp();
   if (lane == 0 && more) ptx::mbar_arrive(pipe.taken + 8 * (k % C::PIECES));
   if (!more) {
-    if (!whole) join_piece<C>(P, job.pc, job.s, job.first, per);
-    if (waits) {
-      ptx::bar_sync(0, kThreads);
-      const Job kept = job_in(pipe, C::PIECES);
-      join_piece<C>(P, kept.pc, kept.s, kept.first, per, true, early);
+    // The last piece's segment, then the first one's. (More rows have their joins in one
+    // place, the instructions for the second one then being in the cache: 8 sequences of up
+    // to 1000 keys, 32 rows of 128 depths, 36 us instead of 44; 8 rows are done sooner
+    // without the loop.)
+    auto join = [&](bool last) {
+      if (!last) ptx::bar_sync(0, kThreads);
+      const Job j = last ? job : job_in(pipe, C::PIECES);
+      join_piece<C>(P, j.pc, j.s, j.first, per, !last, early);
+    };
+    if constexpr (C::RT == 8) {
+      if (!whole) join(true);
+      if (waits) join(false);
+    } else {
+#pragma unroll 1
+      for (int i = whole ? 1 : 0; i <= (waits ? 1 : 0); ++i) join(i == 0);
     }
   }
   return more;

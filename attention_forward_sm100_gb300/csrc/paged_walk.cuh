@@ -249,11 +249,12 @@ constexpr int rounds() { return (C::RT * (C::D / 4) + C::FT - 1) / C::FT; }
 // Sums parts 0 .. n - 1 at slots slot(i) of the segment's `valid` rows; hands
 // (round, row, depth, four sums, maximum, sum) to `put`, whose thread alone
 // holds them (round: of this thread's, a constant after unrolling). Sixteen
-// loads of a thread are in flight: up to four rows, times parts.
-template <class C, class Slot, class Put>
+// loads of a thread are in flight: up to four rows, times parts. ROLLED: `round` need
+// not be a constant.
+template <class C, bool ROLLED, class Slot, class Put>
 __device__ __forceinline__ void join_parts(const StreamParams& P, int n, int valid, Slot slot, Put put) {
   constexpr int D = C::D, ROUNDS = rounds<C>(), IT = min_int(ROUNDS, 4), PB = 16 / IT;
-#pragma unroll
+#pragma unroll (ROLLED ? 1 : ROUNDS / IT)
   for (int g = 0; g < ROUNDS / IT; ++g) {
     float mm[IT], ll[IT];
     float4 o[IT];
@@ -399,7 +400,7 @@ __device__ __forceinline__ void join_piece(const StreamParams& P, const Piece& p
   auto slot_in_hood = [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * hood + i) + (hood == 0 && i == 0 ? 1 : 0); };
   if (!count_in<C>(at.counter(P), in_hood, counted, n)) return;
   if (hoods == 1) {
-    join_parts<C>(P, in_hood, valid, slot_in_hood, finish);
+    join_parts<C, true>(P, in_hood, valid, slot_in_hood, finish);
     return;
   }
   // The joined part overwrites the first one's: every thread its own columns,
@@ -407,7 +408,7 @@ __device__ __forceinline__ void join_piece(const StreamParams& P, const Piece& p
   float2 kept[rounds<C>()];
 #pragma unroll
   for (int i = 0; i < rounds<C>(); ++i) kept[i] = make_float2(0.f, 0.f);
-  join_parts<C>(P, in_hood, valid, slot_in_hood, [&](int round, int row, int d, const float4& o, float mm, float ll) {
+  join_parts<C, false>(P, in_hood, valid, slot_in_hood, [&](int round, int row, int d, const float4& o, float mm, float ll) {
     *reinterpret_cast<float4*>(P.part_o + (slot_in_hood(0) * C::RT + row) * D + d) = o;
     kept[round] = make_float2(mm, ll);
   });
@@ -418,7 +419,7 @@ __device__ __forceinline__ void join_piece(const StreamParams& P, const Piece& p
     if (x < valid * (D / 4) && x % (D / 4) == 0) P.part_ml[slot_in_hood(0) * C::RT + x / (D / 4)] = kept[i];
   }
   if (!count_in<C>(P.counters + 2 * (int)gridDim.x + cta_of(P, c0), hoods)) return;
-  join_parts<C>(P, hoods, valid, [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish);
+  join_parts<C, true>(P, hoods, valid, [&](int i) { return 2 * (int64_t)cta_of(P, c0 + kJoin * i) + (i == 0 ? 1 : 0); }, finish);
 }
 
 // Both: rows of a segment of several CTAs are finished by whichever comes last.

@@ -150,9 +150,10 @@ def test_attend_many_sequences(pkg, batch, hkv, group, new, longest):
 @pytest.mark.parametrize("lens_k,lens_q,hq,hkv,dim,page", [
     ([9000], [256], 4, 4, 128, 64), ([5000], [300], 16, 2, 64, 128),
     ([4100, 1300, 2600, 1029], [200, 900, 1, 130], 8, 2, 128, 32), ([1200] * 40, [70] * 40, 6, 2, 64, 16),
-    ([1500, 0, 1100, 3], [40, 5, 0, 100], 32, 1, 64, 16)])
+    ([1500, 0, 1100, 3], [40, 5, 0, 100], 32, 1, 64, 16), ([1700, 90, 33], [12, 9, 16], 8, 2, 128, 16),
+    ([2100, 12], [33, 12], 2, 2, 64, 128)])
 def test_attend_chunks_over_the_copy_and_without_it(pkg, lens_k, lens_q, hq, hkv, dim, page):
-    """More than 32 rows read a bf16 copy, or, where a bound on the lengths asks for
+    """More than 64 rows read a bf16 copy, or, where a bound on the lengths asks for
     too much scratch memory, go over the cache 32 rows at a time."""
     p = R4.make(lens_k, lens_q, hq, hkv, dim, page, packed=True, seed=29)
     wide = torch.full((len(lens_k), (1 << 23) // page), -1, dtype=torch.int32, device="cuda")
