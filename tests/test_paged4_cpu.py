@@ -133,8 +133,8 @@ def test_other_caches_take_no_block_scales(pkg):
 
 
 @pytest.mark.parametrize("dim", [64, 128])
-def test_more_than_32_rows_are_copied_where_the_copy_fits(pkg, dim):
-    """Two sequences, two KV heads, eight query heads: nine new tokens are 36 rows."""
+def test_more_than_64_rows_are_copied_where_the_copy_fits(pkg, dim):
+    """Two sequences, two KV heads, eight query heads: 17 new tokens are 68 rows."""
     L = _library(pkg)
 
     def size(new, keys):
@@ -147,11 +147,11 @@ def test_more_than_32_rows_are_copied_where_the_copy_fits(pkg, dim):
     def copy(keys):   # K and V as bf16
         return 2 * 2 * 2 * 2 * dim * keys
 
-    assert size(8, 200) == 8192
-    assert size(9, 2000) == 8192 + 256 + copy(2048)   # too few keys for a work list
+    assert size(16, 200) == 8192
+    assert size(17, 2000) == 8192 + 256 + copy(2048)   # too few keys for a work list
     most = (1 << 30) // (16 * dim)
-    assert size(9, most) > copy(most)
-    assert size(9, most + 1) < 256 << 20
+    assert size(17, most) > copy(most)
+    assert size(17, most + 1) < 256 << 20
 
 
 # ---------------------------------------------------------------- the reference itself
