@@ -15,15 +15,25 @@
 //     as in paged_stream.cu; the vectors' scales are applied to the fp32 scores and
 //     weights. For V^T, whose operands are pairs of keys, two keys' bytes are merged
 //     into (key, key) pairs of a depth before they are converted.
-// Measured, GQA 32/8, 128 depths: 16 sequences of up to 32768 keys 84 us (floor 54, the
-// loads alone 68), 64 of up to 8192 88 (50), one of 777 10.4; 24 of up to 4097, five new
-// tokens, 16 heads of 64 depths, pages of 16 slots, 45 (11; the loads alone 31).
-// With each thread copying its own 16-byte pieces (cp.async): 96, 97, 9.7 and 42. With
-// one CTA of 16 warps per SM, of which two or three load and two join and store results:
-// 82, 91, 13 and 40, and a step of 32 sequences of up to 4096, rotation and append
-// included, 59 instead of 53. With shares of the units by the order in which an SM's CTAs
-// start (the first has its instructions issued first and ends 15 % earlier): 83, 88, 11
-// and 47, the step 57.
+//   * a CTA has at most two parts of segments that others have parts of too, its first
+//     piece and its last. The first is counted in when it has been left, but whether it
+//     is the last to come, and joins, is looked at in the end.
+// Measured, GQA 32/8, 128 depths: 16 sequences of up to 32768 keys 78 us (floor 54, the
+// loads alone 68), 64 of up to 8192 82 (50), one of 777 10.1; 24 of up to 4097, five new
+// tokens, 16 heads of 64 depths, pages of 16 slots, 44 (11; the loads alone 31). Instruction
+// issue bounds it (54 % of the slots in the mean, start and end included).
+// Tried (us for these, in this order, and a step of 32 sequences of up to 4096 with rotation
+// and append, 41.5):
+//   each thread copying its own 16-byte pieces (cp.async): 96, 97, 9.7, 42, -
+//   one CTA of 16 warps per SM, two or three that load, two that join and store: 82, 91,
+//     13, 40, 59 (with an append of 13 us in it, in place of 6)
+//   the first part counted in and joined where it ends (5 us of a fence and an atomic
+//     while loads are under way): 85, 89, 10.4, 45, 45.5
+//   both parts counted in at the end: 79, 84, 10.3, 46, 44; by the loading warp, meanwhile:
+//     78, 82, 10.4, 45.6, 41.5
+//   shares of the units by the order in which an SM's CTAs start (the first has its
+//     instructions issued first and ends 10 % earlier): 1 us less for the long ones, 1 to
+//     2 us more for the short ones
 // Slots at or past the sequence's end are loaded with the rest of their page but
 // their scales are set to zero, so whatever they hold cannot reach a result (codes
 // are always finite).
