@@ -157,8 +157,16 @@ __device__ __forceinline__ Job job_in(const Pipe& pipe, int place) {
 template <class C>
 __device__ __forceinline__ Job job_at(const Pipe& pipe, int k) { return job_in(pipe, k % C::PIECES); }
 
-// The warp that loads: every tile of this CTA's pieces, in order.
-template <class C>
+// Whether scales are loaded by the lanes, 16 bytes each, and not by bulk copies, of which
+// pages of few slots take very many small ones. us, by copies / by lanes: pages of 16
+// slots, 24 sequences of up to 4097 keys, five new tokens, 16 heads of 64 depths 44.3 /
+// 34.7; of 32, a step of 32 sequences of up to 4096, 8 heads of 128, 42.1 / 43.9. (Kernels
+// of their own: with both in one, pages of 32 slots and more lost 4 to 9 %, to the
+// instruction cache.)
+bool small_pages(const StreamParams& P) { return P.c.page_shift < 5; }
+
+// The warp that loads: every tile of this CTA's pieces, in order. SMALL as small_pages().
+template <class C, bool SMALL>
 __device__ __forceinline__ void load_tiles(const Stream4Params& P, Walker<C> walk, const Pipe& pipe, uint32_t ring, int x,
                                            int end) {
   const int lane = threadIdx.x & 31;
@@ -167,7 +175,7 @@ __device__ __forceinline__ void load_tiles(const Stream4Params& P, Walker<C> wal
   const int unit = min(C::TILE, 1 << P.c.page_shift), units = C::TILE / unit;
   const int u = lane & 7, what = lane >> 3;   // 0: codes of K, 1: of V, 2: scales of K, 3: of V
   const int page_mask = (1 << P.c.page_shift) - 1;
-  const uint32_t unit_bytes = unit * (2 * C::ROWB + 2 * C::BK + 8);
+  const uint32_t unit_bytes = unit * (2 * C::ROWB + (SMALL ? 0 : 2 * C::BK + 8));
   int count = 0, k = 0;
   bool ok = true;
   while (ok && x < end) {
@@ -195,15 +203,34 @@ __device__ __forceinline__ void load_tiles(const Stream4Params& P, Walker<C> wal
       __syncwarp();
       if (there) {
         const int slot = key & page_mask;
-        if (what < 2) {
+        if (what < 2)
           ptx::tma_load_4d(at + (what ? C::AT_V : 0) + u * unit * C::ROWB, what ? &P.tm_v : &P.tm_k, bar, 0, hk, slot, page);
-        } else {
+        if (SMALL || what >= 2) {
           const int64_t first = (((int64_t)page * P.c.heads_kv + hk) << P.c.page_shift) + slot;
-          const uint8_t* blocks = what == 2 ? P.blocks.k : P.blocks.v;
-          const float* scales = what == 2 ? P.c.k_scale : P.c.v_scale;
-          ptx::bulk_load(at + (what == 2 ? C::AT_KB : C::AT_VB) + u * unit * C::BK, blocks + first * C::BK, unit * C::BK, bar);
-          ptx::bulk_load(at + (what == 2 ? C::AT_KS : C::AT_VS) + u * unit * 4, scales + first, unit * 4, bar);
+          if constexpr (SMALL) {
+            // 16-byte pieces what, what + 4, ... of the unit's scales
+            const int n4 = unit / 4, nb = unit * C::BK / 16;
+            for (int c = what; c < n4; c += 4) {
+              const uint32_t to = at + u * unit * 4 + c * 16;
+              ptx::cp_async16(to + C::AT_KS, P.c.k_scale + first + c * 4);
+              ptx::cp_async16(to + C::AT_VS, P.c.v_scale + first + c * 4);
+            }
+            for (int c = what; c < nb; c += 4) {
+              const uint32_t to = at + u * unit * C::BK + c * 16;
+              ptx::cp_async16(to + C::AT_KB, P.blocks.k + first * C::BK + c * 16);
+              ptx::cp_async16(to + C::AT_VB, P.blocks.v + first * C::BK + c * 16);
+            }
+          } else {
+            const uint8_t* blocks = what == 2 ? P.blocks.k : P.blocks.v;
+            const float* scales = what == 2 ? P.c.k_scale : P.c.v_scale;
+            ptx::bulk_load(at + (what == 2 ? C::AT_KB : C::AT_VB) + u * unit * C::BK, blocks + first * C::BK, unit * C::BK, bar);
+            ptx::bulk_load(at + (what == 2 ? C::AT_KS : C::AT_VS) + u * unit * 4, scales + first, unit * 4, bar);
+          }
         }
+      }
+      if constexpr (SMALL) {
+        __syncwarp();
+        ptx::cp_async_arrive(bar);
       }
       page = next;
     }
@@ -632,7 +659,7 @@ __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem,
   return more;
 }
 
-template <int D, int NT, int WM>
+template <int D, int NT, int WM, bool SMALL>
 __global__ void __launch_bounds__(kAll, (Cfg<D, NT, WM>::CTAS))
     paged_stream4_kernel(const __grid_constant__ Stream4Params P) {
   using C = Cfg<D, NT, WM>;
@@ -650,7 +677,7 @@ __global__ void __launch_bounds__(kAll, (Cfg<D, NT, WM>::CTAS))
     over = 0;
 #pragma unroll
     for (int i = 0; i < C::STAGES; ++i) {
-      ptx::mbar_init(pipe.full + 8 * i, 1);
+      ptx::mbar_init(pipe.full + 8 * i, SMALL ? 33 : 1);   // (the lanes' arrivals)
       ptx::mbar_init(pipe.empty + 8 * i, kThreads / 32);
     }
 #pragma unroll
@@ -675,7 +702,7 @@ __global__ void __launch_bounds__(kAll, (Cfg<D, NT, WM>::CTAS))
   if (x >= end) return;
   if (threadIdx.x >= kThreads) {
     if (P.s.batch > 32) walk.seek(P, x);
-    load_tiles<C>(P, walk, pipe, ptx::smem_u32(smem), x, end);
+    load_tiles<C, SMALL>(P, walk, pipe, ptx::smem_u32(smem), x, end);
     return;
   }
   uint32_t qf[C::NT][D / 16][2];
@@ -692,12 +719,17 @@ __global__ void __launch_bounds__(kAll, (Cfg<D, NT, WM>::CTAS))
   }
 }
 
-template <int D, int NT, int WM>
-cudaError_t launch_t(const Stream4Params& p, int grid, cudaStream_t stream) {
+template <int D, int NT, int WM, bool SMALL>
+cudaError_t launch_s(const Stream4Params& p, int grid, cudaStream_t stream) {
   using C = Cfg<D, NT, WM>;
-  constexpr auto kern = paged_stream4_kernel<D, NT, WM>;
+  constexpr auto kern = paged_stream4_kernel<D, NT, WM, SMALL>;
   return launch_with_smem<kern>(
       C::SMEM, [&]() { return launch_dependent(kern, p, dim3((unsigned)grid), kAll, C::SMEM, stream); });
+}
+
+template <int D, int NT, int WM>
+cudaError_t launch_t(const Stream4Params& p, int grid, cudaStream_t stream) {
+  return small_pages(p) ? launch_s<D, NT, WM, true>(p, grid, stream) : launch_s<D, NT, WM, false>(p, grid, stream);
 }
 
 template <int D>

@@ -406,6 +406,11 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Arrives on the mbarrier (whose count includes this) once all of this thread's earlier
+// copies are there.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // A read-only load that stays where it is written: the compiler otherwise moves
 // it to the use of its value, a loop iteration later.
 __device__ __forceinline__ int ld_global_pinned(const int* p) {
