@@ -20,9 +20,10 @@
 //     is the last to come, and joins, is looked at in the end.
 // Measured, GQA 32/8, 128 depths: 16 sequences of up to 32768 keys 78 us (floor 54, the
 // loads alone 68), 64 of up to 8192 82 (50), one of 777 10.1; 24 of up to 4097, five new
-// tokens, 16 heads of 64 depths, pages of 16 slots, 44 (11; the loads alone 31). Instruction
-// issue bounds it (54 % of the slots in the mean, start and end included).
-// Tried (us for these, in this order, and a step of 32 sequences of up to 4096 with rotation
+// tokens, 16 heads of 64 depths, pages of 16 slots, 35 (11). Instruction issue bounds it
+// (54 % of the slots in the mean, start and end included), and fetch: a loop of 730
+// instructions, a third of whose stalls are for the next one.
+// Tried (us for these, with 44 for the last, in this order, and a step of 32 sequences of up to 4096 with rotation
 // and append, 41.5):
 //   each thread copying its own 16-byte pieces (cp.async): 96, 97, 9.7, 42, -
 //   one CTA of 16 warps per SM, two or three that load, two that join and store: 82, 91,
@@ -34,6 +35,7 @@
 //   shares of the units by the order in which an SM's CTAs start (the first has its
 //     instructions issued first and ends 10 % earlier): 1 us less for the long ones, 1 to
 //     2 us more for the short ones
+//   the products with V in a rolled loop, for fewer instructions: 81, 83, -, -, 42
 // Slots at or past the sequence's end are loaded with the rest of their page but
 // their scales are set to zero, so whatever they hold cannot reach a result (codes
 // are always finite).
@@ -160,9 +162,9 @@ __device__ __forceinline__ Job job_at(const Pipe& pipe, int k) { return job_in(p
 // Whether scales are loaded by the lanes, 16 bytes each, and not by bulk copies, of which
 // pages of few slots take very many small ones. us, by copies / by lanes: pages of 16
 // slots, 24 sequences of up to 4097 keys, five new tokens, 16 heads of 64 depths 44.3 /
-// 34.7; of 32, a step of 32 sequences of up to 4096, 8 heads of 128, 42.1 / 43.9. (Kernels
-// of their own: with both in one, pages of 32 slots and more lost 4 to 9 %, to the
-// instruction cache.)
+// 34.6; 8 heads of 128 and pages of 32, a step of 32 sequences of up to 4096, 42.6 / 43.7;
+// of 64, 64 sequences of up to 8192, 81.8 / 86.1. (Kernels of their own: with both in one,
+// pages of 32 slots and more lost 4 to 9 %, to the instruction cache.)
 bool small_pages(const StreamParams& P) { return P.c.page_shift < 5; }
 
 // The warp that loads: every tile of this CTA's pieces, in order. SMALL as small_pages().
