@@ -83,7 +83,9 @@ constexpr int turn_heads(bool apart) { return apart ? 4 : 8; }   // 128 bytes of
 struct TurnShape {
   const float* table;
   int32_t rot, interleaved, inverse;
-  int32_t items, group, slots;   // of a head; heads of a thread; threads of an item of a token
+  int32_t items, slots;          // of a head; threads of an item of a token
+  int32_t first, first_slots;    // heads of the first segment, and their threads
+  int32_t group, group2;         // heads of a thread, in the first segment and in others
   int32_t turned;                // heads up to this one are turned, those behind copied
 };
 // Sizes of a launch: heads[] of the segments that follow one another, the first `turned`
@@ -98,10 +100,14 @@ inline TurnShape turn_shape(const float* table, int dim, int rot, bool interleav
   t.interleaved = interleaved ? 1 : 0;
   t.inverse = inverse ? 1 : 0;
   t.items = wide && interleaved ? dim / w : dim / w - rot / 2 / w;
-  t.group = turn_heads(!(wide && interleaved));
-  for (int h : heads)
-    while (h % t.group) t.group /= 2;
-  t.slots = (heads[0] + heads[1] + heads[2]) / t.group;
+  // (of each segment's own: with one for all, 88000 tokens with 32 heads of q and 2 of K and
+  // of V, 64 depths, of which 16 turned, took 191 us of a floor of 120, with these 126)
+  t.group = t.group2 = turn_heads(!(wide && interleaved));
+  while (heads[0] % t.group) t.group /= 2;
+  while (heads[1] % t.group2 || heads[2] % t.group2) t.group2 /= 2;
+  t.first = heads[0];
+  t.first_slots = heads[0] / t.group;
+  t.slots = t.first_slots + (heads[1] + heads[2]) / t.group2;
   for (int i = 0; i < turned; ++i) t.turned += heads[i];
   return t;
 }
@@ -131,7 +137,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
   constexpr int HEADS = turn_heads(APART);
   const int half = APART ? T.rot / 2 / W : 0;   // the first items have two parts
   struct Unit {
-    int token, h, item, d, d2;
+    int token, h, heads, item, d, d2;
     bool pair;
   };
   auto unit_at = [&](int x) {
@@ -139,7 +145,9 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
     u.token = x / per_token;
     const int rest = x - u.token * per_token, slot = rest / T.items;
     u.item = rest - slot * T.items;
-    u.h = slot * T.group;
+    const bool first = slot < T.first_slots;
+    u.heads = first ? T.group : T.group2;
+    u.h = first ? slot * T.group : T.first + (slot - T.first_slots) * T.group2;
     u.pair = u.item < half;
     // first value of the item, and of its other part
     u.d = (u.pair || !APART ? u.item : u.item + half) * W;
@@ -157,7 +165,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
     source(u.token, u.h, head);
 #pragma unroll
     for (int y = 0; y < HEADS; ++y) {
-      if (y < T.group) {
+      if (y < u.heads) {
         a[y] = TurnWord<W>::load(head.src + 2 * u.d);
         if (APART && u.pair) b[y % (APART ? HEADS : 1)] = TurnWord<W>::load(head.src + 2 * u.d2);
         head.src += head.src_next;
@@ -189,7 +197,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
           }
 #pragma unroll
           for (int y = 0; y < HEADS; ++y) {
-            if (y < T.group) {
+            if (y < u.heads) {
               uint32_t p[4] = {a[y].x, a[y].y, a[y].z, a[y].w}, q[4] = {b[y].x, b[y].y, b[y].z, b[y].w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) turned2(f2_of(p[i]), f2_of(q[i]), c2[i], s2[i], p[i], q[i]);
@@ -212,7 +220,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
           }
 #pragma unroll
           for (int y = 0; y < HEADS; ++y) {
-            if (y < T.group) {
+            if (y < u.heads) {
               uint32_t p[4] = {a[y].x, a[y].y, a[y].z, a[y].w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {   // (x1, x2) (c, c) + (x2, x1) (-s, s)
@@ -230,7 +238,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
           const float c = __ldg(row + u.item), s0 = __ldg(row + T.rot / 2 + u.item), s = T.inverse ? -s0 : s0;
 #pragma unroll
           for (int y = 0; y < HEADS; ++y) {
-            if (y < T.group) {
+            if (y < u.heads) {
               const float p = __uint_as_float((uint32_t)a[y] << 16), q = __uint_as_float((uint32_t)b[y] << 16);
               a[y] = (uint16_t)ptx::pack_bf16(turned(p, q, c, -s), 0.f);
               b[y] = (uint16_t)ptx::pack_bf16(turned(q, p, c, s), 0.f);
@@ -240,7 +248,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
       }
 #pragma unroll
       for (int y = 0; y < HEADS; ++y) {
-        if (y < T.group) {
+        if (y < u.heads) {
           *reinterpret_cast<Word*>(head.dst + 2 * u.d) = a[y];
           if (APART && u.pair) *reinterpret_cast<Word*>(head.dst + 2 * u.d2) = b[y % (APART ? HEADS : 1)];
           head.dst += head.dst_next;
