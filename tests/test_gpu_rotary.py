@@ -265,6 +265,9 @@ APPEND = {
     "112": ([8, 0, 130, 4], [0, 0, 129, 0], 5, 5, 128, 64, True, 112, False),
     "many_sequences": ([3 + b % 40 for b in range(300)], [1 + b % 3 for b in range(300)], 2, 1, 64, 16, True, 32, False),
     "long": ([3000, 2097], [2090, 2090], 8, 4, 128, 128, False, 128, False),
+    # heads whose numbers have little in common, so that threads take other counts of q's than of the keys
+    "groups": ([50, 9], [33, 9], 24, 3, 128, 16, True, 128, False),
+    "groups_interleaved": ([50, 9], [33, 9], 32, 2, 64, 64, True, 16, True),
 }
 
 
