@@ -77,7 +77,7 @@ __device__ __forceinline__ uint64_t f2_of(uint32_t two) { return ptx::f2_pack(bf
 // Packed rows of 23700 tokens, 40 heads of 128, 64 values of each turned, take 74 us of a
 // floor of 72. (Heads looked up one by one, values turned one by one, tokens found before
 // the first load, 62 % of the threads busy: 139. Appends of 41690 tokens with 48 heads, by
-// shuffles among a head's lanes: 303 of 152, by this 169.)
+// shuffles among a head's lanes: 303 of 152, by this 162.)
 constexpr int turn_heads(bool apart) { return apart ? 4 : 8; }   // 128 bytes of a thread on their way
 
 struct TurnShape {
@@ -87,6 +87,7 @@ struct TurnShape {
   int32_t first, first_slots;    // heads of the first segment, and their threads
   int32_t group, group2;         // heads of a thread, in the first segment and in others
   int32_t turned;                // heads up to this one are turned, those behind copied
+  int32_t twos;                  // 1: 16-byte pieces that are only copied go two by two
 };
 // Sizes of a launch: heads[] of the segments that follow one another, the first `turned`
 // of them turned.
@@ -99,7 +100,12 @@ inline TurnShape turn_shape(const float* table, int dim, int rot, bool interleav
   t.rot = rot;
   t.interleaved = interleaved ? 1 : 0;
   t.inverse = inverse ? 1 : 0;
-  t.items = wide && interleaved ? dim / w : dim / w - rot / 2 / w;
+  // (two by two where their number is even: threads of such pieces alone keep half as much
+  // on its way; 41690 tokens, 40 heads of 128, 64 of them turned, 183 us, with
+  // this 140)
+  const int pairs = rot / 2 / w, rest = dim / w - 2 * pairs;
+  t.twos = wide && !interleaved && rest % 2 == 0 ? 1 : 0;
+  t.items = wide && interleaved ? dim / w : pairs + (t.twos ? rest / 2 : rest);
   // (of each segment's own: with one for all, 88000 tokens with 32 heads of q and 2 of K and
   // of V, 64 depths, of which 16 turned, took 191 us of a floor of 120, with these 126)
   t.group = t.group2 = turn_heads(!(wide && interleaved));
@@ -138,7 +144,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
   const int half = APART ? T.rot / 2 / W : 0;   // the first items have two parts
   struct Unit {
     int token, h, heads, item, d, d2;
-    bool pair;
+    bool pair, two;   // to be turned, with another part
   };
   auto unit_at = [&](int x) {
     Unit u;
@@ -150,8 +156,9 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
     u.h = first ? slot * T.group : T.first + (slot - T.first_slots) * T.group2;
     u.pair = u.item < half;
     // first value of the item, and of its other part
-    u.d = (u.pair || !APART ? u.item : u.item + half) * W;
-    u.d2 = u.d + T.rot / 2;
+    u.two = APART && (u.pair || T.twos);
+    u.d = (u.pair || !APART ? u.item : (T.twos ? 2 * u.item : u.item + half)) * W;
+    u.d2 = u.d + (u.pair ? T.rot / 2 : W);
     if (W == 1 && u.pair && T.interleaved) {
       u.d = 2 * u.item;
       u.d2 = u.d + 1;
@@ -167,7 +174,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
     for (int y = 0; y < HEADS; ++y) {
       if (y < u.heads) {
         a[y] = TurnWord<W>::load(head.src + 2 * u.d);
-        if (APART && u.pair) b[y % (APART ? HEADS : 1)] = TurnWord<W>::load(head.src + 2 * u.d2);
+        if (APART && u.two) b[y % (APART ? HEADS : 1)] = TurnWord<W>::load(head.src + 2 * u.d2);
         head.src += head.src_next;
       }
     }
@@ -250,7 +257,7 @@ __device__ __forceinline__ void turn_rows(const TurnShape& T, int tokens, Source
       for (int y = 0; y < HEADS; ++y) {
         if (y < u.heads) {
           *reinterpret_cast<Word*>(head.dst + 2 * u.d) = a[y];
-          if (APART && u.pair) *reinterpret_cast<Word*>(head.dst + 2 * u.d2) = b[y % (APART ? HEADS : 1)];
+          if (APART && u.two) *reinterpret_cast<Word*>(head.dst + 2 * u.d2) = b[y % (APART ? HEADS : 1)];
           head.dst += head.dst_next;
         }
       }

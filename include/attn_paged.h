@@ -52,6 +52,10 @@
  *           Rounding code * scale to bf16 changes nothing when scales are powers of
  *           two, as append's are (but for products below bf16's subnormals, 2^-133);
  *           other scales move a score by up to 2^-8 of scale * sum_d |q_id K_jd|.
+ *           Over an e2m1 cache, code * block is exact and the scales multiply fp32
+ *           scores and weights; calls of more than 64 rows read a bf16 copy
+ *           (code * block * scale, rounded once) where that takes 1 GiB at most, as
+ *           above, and go over the cache 32 rows at a time, unrounded, elsewhere.
  *           Rows with an empty J_i get O_i = 0 and
  *           LSE_i = -inf. Slots at or past position Lk_b are never used, they
  *           may hold anything; cached values in front of Lk_b that the causal
