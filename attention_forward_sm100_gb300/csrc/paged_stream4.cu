@@ -503,9 +503,16 @@ __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem,
       for (int e = 0; e < 2; ++e) {
         vk[i][e] = ptx::ld_shared_f32(st + at_sc + 4 * C::TILE + 64 * i + 32 * e);
         top = fmaxf(top, fabsf(vk[i][e]));
-        low = fminf(low, fabsf(vk[i][e]));   // (0 behind the end: bf16 will do for a last tile)
+        low = fminf(low, fabsf(vk[i][e]));
       }
     const bool plain = __all_sync(kFull, top <= vref && low >= vref * 0.0625f);
+    if (!plain) {   // a scale of 0, as behind the end, loses nothing in f16
+      low = INFINITY;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) low = fminf(low, vk[i][e] == 0.f ? INFINITY : fabsf(vk[i][e]));
+    }
     if (!plain && __any_sync(kFull, top > vref)) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
