@@ -11,6 +11,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "../../include/attn_paged.h"
 #include "internal.h"
 #include "schedule.cuh"
 
@@ -565,7 +566,9 @@ attn_status attn_fwd_check(void* workspace, attn_stream_t stream) {
   if (e != cudaSuccess) return fail(ATTN_ERR_CUDA, "reading the workspace failed: %s", cudaGetErrorString(e));
   if (w[af::kWsErrorCode] != af::kDevErrNone) {
     const uint32_t info = w[af::kWsErrorInfo];
-    cudaMemset(static_cast<uint32_t*>(workspace) + af::kWsErrorCode, 0, 2 * sizeof(uint32_t));
+    // (only a paged attention, whose workspace is that large, says that it left counters)
+    if (w[af::kWsCountersLeft] != 0u) cudaMemset(workspace, 0, ATTN_PAGED_ZEROED_BYTES);
+    else cudaMemset(static_cast<uint32_t*>(workspace) + af::kWsErrorCode, 0, 2 * sizeof(uint32_t));
     cudaDeviceSynchronize();
     if (w[af::kWsErrorCode] == af::kDevErrBadSeqlens)
       return fail(ATTN_ERR_INVALID_ARG, "cu_seqlens of sequence %u are decreasing or exceed total_q / total_k "

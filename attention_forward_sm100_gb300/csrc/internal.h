@@ -22,7 +22,8 @@ enum WorkspaceWord : int {
   kWsDoneCounter = 1,   // CTAs finished (the last one resets both counters)
   kWsErrorCode = 2,     // 0 or a device error code
   kWsErrorInfo = 3,     // block, role and barrier of the first error
-  kWsWords = 4
+  kWsCountersLeft = 4,  // 1: a timeout may have left counters behind the words (paged attention) at any value
+  kWsWords = 5
 };
 
 // Device error codes recorded in kWsErrorCode.

@@ -124,6 +124,8 @@ struct StreamParams {
 // head's rows of up to a tile's slots of a page.
 struct Stream4Params : StreamParams {
   CUtensorMap tm_k, tm_v;
+  uint64_t timeout_ns;       // limit of every device wait
+  int32_t withhold;          // testing, 1: block 0 never hears of its first tile
 };
 
 // Arguments of the plan and merge kernels of a paged problem on the tcgen05 kernel.

@@ -532,7 +532,7 @@ attn_status launch_tiles(const attn_paged_params* p, const attn_block_scales* bl
 }  // namespace
 
 attn_status af::paged_fwd(const attn_paged_params* params, const attn_block_scales* blocks, void* scratch,
-                          size_t scratch_bytes, cudaStream_t stream) {
+                          size_t scratch_bytes, cudaStream_t stream, bool withhold) {
   report_error(ATTN_OK, "%s", "");
   attn_status st = check_paged(params);
   if (st != ATTN_OK) return st;
@@ -540,6 +540,8 @@ attn_status af::paged_fwd(const attn_paged_params* params, const attn_block_scal
   if (no_rows(params)) return ATTN_OK;
   const attn_paged_params with_rows = planned(params), *p = &with_rows;
   if ((st = check_workspace(p->workspace)) != ATTN_OK) return st;
+  if (withhold && (p->cache.dtype != ATTN_DTYPE_FP4_E2M1 || use_tc05(p)))
+    return report_error(ATTN_ERR_UNSUPPORTED, "only few rows over an e2m1 cache have tiles to withhold");
   const size_t need = scratch_need(p);
   if (p->workspace_bytes < kZeroedBytes + (scratch != nullptr ? 0 : need))
     return report_error(ATTN_ERR_INVALID_ARG, "workspace of at least %zu bytes is required", kZeroedBytes + need);
@@ -585,6 +587,8 @@ attn_status af::paged_fwd(const attn_paged_params* params, const attn_block_scal
   if (p->cache.dtype == ATTN_DTYPE_FP4_E2M1) {
     af::Stream4Params a4;
     static_cast<af::StreamParams&>(a4) = a;
+    a4.withhold = withhold ? 1 : 0;
+    a4.timeout_ns = withhold ? 200000000ull : 2000000000ull;
     const attn_kv_cache& c = p->cache;
     const int tile = af::stream4_tile(plan.row_tile), rows = c.page_size < tile ? c.page_size : tile;
     for (int i = 0; i < 2; ++i) {
@@ -723,6 +727,10 @@ attn_status attn_paged_fwd(const attn_paged_params* p, attn_stream_t stream) {
 
 attn_status attn_paged_fwd_blocks(const attn_paged_params* p, const attn_block_scales* blocks, attn_stream_t stream) {
   return af::paged_fwd(p, blocks, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_paged_fwd_withheld(const attn_paged_params* p, const attn_block_scales* blocks, attn_stream_t stream) {
+  return af::paged_fwd(p, blocks, nullptr, 0, reinterpret_cast<cudaStream_t>(stream), true);
 }
 
 }  // extern "C"

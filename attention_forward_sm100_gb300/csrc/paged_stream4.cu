@@ -40,9 +40,12 @@
 // their scales are set to zero, so whatever they hold cannot reach a result (codes
 // are always finite).
 //
-// Every wait is bounded: when one runs out, the error is recorded, nothing waits any
-// more, the loading warp issues nothing any more and ends when its copies are there, and
-// the others end with their piece.
+// Every wait is bounded. When one runs out, the error is recorded, and with it that the
+// counters of the joins may be left as they are (attn_fwd_check clears them); no wait of
+// that CTA lasts any more, the computing warps leave their piece after that tile, without
+// results, and end, and the loading warp ends at the next tile that is not given back,
+// when its copies are there. (The way out of the loop is its count: a branch out of it,
+// and the loading warp asking for each tile, cost 1.5 %.)
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -107,6 +110,7 @@ struct Pipe {
   int* pieces;              // 12 words each
   volatile int* over;       // a wait has run out
   uint32_t* ws;
+  uint64_t limit;           // of a wait, in ns
 
   // False when it ran out, in this warp or before in another of the CTA.
   __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, int role) const {
@@ -120,7 +124,8 @@ struct Pipe {
         if (*over) return false;
         const uint64_t now = ptx::globaltimer();
         if (since == 0) since = now;
-        if (now - since > 2000000000ull) {
+        if (now - since > limit) {
+          atomicExch(&ws[kWsCountersLeft], 1u);
           if (atomicCAS(&ws[kWsErrorCode], 0u, (uint32_t)kDevErrTimeout) == 0u)
             atomicExch(&ws[kWsErrorInfo], (blockIdx.x << 16) | ((uint32_t)role << 8));
           *over = 1;
@@ -243,7 +248,7 @@ __device__ __forceinline__ void load_tiles(const Stream4Params& P, Walker<C> wal
   for (int j = max(0, count - C::STAGES); j < count; ++j) {
     const uint64_t since = ptx::globaltimer();
     while (!ptx::mbar_try_wait(pipe.full + 8 * (j % C::STAGES), (uint32_t)(j / C::STAGES) & 1u) &&
-           ptx::globaltimer() - since < 1000000000ull) {
+           ptx::globaltimer() - since < pipe.limit) {
     }
   }
 }
@@ -366,7 +371,7 @@ __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem,
 #pragma unroll 1
   for (int j = 0; j < n; ++j, key0 += C::TILE) {
     const uint32_t st = smem0 + stage * C::STAGE;
-    pipe.wait(pipe.full + 8 * stage, parity, 0);
+    if (!pipe.wait(pipe.full + 8 * stage, parity, 0)) n = 0;   // (this piece comes to nothing)
     if (key0 + KW > lk) {
       // slots behind the end: zero scales
       if (key0 + lane >= lk) {
@@ -595,7 +600,8 @@ __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem,
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l[x][e] += __shfl_xor_sync(kFull, l[x][e], o);
 
-  const bool named = pipe.wait(pipe.named + 8 * ((k + 1) % C::PIECES), (uint32_t)((k + 1) / C::PIECES) & 1u, 3);
+  const bool named = __all_sync(kFull, *pipe.over == 0) &&
+                     pipe.wait(pipe.named + 8 * ((k + 1) % C::PIECES), (uint32_t)((k + 1) / C::PIECES) & 1u, 3);
   bool more = false;
   if (named) {
     const Job next = job_at<C>(pipe, k + 1);
@@ -604,8 +610,8 @@ __device__ __forceinline__ bool run_piece(const Stream4Params& P, uint8_t* smem,
   }
 
   // ---- The key groups' results meet in shared memory.
-  // (nobody reads q any more, whose place it is; nor, once a piece has not come in time,
-  // does any warp go on)
+  // (nobody reads q any more, whose place it is; nor, once a tile or a piece has not come
+  // in time, does any warp go on)
   if (ptx::bar_any(0, kThreads, !named)) return false;
   float2* ml = reinterpret_cast<float2*>(smem + C::AT_ML);   // [WK][RT]
   if (n > 0) {
@@ -682,11 +688,13 @@ __global__ void __launch_bounds__(kAll, (Cfg<D, NT, WM>::CTAS))
   pipe.pieces = reinterpret_cast<int*>(smem + C::AT_PIECE);
   pipe.over = &over;
   pipe.ws = P.ws;
+  pipe.limit = P.timeout_ns;
   if (threadIdx.x == 0) {
     over = 0;
 #pragma unroll
     for (int i = 0; i < C::STAGES; ++i) {
-      ptx::mbar_init(pipe.full + 8 * i, SMALL ? 33 : 1);   // (the lanes' arrivals)
+      // (the lanes' arrivals; to withhold a tile, one more, that nobody makes)
+      ptx::mbar_init(pipe.full + 8 * i, (SMALL ? 33 : 1) + (i == 0 && blockIdx.x == 0 ? P.withhold : 0));
       ptx::mbar_init(pipe.empty + 8 * i, kThreads / 32);
     }
 #pragma unroll

@@ -253,7 +253,9 @@ attn_status attn_fwd_noalloc(const attn_fwd_params *p, attn_stream_t stream);
  * if the kernel found packed offsets (cu_seqlens) decreasing or past
  * total_q / total_k (it then skipped that work and wrote nothing outside
  * the tensors; the call's output cannot be trusted), CUDA for a pending CUDA
- * error, else OK. */
+ * error, else OK. What a wait that ran out has left in the zeroed head of a
+ * workspace of attn_paged.h is cleared with the record, so that calls after
+ * it are in order again. */
 attn_status attn_fwd_check(void *workspace, attn_stream_t stream);
 
 /* Validates `p` and reports the launch plan without touching the GPU,

@@ -144,8 +144,9 @@ typedef struct attn_paged_params {
                                   from cu_seqlens_q[B] on are left as they are */
   void *workspace;             /* >= attn_paged_workspace_bytes(p), 256-byte aligned; its first
                                   ATTN_PAGED_ZEROED_BYTES zero-filled once before its first use
-                                  (every call leaves them zeroed). Calls that share a workspace
-                                  must not overlap. */
+                                  (every call leaves them zeroed, but for a wait that ran out:
+                                  then attn_fwd_check, which reports it, zeroes them). Calls
+                                  that share a workspace must not overlap. */
   size_t workspace_bytes;
   int64_t q_stride[3];         /* elements: [0] batch (unused when packed), [1] token, [2] head;
                                   multiples of 16 bytes */
@@ -210,6 +211,12 @@ attn_status attn_cache_append_blocks(const attn_cache_append_params *p, const at
 attn_status attn_cache_read_blocks(const attn_cache_read_params *p, const attn_block_scales *blocks,
                                    attn_stream_t stream);
 attn_status attn_paged_fwd_blocks(const attn_paged_params *p, const attn_block_scales *blocks, attn_stream_t stream);
+
+/* Testing only: attn_paged_fwd_blocks over an e2m1 cache (up to 64 rows that share
+ * keys; others are UNSUPPORTED) whose first CTA never hears of its first tile of keys,
+ * so that a bounded device wait runs out (limit 200 ms instead of 2 s) and
+ * attn_fwd_check reports ATTN_ERR_DEVICE_TIMEOUT. */
+attn_status attn_paged_fwd_withheld(const attn_paged_params *p, const attn_block_scales *blocks, attn_stream_t stream);
 
 /* Workspace bytes attn_paged_fwd needs for `p` on the current device (an
  * invalid `p` or NULL gives ATTN_PAGED_ZEROED_BYTES). Depends on sizes only,
