@@ -5,6 +5,7 @@
 
 #include "paged.h"
 #include "paged_host.h"
+#include "rows_host.h"
 #include "schedule.cuh"
 
 namespace {
@@ -131,6 +132,17 @@ attn_status check_rotary(const attn_cache_append_params* p, const attn_cache_rot
   return check_rows("q_out", r->q_out, r->q_out_stride, first, 3);
 }
 
+// Where the turned queries go, the other rows being in order.
+attn_status check_turned(const attn_cache_append_params* p, const attn_cache_rotary* r) {
+  const bool packed = p->cu_seqlens_q != nullptr;
+  const int64_t n0 = packed ? 1 : p->cache.batch, n1 = packed ? p->total_q : p->seqlen_q, dim = p->cache.head_dim;
+  const af::RowsAt q(r->q, n0, n1, r->num_heads_q, r->q_stride, dim),
+      q_out(r->q_out, n0, n1, r->num_heads_q, r->q_out_stride, dim),
+      k(p->k, n0, n1, p->cache.num_heads_kv, p->k_stride, dim), v(p->v, n0, n1, p->cache.num_heads_kv, p->v_stride, dim);
+  const char* wrong = af::misplaced(q_out, q, {k, v});
+  return wrong == nullptr ? ATTN_OK : report_error(ATTN_ERR_INVALID_ARG, "q_out %s", wrong);
+}
+
 attn_status check_append(const attn_cache_append_params* p, const attn_block_scales* blocks, const attn_cache_rotary* r) {
   if (p == nullptr) return report_error(ATTN_ERR_INVALID_ARG, "params is NULL");
   attn_status st = check_cache(p->cache);
@@ -145,6 +157,7 @@ attn_status check_append(const attn_cache_append_params* p, const attn_block_sca
   if (!rows) return ATTN_OK;
   if ((st = check_rows("k", p->k, p->k_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
   if ((st = check_rows("v", p->v, p->v_stride, packed ? 1 : 0, 3)) != ATTN_OK) return st;
+  if (r != nullptr && r->num_heads_q > 0 && (st = check_turned(p, r)) != ATTN_OK) return st;
   if ((st = check_offsets("seqlens_k", p->seqlens_k, true)) != ATTN_OK) return st;
   if ((st = check_offsets("cu_seqlens_q", p->cu_seqlens_q, false)) != ATTN_OK) return st;
   return check_workspace(p->workspace);

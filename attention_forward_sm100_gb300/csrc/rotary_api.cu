@@ -2,6 +2,7 @@
 #include <string.h>
 
 #include "rotary.h"
+#include "rows_host.h"
 
 namespace {
 
@@ -45,6 +46,15 @@ attn_status check(const attn_rotary_params* p) {
     if ((st = check_rows("k", p->k, p->k_stride, first)) != ATTN_OK) return st;
     if ((st = check_rows("k_out", p->k_out, p->k_out_stride, first)) != ATTN_OK) return st;
   }
+  const int64_t n0 = packed ? 1 : p->batch, n1 = packed ? p->total : p->seqlen;
+  const af::RowsAt q(p->q, n0, n1, p->num_heads_q, p->q_stride, p->head_dim),
+      k(p->k, n0, n1, p->num_heads_k, p->k_stride, p->head_dim),
+      q_out(p->q_out, n0, n1, p->num_heads_q, p->q_out_stride, p->head_dim),
+      k_out(p->k_out, n0, n1, p->num_heads_k, p->k_out_stride, p->head_dim);
+  if (const char* wrong = af::misplaced(q_out, q, {k, k_out}))
+    return report_error(ATTN_ERR_INVALID_ARG, "q_out %s", wrong);
+  if (const char* wrong = af::misplaced(k_out, k, {q, q_out}))
+    return report_error(ATTN_ERR_INVALID_ARG, "k_out %s", wrong);
   if (p->num_positions > 0 && (p->table == nullptr || !aligned(p->table, 16)))
     return report_error(ATTN_ERR_INVALID_ARG, "table must be non-NULL and 16-byte aligned");
   if (!aligned(p->positions, 4) || !aligned(p->seqlens, 4) || !aligned(p->cu_seqlens, 4))

@@ -76,7 +76,8 @@ def cache_append(k, v, k_cache, v_cache, block_table, seqlens_k, *, k_scale=None
     With ``rotary_table`` (fp32 [positions, R], see ``rotary``; R a multiple of
     16) the keys are turned on their way, in fp32, by their position in the cache
     or by ``positions`` (int32, one for every row); ``q``, bf16 queries of the
-    same rows, are turned too and returned (into ``out_q``, which may be ``q``).
+    same rows, are turned too and returned (into ``out_q``, which may be ``q``, but not
+    otherwise share memory with the call's rows).
 
     Asynchronous on ``stream`` (default: the current torch stream).
     """

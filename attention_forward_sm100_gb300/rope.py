@@ -71,7 +71,8 @@ def rotary(q, k, table, *, positions=None, seqlens=None, cu_seqlens=None, interl
     ``check``; rows in front of the first packed sequence and behind the last one
     stay as they are.
 
-    ``out_q`` and ``out_k`` may be ``q`` and ``k`` themselves. Strides are multiples
+    ``out_q`` and ``out_k`` may be ``q`` and ``k`` themselves, or parts of their memory with the
+    same strides that no row of the call uses; any other overlap is refused. Strides are multiples
     of 16 bytes and D a multiple of 8. Tables whose R is a multiple of 16 (8 with
     ``interleaved``) are read 16 bytes at a time, others value by value.
     Asynchronous on ``stream`` (default: the current torch stream).

@@ -190,7 +190,8 @@ typedef struct attn_cache_rotary {
                                   token goes in the cache */
   const void *q;               /* bf16, fixed [B][Sq][Hq][D] / packed [Tq][Hq][D]; NULL: none
                                   (num_heads_q = 0) */
-  void *q_out;                 /* bf16, q's shape, written; may be q itself with q's strides */
+  void *q_out;                 /* bf16, q's shape, written; may be q itself with q's strides, and
+                                  else shares no memory with the new rows (attn_rotary.h) */
   int64_t q_stride[3];         /* elements: [0] batch (unused when packed), [1] token, [2] head;
                                   multiples of 16 bytes */
   int64_t q_out_stride[3];

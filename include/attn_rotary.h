@@ -35,7 +35,9 @@ extern "C" {
 typedef struct attn_rotary_params {
   const void *q;               /* bf16: fixed [B][S][Hq][D] / packed [T][Hq][D] */
   const void *k;               /* the same with Hk heads; NULL: none (num_heads_k = 0) */
-  void *q_out;                 /* bf16, q's shape, written; may be q itself with q's strides */
+  void *q_out;                 /* bf16, q's shape, written; may be q itself with q's strides, and
+                                  else shares no memory with q or k (rows of other strides may
+                                  not even lie among q's), nor its rows with one another */
   void *k_out;
   const float *table;          /* [num_positions][rotary_dim] contiguous, 16-byte aligned: cosines,
                                   then sines */

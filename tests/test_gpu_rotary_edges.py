@@ -1,0 +1,52 @@
+"""Edges of rotary positions on the GPU: rows beside one another in one buffer."""
+import pytest
+import torch
+
+import paged4_reference as R4
+import paged_reference as R
+import test_gpu_rotary as T
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import attention_forward_sm100_gb300 as m
+    return m
+
+
+def test_outputs_beside_their_inputs(pkg):
+    """Outputs between the inputs' rows are written there; outputs across them are refused."""
+    buf = T.randn(2, 9, 12, 64, seed=31)
+    before = buf.clone()
+    table = R4.angles(9, 64)
+    at = torch.arange(9, device="cuda").repeat(2)
+    q, k, oq, ok = buf[:, :, :4], buf[:, :, 4:6], buf[:, :, 6:10], buf[:, :, 10:]
+    pkg.rotary(q, k, table, out_q=oq, out_k=ok)
+    pkg.check()
+    for x, o, part in ((q, oq, slice(0, 4)), (k, ok, slice(4, 6))):
+        assert torch.equal(x, before[:, :, part])
+        T.check_turned(o.flatten(0, 1), x.flatten(0, 1), table, at)
+    for out_q, out_k in ((buf[:, :, 1:5], None), (buf[:, :, 2:6], None), (None, buf[:, :, 3:5]), (oq, buf[:, :, 8:10]),
+                         (buf[:, :, ::2][:, :, :4], None)):
+        with pytest.raises(pkg.AttnError, match="shares memory|in one place"):
+            pkg.rotary(q, k, table, out_q=out_q, out_k=out_k)
+    with pytest.raises(pkg.AttnError, match="in one place"):
+        pkg.rotary(q, None, table, out_q=T.randn(1, 1, 1, 64).expand(2, 9, 4, 64))
+    assert torch.equal(buf[:, :, :6], before[:, :, :6])
+
+
+def test_append_refuses_queries_on_other_rows(pkg):
+    p = R.make([40, 30], [3, 3], 4, 2, 64, 16, seed=32)
+    fused = torch.cat([p.q, p.k_new, p.v_new], 2)
+    q, k, v = fused[:, :, :4], fused[:, :, 4:6], fused[:, :, 6:]
+    before = [x.clone() for x in (p.k_cache, p.v_cache, fused)]
+    table = R4.angles(40, 64)
+    for out in (fused[:, :, 1:5], fused[:, :, 2:6], fused[:, :, 4:8]):
+        with pytest.raises(pkg.AttnError, match="shares memory"):
+            pkg.cache_append(k, v, *p.cache, rotary_table=table, q=q, out_q=out)
+    pkg.check()
+    for x, y in zip((p.k_cache, p.v_cache, fused), before):
+        assert torch.equal(R.bits(x), R.bits(y))
+    assert pkg.cache_append(k, v, *p.cache, rotary_table=table, q=q, out_q=q) is q
+    T.check_turned(q.flatten(0, 1), p.q.flatten(0, 1), table, torch.tensor([37, 38, 39, 27, 28, 29], device="cuda"))
