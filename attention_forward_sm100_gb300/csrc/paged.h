@@ -62,7 +62,7 @@ struct AppendParams {
   const uint8_t* v;
   int64_t k_b, k_t, k_h, v_b, v_t, v_h;   // bytes
   int64_t tokens;
-  int32_t wide;                           // 1: k, v, q and their strides are multiples of 32 bytes
+  int32_t wide;                           // 1: k, v and their strides are multiples of 32 bytes
   int32_t block_tokens;                   // set by the launch, as `magic` and
   uint32_t magic;
   uint32_t* ws;

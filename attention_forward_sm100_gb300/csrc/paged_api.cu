@@ -672,8 +672,6 @@ attn_status attn_cache_append_blocks(const attn_cache_append_params* p, const at
   a.wide = wide_rows(p->k, p->k_stride, packed ? 1 : 0, 3) && wide_rows(p->v, p->v_stride, packed ? 1 : 0, 3);
   a.blocks = blocks_of(blocks);
   if (rotary != nullptr) {
-    const bool q = rotary->num_heads_q > 0;
-    a.wide = a.wide && (!q || wide_rows(rotary->q, rotary->q_stride, packed ? 1 : 0, 3));
     a.r.table = rotary->table;
     a.r.positions = rotary->positions;
     a.r.q = static_cast<const uint8_t*>(rotary->q);

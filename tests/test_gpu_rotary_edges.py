@@ -1,4 +1,5 @@
-"""Edges of rotary positions on the GPU: rows beside one another in one buffer."""
+"""Edges of rotary positions on the GPU: rows beside one another in one buffer, and on
+boundaries of 16 and 32 bytes."""
 import pytest
 import torch
 
@@ -50,3 +51,33 @@ def test_append_refuses_queries_on_other_rows(pkg):
         assert torch.equal(R.bits(x), R.bits(y))
     assert pkg.cache_append(k, v, *p.cache, rotary_table=table, q=q, out_q=q) is q
     T.check_turned(q.flatten(0, 1), p.q.flatten(0, 1), table, torch.tensor([37, 38, 39, 27, 28, 29], device="cuda"))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e2m1"])
+def test_append_whatever_the_rows_boundaries(pkg, kind):
+    """New rows and queries on 32-byte boundaries or odd multiples of 16 bytes, each by itself."""
+    lens_k, new, hq, hkv, dim, rot = [70, 33], 21, 4, 2, 128, 64
+    table = R4.angles(70, rot)
+    at = torch.cat([torch.arange(k - new, k) for k in lens_k]).cuda()
+    wants = None
+    for wide_q, wide_kv in ((True, True), (False, True), (True, False), (False, False)):
+        four = kind == "e2m1"
+        m = R4 if four else R
+        p = m.make(lens_k, [new] * 2, hq, hkv, dim, 32, seed=33, **({} if four else dict(fp8=kind == "e4m3")))
+        x = p.p if four else p
+
+        def placed(rows, wide):
+            room = torch.zeros(rows.shape[:-1] + (dim + 16,), dtype=torch.bfloat16, device="cuda")
+            at = 16 if wide else 8
+            room[..., at:at + dim] = rows
+            return room[..., at:at + dim]
+
+        q, k, v = placed(x.q, wide_q), placed(x.k_new, wide_kv), placed(x.v_new, wide_kv)
+        assert (q.data_ptr() % 32 == 0) == wide_q and (k.data_ptr() % 32 == 0) == wide_kv
+        got = pkg.cache_append(k, v, *p.cache, rotary_table=table, q=q, **p.scales)
+        pkg.check()
+        T.check_turned(got.flatten(0, 1), x.q.flatten(0, 1), table, at)
+        held = p.all() if four else [t for t in (p.k_cache, p.v_cache, p.k_scale, p.v_scale) if t is not None]
+        held = [R.bits(t) for t in held]
+        wants = wants or held
+        assert all(torch.equal(a, b) for a, b in zip(held, wants))
