@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads)
       }
       float f[E];
       if constexpr (ROT)
-        rotate_lanes<E, L>(in, f, P.r.table + (int64_t)s.angle * P.r.rot, P.r.rot, P.r.interleaved != 0, ok && !w.v);
+        rotate_lanes<L>(in, f, P.r.table + (int64_t)s.angle * P.r.rot, P.r.rot, P.r.interleaved != 0, ok && !w.v);
       uint8_t* dst = w.v ? P.c.v + s.page * P.c.v_page + s.slot * P.c.v_tok + w.h * P.c.v_head
                          : P.c.k + s.page * P.c.k_page + s.slot * P.c.k_tok + w.h * P.c.k_head;
       const int64_t at = (((int64_t)s.page * P.c.heads_kv + w.h) << P.c.page_shift) + s.slot;   // of its scales

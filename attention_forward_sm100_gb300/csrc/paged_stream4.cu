@@ -7,7 +7,8 @@
 // copy rate, and about 250 warp instructions at best. So
 //   * a warp of its own loads: TMA boxes for the codes of up to a tile's keys of a
 //     page, bulk copies for the two kinds of scales, six copies for every page of a
-//     tile, one per lane.
+//     tile by four lanes (K's and V's codes; two kinds of scales each). In pages of 16
+//     slots the lanes copy the scales themselves, 16 bytes at a time.
 //   * four warps compute, each on 32 keys of a tile of 128 (with 32 rows two warps
 //     share their keys), three CTAs per SM, two for more than 8 rows.
 //   * codes become f16 two at a time and are multiplied by their block's scale,

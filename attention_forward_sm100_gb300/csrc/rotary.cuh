@@ -286,24 +286,23 @@ inline int turn_tokens(const TurnShape& t, int64_t tokens, int threads, int most
   return best;
 }
 
-// Rotates the E = 8 or 16 values (pieces of eight) that each of the L lanes of a
+// Rotates the sixteen values (two pieces of eight) that each of the L lanes of a
 // vector holds; `x` their bf16 bits, `row` the position's line of the table, of
 // `rot` values (a multiple of 16). All lanes of the warp call it; where `on` is
 // false the values are only widened.
-template <int E, int L>
-__device__ __forceinline__ void rotate_lanes(const uint32_t (&x)[E / 2], float (&f)[E], const float* row, int rot,
+template <int L>
+__device__ __forceinline__ void rotate_lanes(const uint32_t (&x)[8], float (&f)[16], const float* row, int rot,
                                              bool interleaved, bool on) {
-  constexpr int P = E / 8;
   const int lane = threadIdx.x % L;
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) {
+  for (int i = 0; i < 8; ++i) {
     f[2 * i] = bf16_lo(x[i]);
     f[2 * i + 1] = bf16_hi(x[i]);
   }
   if (interleaved) {
 #pragma unroll
-    for (int s = 0; s < P; ++s) {
-      const int p = lane * P + s;
+    for (int s = 0; s < 2; ++s) {
+      const int p = 2 * lane + s;
       if (on && 8 * p < rot) {
         float c[4], n[4];
         load_angles<4>(row, 4 * p, c);
@@ -320,16 +319,15 @@ __device__ __forceinline__ void rotate_lanes(const uint32_t (&x)[E / 2], float (
     // the other of piece p's pairs is piece p + half or p - half, in another lane or in this one
     const int half = rot / 16;
 #pragma unroll
-    for (int s = 0; s < P; ++s) {
-      const int p = lane * P + s;
+    for (int s = 0; s < 2; ++s) {
+      const int p = 2 * lane + s;
       const bool first = p < half;
       const int q = first ? p + half : (p < 2 * half ? p - half : p);
       uint32_t y[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t mine = x[4 * s + i];
-        if (P == 2 && (half & 1)) mine = x[(4 * (s ^ 1) + i) % (E / 2)];   // (the other slot: half is odd)
-        y[i] = __shfl_sync(0xffffffffu, mine, q / P, L);
+        const uint32_t mine = x[4 * ((half & 1) ? s ^ 1 : s) + i];   // (half odd: the other's piece is in the other slot)
+        y[i] = __shfl_sync(0xffffffffu, mine, q / 2, L);
       }
       if (on && p < 2 * half) {
         float c[8], n[8];
