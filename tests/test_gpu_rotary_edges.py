@@ -81,3 +81,47 @@ def test_append_whatever_the_rows_boundaries(pkg, kind):
         held = [R.bits(t) for t in held]
         wants = wants or held
         assert all(torch.equal(a, b) for a, b in zip(held, wants))
+
+
+QUANTISED = {
+    # lens_k, lens_q, Hkv, D, page, packed, R, interleaved
+    "step": ([5, 16, 300], [1] * 3, 8, 128, 16, False, 128, False),
+    "chunk_interleaved": ([40, 100], [37, 37], 2, 128, 32, False, 64, True),
+    "forty_eight": ([70, 9, 200, 33], [70, 1, 0, 30], 3, 64, 32, True, 48, False),
+    "sixteen_interleaved": ([70, 9, 200, 33], [70, 1, 0, 30], 1, 64, 16, True, 16, True),
+    "112": ([8, 0, 130, 4], [0, 0, 129, 0], 5, 128, 64, True, 112, False),
+}
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("name", list(QUANTISED))
+def test_quantised_appends_with_positions_and_without_queries(pkg, name, kind):
+    """Positions other than the cache's, and keys that are turned with no queries beside
+    them, into caches whose kernels turn keys by themselves; bit for bit."""
+    lens_k, lens_q, hkv, dim, page, packed, rot, inter = QUANTISED[name]
+    table = R4.angles(500, rot)
+    for given in (True, False):
+        four = kind == "e2m1"
+        p = R4.make(lens_k, lens_q, hkv, hkv, dim, page, packed=packed, seed=34) if four else \
+            R.make(lens_k, lens_q, hkv, hkv, dim, page, fp8=True, packed=packed, seed=34)
+        x = p.p if four else p
+        rows = x.k_new.shape[:-2]
+        pos = torch.randint(0, 500, rows, generator=torch.Generator().manual_seed(35)).to(torch.int32).cuda()
+        at = pos.reshape(-1) if given else torch.cat([torch.arange(k - n, k) for k, n in zip(lens_k, lens_q)]).cuda()
+        if four:
+            want = R4.append(p, table, positions=at, interleaved=inter)
+        else:
+            new = p.k_new
+            p.k_new = R4.rotated(new.reshape(-1, hkv, dim), table, at, inter).view(new.shape)
+            want = R.append(p)
+            p.k_new = new
+        kw = dict(rotary_table=table, interleaved=inter, cu_seqlens_q=x.cu_q, **p.scales)
+        if given:
+            kw["positions"] = pos
+        assert pkg.cache_append(x.k_new, x.v_new, *p.cache, **kw) is None
+        pkg.check()
+        if four:
+            R4.same(p.all(), want)
+        else:
+            for g, w in zip((p.k_cache, p.v_cache, p.k_scale, p.v_scale), want):
+                assert torch.equal(R.bits(g), R.bits(w))
