@@ -16,7 +16,8 @@ from . import _binding
 from .paged import _on, _result
 
 
-def rotary_frequencies(dim, *, base=10000.0, factor=1.0, original_length=None, slow_turns=1.0, fast_turns=32.0):
+def rotary_frequencies(dim, *, base=10000.0, factor=1.0, original_length=None, slow_turns=1.0, fast_turns=32.0,
+                       ramp="log"):
     """Angle per position of each of the ``dim // 2`` pairs, float64 [dim // 2].
 
     Pair i turns by base ** (-2 i / dim). For contexts ``factor`` times as long
@@ -24,20 +25,44 @@ def rotary_frequencies(dim, *, base=10000.0, factor=1.0, original_length=None, s
     divided by ``factor`` (interpolated positions). With it, pairs that make
     ``fast_turns`` turns or more over the original length stay as they are, those
     that make ``slow_turns`` or fewer are divided, and between them the two are
-    mixed in proportion to the logarithm of the turns. (Scaling by a larger
+    mixed, in a way that a model was trained with and that ``ramp`` names:
+
+    - ``"log"``: in proportion to the logarithm of the turns;
+    - ``"turns"``: in proportion to the turns;
+    - ``"pairs"``: in proportion to i, between whole numbers: the last i with
+      ``fast_turns`` or more (0 at least) and the first with ``slow_turns`` or fewer
+      (dim - 1 at most), turns taken as a function of any real i.
+
+    With dim 128, base 10000, factor 32 and an original length of 4096, ``"log"``
+    and ``"pairs"`` are up to 2.1 times apart. (Scaling by a larger
     ``base`` needs nothing else.)
     """
     if dim < 2 or dim % 2:
         raise ValueError("dim must be even and at least 2")
     if not (base > 0 and factor > 0):
         raise ValueError("base and factor must be positive")
+    if ramp not in ("log", "turns", "pairs"):
+        raise ValueError("ramp must be 'log', 'turns' or 'pairs'")
     own = float(base) ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
     if original_length is None:
+        if ramp != "log":
+            raise ValueError("ramp goes with original_length")
         return own / factor
     if not (original_length > 0 and 0 < slow_turns < fast_turns):
         raise ValueError("original_length must be positive, and 0 < slow_turns < fast_turns")
     turns = original_length * own / (2 * math.pi)
-    keep = ((turns / slow_turns).log() / math.log(fast_turns / slow_turns)).clamp(0, 1)
+    if ramp == "log":
+        keep = ((turns / slow_turns).log() / math.log(fast_turns / slow_turns)).clamp(0, 1)
+    elif ramp == "turns":
+        keep = ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+    else:
+        if base <= 1:
+            raise ValueError("a ramp over pairs needs a base above 1: their turns must fall")
+        fast, slow = (dim * math.log(original_length / (2 * math.pi * n)) / (2 * math.log(base))
+                      for n in (fast_turns, slow_turns))   # i where a pair makes n turns
+        fast, slow = max(math.floor(fast), 0), min(math.ceil(slow), dim - 1)
+        i = torch.arange(dim // 2, dtype=torch.float64)
+        keep = ((slow - i) / (slow - fast)).clamp(0, 1) if slow > fast else (i <= fast).double()
     return own * keep + own / factor * (1 - keep)
 
 

@@ -1,8 +1,11 @@
-"""Rows that a rotation writes and where they may lie, without a GPU. (Calls that
-would be taken have no workspace, which is looked at last.)"""
+"""Frequencies of scaled positions, and rows that a rotation writes and where they may
+lie, without a GPU. (Calls that would be taken have no workspace, which is looked at
+last.)"""
+import math
 import random
 
 import pytest
+import torch
 
 import test_paged4_cpu as C4
 import test_paged_cpu as C
@@ -91,3 +94,42 @@ def test_queries_of_an_append(pkg, change, bad):  # noqa: F811
         p = C.APPEND.pack(*C._cache(**cache), 4 << 20, 5 << 20, 6 << 20, 0, 0, *(256, 128, 64) * 2, 1, 0)
         got = _verdict(L, L.attn_cache_append_blocks(p, blocks, C4._turn(**change), None))
         assert (got is None) == (bad is None) and (bad is None or bad in got)
+
+
+@pytest.mark.parametrize("dim,base,length,slow,fast", [
+    (128, 10000.0, 4096, 1.0, 32.0), (64, 1e6, 64, 0.5, 4.0), (64, 10000.0, 100, 1.0, 32.0), (128, 500000.0, 8192, 1.0, 4.0),
+    (8, 10.0, 12, 1.0, 1.25), (16, 1e4, 1 << 40, 1.0, 32.0), (32, 1e4, 3, 1.0, 32.0)])
+def test_ramps_between_kept_and_divided_frequencies(pkg, dim, base, length, slow, fast):  # noqa: F811
+    """Pair by pair with Python's own arithmetic; the bounds over pairs by counting."""
+    factor = 32.0
+
+    def turns(i):
+        return length * base ** (-2 * i / dim) / (2 * math.pi)
+
+    lo = max((i for i in range(-4 * dim, 4 * dim) if turns(i) >= fast), default=0)
+    hi = min((i for i in range(-4 * dim, 4 * dim) if turns(i) <= slow), default=dim - 1)
+    lo, hi = max(lo, 0), min(hi, dim - 1)
+    for ramp in ("log", "turns", "pairs"):
+        got = pkg.rotary_frequencies(dim, base=base, factor=factor, original_length=length, slow_turns=slow, fast_turns=fast,
+                                     ramp=ramp)
+        assert got.dtype == torch.float64 and got.shape == (dim // 2,)
+        for i in range(dim // 2):
+            w, t = base ** (-2 * i / dim), turns(i)
+            keep = {"log": math.log(t / slow) / math.log(fast / slow), "turns": (t - slow) / (fast - slow),
+                    "pairs": (hi - i) / (hi - lo) if hi > lo else float(i <= lo)}[ramp]
+            keep = min(max(keep, 0.0), 1.0)
+            # both terms are doubles of a few roundings each; of the shares, the logarithms' quotient most
+            assert abs(got[i].item() - (w * keep + w / factor * (1 - keep))) <= 2.0 ** -44 * w
+    same = pkg.rotary_frequencies(dim, base=base, factor=factor, original_length=length, slow_turns=slow, fast_turns=fast)
+    assert torch.equal(same, pkg.rotary_frequencies(dim, base=base, factor=factor, original_length=length, slow_turns=slow,
+                                                    fast_turns=fast, ramp="log"))
+
+
+def test_ramps_differ_as_documented(pkg):  # noqa: F811
+    f = [pkg.rotary_frequencies(128, factor=32.0, original_length=4096, ramp=r) for r in ("log", "pairs", "turns")]
+    assert 2.1 < (f[1] / f[0]).max().item() < 2.15
+    assert all(bool((x[:20] == f[0][:20]).all()) and bool((x[48:] * 32 / f[0][48:] / 32 - 1).abs().max() < 1e-12) for x in f)
+    for bad in (dict(ramp="linear"), dict(ramp="pairs"), dict(ramp="turns"),
+                dict(ramp="pairs", original_length=64, base=1.0), dict(ramp="pairs", original_length=64, base=0.5)):
+        with pytest.raises(ValueError):
+            pkg.rotary_frequencies(8, **bad)
