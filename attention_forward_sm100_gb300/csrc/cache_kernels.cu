@@ -279,9 +279,9 @@ __device__ __forceinline__ void append_rows(const TurnedAppendParams& P, int blo
         return s.angle;
       });
 }
-// An append with rotation into a bf16 cache. With four blocks to an SM (64 registers, a few
-// of them spilled) 41690 tokens, 32 query heads and 8 of 128 in the cache, took 169 us of a
-// floor of 152, with three 180.
+// An append with rotation into a bf16 cache: four blocks to an SM (64 registers, a few of
+// them spilled). 41690 tokens, 32 query heads and 8 of 128 in the cache, floor 152 us, caches
+// flushed, four blocks / three: pairs apart 168 / 186, neighbouring pairs 164 / 160.
 template <bool APART>
 __global__ void __launch_bounds__(kThreads, 4) append_rows_kernel(const __grid_constant__ TurnedAppendParams P) {
   __shared__ Slot slots[kMaxTokens];

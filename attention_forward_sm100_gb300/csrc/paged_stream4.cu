@@ -20,10 +20,12 @@
 //     piece and its last. The first is counted in when it has been left, but whether it
 //     is the last to come, and joins, is looked at in the end.
 // Measured, GQA 32/8, 128 depths: 16 sequences of up to 32768 keys 78 us (floor 54, the
-// loads alone 68), 64 of up to 8192 82 (50), one of 777 10.1; 24 of up to 4097, five new
-// tokens, 16 heads of 64 depths, pages of 16 slots, 35 (11). Instruction issue bounds it
-// (54 % of the slots in the mean, start and end included), and fetch: a loop of 730
-// instructions, a third of whose stalls are for the next one.
+// loads alone 68), 64 of up to 8192 82 (50), one of 777 9.9; 24 of up to 4097, five new
+// tokens, 16 heads of 64 depths, pages of 16 slots, 35 (11). Issue bounds it: 632 warp
+// instructions for 32 keys of a head (smsp__inst_executed of the first of these, loading,
+// start and end included) take 57 % of the slots in the mean and 50 % of the integer
+// pipe's; a warp waits for a fixed latency 1.3 times per instruction issued, for its turn
+// 0.9, for a pipe 0.7, for memory 0.7, for its next instruction 0.3.
 // Tried (us for these, with 44 for the last, in this order, and a step of 32 sequences of up to 4096 with rotation
 // and append, 41.5):
 //   each thread copying its own 16-byte pieces (cp.async): 96, 97, 9.7, 42, -

@@ -143,9 +143,10 @@ def paged_forward(q, k_cache, v_cache, block_table, seqlens_k, *, causal=True, s
 
     A 4-bit cache is read exactly by up to 64 rows. More of them take a bf16 copy of
     the sequences in scratch memory, as above (code * block scale * scale rounded to
-    bf16: without effect for scales that are powers of two), where that fits 1 GiB;
-    elsewhere rows go through the cache 32 at a time, so that a tight
-    ``max_seqlen_k`` matters there.
+    bf16: without effect for scales that are powers of two), where that fits 1 GiB:
+    4 * Hkv * D bytes times B times ``max_seqlen_k``, whatever the lengths are.
+    Elsewhere rows go through the cache 32 at a time, several times as slow, so a
+    tight ``max_seqlen_k`` matters, and calls of fewer sequences are faster.
 
     Asynchronous on ``stream`` (default: the current torch stream).
     """

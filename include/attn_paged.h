@@ -38,8 +38,8 @@
  *             O_i   = sum_{j in J_i} exp(s_ij - LSE_i) * V_j     bf16, rounded once
  *           (the causal mask is aligned to the END of the keys: the new
  *           tokens are the last ones cached). The weights are rounded to bf16
- *           before the P.V product, as in attn_fwd (to f16 where an e4m3 cache
- *           allows); sums and the softmax statistics are fp32. Over an e4m3 cache,
+ *           before the P.V product, as in attn_fwd (to f16 where an e4m3 cache,
+ *           or up to 64 rows over an e2m1 one, allows); sums and the softmax statistics are fp32. Over an e4m3 cache,
  *           calls of more than 32 rows (seqlen_q * Hq / Hkv) round more:
  *             V: code * scale, to bf16, once.
  *             K, D = 64: the same.
